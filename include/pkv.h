@@ -56,6 +56,7 @@ extern "C" {
 #define PKV_DERR_SLOT_RANGE 0x100  /* a slot read from a table was outside [0, num_slots)     */
 #define PKV_DERR_TIMEOUT    0x200  /* a bounded wait inside a kernel gave up (low byte: which) */
 #define PKV_DERR_POSITION   0x400  /* a work item addressed positions outside its row         */
+#define PKV_DERR_NO_PAGES   0x800  /* a step needs more pages than the free list has           */
 
 const char *pkv_strerror(int code);
 int pkv_version(void);  /* major*10000 + minor*100 + patch */
@@ -326,6 +327,93 @@ int pkv_attn_decode_noalloc(const pkv_pool *pool, const pkv_batch *batch, const 
  * call itself it allocates nothing; on a device with no earlier call it looks up the array's
  * address first. */
 int pkv_get_noalloc_device_error(void *stream, int32_t *raw);
+
+/* ------------------------------------------------------------------------------------ */
+/* the block-scaled 8-bit pool: a serving step that stays on the device                   */
+/*                                                                                      */
+/* A cache of e4m3 codes in pages of page_size tokens, with one exponent byte per (page,  */
+/* KV head) for K and one for V: a code c under byte b stands for c * 2^(b - 127).  ([RT] */
+/* §显存分级管理机制 names an fp8_e4m3 KV dtype; here its scale follows the data instead of */
+/* being one number for the whole pool.)  A power of two divides a bf16 value exactly, so a */
+/* stored code is one rounding of its value, and a page whose scale has to grow is rescaled */
+/* without a second rounding (but for e4m3's subnormals).  Bytes are in [10, 245]; another  */
+/* one is read as the nearer end of that range.                                            */
+/* The four calls below make a step: tables and slots from the requests' lengths, the store  */
+/* of the new rows, attention over the pages.  Page ids are pkv_batch's (page_size > 1):     */
+/* position t of a request is slot req_to_token[row][t / P] * P + t % P.                     */
+
+typedef struct pkv_block_pool {
+    void    *k;            /* device, slot s's K row of [num_kv_heads][head_dim] codes at byte  */
+                           /* s * slot_stride; 16-byte aligned                                */
+    void    *v;            /* device, the same for V                                          */
+    uint8_t *k_exp;        /* device, [num_pages][num_kv_heads]                               */
+    uint8_t *v_exp;
+    int64_t  num_pages;    /* num_pages * page_size * num_kv_heads must be < 2^31             */
+    int32_t  page_size;    /* 16, 32, 64, 128 or 256                                          */
+    int32_t  num_kv_heads;
+    int32_t  head_dim;     /* 64 or 128                                                       */
+    int64_t  slot_stride;  /* bytes from one slot's row to the next, a multiple of 16; 0 means */
+                           /* num_kv_heads * head_dim                                         */
+} pkv_block_pool;
+
+/* A step's tables from the requests' lengths, on the device (pkv_fill_batch_table and the slot
+ * allocator do this on the host).  Request r has seq_lens[r] positions after the step, the last
+ * new_lens[r] of them new (0 <= new_lens[r] <= seq_lens[r]).  With had = ceil((seq - new) / P)
+ * and has = ceil(seq / P), its table entries [had, has) receive the next has - had pages of the
+ * free list, in request order.  Query row qo_indptr[r] + i is new token i of request r:
+ *   positions[..]      its position seq - new + i
+ *   out_cache_loc[..]  its slot
+ * Both maps hold -1 from the last token to cap.
+ *   batch          req_to_token is written (rows of different requests must differ); page_size
+ *                  any power of two up to 4096, 0 or 1 = a token table; batch <= 16384
+ *   free_pages     device int32 [num_free]; entries [*free_head, num_free) are free
+ *   free_head      device int32; *free_head_out receives it plus the pages taken (the two may
+ *                  be the same word)
+ *   out_cache_loc, positions  device int32 [cap]
+ *   qo_indptr      device int32 [batch + 1]
+ *   workspace      device, >= 256 bytes, zeroed once; its first word is the error word.  Calls
+ *                  that may overlap on the GPU need a workspace each.
+ * A step that has a request with lengths or a row out of range, or more than cap new tokens
+ * (PKV_DERR_POSITION), or too few free pages (PKV_DERR_NO_PAGES), is refused whole: no table
+ * entry is written, the maps hold -1 everywhere, qo_indptr 0, and the head stays. */
+int pkv_build_block_tables(const pkv_batch *batch, const int32_t *new_lens, const int32_t *free_pages,
+                           int64_t num_free, const int32_t *free_head, int32_t *free_head_out,
+                           int32_t *out_cache_loc, int32_t *positions, int64_t cap, int32_t *qo_indptr,
+                           void *workspace, size_t ws_bytes, void *stream);
+
+/* Quantises new K/V rows into their slots.  Arguments as pkv_kv_store, and: tokens of one page
+ * stand next to each other in the call, at consecutive slots (the order pkv_build_block_tables
+ * gives), and a page's rows are filled from its offset 0 on.  Per KV head and tensor, the run of
+ * a page's new tokens needs the smallest exponent e with max |x| <= 448 * 2^e over its finite
+ * values.  A run that starts its page (offset 0) sets that exponent; what the page held before
+ * is dead.  A later run keeps the page's exponent if that is as large, else raises it and
+ * rescales the page's earlier rows.  Codes are x * 2^-e rounded to nearest even, saturating;
+ * infinities saturate, NaN is stored as NaN (0x7F).
+ *   out_cache_loc  -1 is padding and skipped; another slot outside the pool is skipped and sets
+ *                  PKV_DERR_SLOT_RANGE in the workspace's error word (workspace may be NULL) */
+int pkv_kv_store_block(const pkv_block_pool *pool, const void *k_new, const void *v_new,
+                       const int32_t *out_cache_loc, int64_t n, void *workspace, void *stream);
+
+/* Decode over a block-scaled pool: one query per request (row r of q, [batch][num_q_heads]
+ * [head_dim] bf16) over its positions [0, seq_lens[r]), its own just-stored token included.
+ * There is no plan: the work is divided on the device from seq_lens, so a captured graph follows
+ * lengths, rows and tables that change between replays.  A request of length 0 gets zeros (a
+ * padded batch), and so does one whose row or length is out of range, which also sets
+ * PKV_DERR_POSITION; a page outside the pool reads as zero rows and sets PKV_DERR_SLOT_RANGE.
+ * num_q_heads / num_kv_heads is 1, 2, 4 or 8.  Accumulation is fp32; weights enter the product
+ * as f16 (11 bits), codes exactly.
+ *   workspace  device, 256-byte aligned, >= pkv_decode_block_workspace bytes (whatever the
+ *              batch), first word zeroed once.  Calls that may overlap on the GPU need one each. */
+int pkv_decode_block_workspace(const pkv_block_pool *pool, int32_t num_q_heads, size_t *bytes);
+int pkv_attn_decode_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o,
+                          int32_t num_q_heads, float sm_scale, void *workspace, size_t ws_bytes, void *stream);
+
+/* pkv_attn_extend over a block-scaled pool: the same plans (pkv_plan_extend, cascade included,
+ * without fuse_store), workspace and errors.  Each key run is turned once into the bf16 values its
+ * codes stand for. */
+int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o, float sm_scale,
+                          const pkv_plan_info *info, const void *plan_dev, void *workspace, size_t ws_bytes,
+                          void *stream);
 
 /* ------------------------------------------------------------------------------------ */
 /* host radix tree ([RC]): token ids -> pool slots, with LRU eviction and lock_ref       */

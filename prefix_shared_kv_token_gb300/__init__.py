@@ -16,6 +16,11 @@ memory -- and forwards to the library.  Names follow the C entry points without 
                   and straight into the gathered rows (the gather reads cached positions only)
     plan_extend_ctx / attn_extend_ctx  chunked prefill over a caller-kept context buffer: each
                   chunk is stored into the pool and its context rows in one pass, nothing gathered
+    BlockPool     an 8-bit pool with an exponent per page and KV head; its calls follow lengths and
+                  tables that live on the device, so a decode step can be captured whole:
+    build_block_tables  page table entries, slots and positions of a step from its lengths
+    kv_store_block  scatter new K/V rows into pages, raising a page's exponent where they need it
+    attn_decode_block / attn_extend_block  the two attention calls over such a pool
     RadixTree     host radix tree: match_prefix (with split), insert, LRU evict, lock_ref,
                   cascade extraction
     Allocator     token-slot free list
@@ -30,12 +35,13 @@ from dataclasses import dataclass
 
 import numpy as np
 
-from ._lib import (PKV_BF16, PKV_FP8_E4M3, PkvBatch, PkvCascade, PkvError, PkvPlanInfo, PkvPlanOpts, PkvPool,
+from ._lib import (PKV_BF16, PKV_FP8_E4M3, PkvBatch, PkvBlockPool, PkvCascade, PkvError, PkvPlanInfo, PkvPlanOpts, PkvPool,
                    check, lib)
 
 __all__ = ["Pool", "Batch", "Plan", "Cascade", "kv_store", "check_out_cache_loc", "plan_decode", "plan_extend",
            "plan_extend_ctx", "attn_decode", "attn_extend", "attn_extend_store", "attn_extend_ctx", "get_device_error", "get_noalloc_device_error", "set_kernel_events",
-           "set_wait_limit_ns", "get_wait_limit_ns", "fill_batch_table",
+           "set_wait_limit_ns", "get_wait_limit_ns", "fill_batch_table", "BlockPool", "build_block_tables",
+           "kv_store_block", "decode_block_workspace", "attn_decode_block", "attn_extend_block",
            "RadixTree", "Allocator", "PkvError", "version"]
 
 
@@ -107,6 +113,71 @@ class Pool:
         return PkvPool(_ptr(self.k), _ptr(self.v), self.k.shape[0], self.k.shape[1], self.k.shape[2],
                        PKV_BF16 if self.dtype == "bf16" else PKV_FP8_E4M3, self.k_scale, self.v_scale,
                        int(self.k.stride(0)))
+
+
+def _on_gpu(name, t, dtype, *shape) -> None:
+    """A contiguous tensor of the given dtype and shape (None: any extent) on the current device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor, got {t.dtype}")
+    if len(shape) != t.dim() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+@dataclass(frozen=True)
+class BlockPool:
+    """Block-scaled 8-bit pool: k, v uint8 e4m3 codes [num_pages * page_size, num_kv_heads,
+    head_dim] (dense, or the two halves of an interleaved array), k_exp, v_exp uint8 exponent
+    bytes [num_pages, num_kv_heads].  A code c under byte b stands for c * 2^(b - 127)."""
+    k: object
+    v: object
+    k_exp: object
+    v_exp: object
+    page_size: int
+
+    @classmethod
+    def allocate(cls, num_pages, page_size, num_kv_heads, head_dim, device="cuda", layout="separate"):
+        import torch
+        slots = num_pages * page_size
+        if layout == "interleaved":
+            kv = torch.zeros((slots, 2, num_kv_heads, head_dim), dtype=torch.uint8, device=device)
+            k, v = kv[:, 0], kv[:, 1]
+        elif layout == "separate":
+            k = torch.zeros((slots, num_kv_heads, head_dim), dtype=torch.uint8, device=device)
+            v = torch.zeros_like(k)
+        else:
+            raise ValueError(f"unknown pool layout {layout!r}")
+        exps = torch.full((2, num_pages, num_kv_heads), 127, dtype=torch.uint8, device=device)
+        return cls(k, v, exps[0], exps[1], int(page_size))
+
+    def __post_init__(self):
+        import torch
+        k, v = self.k, self.v
+        for name, t in (("k", k), ("v", v), ("k_exp", self.k_exp), ("v_exp", self.v_exp)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.device != k.device:
+                raise ValueError(f"BlockPool.{name} must be a uint8 tensor on the pool's device")
+        if k.dim() != 3 or v.shape != k.shape or v.stride() != k.stride() or k.stride(2) != 1 or k.stride(1) != k.shape[2]:
+            raise ValueError("BlockPool.k and .v must be [slots, heads, head_dim] with dense rows and equal strides")
+        if self.page_size < 1 or k.shape[0] % self.page_size:
+            raise ValueError("BlockPool holds whole pages: slots must be a multiple of page_size")
+        pages = k.shape[0] // self.page_size
+        for name, t in (("k_exp", self.k_exp), ("v_exp", self.v_exp)):
+            if tuple(t.shape) != (pages, k.shape[1]) or not t.is_contiguous():
+                raise ValueError(f"BlockPool.{name} must be contiguous [pages, heads] = {(pages, k.shape[1])}")
+        object.__setattr__(self, "_c", PkvBlockPool(_ptr(k), _ptr(v), _ptr(self.k_exp), _ptr(self.v_exp), pages,
+                                                    int(self.page_size), k.shape[1], k.shape[2], int(k.stride(0))))
+
+    @property
+    def num_pages(self):
+        return self.k_exp.shape[0]
+
+    def c(self) -> PkvBlockPool:
+        import torch
+        if not self.k.is_cuda or self.k.device.index != torch.cuda.current_device():
+            raise ValueError("BlockPool is not on the current CUDA device")
+        return self._c
 
 
 @dataclass
@@ -272,6 +343,94 @@ def attn_extend_ctx(pool: Pool, q, o, sm_scale, k_new, v_new, out_cache_loc, ctx
         C.byref(p), _ptr(q), _ptr(o), float(sm_scale), _ptr(k_new), _ptr(v_new), _ptr(out_cache_loc), _ptr(ctx_k),
         _ptr(ctx_v), int(ctx_k.shape[0]), C.byref(plan.info), _ptr(plan_dev), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------------------
+# the block-scaled 8-bit pool
+
+
+def _workspace(workspace) -> int:
+    _on_gpu("workspace", workspace, workspace.dtype, *workspace.shape)
+    return workspace.numel() * workspace.element_size()
+
+
+def _block_batch(batch: Batch) -> PkvBatch:
+    import torch
+    _on_gpu("req_to_token", batch.req_to_token, torch.int32, None, None)
+    _on_gpu("req_pool_indices", batch.req_pool_indices, torch.int32, None)
+    _on_gpu("seq_lens", batch.seq_lens, torch.int32, batch.req_pool_indices.shape[0])
+    return batch.c()
+
+
+def build_block_tables(req_to_token, req_pool_indices, seq_lens, new_lens, free_pages, free_head, free_head_out,
+                       out_cache_loc, positions, qo_indptr, page_size, workspace, stream=None) -> None:
+    """Page table entries, slots, positions and query offsets of a step from its lengths (see
+    pkv_build_block_tables); every argument is an int32 tensor on the GPU, req_to_token is written
+    in place."""
+    import torch
+    batch = Batch(req_to_token, req_pool_indices, seq_lens, int(page_size))
+    b = _block_batch(batch)
+    n = req_pool_indices.shape[0]
+    _on_gpu("new_lens", new_lens, torch.int32, n)
+    _on_gpu("free_pages", free_pages, torch.int32, None)
+    _on_gpu("free_head", free_head, torch.int32, 1)
+    _on_gpu("free_head_out", free_head_out, torch.int32, 1)
+    _on_gpu("out_cache_loc", out_cache_loc, torch.int32, None)
+    _on_gpu("positions", positions, torch.int32, out_cache_loc.shape[0])
+    _on_gpu("qo_indptr", qo_indptr, torch.int32, n + 1)
+    size = _workspace(workspace)
+    check("pkv_build_block_tables", lib.pkv_build_block_tables(
+        C.byref(b), _ptr(new_lens), _ptr(free_pages), free_pages.shape[0], _ptr(free_head), _ptr(free_head_out),
+        _ptr(out_cache_loc), _ptr(positions), out_cache_loc.shape[0], _ptr(qo_indptr), _ptr(workspace), size,
+        _stream(stream)))
+
+
+def kv_store_block(pool: BlockPool, k_new, v_new, out_cache_loc, workspace=None, stream=None) -> None:
+    """Quantises k_new, v_new (bf16 [n, heads, head_dim]) into the slots out_cache_loc; tokens of
+    one page are neighbours at consecutive slots, -1 is padding (see pkv_kv_store_block)."""
+    import torch
+    p = pool.c()
+    _on_gpu("out_cache_loc", out_cache_loc, torch.int32, None)
+    n = out_cache_loc.shape[0]
+    _on_gpu("k_new", k_new, torch.bfloat16, n, p.num_kv_heads, p.head_dim)
+    _on_gpu("v_new", v_new, torch.bfloat16, n, p.num_kv_heads, p.head_dim)
+    check("pkv_kv_store_block", lib.pkv_kv_store_block(C.byref(p), _ptr(k_new), _ptr(v_new), _ptr(out_cache_loc), n,
+                                                       _ptr(workspace), _stream(stream)))
+
+
+def decode_block_workspace(pool: BlockPool, num_q_heads: int) -> int:
+    """Bytes of attn_decode_block's workspace (whatever the batch)."""
+    n = C.c_size_t(0)
+    check("pkv_decode_block_workspace", lib.pkv_decode_block_workspace(C.byref(pool._c), int(num_q_heads), C.byref(n)))
+    return n.value
+
+
+def attn_decode_block(pool: BlockPool, batch: Batch, q, o, sm_scale, workspace, stream=None) -> None:
+    """One query per request (q, o bf16 [batch, num_q_heads, head_dim]) over its pages; no plan, and
+    a request of length 0 gets zeros (see pkv_attn_decode_block)."""
+    import torch
+    p, b = pool.c(), _block_batch(batch)
+    _on_gpu("q", q, torch.bfloat16, b.batch, None, p.head_dim)
+    _on_gpu("o", o, torch.bfloat16, *q.shape)
+    size = _workspace(workspace)
+    check("pkv_attn_decode_block", lib.pkv_attn_decode_block(C.byref(p), C.byref(b), _ptr(q), _ptr(o), q.shape[1],
+                                                             float(sm_scale), _ptr(workspace), size, _stream(stream)))
+
+
+def attn_extend_block(pool: BlockPool, batch: Batch, q, o, sm_scale, plan: Plan, plan_dev, workspace,
+                      stream=None) -> None:
+    """attn_extend over a block-scaled pool (the same plans and workspace)."""
+    import torch
+    p, b = pool.c(), _block_batch(batch)
+    _on_gpu("q", q, torch.bfloat16, plan.info.total_q, plan.info.num_q_heads, p.head_dim)
+    _on_gpu("o", o, torch.bfloat16, *q.shape)
+    _on_gpu("plan_dev", plan_dev, torch.uint8, None)
+    if plan_dev.shape[0] < plan.info.plan_bytes:
+        raise ValueError("plan_dev is shorter than the plan")
+    size = _workspace(workspace)
+    check("pkv_attn_extend_block", lib.pkv_attn_extend_block(C.byref(p), C.byref(b), _ptr(q), _ptr(o), float(sm_scale),
+                                                             C.byref(plan.info), _ptr(plan_dev), _ptr(workspace), size,
+                                                             _stream(stream)))
 
 
 def get_device_error(workspace, stream=None) -> int:

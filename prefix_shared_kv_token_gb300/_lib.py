@@ -29,6 +29,12 @@ class PkvPool(C.Structure):
                 ("slot_stride", C.c_int64)]
 
 
+class PkvBlockPool(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
+                ("num_pages", C.c_int64), ("page_size", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("slot_stride", C.c_int64)]
+
+
 class PkvBatch(C.Structure):
     _fields_ = [("req_to_token", C.c_void_p), ("stride", C.c_int64), ("num_rows", C.c_int32),
                 ("req_pool_indices", C.c_void_p), ("seq_lens", C.c_void_p), ("batch", C.c_int32),
@@ -79,6 +85,12 @@ SIGNATURES = {
                                   _P, _SZ, _P]),
     "pkv_attn_extend": (C.c_int, [C.POINTER(PkvPool), C.POINTER(PkvBatch), _P, _P, _F, C.POINTER(PkvPlanInfo), _P,
                                   _P, _SZ, _P]),
+    "pkv_build_block_tables": (C.c_int, [C.POINTER(PkvBatch), _P, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "pkv_kv_store_block": (C.c_int, [C.POINTER(PkvBlockPool), _P, _P, _P, _I64, _P, _P]),
+    "pkv_decode_block_workspace": (C.c_int, [C.POINTER(PkvBlockPool), _I32, C.POINTER(_SZ)]),
+    "pkv_attn_decode_block": (C.c_int, [C.POINTER(PkvBlockPool), C.POINTER(PkvBatch), _P, _P, _I32, _F, _P, _SZ, _P]),
+    "pkv_attn_extend_block": (C.c_int, [C.POINTER(PkvBlockPool), C.POINTER(PkvBatch), _P, _P, _F,
+                                        C.POINTER(PkvPlanInfo), _P, _P, _SZ, _P]),
     "pkv_get_device_error": (C.c_int, [_P, _P, _PI32]),
     "pkv_set_kernel_events": (C.c_int, [_P, _P]),
     "pkv_set_wait_limit_ns": (C.c_int, [C.c_uint64]),

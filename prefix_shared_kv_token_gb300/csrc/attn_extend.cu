@@ -42,6 +42,7 @@
 #include <algorithm>
 
 #include "../../include/pkv.h"
+#include "block.cuh"
 #include "common.cuh"
 #include "launch.h"
 
@@ -140,6 +141,10 @@ struct GatherParams {
     uint4 *q_out;
     const int32_t *q_rows;
     int32_t q_batch, q_row_vecs;
+    // block-scaled pools: exponent bytes [page][Hkv] of 2^block_shift slots a page
+    const uint8_t *k_exp;
+    const uint8_t *v_exp;
+    int32_t block_shift;
     int32_t *err;
     int32_t pdl_wait_start;  // 1: wait for the preceding kernel first; 0: it wrote nothing this
                              // gather reads, wait for it only before exiting
@@ -147,18 +152,23 @@ struct GatherParams {
 
 // One CTA per unit of <= 32 keys: thread t moves 16-byte pieces of the units' slot rows
 // (Hkv * D elements, contiguous in the pool and in the output).
-template <int D, bool FP8>
+// What the pool holds: bf16 rows, e4m3 codes under a scale of the whole pool (converted as they
+// are, the scale applied to the logits and the output), or codes under an exponent per page and KV
+// head (converted to the values they stand for, which are bf16 values).
+enum class Rows { kBf16, kFp8, kBlock };
+
+template <int D, Rows R>
 PKV_DEV void gather_body(const GatherParams &p);
 
-template <int D, bool FP8>
+template <int D, Rows R>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
     if (p.pdl_wait_start) pdl_wait();  // the pool rows and tables may come from the preceding kernel
     pdl_trigger();
-    gather_body<D, FP8>(p);
+    gather_body<D, R>(p);
     if (!p.pdl_wait_start) pdl_wait();  // complete only after the preceding kernel
 }
 
-template <int D, bool FP8>
+template <int D, Rows R>
 PKV_DEV void gather_body(const GatherParams &p) {
     if ((int)blockIdx.x >= p.nunits) {  // a query row
         const int i = blockIdx.x - p.nunits, r = __ldg(p.q_rows + i);
@@ -207,7 +217,7 @@ PKV_DEV void gather_body(const GatherParams &p) {
             const int32_t slot = s_slot[key];
             if (slot < 0) continue;
             const uint8_t *pool = tensor ? p.v_pool : p.k_pool;
-            if constexpr (!FP8) {
+            if constexpr (R == Rows::kBf16) {
                 y[k] = __ldg(reinterpret_cast<const uint4 *>(pool + (int64_t)slot * p.slot_bytes) + v);
             } else {
                 const uint2 x = __ldg(reinterpret_cast<const uint2 *>(pool + (int64_t)slot * p.slot_bytes) + v);
@@ -215,6 +225,15 @@ PKV_DEV void gather_body(const GatherParams &p) {
                 y[k].y = e4m3x2_to_bf16x2((uint16_t)(x.x >> 16));
                 y[k].z = e4m3x2_to_bf16x2((uint16_t)(x.y & 0xFFFFu));
                 y[k].w = e4m3x2_to_bf16x2((uint16_t)(x.y >> 16));
+                if constexpr (R == Rows::kBlock) {
+                    const uint8_t *exps = tensor ? p.v_exp : p.k_exp;
+                    const uint32_t e = clamp_exp(__ldg(exps + (int64_t)(slot >> p.block_shift) * p.hkv + v / (D / 8)));
+                    const uint32_t f = (e << 7) | (e << 23);  // 2^(e - 127), twice
+                    y[k].x = mul_bf16x2(y[k].x, f);
+                    y[k].y = mul_bf16x2(y[k].y, f);
+                    y[k].z = mul_bf16x2(y[k].z, f);
+                    y[k].w = mul_bf16x2(y[k].w, f);
+                }
             }
         }
 #pragma unroll
@@ -827,7 +846,8 @@ static int dispatch_extend(int G, const ExtendParams &p, const XMaps &mp, int n,
 
 template <int D>
 static int launch_gather(const GatherParams &p, bool fp8, int nunits, cudaStream_t s) {
-    return launch_pdl(fp8 ? gather_kernel<D, true> : gather_kernel<D, false>, dim3(nunits), dim3(256), 0, s, true, p) ==
+    auto kern = !fp8 ? gather_kernel<D, Rows::kBf16> : p.k_exp ? gather_kernel<D, Rows::kBlock> : gather_kernel<D, Rows::kFp8>;
+    return launch_pdl(kern, dim3(nunits), dim3(256), 0, s, true, p) ==
                    cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
@@ -908,6 +928,8 @@ int decode_span_gather(const pkv_pool *pool, const pkv_batch *batch, const void 
     gp.units = reinterpret_cast<const GatherUnit *>(plan + info->offsets[9]);
     gp.k_out = b.kg;
     gp.v_out = b.vg;
+    gp.k_exp = gp.v_exp = nullptr;
+    gp.block_shift = 0;
     gp.err = reinterpret_cast<int32_t *>(ws);
     gp.pdl_wait_start = 1;
     // one launch: the span keys, then the member query rows
@@ -1040,7 +1062,7 @@ namespace pkv {
 static int extend_call(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o, float sm_scale,
                        const void *k_new, const void *v_new, const int32_t *out_cache_loc, bool store,
                        const pkv_plan_info *info, const void *plan_dev, void *workspace, size_t ws_bytes,
-                       void *stream) {
+                       void *stream, const pkv_block_pool *block = nullptr) {
     int rc = check_call(pool, batch, q, o, info, plan_dev, workspace, ws_bytes, 2);
     if (rc) return rc;
     if (info->offsets[16] != (store ? 2 : 0)) return PKV_E_PLAN;
@@ -1075,6 +1097,9 @@ static int extend_call(const pkv_pool *pool, const pkv_batch *batch, const void 
     gp.units = reinterpret_cast<const GatherUnit *>(plan + info->offsets[4]);
     gp.k_out = kg;
     gp.v_out = vg;
+    gp.k_exp = block ? block->k_exp : nullptr;
+    gp.v_exp = block ? block->v_exp : nullptr;
+    gp.block_shift = block ? log2_of(block->page_size) : 0;
     gp.err = reinterpret_cast<int32_t *>(ws);
     gp.pdl_wait_start = 1;
     const int nunits = (int)info->offsets[5];
@@ -1104,6 +1129,28 @@ extern "C" int pkv_attn_extend(const pkv_pool *pool, const pkv_batch *batch, con
                                void *stream) {
     return pkv::extend_call(pool, batch, q, o, sm_scale, nullptr, nullptr, nullptr, false, info, plan_dev, workspace,
                             ws_bytes, stream);
+}
+
+// The same over a block-scaled pool: the gather turns codes into the bf16 values they stand for,
+// so the attention kernel and its plan are those of a bf16 pool.
+extern "C" int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o,
+                                     float sm_scale, const pkv_plan_info *info, const void *plan_dev, void *workspace,
+                                     size_t ws_bytes, void *stream) {
+    using namespace pkv;
+    const int rc = validate_block_pool(pool);
+    if (rc) return rc;
+    if (!batch || batch->page_size != pool->page_size) return PKV_E_INVALID;
+    pkv_pool rows{};
+    rows.k = pool->k;
+    rows.v = pool->v;
+    rows.num_slots = pool->num_pages * pool->page_size;
+    rows.num_kv_heads = pool->num_kv_heads;
+    rows.head_dim = pool->head_dim;
+    rows.dtype = PKV_FP8_E4M3;
+    rows.k_scale = rows.v_scale = 1.f;
+    rows.slot_stride = pool->slot_stride;
+    return extend_call(&rows, batch, q, o, sm_scale, nullptr, nullptr, nullptr, false, info, plan_dev, workspace, ws_bytes,
+                       stream, pool);
 }
 
 extern "C" int pkv_attn_extend_store(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o,

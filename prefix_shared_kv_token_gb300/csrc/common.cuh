@@ -18,6 +18,7 @@ enum DeviceError : int32_t {
     DERR_SLOT_RANGE = 0x100,      // a slot read from req_to_token / out_cache_loc is out of range
     DERR_TIMEOUT = 0x200,         // a bounded wait gave up (low byte: which wait)
     DERR_POSITION = 0x400,        // a work item asked for positions outside the row
+    DERR_NO_PAGES = 0x800,        // a step needs more pages than the free list has
 };
 
 PKV_DEV void set_error(int32_t *err, int32_t code) {
