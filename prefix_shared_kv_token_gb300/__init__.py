@@ -115,15 +115,26 @@ class Pool:
                        int(self.k.stride(0)))
 
 
-def _on_gpu(name, t, dtype, *shape) -> None:
-    """A contiguous tensor of the given dtype and shape (None: any extent) on the current device."""
+def _refuse(name, t, dtype, device, shape) -> None:
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
         raise ValueError(f"{name} must be a tensor on the current CUDA device")
     if t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor, got {t.dtype}")
-    if len(shape) != t.dim() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _fits(name, t, dtype, device, shape) -> int:
+    """The address of a contiguous tensor of this dtype, device and shape (a tuple, or the number
+    of dimensions); anything else is refused.  One expression: a decode step makes some twenty of
+    these checks, and they are most of what its Python costs."""
+    try:
+        if (t.get_device() == device and t.dtype is dtype and t.is_contiguous()
+                and (t.dim() == shape if type(shape) is int else t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(name, t, dtype, device, shape)
 
 
 @dataclass(frozen=True)
@@ -168,14 +179,14 @@ class BlockPool:
                 raise ValueError(f"BlockPool.{name} must be contiguous [pages, heads] = {(pages, k.shape[1])}")
         object.__setattr__(self, "_c", PkvBlockPool(_ptr(k), _ptr(v), _ptr(self.k_exp), _ptr(self.v_exp), pages,
                                                     int(self.page_size), k.shape[1], k.shape[2], int(k.stride(0))))
+        object.__setattr__(self, "_device", k.get_device())
 
     @property
     def num_pages(self):
         return self.k_exp.shape[0]
 
-    def c(self) -> PkvBlockPool:
-        import torch
-        if not self.k.is_cuda or self.k.device.index != torch.cuda.current_device():
+    def c(self, device) -> PkvBlockPool:
+        if self._device != device:
             raise ValueError("BlockPool is not on the current CUDA device")
         return self._c
 
@@ -349,17 +360,26 @@ def attn_extend_ctx(pool: Pool, q, o, sm_scale, k_new, v_new, out_cache_loc, ctx
 # the block-scaled 8-bit pool
 
 
-def _workspace(workspace) -> int:
-    _on_gpu("workspace", workspace, workspace.dtype, *workspace.shape)
-    return workspace.numel() * workspace.element_size()
-
-
-def _block_batch(batch: Batch) -> PkvBatch:
+def _current():
+    """(index, stream handle) of the current CUDA device."""
     import torch
-    _on_gpu("req_to_token", batch.req_to_token, torch.int32, None, None)
-    _on_gpu("req_pool_indices", batch.req_pool_indices, torch.int32, None)
-    _on_gpu("seq_lens", batch.seq_lens, torch.int32, batch.req_pool_indices.shape[0])
-    return batch.c()
+    device = torch.cuda.current_device()
+    return device, torch.cuda.current_stream(device).cuda_stream
+
+
+def _space(workspace, device):
+    """(address, bytes) of a workspace."""
+    at = _fits("workspace", workspace, workspace.dtype, device, workspace.shape)
+    return at, workspace.numel() * workspace.element_size()
+
+
+def _block_batch(batch: Batch, device) -> PkvBatch:
+    import torch
+    table, rows, i32 = batch.req_to_token, batch.req_pool_indices, torch.int32
+    at, rows_at = _fits("req_to_token", table, i32, device, 2), _fits("req_pool_indices", rows, i32, device, 1)
+    n, stride = table.shape
+    return PkvBatch(at, stride, n, rows_at, _fits("seq_lens", batch.seq_lens, i32, device, rows.shape), rows.shape[0],
+                    batch.page_size)
 
 
 def build_block_tables(req_to_token, req_pool_indices, seq_lens, new_lens, free_pages, free_head, free_head_out,
@@ -368,40 +388,38 @@ def build_block_tables(req_to_token, req_pool_indices, seq_lens, new_lens, free_
     pkv_build_block_tables); every argument is an int32 tensor on the GPU, req_to_token is written
     in place."""
     import torch
-    batch = Batch(req_to_token, req_pool_indices, seq_lens, int(page_size))
-    b = _block_batch(batch)
-    n = req_pool_indices.shape[0]
-    _on_gpu("new_lens", new_lens, torch.int32, n)
-    _on_gpu("free_pages", free_pages, torch.int32, None)
-    _on_gpu("free_head", free_head, torch.int32, 1)
-    _on_gpu("free_head_out", free_head_out, torch.int32, 1)
-    _on_gpu("out_cache_loc", out_cache_loc, torch.int32, None)
-    _on_gpu("positions", positions, torch.int32, out_cache_loc.shape[0])
-    _on_gpu("qo_indptr", qo_indptr, torch.int32, n + 1)
-    size = _workspace(workspace)
+    i32 = torch.int32
+    device, current = _current()
+    b = _block_batch(Batch(req_to_token, req_pool_indices, seq_lens, int(page_size)), device)
+    ws, size = _space(workspace, device)
+    free = _fits("free_pages", free_pages, i32, device, 1)
+    loc = _fits("out_cache_loc", out_cache_loc, i32, device, 1)
     check("pkv_build_block_tables", lib.pkv_build_block_tables(
-        C.byref(b), _ptr(new_lens), _ptr(free_pages), free_pages.shape[0], _ptr(free_head), _ptr(free_head_out),
-        _ptr(out_cache_loc), _ptr(positions), out_cache_loc.shape[0], _ptr(qo_indptr), _ptr(workspace), size,
-        _stream(stream)))
+        b, _fits("new_lens", new_lens, i32, device, req_pool_indices.shape), free, free_pages.shape[0],
+        _fits("free_head", free_head, i32, device, (1,)), _fits("free_head_out", free_head_out, i32, device, (1,)), loc,
+        _fits("positions", positions, i32, device, out_cache_loc.shape), out_cache_loc.shape[0],
+        _fits("qo_indptr", qo_indptr, i32, device, (b.batch + 1,)), ws, size,
+        current if stream is None else _stream(stream)))
 
 
 def kv_store_block(pool: BlockPool, k_new, v_new, out_cache_loc, workspace=None, stream=None) -> None:
     """Quantises k_new, v_new (bf16 [n, heads, head_dim]) into the slots out_cache_loc; tokens of
     one page are neighbours at consecutive slots, -1 is padding (see pkv_kv_store_block)."""
     import torch
-    p = pool.c()
-    _on_gpu("out_cache_loc", out_cache_loc, torch.int32, None)
+    device, current = _current()
+    p = pool.c(device)
+    loc = _fits("out_cache_loc", out_cache_loc, torch.int32, device, 1)
     n = out_cache_loc.shape[0]
-    _on_gpu("k_new", k_new, torch.bfloat16, n, p.num_kv_heads, p.head_dim)
-    _on_gpu("v_new", v_new, torch.bfloat16, n, p.num_kv_heads, p.head_dim)
-    check("pkv_kv_store_block", lib.pkv_kv_store_block(C.byref(p), _ptr(k_new), _ptr(v_new), _ptr(out_cache_loc), n,
-                                                       _ptr(workspace), _stream(stream)))
+    rows = (n, p.num_kv_heads, p.head_dim)
+    check("pkv_kv_store_block", lib.pkv_kv_store_block(
+        p, _fits("k_new", k_new, torch.bfloat16, device, rows), _fits("v_new", v_new, torch.bfloat16, device, rows), loc,
+        n, None if workspace is None else _space(workspace, device)[0], current if stream is None else _stream(stream)))
 
 
 def decode_block_workspace(pool: BlockPool, num_q_heads: int) -> int:
     """Bytes of attn_decode_block's workspace (whatever the batch)."""
     n = C.c_size_t(0)
-    check("pkv_decode_block_workspace", lib.pkv_decode_block_workspace(C.byref(pool._c), int(num_q_heads), C.byref(n)))
+    check("pkv_decode_block_workspace", lib.pkv_decode_block_workspace(pool._c, int(num_q_heads), C.byref(n)))
     return n.value
 
 
@@ -409,28 +427,29 @@ def attn_decode_block(pool: BlockPool, batch: Batch, q, o, sm_scale, workspace, 
     """One query per request (q, o bf16 [batch, num_q_heads, head_dim]) over its pages; no plan, and
     a request of length 0 gets zeros (see pkv_attn_decode_block)."""
     import torch
-    p, b = pool.c(), _block_batch(batch)
-    _on_gpu("q", q, torch.bfloat16, b.batch, None, p.head_dim)
-    _on_gpu("o", o, torch.bfloat16, *q.shape)
-    size = _workspace(workspace)
-    check("pkv_attn_decode_block", lib.pkv_attn_decode_block(C.byref(p), C.byref(b), _ptr(q), _ptr(o), q.shape[1],
-                                                             float(sm_scale), _ptr(workspace), size, _stream(stream)))
+    device, current = _current()
+    p, b = pool.c(device), _block_batch(batch, device)
+    rows = (b.batch, q.shape[1] if q.dim() == 3 else 0, p.head_dim)
+    ws, size = _space(workspace, device)
+    check("pkv_attn_decode_block", lib.pkv_attn_decode_block(
+        p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), rows[1], sm_scale,
+        ws, size, current if stream is None else _stream(stream)))
 
 
 def attn_extend_block(pool: BlockPool, batch: Batch, q, o, sm_scale, plan: Plan, plan_dev, workspace,
                       stream=None) -> None:
     """attn_extend over a block-scaled pool (the same plans and workspace)."""
     import torch
-    p, b = pool.c(), _block_batch(batch)
-    _on_gpu("q", q, torch.bfloat16, plan.info.total_q, plan.info.num_q_heads, p.head_dim)
-    _on_gpu("o", o, torch.bfloat16, *q.shape)
-    _on_gpu("plan_dev", plan_dev, torch.uint8, None)
-    if plan_dev.shape[0] < plan.info.plan_bytes:
+    device, current = _current()
+    p, b, info = pool.c(device), _block_batch(batch, device), plan.info
+    rows = (info.total_q, info.num_q_heads, p.head_dim)
+    at = _fits("plan_dev", plan_dev, torch.uint8, device, 1)
+    if plan_dev.shape[0] < info.plan_bytes:
         raise ValueError("plan_dev is shorter than the plan")
-    size = _workspace(workspace)
-    check("pkv_attn_extend_block", lib.pkv_attn_extend_block(C.byref(p), C.byref(b), _ptr(q), _ptr(o), float(sm_scale),
-                                                             C.byref(plan.info), _ptr(plan_dev), _ptr(workspace), size,
-                                                             _stream(stream)))
+    ws, size = _space(workspace, device)
+    check("pkv_attn_extend_block", lib.pkv_attn_extend_block(
+        p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), sm_scale, info, at,
+        ws, size, current if stream is None else _stream(stream)))
 
 
 def get_device_error(workspace, stream=None) -> int:

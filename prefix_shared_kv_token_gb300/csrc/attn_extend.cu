@@ -1131,8 +1131,18 @@ extern "C" int pkv_attn_extend(const pkv_pool *pool, const pkv_batch *batch, con
                             ws_bytes, stream);
 }
 
-// The same over a block-scaled pool: the gather turns codes into the bf16 values they stand for,
-// so the attention kernel and its plan are those of a bf16 pool.
+namespace pkv {
+
+// block_decode.cu: few query tokens a request, 8 / G of them at a time over the pages themselves
+int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const int32_t *indptr, int64_t q_rows, const void *q,
+                     void *o, int32_t num_q_heads, float sm_scale, void *workspace, size_t ws_bytes, cudaStream_t s);
+
+}  // namespace pkv
+
+// The same over a block-scaled pool.  Many query tokens: the gather turns codes into the bf16 values
+// they stand for, so the attention kernel and its plan are those of a bf16 pool.  Few (the plan
+// says which): the decode kernel, with the plan's query rows; its records fit where the gathered
+// rows would go.
 extern "C" int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o,
                                      float sm_scale, const pkv_plan_info *info, const void *plan_dev, void *workspace,
                                      size_t ws_bytes, void *stream) {
@@ -1149,6 +1159,16 @@ extern "C" int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch
     rows.dtype = PKV_FP8_E4M3;
     rows.k_scale = rows.v_scale = 1.f;
     rows.slot_stride = pool->slot_stride;
+    if (info && info->op == 2 && info->offsets[16] == 0 && info->offsets[18] != 0) {
+        const int err = check_call(&rows, batch, q, o, info, plan_dev, workspace, ws_bytes, 2);
+        if (err) return err;
+        if (batch->stride < 0 || batch->stride >= ((int64_t)1 << 31) || batch->num_rows < 0) return PKV_E_INVALID;
+        if (info->total_q == 0) return PKV_OK;
+        const int32_t *indptr =
+            reinterpret_cast<const int32_t *>(static_cast<const uint8_t *>(plan_dev) + info->offsets[17]);
+        return block_attend_few(pool, batch, indptr, info->total_q, q, o, info->num_q_heads, sm_scale, workspace, ws_bytes,
+                                reinterpret_cast<cudaStream_t>(stream));
+    }
     return extend_call(&rows, batch, q, o, sm_scale, nullptr, nullptr, nullptr, false, info, plan_dev, workspace, ws_bytes,
                        stream, pool);
 }

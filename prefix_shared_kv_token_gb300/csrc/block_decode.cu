@@ -11,19 +11,24 @@
 // size 1 whatever the pages' exponents; the result is acc / l * 2^ea.
 //
 // Design.  The work is a stream of codes, so what counts is bytes in flight:
-//   * 16-key tiles of all requests, laid end to end, are cut into equal contiguous ranges, one
-//     per warp and KV head (each CTA scans the lengths itself: no host plan, no set-up kernel,
-//     ragged batches balance to a tile, and a captured graph follows the lengths).  A request
-//     inside one range is written directly; one that crosses ranges leaves a record (R, l, acc)
-//     in each, joined by a second kernel.
-//   * A warp loads its codes straight into registers in fragment order: K rows are the A operand
-//     (16 keys) of S^T = K Q^T, V^T the A operand of O^T = V^T P^T, and the query heads are the 8
-//     columns of B.  So a group of up to 8 heads shares one MMA, the accumulators are d x 8, no
-//     shared memory is used and 16 warps an SM keep 64 KB in flight.
+//   * 16-key tiles of all requests, laid end to end, are cut into equal contiguous ranges (each CTA
+//     scans the lengths itself: no host plan, no set-up kernel, ragged batches balance to a tile,
+//     and a captured graph follows the lengths).  A request inside one range is written directly;
+//     one that crosses ranges leaves a record (R, l, acc, ea) in each, joined by a second kernel.
+//   * A CTA has a consumer warp for each of 8 KV heads (fewer heads: several ranges side by side)
+//     and a producer warp that keeps a ring of tiles full: per head, tensor and tile one 16-row
+//     TMA box, swizzled, 96 KB of ring a CTA and two CTAs an SM.  (Loading codes straight into
+//     registers, one tile ahead, left each warp waiting for half its time: 4.6 of 5.3 TB/s.)
+//   * K rows are the A operand (16 keys) of S^T = K Q^T, V^T the A operand of O^T = V^T P^T, and the
+//     query rows are the 8 columns of B: a group of up to 8 heads shares one MMA and the accumulators
+//     are d x 8.  V's bytes are paired by key with byte permutes on their way to f16.
 //   * mma.sync m16n8k16 in f16: an e4m3 code is an f16 value, and so is a query element over a
 //     power of two that brings its row's largest to [2^14, 2^15) (elements below 2^-31 of it
 //     round, far under the fp32 sum's own rounding).  Weights are f16 times 2^15: 11 bits down to
 //     2^-29 of the largest, against bf16's 8.
+// A request may also have several query tokens (the last ext[r] positions of its context): each
+// block of 8 / G of them is a *stream* of its own over the same keys, which only the first finds in
+// HBM.
 
 #include <algorithm>
 
@@ -33,26 +38,31 @@ namespace pkv {
 
 constexpr int kTile = 16;         // keys
 constexpr int kMinTiles = 4;      // per range, while there are few
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;         // consumers
+constexpr int kRingBytes = 96 * 1024;
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr float kBias = 15.f;     // weights carry 2^15
 constexpr float kUnbias = 1.f / (1 << 15);
 constexpr float kLog2eB = 1.4426950408889634f;
 
 struct BlockDecodeParams {
-    const uint8_t *k, *v, *k_exp, *v_exp;
-    int64_t num_pages, slot_bytes;
+    const uint8_t *k_exp, *v_exp;
+    int64_t num_pages;
     int32_t shift, hkv, hg, groups;  // hg KV heads read side by side, `groups` times
     const int32_t *table;
     int64_t stride;
     int32_t num_rows, batch;
     const int32_t *rows, *lens;
+    const int32_t *indptr;  // NULL: one query token a request; else request r's are rows
+                            // [indptr[r], indptr[r + 1]) of q, its last positions
     const uint16_t *q;
     uint16_t *o;
     float scale_log2;
     int32_t ranges;  // at most
-    float *rec;      // [range][2][hg][G][D], then (R, l, ea, -) [range][2][hg][G][4]
+    float *rec;      // [range][2][hg][8 columns][D], then (R, l, ea, -) [range][2][hg][8][4]
     float *rec_ml;
     int32_t *err;
+    WaitPolicy wait;
 };
 
 // A request's length as the kernels use it: 0 where its row or length is out of range.
@@ -73,13 +83,17 @@ struct Cut {
     int32_t n;
     PKV_DEV Cut(int64_t total, int32_t most) {
         n = (int32_t)min((int64_t)most, max((int64_t)1, total / kMinTiles));
-        size = total / n;
+        size = divide(total, n);
         extra = total - size * n;
     }
     PKV_DEV int64_t start(int32_t i) const { return size * i + min((int64_t)i, extra); }
     PKV_DEV int32_t range_of(int64_t t) const {
         const int64_t big = extra * (size + 1);
-        return (int32_t)(t < big ? t / (size + 1) : extra + (t - big) / size);
+        return (int32_t)(t < big ? divide(t, size + 1) : extra + divide(t - big, size));
+    }
+    // (a 64-bit division takes hundreds of cycles, and a kernel's start waits for several)
+    static PKV_DEV int64_t divide(int64_t a, int64_t b) {
+        return a < ((int64_t)1 << 32) && b < ((int64_t)1 << 32) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
     }
 };
 
@@ -100,31 +114,37 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
     return r;
 }
-PKV_DEV int64_t block_sum(int64_t x, int64_t *warp_sums) {  // kWarps warps; every thread gets it
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) x += warp_sums[w];
-    return x;
+// Query tokens of request r: (first row of q, how many), and of them the streams.
+PKV_DEV int2 query_rows(const BlockDecodeParams &p, int r, int32_t len) {
+    if (!p.indptr) return make_int2(r, 1);
+    const int32_t a = __ldg(p.indptr + r), n = __ldg(p.indptr + r + 1) - a;
+    return make_int2(a, min(n, len));
+}
+// Keys that the last token of stream s of a request sees (streams of M = 8 / G tokens).
+PKV_DEV int32_t stream_len(int32_t len, int32_t ext, int32_t s, int32_t M) { return len - ext + min(ext, (s + 1) * M); }
+
+PKV_DEV int64_t request_tiles(const BlockDecodeParams &p, int r, int32_t M, bool report) {
+    const int32_t len = checked_len(p, r, report);
+    if (!p.indptr) return tiles_of(len);
+    int64_t n = 0;
+    const int32_t ext = query_rows(p, r, len).y;
+    for (int32_t s = 0; s * M < ext; ++s) n += tiles_of(stream_len(len, ext, s, M));
+    return n;
 }
 
-// Query rows of the group as B fragments, in the d order that K's 16-byte pieces have: k-step
-// (half, j) holds d = 64 half + 16 c + 4 j + {0, 1 | 2, 3} of head g.  Returns the power of two
-// taken out of head g's row.
-template <int D, int G>
-PKV_DEV int load_query(const BlockDecodeParams &p, int r, int kv_head, uint32_t (&qb)[D / 16][2]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+// Query rows as B fragments, in the d order that K's 16-byte pieces have: k-step (half, j) holds
+// d = 64 half + 16 c + 4 j + {0, 1 | 2, 3} of column g.  Returns the power of two taken out of
+// column g.  `row`: column g's row of q (of num_q_heads * D elements at its head), NULL for none.
+template <int D>
+PKV_DEV int load_query(const uint16_t *row, uint32_t (&qb)[D / 16][2]) {
+    const int c = threadIdx.x & 3;
     uint32_t w[D / 8];
-    const uint16_t *row = p.q + ((int64_t)r * p.hkv * G + kv_head * G + (g < G ? g : 0)) * D + 16 * c;
     uint32_t amax = 0;
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + 64 * h) + u);
+            const uint4 x = row ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * h + 16 * c) + u) : make_uint4(0u, 0u, 0u, 0u);
             w[8 * h + 4 * u] = x.x;
             w[8 * h + 4 * u + 1] = x.y;
             w[8 * h + 4 * u + 2] = x.z;
@@ -132,7 +152,6 @@ PKV_DEV int load_query(const BlockDecodeParams &p, int r, int kv_head, uint32_t 
         }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-        if (g >= G) w[i] = 0u;
         const uint32_t a = w[i] & 0x7FFFu, b = (w[i] >> 16) & 0x7FFFu;
         if (a < 0x7F80u) amax = max(amax, a);
         if (b < 0x7F80u) amax = max(amax, b);
@@ -152,49 +171,17 @@ PKV_DEV int load_query(const BlockDecodeParams &p, int r, int kv_head, uint32_t 
     return e;
 }
 
-// One tile's codes: K rows g and g + 8, V rows 2c, 2c + 1, 2c + 8, 2c + 9.
+// One (head, tensor) tile in shared memory: 16 rows of D bytes, 16-byte pieces swizzled by TMA (128
+// bytes: piece ^ row mod 8; 64 bytes: piece ^ (row / 2) mod 4).  MMA row r holds key_of(r), an order
+// under which the 8 lanes of a 16-byte access hit 8 different pieces (d = 128).
 template <int D>
-struct TileRegs {
-    uint4 k[2][D / 64];
-    uint32_t v[4][D / 32];
-    int ek, ev;
-};
-
-template <int D>
-PKV_DEV void load_k(const BlockDecodeParams &p, TileRegs<D> &x, int64_t slot, bool ok, int head) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint8_t *row = p.k + (slot + g + 8 * h) * p.slot_bytes + (int64_t)head * D + 16 * c;
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u)
-            x.k[h][u] = ok ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * u)) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    x.ek = ok ? clamp_exp(__ldg(p.k_exp + (slot >> p.shift) * p.hkv + head)) : 127;
+PKV_DEV int key_of(int r) {
+    if constexpr (D == 128) return (int)((0x37156240u >> (4 * (r & 7))) & 7u) + (r & 8);
+    return r;
 }
-
-// Rows at or past `valid` read as zeros: a weight of 0 does not undo a NaN or an infinity.
 template <int D>
-PKV_DEV void load_v(const BlockDecodeParams &p, TileRegs<D> &x, int64_t slot, bool ok, int head, int valid) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-        const uint8_t *at = p.v + (slot + key) * p.slot_bytes + (int64_t)head * D + g * (D / 8);
-        const bool on = ok && key < valid;
-        if constexpr (D == 128) {
-            const uint4 y = on ? __ldg(reinterpret_cast<const uint4 *>(at)) : make_uint4(0u, 0u, 0u, 0u);
-            x.v[i][0] = y.x;
-            x.v[i][1] = y.y;
-            x.v[i][2] = y.z;
-            x.v[i][3] = y.w;
-        } else {
-            const uint2 y = on ? __ldg(reinterpret_cast<const uint2 *>(at)) : make_uint2(0u, 0u);
-            x.v[i][0] = y.x;
-            x.v[i][1] = y.y;
-        }
-    }
-    x.ev = ok ? clamp_exp(__ldg(p.v_exp + (slot >> p.shift) * p.hkv + head)) : 127;
+PKV_DEV int piece_at(int key, int piece) {
+    return D == 128 ? key * 128 + ((piece ^ (key & 7)) << 4) : key * 64 + ((piece ^ ((key >> 1) & 3)) << 4);
 }
 
 // Running state of one warp: columns 2c and 2c + 1 (query heads) of this lane.
@@ -207,26 +194,65 @@ struct DecodeState {
 // The result of a row from its sums.
 PKV_DEV float row_scale(float l, float ea) { return l == 0.f ? 0.f : kUnbias / l * exp_value((int)ea + 127); }
 
+// Logits of a tile's 16 keys: this lane's MMA rows g and g + 8 of columns 2c and 2c + 1.  The rows
+// g + 8 are 8 D bytes behind the rows g, under the same swizzle.
 template <int D>
-PKV_DEV void attend_tile(DecodeState<D> &st, const uint32_t (&qb)[D / 16][2], const TileRegs<D> &x, const float (&cs)[2],
-                         int valid) {
-    const int lane = threadIdx.x & 31, g = lane >> 2;
+PKV_DEV void tile_scores(float (&t)[4], const uint32_t (&qb)[D / 16][2], const uint8_t *k, const int (&off)[D / 64]) {
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of MMAs
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
-        const uint32_t a[4] = {x.k[0][u].x, x.k[0][u].y, x.k[0][u].z, x.k[0][u].w};
-        const uint32_t b[4] = {x.k[1][u].x, x.k[1][u].y, x.k[1][u].z, x.k[1][u].w};
+        const uint4 x = *reinterpret_cast<const uint4 *>(k + off[u]), y = *reinterpret_cast<const uint4 *>(k + off[u] + 8 * D);
+        const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             mma_f16_16816(s[j & 1], e4m3x2_to_f16x2(a[j]), e4m3x2_to_f16x2(b[j]), e4m3x2_hi_to_f16x2(a[j]),
                           e4m3x2_hi_to_f16x2(b[j]), qb[4 * u + j][0], qb[4 * u + j][1]);
     }
-    const float kf = exp_value(x.ek), ev = (float)(x.ev - 127);
-    float t[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        t[e] = (s[0][e] + s[1][e]) * (cs[e & 1] * kf) + ev;
-        if (g + 8 * (e >> 1) >= valid) t[e] = -INFINITY;
+    for (int e = 0; e < 4; ++e) t[e] = s[0][e] + s[1][e];
+}
+
+// V rows of MMA k 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 bytes each.  Rows at or past `valid` read as
+// zeros: a weight of 0 does not undo a NaN or an infinity.
+template <int D>
+PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off)[2], int valid) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t *row = at + off[i & 1] + (i >> 1) * 8 * D;
+        if constexpr (D == 128) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(row);
+            v[i][0] = y.x;
+            v[i][1] = y.y;
+            v[i][2] = y.z;
+            v[i][3] = y.w;
+        } else {
+            const uint2 y = *reinterpret_cast<const uint2 *>(row);
+            v[i][0] = y.x;
+            v[i][1] = y.y;
+        }
+    }
+    if (valid < kTile) {
+        const int c = threadIdx.x & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (key_of<D>(2 * c + (i & 1) + 8 * (i >> 1)) >= valid)
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) v[i][j] = 0u;
+    }
+}
+
+// Folds the tile's weights (as B fragments b0, b1) and its maximum into the running state.
+template <int D>
+PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int ek, int ev_byte, int key,
+                          const int32_t (&sees)[2], int32_t full, uint32_t &b0, uint32_t &b1) {
+    const float kf = exp_value(clamp_exp(ek)), ev = (float)(clamp_exp(ev_byte) - 127);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + ev;
+    if (key + kTile > full) {  // some column does not see the whole tile
+        const int mine = key + key_of<D>((threadIdx.x & 31) >> 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (mine + 8 * (e >> 1) >= sees[e & 1]) t[e] = -INFINITY;
     }
     float mn[2];
 #pragma unroll
@@ -254,41 +280,54 @@ PKV_DEV void attend_tile(DecodeState<D> &st, const uint32_t (&qb)[D / 16][2], co
             for (int e = 0; e < 4; ++e) st.acc[i][e] *= al[e & 1];
     }
     float w[4];
+    float rw[2], rl[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float m = mn[h] == -INFINITY ? 0.f : mn[h];  // a column that has seen no key yet
+        rw[h] = m - kBias;
+        rl[h] = m + (ev - st.ea[h]);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float rel = t[e] - (mn[e & 1] == -INFINITY ? 0.f : mn[e & 1]);
-        w[e] = ex2(rel + kBias);
-        st.l[e & 1] += ex2(rel - (ev - st.ea[e & 1]));
+        w[e] = ex2(t[e] - rw[e & 1]);
+        st.l[e & 1] += ex2(t[e] - rl[e & 1]);
     }
-    const uint32_t b0 = transpose_8x8(pack_f16x2(w[0], w[1])), b1 = transpose_8x8(pack_f16x2(w[2], w[3]));
+    b0 = transpose_8x8(pack_f16x2(w[0], w[1]));
+    b1 = transpose_8x8(pack_f16x2(w[2], w[3]));
+}
+
+template <int D>
+PKV_DEV void tile_product(DecodeState<D> &st, const uint32_t (&v)[4][D / 32], uint32_t b0, uint32_t b1) {
 #pragma unroll
     for (int j = 0; j < D / 32; ++j)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             // bytes (key, key + 1) of d and d + 1 next to each other
-            const uint32_t lo = __byte_perm(x.v[0][j], x.v[1][j], u ? 0x7362 : 0x5140);
-            const uint32_t hi = __byte_perm(x.v[2][j], x.v[3][j], u ? 0x7362 : 0x5140);
+            const uint32_t lo = __byte_perm(v[0][j], v[1][j], u ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(v[2][j], v[3][j], u ? 0x7362 : 0x5140);
             mma_f16_16816(st.acc[2 * j + u], e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
                           e4m3x2_hi_to_f16x2(hi), b0, b1);
         }
 }
 
+// The result (rec < 0) or record of a stream's piece.  Column 2c + h of this lane belongs to query
+// row `row[h]` (-1: none) and head `hd[h]` of the group.
 template <int D, int G>
-PKV_DEV void write_segment(const BlockDecodeParams &p, DecodeState<D> &st, int r, int kv_head, int32_t rec, int hl) {
+PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_head, const int32_t (&row)[2], int32_t rec, int hl) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) st.l[h] += __shfl_xor_sync(0xffffffffu, st.l[h], d);
-        const int head = 2 * c + h;
-        if (head >= G) continue;
+        const int col = 2 * c + h;
+        if (row[h] < 0) continue;
         if (rec < 0) {
             const float inv = row_scale(st.l[h], st.ea[h]);
-            uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + ((int64_t)r * p.hkv * G + kv_head * G + head) * D + g * (D / 8));
+            uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + ((int64_t)row[h] * p.hkv * G + kv_head * G + col % G) * D + g * (D / 8));
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) dst[i] = pack_bf16x2(st.acc[i][h] * inv, st.acc[i][2 + h] * inv);
         } else {
-            const int64_t at = ((int64_t)rec * p.hg + hl) * G + head;
+            const int64_t at = ((int64_t)rec * p.hg + hl) * 8 + col;
             float2 *dst = reinterpret_cast<float2 *>(p.rec + at * D + g * (D / 8));
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) dst[i] = make_float2(st.acc[i][h], st.acc[i][2 + h]);
@@ -297,159 +336,355 @@ PKV_DEV void write_segment(const BlockDecodeParams &p, DecodeState<D> &st, int r
     }
 }
 
+// A piece: tiles [j0, j1) of stream s of request r, inside one range.
+struct Piece {
+    int32_t r, s, len, ext, q0;  // request, stream, its length, query tokens and first query row
+    int32_t head0;               // first KV head of the group of heads
+    int32_t j0, j1;
+    int32_t rec;                 // record, -1 for a whole stream
+};
+
+// Calls f(piece) for every piece of tiles [at, end) of the line; base: tiles before each of the 256
+// chunks of requests; n tiles in a group of heads.  f returns false to stop.
+template <int G, class F>
+PKV_DEV void for_pieces(const BlockDecodeParams &p, const int64_t *base, int chunk, int64_t n, int32_t range, int64_t at,
+                        int64_t end, F f) {
+    constexpr int32_t M = 8 / G;
+    const int64_t begin = at;
+    while (at < end) {
+        const int32_t grp = p.groups == 1 ? 0 : (int32_t)(at / n);
+        const int64_t off = (int64_t)grp * n, stop = min(end, off + n);
+        int lo = 0, hi = 32 * kWarps;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (base[mid] <= at - off) lo = mid; else hi = mid;
+        }
+        int64_t first = off + base[lo];  // the stream's first tile
+        for (int r = lo * chunk; at < stop; ++r) {
+            if (r >= p.batch) return;  // the lengths changed under the call
+            const int32_t len = checked_len(p, r, false);
+            const int2 qr = query_rows(p, r, len);
+            for (int32_t s = 0; s * M < qr.y && at < stop; ++s) {
+                const int32_t tiles = tiles_of(p.indptr ? stream_len(len, qr.y, s, M) : len);
+                if (first + tiles > at) {
+                    Piece x;
+                    x.r = r;
+                    x.s = s;
+                    x.len = len;
+                    x.ext = qr.y;
+                    x.q0 = qr.x;
+                    x.head0 = grp * p.hg;
+                    x.j0 = (int32_t)(at - first);
+                    x.j1 = (int32_t)min((int64_t)tiles, stop - first);
+                    x.rec = x.j0 == 0 && x.j1 == tiles ? -1 : 2 * range + (first < begin ? 0 : 1);
+                    if (!f(x)) return;
+                    at = first + x.j1;
+                }
+                first += tiles;
+            }
+        }
+    }
+}
+
+// A bounded wait of the ring (see WaitPolicy).
+PKV_DEV bool ring_wait(uint64_t *bar, uint32_t parity, int32_t *abort_flag, const BlockDecodeParams &p, int where) {
+    if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if ((it & p.wait.check_mask) == 0) {
+            if (*reinterpret_cast<volatile int32_t *>(abort_flag)) return false;
+            if (global_timer_ns() - t0 > p.wait.limit_ns) {
+                set_error(p.err, DERR_TIMEOUT | where);
+                *reinterpret_cast<volatile int32_t *>(abort_flag) = 1;
+                return false;
+            }
+        }
+    }
+}
+
+template <int D>
+struct Ring {
+    static constexpr int kBox = kTile * D;                      // a head's K or V tile
+    static constexpr int kStages = kRingBytes / (kWarps * 2 * kBox);  // 3 (d = 128), 6 (d = 64)
+    static constexpr int kSmem = kRingBytes + 1024;             // + alignment
+};
+
 template <int D, int G>
-__global__ void __launch_bounds__(32 * kWarps, 2) block_decode_kernel(const BlockDecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 2)
+    block_decode_kernel(const BlockDecodeParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using R = Ring<D>;
+    extern __shared__ uint8_t dyn[];
     __shared__ int64_t warp_sums[kWarps];
     __shared__ int64_t base[32 * kWarps + 1];  // tiles before each thread's chunk of requests
+    __shared__ uint64_t full[kWarps][R::kStages], empty[kWarps][R::kStages];  // per group of hg warps
+    __shared__ int32_t abort_flag;
+    uint8_t *ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
+    constexpr int32_t M = 8 / G;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int groups = kWarps / p.hg;
+    if (tid == 0) {
+        for (int i = 0; i < groups; ++i)
+            for (int s = 0; s < R::kStages; ++s) {
+                mbar_init(&full[i][s], 1);
+                mbar_init(&empty[i][s], p.hg);
+            }
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, warp = tid >> 5;
     const int chunk = (p.batch + 32 * kWarps - 1) / (32 * kWarps);
     int64_t mine = 0;
-    for (int r = tid * chunk; r < min((tid + 1) * chunk, p.batch); ++r)
-        mine += tiles_of(checked_len(p, r, blockIdx.x == 0));
+    if (warp < kWarps)
+        for (int r = tid * chunk; r < min((tid + 1) * chunk, p.batch); ++r) mine += request_tiles(p, r, M, blockIdx.x == 0);
     int64_t scan = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, scan, d);
-        if ((tid & 31) >= d) scan += y;
+        if (lane >= d) scan += y;
     }
-    if ((tid & 31) == 31) warp_sums[warp] = scan;
+    if (lane == 31 && warp < kWarps) warp_sums[warp] = scan;
     __syncthreads();
     int64_t before = 0, n = 0;
     for (int w = 0; w < kWarps; ++w) {
         if (w == warp) before = n;
         n += warp_sums[w];
     }
-    base[tid] = before + scan - mine;
+    if (warp < kWarps) base[tid] = before + scan - mine;
     if (tid == 0) base[32 * kWarps] = n;
     __syncthreads();
     if (n == 0) return;
 
     const Cut cut(n * p.groups, p.ranges);
-    const int hl = warp % p.hg;
-    const int32_t range = blockIdx.x * (kWarps / p.hg) + warp / p.hg;
-    if (range >= cut.n) return;
-    int64_t at = cut.start(range);
-    const int64_t end = cut.start(range + 1);
-    const int64_t begin = at;
-
-    while (at < end) {
-        const int grp = (int)(at / n);
-        const int head = grp * p.hg + hl;
-        const int64_t off = (int64_t)grp * n;
-        // the chunk of requests that holds tile at - off, then the request
-        int lo = 0, hi = 32 * kWarps;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (base[mid] <= at - off) lo = mid; else hi = mid;
-        }
-        int r = lo * chunk;
-        int64_t first = off + base[lo];  // request r's first tile
-        const int64_t stop = min(end, off + n);
-        for (; at < stop; ++r) {
-            if (r >= p.batch) return;  // the lengths changed under the call
-            const int32_t len = checked_len(p, r, false);
-            const int32_t tiles = tiles_of(len);
-            if (first + tiles <= at) {
-                first += tiles;
-                continue;
+    const int tpp = p.shift - 4;  // log2 of the tiles in a page
+    const int grp_bytes = p.hg * 2 * R::kBox;                // one stage of one group of warps
+    if (warp == kWarps) {
+        // ------------------------------------------------- producer: lane i feeds group i's ring
+        const int32_t range = blockIdx.x * groups + lane;
+        if (lane >= groups || range >= cut.n) return;
+        uint8_t *mine_at = ring + lane * R::kStages * grp_bytes;
+        uint32_t t = 0;
+        bool bad = false;
+        for_pieces<G>(p, base, chunk, n, range, cut.start(range), cut.start(range + 1), [&](const Piece &x) {
+            const int32_t *row = p.table + (int64_t)__ldg(p.rows + x.r) * p.stride;
+            int32_t next = __ldg(row + (x.j0 >> tpp));
+            for (int32_t j = x.j0; j < x.j1; ++j, ++t) {
+                const int32_t page = next;
+                next = __ldg(row + (min(j + 1, x.j1 - 1) >> tpp));
+                const int st = t % R::kStages;
+                if (t >= R::kStages && !ring_wait(&empty[lane][st], (t / R::kStages - 1) & 1, &abort_flag, p, 0x41)) return false;
+                // a page outside the pool: rows past the maps' last, which read as zeros
+                const bool ok = (uint32_t)page < (uint64_t)p.num_pages;
+                bad |= !ok;
+                const int32_t slot = ok ? (page << p.shift) + (j * kTile & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
+                uint64_t *bar = &full[lane][st];
+                mbar_arrive_expect_tx(bar, grp_bytes);
+                const uint32_t dst = smem_u32(mine_at + st * grp_bytes);
+                for (int h = 0; h < p.hg; ++h) {
+                    tma_load_3d(dst + 2 * h * R::kBox, &kmap, 0, x.head0 + h, slot, bar);
+                    tma_load_3d(dst + (2 * h + 1) * R::kBox, &vmap, 0, x.head0 + h, slot, bar);
+                }
             }
-            const int32_t j0 = (int32_t)(at - first), j1 = (int32_t)min((int64_t)tiles, stop - first);
-            const int32_t *row = p.table + (int64_t)__ldg(p.rows + r) * p.stride;
-            uint32_t qb[D / 16][2];
-            const int e = load_query<D, G>(p, r, head, qb);
-            // this lane's columns are heads 2c and 2c + 1, whose exponents lanes 8c and 8c + 4 hold
-            float cs[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * (tid & 3) + 4 * h));
-            DecodeState<D> st;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
-            st.m[0] = st.m[1] = -INFINITY;
-            st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
-            for (int j = j0; j < j1; ++j) {
-                const int32_t key = j * kTile;
-                const int32_t page = __ldg(row + (key >> p.shift));
-                const bool ok = page >= 0 && (int64_t)page < p.num_pages;
-                if (!ok && (tid & 31) == 0) set_error(p.err, DERR_SLOT_RANGE);
-                const int64_t slot = ((int64_t)(ok ? page : 0) << p.shift) + (key & ((1 << p.shift) - 1));
-                TileRegs<D> x;
-                load_k<D>(p, x, slot, ok, head);
-                load_v<D>(p, x, slot, ok, head, len - key);
-                attend_tile<D>(st, qb, x, cs, len - key);
-            }
-            const bool whole = j0 == 0 && j1 == tiles;
-            write_segment<D, G>(p, st, r, head, whole ? -1 : 2 * range + (first < begin ? 0 : 1), hl);
-            at = first + j1;
-            first += tiles;
-        }
+            return true;
+        });
+        if (bad) set_error(p.err, DERR_SLOT_RANGE);
+        // every copy lands before the CTA ends, also when the consumers gave up
+        for (uint32_t u = t > R::kStages ? t - R::kStages : 0; u < t; ++u)
+            mbar_wait(&full[lane][u % R::kStages], (u / R::kStages) & 1);
+        return;
     }
+
+    // --------------------------------------------------------------- consumer: one KV head a warp
+    const int hl = warp % p.hg, grp = warp / p.hg;
+    const int32_t range = blockIdx.x * groups + grp;
+    if (range >= cut.n) return;
+    const int g = lane >> 2, c = lane & 3;
+    int k_off[D / 64], v_off[2];
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u) k_off[u] = piece_at<D>(key_of<D>(g), 4 * u + c);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        v_off[i] = D == 128 ? piece_at<D>(key_of<D>(2 * c + i), g) : piece_at<D>(key_of<D>(2 * c + i), g >> 1) + 8 * (g & 1);
+    const uint8_t *mine_at = ring + grp * R::kStages * grp_bytes + 2 * hl * R::kBox;
+    uint32_t t = 0;
+    for_pieces<G>(p, base, chunk, n, range, cut.start(range), cut.start(range + 1), [&](const Piece &x) {
+        const int kv_head = x.head0 + hl;
+        const int32_t *row = p.table + (int64_t)__ldg(p.rows + x.r) * p.stride;
+        auto page_exp = [&](const uint8_t *e, int32_t page) {
+            return (uint32_t)page < (uint64_t)p.num_pages ? (int)__ldg(e + (int64_t)page * p.hkv + kv_head) : 127;
+        };
+        // exponents come a tile ahead, the page they are read by two tiles ahead
+        int32_t page = __ldg(row + (x.j0 >> tpp));
+        int ek = page_exp(p.k_exp, page), ev = page_exp(p.v_exp, page);
+        page = __ldg(row + (min(x.j0 + 1, x.j1 - 1) >> tpp));
+        // columns: token s M + col / G of the request, head col % G of the group
+        const int32_t tok = x.s * M + g / G;
+        uint32_t qb[D / 16][2];
+        const int e = load_query<D>(g / G < M && tok < x.ext ? p.q + ((int64_t)(x.q0 + tok) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
+        float cs[2];
+        int32_t sees[2], out[2];
+        const int32_t last = p.indptr ? stream_len(x.len, x.ext, x.s, M) : x.len;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
+            const int32_t tk = x.s * M + (2 * c + h) / G;
+            const bool on = (2 * c + h) / G < M && tk < x.ext;
+            out[h] = on ? x.q0 + tk : -1;
+            sees[h] = on ? x.len - x.ext + tk + 1 : last;
+        }
+        const int32_t all_see = x.len - x.ext + x.s * M + 1;  // keys that every column sees
+        DecodeState<D> st;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
+        st.m[0] = st.m[1] = -INFINITY;
+        st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
+#pragma unroll 1
+        for (int32_t j = x.j0; j < x.j1; ++j, ++t) {
+            const int sg = t % R::kStages;
+            const int next_ek = page_exp(p.k_exp, page), next_ev = page_exp(p.v_exp, page);
+            page = __ldg(row + (min(j + 2, x.j1 - 1) >> tpp));
+            if (!__all_sync(0xffffffffu, ring_wait(&full[grp][sg], (t / R::kStages) & 1, &abort_flag, p, 0x42))) return false;
+            const uint8_t *at = mine_at + sg * grp_bytes;
+            float w[4];
+            tile_scores<D>(w, qb, at, k_off);
+            uint32_t v[4][D / 32];
+            read_v<D>(v, at + R::kBox, v_off, last - j * kTile);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[grp][sg]);
+            uint32_t b0, b1;
+            tile_weights<D>(st, w, cs, ek, ev, j * kTile, sees, all_see, b0, b1);
+            tile_product<D>(st, v, b0, b1);
+            ek = next_ek;
+            ev = next_ev;
+        }
+        write_piece<D, G>(p, st, kv_head, out, x.rec, hl);
+        return true;
+    });
 }
 
-// Joins the records of the requests that cross ranges and clears the rows of empty ones.  A CTA
-// takes one (request, KV head): its warps share each query head's records and combine through
-// shared memory.
-template <int D, int G>
-__global__ void __launch_bounds__(32 * kWarps) block_merge_kernel(const BlockDecodeParams p) {
-    __shared__ int64_t warp_sums[kWarps];
-    __shared__ float s_acc[kWarps][D];
-    __shared__ float4 s_ml[kWarps];
-    const int r = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t tiles = tiles_of(checked_len(p, r, false));
-    int64_t mine = 0, all = 0;
-    for (int i = tid; i < p.batch; i += 32 * kWarps) {
-        const int32_t t = tiles_of(checked_len(p, i, false));
-        all += t;
-        if (i < r) mine += t;
+// Joins the records of the streams that cross ranges and clears the rows of empty requests.  A CTA
+// takes Q query heads of one (query row, KV head): its warps share each head's records, four in
+// flight a warp, and combine through shared memory.  Q is the whole group, or 1 where that would
+// leave SMs idle: a request alone in the batch may have a record of every range, and gets 32 warps a
+// head (100,001 keys: 24 us with 8 warps, REPLACE with 32).
+template <int D, int G, int Q, int W>
+__global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodeParams p) {
+    __shared__ int64_t warp_sums[2 * W];
+    __shared__ float s_acc[W][D];
+    __shared__ float4 s_ml[W];
+    __shared__ int32_t s_req;
+    constexpr int32_t M = 8 / G;
+    const int head = blockIdx.y / (G / Q), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t r = blockIdx.x, tok = 0;
+    if (p.indptr) {  // the request of this query row
+        if (tid == 0) s_req = -1;
+        __syncthreads();
+        for (int i = tid; i < p.batch; i += 32 * W)
+            if (__ldg(p.indptr + i) <= r && r < __ldg(p.indptr + i + 1)) s_req = i;
+        __syncthreads();
+        tok = s_req < 0 ? 0 : r - __ldg(p.indptr + s_req);
+        r = s_req;
     }
-    const int64_t before = block_sum(mine, warp_sums);
+    int64_t before = 0, n = 0;
+    for (int i = tid; i < p.batch; i += 32 * W) {
+        const int64_t t = request_tiles(p, i, M, false);
+        n += t;
+        if (i < r) before += t;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, d);
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    if (lane == 0) {
+        warp_sums[warp] = n;
+        warp_sums[W + warp] = before;
+    }
     __syncthreads();
-    const int64_t n = block_sum(all, warp_sums);
+    n = before = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        n += warp_sums[w];
+        before += warp_sums[W + w];
+    }
+    const int32_t len = r < 0 ? 0 : checked_len(p, r, false);
+    int32_t tiles = tiles_of(len);
+    if (p.indptr && r >= 0) {
+        const int32_t ext = query_rows(p, r, len).y, s = tok / M;
+        for (int32_t i = 0; i < s; ++i) before += tiles_of(stream_len(len, ext, i, M));
+        tiles = tok < ext ? tiles_of(stream_len(len, ext, s, M)) : 0;
+    }
     pdl_wait();  // the records
     pdl_trigger();
-    uint16_t *out = p.o + ((int64_t)r * p.hkv + head) * G * D;
+    constexpr int V = D / 32;            // elements a lane holds
+    constexpr int kShare = W / Q;   // warps of one query head
+    const int q = blockIdx.y % (G / Q) * Q + warp / kShare, sub = warp % kShare;
+    const int col = tok % M * G + q;
+    uint32_t *out = reinterpret_cast<uint32_t *>(p.o + (((int64_t)blockIdx.x * p.hkv + head) * G + q) * D + lane * V);
     if (tiles == 0) {
-        for (int i = tid; i < G * D / 8; i += 32 * kWarps) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (sub == 0)
+#pragma unroll
+            for (int v = 0; v < V; v += 2) out[v / 2] = 0u;
         return;
     }
     const Cut cut(n * p.groups, p.ranges);
     const int64_t first = (int64_t)(head / p.hg) * n + before;
     const int32_t i0 = cut.range_of(first), i1 = cut.range_of(first + tiles - 1);
     if (i0 == i1) return;
-    constexpr int V = D / 32;            // elements a lane holds
-    constexpr int kShare = kWarps / G;   // warps of one query head
-    const int q = warp / kShare, sub = warp % kShare;
-    float M = -INFINITY, L = 0.f, E = 0.f, O[V];
+    float top = -INFINITY, L = 0.f, E = 0.f, O[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) O[v] = 0.f;
-    // folds in a record (or another warp's sums): its acc scaled by the returned factor
+    // folds in a record (or another warp's sums)
     auto join = [&](const float4 &x, const float *a) {
-        if (x.x > M) {
-            const float f = ex2(M - x.x);
-            L *= ex2(M - x.x + (x.z - E));
+        if (x.x > top) {
+            const float f = ex2(top - x.x);
+            L *= ex2(top - x.x + (x.z - E));
 #pragma unroll
             for (int v = 0; v < V; ++v) O[v] *= f;
-            M = x.x;
+            top = x.x;
             E = x.z;
         }
         if (x.x == -INFINITY) return;
-        const float w = ex2(x.x - M);
-        L += x.y * ex2(x.x - M - (x.z - E));
+        const float w = ex2(x.x - top);
+        L += x.y * ex2(x.x - top - (x.z - E));
 #pragma unroll
         for (int v = 0; v < V; ++v) O[v] += a[v] * w;
     };
-    for (int32_t i = i0 + sub; i <= i1; i += kShare) {
-        const int64_t rec = (((int64_t)i * 2 + (first < cut.start(i) ? 0 : 1)) * p.hg + head % p.hg) * G + q;
-        float a[V];
+    constexpr int kBatch = 4;
+    for (int32_t i = i0 + sub; i <= i1; i += kShare * kBatch) {
+        float4 ml[kBatch];
+        float a[kBatch][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[v] = p.rec[rec * D + lane * V + v];
-        join(*reinterpret_cast<const float4 *>(p.rec_ml + rec * 4), a);
+        for (int b = 0; b < kBatch; ++b) {
+            const int32_t k = i + b * kShare;
+            ml[b] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[b][v] = 0.f;
+            if (k > i1) continue;
+            // a stream's first range ends inside it (slot 1); the others begin inside it (slot 0)
+            const int64_t rec = (((int64_t)k * 2 + (k == i0 && first >= cut.start(i0) ? 1 : 0)) * p.hg + head % p.hg) * 8 + col;
+            ml[b] = *reinterpret_cast<const float4 *>(p.rec_ml + rec * 4);
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(p.rec + rec * D + lane * V);
+                a[b][0] = y.x;
+                a[b][1] = y.y;
+                a[b][2] = y.z;
+                a[b][3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2 *>(p.rec + rec * D + lane * V);
+                a[b][0] = y.x;
+                a[b][1] = y.y;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) join(ml[b], a[b]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = O[v];
-    if (lane == 0) s_ml[warp] = make_float4(M, L, E, 0.f);
+    if (lane == 0) s_ml[warp] = make_float4(top, L, E, 0.f);
     __syncthreads();
     if (sub != 0) return;
     for (int w = 1; w < kShare; ++w) {
@@ -460,8 +695,7 @@ __global__ void __launch_bounds__(32 * kWarps) block_merge_kernel(const BlockDec
     }
     const float inv = row_scale(L, E);
 #pragma unroll
-    for (int v = 0; v < V; v += 2)
-        reinterpret_cast<uint32_t *>(out + q * D + lane * V)[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
+    for (int v = 0; v < V; v += 2) out[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
 }
 
 static int head_group(int32_t hkv) {
@@ -471,28 +705,38 @@ static int head_group(int32_t hkv) {
 }
 static int decode_ctas() { return 2 * num_sms(); }
 
-static size_t decode_workspace(int32_t hkv, int32_t G, int32_t d) {
+// Bytes of a range's two records.
+static size_t range_bytes(int hg, int32_t d) { return 2 * (size_t)hg * 8 * (d + 4) * sizeof(float); }
+
+static size_t decode_workspace(int32_t hkv, int32_t d) {
     const int hg = head_group(hkv);
-    const size_t ranges = (size_t)decode_ctas() * (kWarps / hg);
-    return kWorkspaceHeader + ranges * 2 * hg * G * (d + 4) * sizeof(float);
+    return kWorkspaceHeader + (size_t)decode_ctas() * (kWarps / hg) * range_bytes(hg, d);
 }
 
 template <int D, int G>
-static int launch(const BlockDecodeParams &p, cudaStream_t s) {
-    if (launch_pdl(block_decode_kernel<D, G>, dim3(decode_ctas()), dim3(32 * kWarps), 0, s, true, p) != cudaSuccess)
+static int launch(const BlockDecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows, cudaStream_t s) {
+    constexpr int smem = Ring<D>::kSmem;
+    if (cudaFuncSetAttribute(block_decode_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return PKV_E_CUDA;
-    return launch_pdl(block_merge_kernel<D, G>, dim3(p.batch, p.hkv), dim3(32 * kWarps), 0, s, true, p) == cudaSuccess
+    const int per_cta = kWarps / p.hg;
+    if (launch_pdl(block_decode_kernel<D, G>, dim3((p.ranges + per_cta - 1) / per_cta), dim3(kThreads), smem, s, true, p, kmap,
+                   vmap) != cudaSuccess)
+        return PKV_E_CUDA;
+    const bool few = q_rows * p.hkv < 2 * num_sms();
+    auto merge = few ? block_merge_kernel<D, G, 1, 32> : block_merge_kernel<D, G, G, kWarps>;
+    return launch_pdl(merge, dim3((unsigned)q_rows, p.hkv * (few ? G : 1)), dim3(few ? 1024 : 32 * kWarps), 0, s, true, p) == cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
 }
 
 template <int D>
-static int launch_group(int G, const BlockDecodeParams &p, cudaStream_t s) {
+static int launch_group(int G, const BlockDecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows,
+                        cudaStream_t s) {
     switch (G) {
-        case 1: return launch<D, 1>(p, s);
-        case 2: return launch<D, 2>(p, s);
-        case 4: return launch<D, 4>(p, s);
-        default: return launch<D, 8>(p, s);
+        case 1: return launch<D, 1>(p, kmap, vmap, q_rows, s);
+        case 2: return launch<D, 2>(p, kmap, vmap, q_rows, s);
+        case 4: return launch<D, 4>(p, kmap, vmap, q_rows, s);
+        default: return launch<D, 8>(p, kmap, vmap, q_rows, s);
     }
 }
 
@@ -500,6 +744,55 @@ static int check_group(const pkv_block_pool *pool, int32_t num_q_heads) {
     if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads) return PKV_E_INVALID;
     const int32_t G = num_q_heads / pool->num_kv_heads;
     return G == 1 || G == 2 || G == 4 || G == 8 ? PKV_OK : PKV_E_UNSUPPORTED;
+}
+
+// [slot][head][d] codes as 16-slot boxes of one head.
+static int code_map(CUtensorMap *m, const pkv_block_pool *pool, void *codes) {
+    const cuuint64_t dims[3] = {(cuuint64_t)pool->head_dim, (cuuint64_t)pool->num_kv_heads,
+                                (cuuint64_t)(pool->num_pages * pool->page_size)};
+    const cuuint64_t strides[2] = {(cuuint64_t)pool->head_dim, (cuuint64_t)block_slot_bytes(pool)};
+    const cuuint32_t box[3] = {(cuuint32_t)pool->head_dim, 1, kTile};
+    return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box,
+                        pool->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) == CUDA_SUCCESS
+               ? PKV_OK
+               : PKV_E_CUDA;
+}
+
+// Few query tokens a request (indptr NULL: one), over as many ranges as the workspace has records for.
+int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const int32_t *indptr, int64_t q_rows, const void *q,
+                     void *o, int32_t num_q_heads, float sm_scale, void *workspace, size_t ws_bytes, cudaStream_t s) {
+    const int32_t hkv = pool->num_kv_heads, G = num_q_heads / hkv, D = pool->head_dim;
+    BlockDecodeParams p;
+    p.k_exp = pool->k_exp;
+    p.v_exp = pool->v_exp;
+    p.num_pages = pool->num_pages;
+    p.shift = log2_of(pool->page_size);
+    p.hkv = hkv;
+    p.hg = head_group(hkv);
+    p.groups = hkv / p.hg;
+    p.table = batch->req_to_token;
+    p.stride = batch->stride;
+    p.num_rows = batch->num_rows;
+    p.batch = batch->batch;
+    p.rows = batch->req_pool_indices;
+    p.lens = batch->seq_lens;
+    p.indptr = indptr;
+    p.q = static_cast<const uint16_t *>(q);
+    p.o = static_cast<uint16_t *>(o);
+    p.scale_log2 = sm_scale * kLog2eB;
+    const size_t room = ws_bytes < kWorkspaceHeader ? 0 : (ws_bytes - kWorkspaceHeader) / range_bytes(p.hg, D);
+    p.ranges = (int32_t)std::min<size_t>((size_t)decode_ctas() * (kWarps / p.hg), room);
+    if (p.ranges < 1) return PKV_E_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.err = reinterpret_cast<int32_t *>(ws);
+    p.rec = reinterpret_cast<float *>(ws + kWorkspaceHeader);
+    p.rec_ml = p.rec + (size_t)p.ranges * 2 * p.hg * 8 * D;
+    p.wait = wait_policy(wait_limit_ns());
+    CUtensorMap kmap, vmap;
+    int rc = code_map(&kmap, pool, pool->k);
+    if (!rc) rc = code_map(&vmap, pool, pool->v);
+    if (rc) return rc;
+    return D == 128 ? launch_group<128>(G, p, kmap, vmap, q_rows, s) : launch_group<64>(G, p, kmap, vmap, q_rows, s);
 }
 
 }  // namespace pkv
@@ -510,7 +803,7 @@ extern "C" int pkv_decode_block_workspace(const pkv_block_pool *pool, int32_t nu
     if (!rc) rc = check_group(pool, num_q_heads);
     if (rc) return rc;
     if (!bytes) return PKV_E_INVALID;
-    *bytes = decode_workspace(pool->num_kv_heads, num_q_heads / pool->num_kv_heads, pool->head_dim);
+    *bytes = decode_workspace(pool->num_kv_heads, pool->head_dim);
     return PKV_OK;
 }
 
@@ -528,36 +821,10 @@ extern "C" int pkv_attn_decode_block(const pkv_block_pool *pool, const pkv_batch
     if (batch->page_size != pool->page_size || batch->stride < 0 || batch->stride >= ((int64_t)1 << 31) ||
         batch->num_rows < 0)
         return PKV_E_INVALID;
-    if (pool->num_kv_heads > 65535) return PKV_E_UNSUPPORTED;
+    if (num_q_heads > 65535) return PKV_E_UNSUPPORTED;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o)) & 15) return PKV_E_INVALID;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_E_INVALID;
-    const int32_t hkv = pool->num_kv_heads, G = num_q_heads / hkv, D = pool->head_dim;
-    if (ws_bytes < decode_workspace(hkv, G, D)) return PKV_E_WORKSPACE;
-    BlockDecodeParams p;
-    p.k = static_cast<const uint8_t *>(pool->k);
-    p.v = static_cast<const uint8_t *>(pool->v);
-    p.k_exp = pool->k_exp;
-    p.v_exp = pool->v_exp;
-    p.num_pages = pool->num_pages;
-    p.slot_bytes = block_slot_bytes(pool);
-    p.shift = log2_of(pool->page_size);
-    p.hkv = hkv;
-    p.hg = head_group(hkv);
-    p.groups = hkv / p.hg;
-    p.table = batch->req_to_token;
-    p.stride = batch->stride;
-    p.num_rows = batch->num_rows;
-    p.batch = batch->batch;
-    p.rows = batch->req_pool_indices;
-    p.lens = batch->seq_lens;
-    p.q = static_cast<const uint16_t *>(q);
-    p.o = static_cast<uint16_t *>(o);
-    p.scale_log2 = sm_scale * kLog2eB;
-    p.ranges = decode_ctas() * (kWarps / p.hg);
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.err = reinterpret_cast<int32_t *>(ws);
-    p.rec = reinterpret_cast<float *>(ws + kWorkspaceHeader);
-    p.rec_ml = p.rec + (size_t)p.ranges * 2 * p.hg * G * D;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return D == 128 ? launch_group<128>(G, p, s) : launch_group<64>(G, p, s);
+    if (ws_bytes < decode_workspace(pool->num_kv_heads, pool->head_dim)) return PKV_E_WORKSPACE;
+    return block_attend_few(pool, batch, nullptr, batch->batch, q, o, num_q_heads, sm_scale, workspace, ws_bytes,
+                            reinterpret_cast<cudaStream_t>(stream));
 }

@@ -100,6 +100,29 @@ int64_t extend_item_cost(const ExtendItem &x, int32_t tq, const std::vector<Pack
     return tiles * per + 4;
 }
 
+// An extend call over a block-scaled pool has two ways: gather every key run as bf16 rows, then the
+// tensor-core kernel; or the decode kernel, 8 / G query tokens of a request at a time, each such
+// stream reading the codes again (from L2 after the first).  The estimates, in microseconds, use
+// rates measured on GB300: streams take 0.036 ns a key and KV head (the decode kernel's own work, at
+// d = 128), the gather moves 6 bytes a code at 4.6 TB/s, an extend item costs 0.38 a unit of
+// extend_item_cost; each way starts in about 10.  (4 requests of 5 tokens after 9,000: 142 by the
+// gather, REPLACE by streams; 64 of 200 after 1,800: 440 against 5,000.)
+bool few_tokens_are_streams(int32_t batch, const int32_t *seq_lens, const int32_t *extend_lens, int32_t hq, int32_t hkv,
+                            int32_t d, int64_t gathered, const std::vector<ExtendItem> &items,
+                            const std::vector<PackInfo> &packs, int32_t num_sms) {
+    const int32_t G = hq / hkv, M = 8 / G;
+    double keys = 0.0;
+    for (int32_t r = 0; r < batch; ++r) keys += (double)((extend_lens[r] + M - 1) / M) * seq_lens[r];
+    const double streams = keys * hkv * (d == 128 ? 0.036e-3 : 0.024e-3) + 10.0;
+    double sum = 0.0, longest = 0.0;
+    for (const ExtendItem &x : items) {
+        const double c = 0.38 * (double)extend_item_cost(x, 128 / G, &packs);
+        sum += c;
+        longest = std::max(longest, c);
+    }
+    return streams < (double)gathered * hkv * d * 6.0 / 4.6e6 + std::max(sum / num_sms, longest) + 10.0;
+}
+
 // Keys per gather unit (one CTA each): up to 32, fewer when the gather is small, so that it
 // still spreads over about 4 CTAs per SM.
 int32_t gather_unit_keys(int64_t total_keys, int32_t num_sms) {
@@ -805,7 +828,14 @@ static int plan_extend_impl(int32_t batch, const int32_t *seq_lens, const int32_
     info->offsets[14] = (int64_t)packs.size();
     info->offsets[15] = (int64_t)off; off = align16(off + tok_row.size() * sizeof(int32_t));
     info->offsets[16] = ctx ? 1 : (fuse ? 2 : 0);
+    // for block-scaled pools: the query rows of each request, and whether its few query tokens are
+    // better attended as decode streams (see few_tokens_are_streams)
+    std::vector<int32_t> rows(qo_indptr, qo_indptr + batch + 1);
+    info->offsets[17] = (int64_t)off; off = align16(off + rows.size() * sizeof(int32_t));
+    info->offsets[18] = !ctx && !fuse && few_tokens_are_streams(batch, seq_lens, extend_lens, num_q_heads, num_kv_heads, head_dim,
+                                                                nkeys, items, packs, num_sms);
     std::vector<uint8_t> blob(std::max<size_t>(off, 16), 0);
+    put(blob, (size_t)info->offsets[17], rows);
     put(blob, (size_t)info->offsets[0], placed);
     put(blob, (size_t)info->offsets[13], packs);
     put(blob, (size_t)info->offsets[7], cta_off);

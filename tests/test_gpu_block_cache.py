@@ -452,7 +452,10 @@ EXTEND_EPS, EXTEND_LOG_EPS = 2.0 ** -7, 2.0 ** -8
     (2, 4, 64, 32, 0, [0, 31], [1, 2]), (5, 2, 128, 64, 0, [100], [190]), (16, 1, 64, 128, 128, [128, 200], [33, 3]),
     (1, 8, 128, 16, 0, [1000, 7], [3, 100]), (3, 8, 64, 256, 0, [5, 255], [251, 2])])
 @pytest.mark.parametrize("layout", ["separate", "interleaved"])
-def test_extend(pkv, hkv, g, d, page, shared, old, new, layout):
+@pytest.mark.parametrize("streams", [0, 1])
+def test_extend(pkv, hkv, g, d, page, shared, old, new, layout, streams):
+    """Both ways an extend call has (the plan chooses one): gathered rows on the tensor cores, and
+    few tokens at a time over the pages."""
     rng = np.random.default_rng(d + page)
     lens = [a + b for a, b in zip(old, new)]
     pages = sum(-(-n // page) for n in lens) + 1
@@ -464,6 +467,7 @@ def test_extend(pkv, hkv, g, d, page, shared, old, new, layout):
     if shared:
         cascade = pkv.Cascade(*(np.asarray(a, np.int32) for a in ([0], [0], [shared], [0, len(old)], range(len(old)))))
     plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d, cascade)
+    plan.info.offsets[18] = streams
     qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
     o = torch.full_like(qt, float("nan"))
     ws = words((plan.info.workspace_bytes + 3) // 4)
@@ -473,9 +477,48 @@ def test_extend(pkv, hkv, g, d, page, shared, old, new, layout):
     got = values(o)
     for r in range(len(old)):
         k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
-        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, np.arange(old[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
+        at = np.arange(old[r], lens[r])
+        if streams:
+            e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+            want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, at, DECODE_EPS, v_exp=e)
+        else:
+            want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, at, EXTEND_EPS, EXTEND_LOG_EPS)
         assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
 
+
+def test_extend_chooses_by_the_tokens(pkv):
+    """A few tokens after a long context are streams; many are gathered."""
+    few = pkv.plan_extend([9000] * 4, [5] * 4, np.arange(5) * 5, 32, 8, 128)
+    many = pkv.plan_extend([2000] * 64, [200] * 64, np.arange(65) * 200, 32, 8, 128)
+    assert few.info.offsets[18] == 1 and many.info.offsets[18] == 0
+
+
+@pytest.mark.parametrize("b,old,new", [(2, 20000, 3), (60, 700, 9), (300, 1, 2)])
+def test_extend_streams_over_many_ranges(pkv, b, old, new):
+    """Streams cut into many ranges, and more streams than ranges."""
+    rng = np.random.default_rng(b)
+    page, hkv, g, d = 16, 8, 4, 128
+    old = np.maximum(old - rng.integers(0, old // 3 + 1, b), 0)
+    ext = rng.integers(1, new + 1, b)
+    lens = (old + ext).tolist()
+    pages = sum(-(-n // page) for n in lens)
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    table, rows, batch = paged_batch(pkv, rng, lens, page, pages)
+    kill_tails(pool, was, table, rows, lens, page)
+    qo = np.concatenate([[0], np.cumsum(ext)])
+    plan = pkv.plan_extend(lens, ext, qo, hkv * g, hkv, d)
+    plan.info.offsets[18] = 1
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
+    o = torch.full_like(qt, float("nan"))
+    ws = words((plan.info.workspace_bytes + 3) // 4)
+    pkv.attn_extend_block(pool, batch, qt, o, d ** -0.5, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0 and torch.isfinite(o).all()
+    got = values(o)
+    for r in (range(b) if b < 5 else rng.permutation(b)[:6]):
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, d ** -0.5, np.arange(old[r], lens[r]), DECODE_EPS, v_exp=e)
+        assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
 
 def test_python_calls_check_their_tensors(pkv):
     rng = np.random.default_rng(0)

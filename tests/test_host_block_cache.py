@@ -131,7 +131,7 @@ def test_block_pool_checks_its_tensors():
     with pytest.raises(ValueError):
         pkv.BlockPool.allocate(4, 16, 2, 64, device="cpu", layout="striped")
     with pytest.raises(ValueError):    # no call takes a pool in host memory
-        good.c()
+        good.c(0)
     assert pkv.decode_block_workspace(good, 8) > 256
     with pytest.raises(pkv.PkvError):
         pkv.decode_block_workspace(good, 7)
