@@ -15,10 +15,9 @@
 //     scans the lengths itself: no host plan, no set-up kernel, ragged batches balance to a tile,
 //     and a captured graph follows the lengths).  A request inside one range is written directly;
 //     one that crosses ranges leaves a record (R, l, acc, ea) in each, joined by a second kernel.
-//   * A CTA has a consumer warp for each of 8 KV heads (fewer heads: several ranges side by side)
-//     and a producer warp that keeps a ring of tiles full: per head, tensor and tile one 16-row
-//     TMA box, swizzled, 96 KB of ring a CTA and two CTAs an SM.  (Loading codes straight into
-//     registers, one tile ahead, left each warp waiting for half its time: 4.6 of 5.3 TB/s.)
+//   * A CTA has a warp for each of 8 KV heads (fewer heads: several ranges side by side).  Each warp
+//     keeps a ring of its own full, asking for tiles 3 (d = 64: 6) ahead over the ends of requests:
+//     one 16-row TMA box, swizzled, for K and one for V; two CTAs an SM, 192 KB of ring.
 //   * K rows are the A operand (16 keys) of S^T = K Q^T, V^T the A operand of O^T = V^T P^T, and the
 //     query rows are the 8 columns of B: a group of up to 8 heads shares one MMA and the accumulators
 //     are d x 8.  V's bytes are paired by key with byte permutes on their way to f16.
@@ -38,9 +37,10 @@ namespace pkv {
 
 constexpr int kTile = 16;         // keys
 constexpr int kMinTiles = 4;      // per range, while there are few
-constexpr int kWarps = 8;         // consumers
+constexpr int kWarps = 8;
 constexpr int kRingBytes = 96 * 1024;
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBatch = 4;         // records a merging warp has in flight
 constexpr float kBias = 15.f;     // weights carry 2^15
 constexpr float kUnbias = 1.f / (1 << 15);
 constexpr float kLog2eB = 1.4426950408889634f;
@@ -79,23 +79,25 @@ PKV_DEV int32_t tiles_of(int32_t len) { return (int32_t)(((int64_t)len + kTile -
 
 // The cut of `total` tiles into n ranges whose sizes differ by at most one.
 struct Cut {
-    int64_t size, extra;
-    int32_t n;
-    PKV_DEV Cut(int64_t total, int32_t most) {
-        n = (int32_t)min((int64_t)most, max((int64_t)1, total / kMinTiles));
-        size = divide(total, n);
+    int32_t size, extra, n;
+    PKV_DEV Cut(int32_t total, int32_t most) {
+        n = min(most, max(1, total / kMinTiles));
+        size = (int32_t)((uint32_t)total / (uint32_t)n);
         extra = total - size * n;
     }
-    PKV_DEV int64_t start(int32_t i) const { return size * i + min((int64_t)i, extra); }
-    PKV_DEV int32_t range_of(int64_t t) const {
-        const int64_t big = extra * (size + 1);
-        return (int32_t)(t < big ? divide(t, size + 1) : extra + divide(t - big, size));
-    }
-    // (a 64-bit division takes hundreds of cycles, and a kernel's start waits for several)
-    static PKV_DEV int64_t divide(int64_t a, int64_t b) {
-        return a < ((int64_t)1 << 32) && b < ((int64_t)1 << 32) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+    PKV_DEV int32_t start(int32_t i) const { return size * i + min(i, extra); }
+    PKV_DEV int32_t range_of(int32_t t) const {
+        const int32_t big = extra * (size + 1);
+        return t < big ? (int32_t)((uint32_t)t / (uint32_t)(size + 1)) : extra + (int32_t)((uint32_t)(t - big) / (uint32_t)size);
     }
 };
+// The line's length for one group of heads as the kernels use it: 0 for one past 2^31 tiles in all
+// (34 billion keys).
+PKV_DEV int32_t line_length(const BlockDecodeParams &p, int64_t n, bool report) {
+    if (n * p.groups <= 0x7FFFFFFF) return (int32_t)n;
+    if (report) set_error(p.err, DERR_POSITION);
+    return 0;
+}
 
 PKV_DEV void mma_f16_16816(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -336,78 +338,75 @@ PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_
     }
 }
 
-// A piece: tiles [j0, j1) of stream s of request r, inside one range.
-struct Piece {
-    int32_t r, s, len, ext, q0;  // request, stream, its length, query tokens and first query row
-    int32_t head0;               // first KV head of the group of heads
-    int32_t j0, j1;
-    int32_t rec;                 // record, -1 for a whole stream
-};
+// A place on the line: stream s of request r for one group of heads, whose first tile is tile `first`
+// of the line.
+template <int G>
+struct Walk {
+    static constexpr int32_t M = 8 / G;
+    int32_t grp, r, s, len, ext, q0, first, tiles;
 
-// Calls f(piece) for every piece of tiles [at, end) of the line; base: tiles before each of the 256
-// chunks of requests; n tiles in a group of heads.  f returns false to stop.
-template <int G, class F>
-PKV_DEV void for_pieces(const BlockDecodeParams &p, const int64_t *base, int chunk, int64_t n, int32_t range, int64_t at,
-                        int64_t end, F f) {
-    constexpr int32_t M = 8 / G;
-    const int64_t begin = at;
-    while (at < end) {
-        const int32_t grp = p.groups == 1 ? 0 : (int32_t)(at / n);
-        const int64_t off = (int64_t)grp * n, stop = min(end, off + n);
+    PKV_DEV void load(const BlockDecodeParams &p) {
+        len = checked_len(p, r, false);
+        const int2 qr = query_rows(p, r, len);
+        q0 = qr.x;
+        ext = qr.y;
+        s = 0;
+        size(p);
+    }
+    PKV_DEV void size(const BlockDecodeParams &p) {
+        tiles = s * M < ext ? tiles_of(p.indptr ? stream_len(len, ext, s, M) : len) : 0;
+    }
+    // To the stream that holds tile `at` of the line, from one at or before it.  False when there is
+    // none (the lengths changed under the call).
+    PKV_DEV bool seek(const BlockDecodeParams &p, int32_t at) {
+        while (at - first >= tiles) {
+            first += tiles;
+            if ((s + 1) * M < ext) {
+                ++s;
+                size(p);
+                continue;
+            }
+            if (++r >= p.batch) {
+                r = 0;
+                if (++grp >= p.groups) return false;
+            }
+            load(p);
+        }
+        return true;
+    }
+    // base: tiles before each of the 256 chunks of requests; n tiles in a group of heads
+    PKV_DEV bool start(const BlockDecodeParams &p, const int32_t *base, int chunk, int32_t n, int32_t at) {
+        grp = p.groups == 1 ? 0 : at / n;
         int lo = 0, hi = 32 * kWarps;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (base[mid] <= at - off) lo = mid; else hi = mid;
+            if (base[mid] <= at - grp * n) lo = mid; else hi = mid;
         }
-        int64_t first = off + base[lo];  // the stream's first tile
-        for (int r = lo * chunk; at < stop; ++r) {
-            if (r >= p.batch) return;  // the lengths changed under the call
-            const int32_t len = checked_len(p, r, false);
-            const int2 qr = query_rows(p, r, len);
-            for (int32_t s = 0; s * M < qr.y && at < stop; ++s) {
-                const int32_t tiles = tiles_of(p.indptr ? stream_len(len, qr.y, s, M) : len);
-                if (first + tiles > at) {
-                    Piece x;
-                    x.r = r;
-                    x.s = s;
-                    x.len = len;
-                    x.ext = qr.y;
-                    x.q0 = qr.x;
-                    x.head0 = grp * p.hg;
-                    x.j0 = (int32_t)(at - first);
-                    x.j1 = (int32_t)min((int64_t)tiles, stop - first);
-                    x.rec = x.j0 == 0 && x.j1 == tiles ? -1 : 2 * range + (first < begin ? 0 : 1);
-                    if (!f(x)) return;
-                    at = first + x.j1;
-                }
-                first += tiles;
-            }
-        }
+        r = lo * chunk;
+        first = grp * n + base[lo];
+        load(p);
+        return seek(p, at);
     }
-}
+};
 
-// A bounded wait of the ring (see WaitPolicy).
-PKV_DEV bool ring_wait(uint64_t *bar, uint32_t parity, int32_t *abort_flag, const BlockDecodeParams &p, int where) {
+// A bounded wait for a tile (see WaitPolicy).
+PKV_DEV bool tile_wait(uint64_t *bar, uint32_t parity, const BlockDecodeParams &p) {
     if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
         if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if ((it & p.wait.check_mask) == 0) {
-            if (*reinterpret_cast<volatile int32_t *>(abort_flag)) return false;
-            if (global_timer_ns() - t0 > p.wait.limit_ns) {
-                set_error(p.err, DERR_TIMEOUT | where);
-                *reinterpret_cast<volatile int32_t *>(abort_flag) = 1;
-                return false;
-            }
+        if ((it & p.wait.check_mask) == 0 && global_timer_ns() - t0 > p.wait.limit_ns) {
+            set_error(p.err, DERR_TIMEOUT | 0x41);
+            return false;
         }
     }
 }
 
 template <int D>
 struct Ring {
-    static constexpr int kBox = kTile * D;                      // a head's K or V tile
-    static constexpr int kStages = kRingBytes / (kWarps * 2 * kBox);  // 3 (d = 128), 6 (d = 64)
-    static constexpr int kSmem = kRingBytes + 1024;             // + alignment
+    static constexpr int kBox = kTile * D;                            // a head's K or V tile
+    static constexpr int kStages = kRingBytes / (kWarps * 2 * kBox);  // of one warp: 3 (d = 128), 6 (d = 64)
+    static constexpr int kSmem = kRingBytes + 1024;                   // + alignment
 };
 
 template <int D, int G>
@@ -416,91 +415,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     using R = Ring<D>;
     extern __shared__ uint8_t dyn[];
     __shared__ int64_t warp_sums[kWarps];
-    __shared__ int64_t base[32 * kWarps + 1];  // tiles before each thread's chunk of requests
-    __shared__ uint64_t full[kWarps][R::kStages], empty[kWarps][R::kStages];  // per group of hg warps
-    __shared__ int32_t abort_flag;
-    uint8_t *ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
+    __shared__ int32_t base[kThreads + 1];  // tiles before each thread's chunk of requests
+    __shared__ uint64_t full[kWarps][R::kStages];
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = kWarps / p.hg;
     if (tid == 0) {
-        for (int i = 0; i < groups; ++i)
-            for (int s = 0; s < R::kStages; ++s) {
-                mbar_init(&full[i][s], 1);
-                mbar_init(&empty[i][s], p.hg);
-            }
-        abort_flag = 0;
+        for (int i = 0; i < kWarps * R::kStages; ++i) mbar_init(&full[0][0] + i, 1);
         fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
     pdl_wait();
     pdl_trigger();
-    const int chunk = (p.batch + 32 * kWarps - 1) / (32 * kWarps);
+    const int chunk = (p.batch + kThreads - 1) / kThreads;
     int64_t mine = 0;
-    if (warp < kWarps)
-        for (int r = tid * chunk; r < min((tid + 1) * chunk, p.batch); ++r) mine += request_tiles(p, r, M, blockIdx.x == 0);
+    for (int r = tid * chunk; r < min((tid + 1) * chunk, p.batch); ++r) mine += request_tiles(p, r, M, blockIdx.x == 0);
     int64_t scan = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, scan, d);
         if (lane >= d) scan += y;
     }
-    if (lane == 31 && warp < kWarps) warp_sums[warp] = scan;
+    if (lane == 31) warp_sums[warp] = scan;
     __syncthreads();
-    int64_t before = 0, n = 0;
+    int64_t before = 0, all = 0;
     for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) before = n;
-        n += warp_sums[w];
+        if (w == warp) before = all;
+        all += warp_sums[w];
     }
-    if (warp < kWarps) base[tid] = before + scan - mine;
-    if (tid == 0) base[32 * kWarps] = n;
+    const int32_t n = line_length(p, all, blockIdx.x == 0 && tid == 0);
+    base[tid] = (int32_t)(before + scan - mine);
+    if (tid == 0) base[kThreads] = n;
     __syncthreads();
     if (n == 0) return;
 
     const Cut cut(n * p.groups, p.ranges);
     const int tpp = p.shift - 4;  // log2 of the tiles in a page
-    const int grp_bytes = p.hg * 2 * R::kBox;                // one stage of one group of warps
-    if (warp == kWarps) {
-        // ------------------------------------------------- producer: lane i feeds group i's ring
-        const int32_t range = blockIdx.x * groups + lane;
-        if (lane >= groups || range >= cut.n) return;
-        uint8_t *mine_at = ring + lane * R::kStages * grp_bytes;
-        uint32_t t = 0;
-        bool bad = false;
-        for_pieces<G>(p, base, chunk, n, range, cut.start(range), cut.start(range + 1), [&](const Piece &x) {
-            const int32_t *row = p.table + (int64_t)__ldg(p.rows + x.r) * p.stride;
-            int32_t next = __ldg(row + (x.j0 >> tpp));
-            for (int32_t j = x.j0; j < x.j1; ++j, ++t) {
-                const int32_t page = next;
-                next = __ldg(row + (min(j + 1, x.j1 - 1) >> tpp));
-                const int st = t % R::kStages;
-                if (t >= R::kStages && !ring_wait(&empty[lane][st], (t / R::kStages - 1) & 1, &abort_flag, p, 0x41)) return false;
-                // a page outside the pool: rows past the maps' last, which read as zeros
-                const bool ok = (uint32_t)page < (uint64_t)p.num_pages;
-                bad |= !ok;
-                const int32_t slot = ok ? (page << p.shift) + (j * kTile & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
-                uint64_t *bar = &full[lane][st];
-                mbar_arrive_expect_tx(bar, grp_bytes);
-                const uint32_t dst = smem_u32(mine_at + st * grp_bytes);
-                for (int h = 0; h < p.hg; ++h) {
-                    tma_load_3d(dst + 2 * h * R::kBox, &kmap, 0, x.head0 + h, slot, bar);
-                    tma_load_3d(dst + (2 * h + 1) * R::kBox, &vmap, 0, x.head0 + h, slot, bar);
-                }
-            }
-            return true;
-        });
-        if (bad) set_error(p.err, DERR_SLOT_RANGE);
-        // every copy lands before the CTA ends, also when the consumers gave up
-        for (uint32_t u = t > R::kStages ? t - R::kStages : 0; u < t; ++u)
-            mbar_wait(&full[lane][u % R::kStages], (u / R::kStages) & 1);
-        return;
-    }
-
-    // --------------------------------------------------------------- consumer: one KV head a warp
-    const int hl = warp % p.hg, grp = warp / p.hg;
-    const int32_t range = blockIdx.x * groups + grp;
+    const int hl = warp % p.hg;
+    const int32_t range = blockIdx.x * (kWarps / p.hg) + warp / p.hg;
     if (range >= cut.n) return;
+    const int32_t begin = cut.start(range);
+    int32_t end = cut.start(range + 1);
     const int g = lane >> 2, c = lane & 3;
     int k_off[D / 64], v_off[2];
 #pragma unroll
@@ -508,164 +463,145 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         v_off[i] = D == 128 ? piece_at<D>(key_of<D>(2 * c + i), g) : piece_at<D>(key_of<D>(2 * c + i), g >> 1) + 8 * (g & 1);
-    const uint8_t *mine_at = ring + grp * R::kStages * grp_bytes + 2 * hl * R::kBox;
-    uint32_t t = 0;
-    for_pieces<G>(p, base, chunk, n, range, cut.start(range), cut.start(range + 1), [&](const Piece &x) {
-        const int kv_head = x.head0 + hl;
-        const int32_t *row = p.table + (int64_t)__ldg(p.rows + x.r) * p.stride;
+    uint8_t *ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023) + warp * R::kStages * 2 * R::kBox;
+    uint64_t *bars = full[warp];
+
+    // The asking side runs up to kStages tiles ahead, over the ends of streams; the page of the
+    // tile that it asks for next is already there or on its way.
+    Walk<G> ask, cur;
+    if (!ask.start(p, base, chunk, n, begin)) return;
+    cur = ask;
+    int32_t ask_at = begin, ask_page = 0;
+    const int32_t *ask_row = nullptr;
+    bool bad = false;
+    auto next_page = [&] {
+        if (ask_at >= end) return;
+        if (ask_row == nullptr || ask_at - ask.first >= ask.tiles) {
+            if (!ask.seek(p, ask_at)) {  // no such tile: what was asked for is all there is
+                end = ask_at;
+                return;
+            }
+            ask_row = p.table + (int64_t)__ldg(p.rows + ask.r) * p.stride;
+        }
+        ask_page = __ldg(ask_row + ((ask_at - ask.first) >> tpp));
+    };
+    auto ask_tile = [&](uint32_t st) {
+        if (ask_at >= end) return;
+        // a page outside the pool: rows past the maps' last, which read as zeros
+        const bool in = (uint32_t)ask_page < (uint64_t)p.num_pages;
+        bad |= !in;
+        const int32_t key = (ask_at - ask.first) * kTile;
+        const int32_t slot = in ? (ask_page << p.shift) + (key & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bars[st], 2 * R::kBox);
+            const uint32_t dst = smem_u32(ring + st * 2 * R::kBox);
+            tma_load_3d(dst, &kmap, 0, ask.grp * p.hg + hl, slot, &bars[st]);
+            tma_load_3d(dst + R::kBox, &vmap, 0, ask.grp * p.hg + hl, slot, &bars[st]);
+        }
+        ++ask_at;
+        next_page();
+    };
+    next_page();
+    for (uint32_t st = 0; st < R::kStages; ++st) ask_tile(st);
+
+    uint32_t sg = 0, phase = 0;
+    int32_t at = begin;
+    bool ok = true;
+    while (at < end && cur.seek(p, at)) {
+        const int32_t j0 = at - cur.first, j1 = min(cur.tiles, end - cur.first);
+        const int kv_head = cur.grp * p.hg + hl;
+        const int32_t *row = p.table + (int64_t)__ldg(p.rows + cur.r) * p.stride;
         auto page_exp = [&](const uint8_t *e, int32_t page) {
             return (uint32_t)page < (uint64_t)p.num_pages ? (int)__ldg(e + (int64_t)page * p.hkv + kv_head) : 127;
         };
         // exponents come a tile ahead, the page they are read by two tiles ahead
-        int32_t page = __ldg(row + (x.j0 >> tpp));
+        int32_t page = __ldg(row + (j0 >> tpp));
         int ek = page_exp(p.k_exp, page), ev = page_exp(p.v_exp, page);
-        page = __ldg(row + (min(x.j0 + 1, x.j1 - 1) >> tpp));
+        page = __ldg(row + (min(j0 + 1, j1 - 1) >> tpp));
         // columns: token s M + col / G of the request, head col % G of the group
-        const int32_t tok = x.s * M + g / G;
+        const int32_t tok = cur.s * M + g / G;
         uint32_t qb[D / 16][2];
-        const int e = load_query<D>(g / G < M && tok < x.ext ? p.q + ((int64_t)(x.q0 + tok) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
+        const int e = load_query<D>(
+            g / G < M && tok < cur.ext ? p.q + ((int64_t)(cur.q0 + tok) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
         float cs[2];
         int32_t sees[2], out[2];
-        const int32_t last = p.indptr ? stream_len(x.len, x.ext, x.s, M) : x.len;
+        const int32_t last = p.indptr ? stream_len(cur.len, cur.ext, cur.s, M) : cur.len;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
-            const int32_t tk = x.s * M + (2 * c + h) / G;
-            const bool on = (2 * c + h) / G < M && tk < x.ext;
-            out[h] = on ? x.q0 + tk : -1;
-            sees[h] = on ? x.len - x.ext + tk + 1 : last;
+            const int32_t tk = cur.s * M + (2 * c + h) / G;
+            const bool on = (2 * c + h) / G < M && tk < cur.ext;
+            out[h] = on ? cur.q0 + tk : -1;
+            sees[h] = on ? cur.len - cur.ext + tk + 1 : last;
         }
-        const int32_t all_see = x.len - x.ext + x.s * M + 1;  // keys that every column sees
+        const int32_t all_see = cur.len - cur.ext + cur.s * M + 1;  // keys that every column sees
         DecodeState<D> st;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
         st.m[0] = st.m[1] = -INFINITY;
         st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
+        int32_t j = j0;
 #pragma unroll 1
-        for (int32_t j = x.j0; j < x.j1; ++j, ++t) {
-            const int sg = t % R::kStages;
+        for (; j < j1; ++j) {
             const int next_ek = page_exp(p.k_exp, page), next_ev = page_exp(p.v_exp, page);
-            page = __ldg(row + (min(j + 2, x.j1 - 1) >> tpp));
-            if (!__all_sync(0xffffffffu, ring_wait(&full[grp][sg], (t / R::kStages) & 1, &abort_flag, p, 0x42))) return false;
-            const uint8_t *at = mine_at + sg * grp_bytes;
+            page = __ldg(row + (min(j + 2, j1 - 1) >> tpp));
+            ok = __all_sync(0xffffffffu, tile_wait(&bars[sg], phase, p));
+            if (!ok) break;
+            const uint8_t *tile = ring + sg * 2 * R::kBox;
             float w[4];
-            tile_scores<D>(w, qb, at, k_off);
+            tile_scores<D>(w, qb, tile, k_off);
             uint32_t v[4][D / 32];
-            read_v<D>(v, at + R::kBox, v_off, last - j * kTile);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[grp][sg]);
+            read_v<D>(v, tile + R::kBox, v_off, last - j * kTile);
+            __syncwarp();  // every lane has read the stage: ask for the tile kStages ahead
+            ask_tile(sg);
+            if (++sg == R::kStages) {
+                sg = 0;
+                phase ^= 1;
+            }
             uint32_t b0, b1;
             tile_weights<D>(st, w, cs, ek, ev, j * kTile, sees, all_see, b0, b1);
             tile_product<D>(st, v, b0, b1);
             ek = next_ek;
             ev = next_ev;
         }
-        write_piece<D, G>(p, st, kv_head, out, x.rec, hl);
-        return true;
-    });
+        at = cur.first + j;
+        if (!ok) break;
+        const bool whole = j0 == 0 && j1 == cur.tiles;
+        write_piece<D, G>(p, st, kv_head, out, whole ? -1 : 2 * range + (cur.first < begin ? 0 : 1), hl);
+    }
+    if (bad && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+    // after a wait that gave up: what was asked for lands before the CTA ends
+    for (int32_t left = ask_at - at; left > 0; --left) {
+        mbar_wait(&bars[sg], phase);
+        if (++sg == R::kStages) {
+            sg = 0;
+            phase ^= 1;
+        }
+    }
 }
 
-// Joins the records of the streams that cross ranges and clears the rows of empty requests.  A CTA
-// takes Q query heads of one (query row, KV head): its warps share each head's records, four in
-// flight a warp, and combine through shared memory.  Q is the whole group, or 1 where that would
-// leave SMs idle: a request alone in the batch may have a record of every range, and gets 32 warps a
-// head (100,001 keys: 24 us with 8 warps, REPLACE with 32).
-template <int D, int G, int Q, int W>
-__global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodeParams p) {
-    __shared__ int64_t warp_sums[2 * W];
-    __shared__ float s_acc[W][D];
-    __shared__ float4 s_ml[W];
-    __shared__ int32_t s_req;
-    constexpr int32_t M = 8 / G;
-    const int head = blockIdx.y / (G / Q), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int32_t r = blockIdx.x, tok = 0;
-    if (p.indptr) {  // the request of this query row
-        if (tid == 0) s_req = -1;
-        __syncthreads();
-        for (int i = tid; i < p.batch; i += 32 * W)
-            if (__ldg(p.indptr + i) <= r && r < __ldg(p.indptr + i + 1)) s_req = i;
-        __syncthreads();
-        tok = s_req < 0 ? 0 : r - __ldg(p.indptr + s_req);
-        r = s_req;
-    }
-    int64_t before = 0, n = 0;
-    for (int i = tid; i < p.batch; i += 32 * W) {
-        const int64_t t = request_tiles(p, i, M, false);
-        n += t;
-        if (i < r) before += t;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        n += __shfl_xor_sync(0xffffffffu, n, d);
-        before += __shfl_xor_sync(0xffffffffu, before, d);
-    }
-    if (lane == 0) {
-        warp_sums[warp] = n;
-        warp_sums[W + warp] = before;
-    }
-    __syncthreads();
-    n = before = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        n += warp_sums[w];
-        before += warp_sums[W + w];
-    }
-    const int32_t len = r < 0 ? 0 : checked_len(p, r, false);
-    int32_t tiles = tiles_of(len);
-    if (p.indptr && r >= 0) {
-        const int32_t ext = query_rows(p, r, len).y, s = tok / M;
-        for (int32_t i = 0; i < s; ++i) before += tiles_of(stream_len(len, ext, i, M));
-        tiles = tok < ext ? tiles_of(stream_len(len, ext, s, M)) : 0;
-    }
-    pdl_wait();  // the records
-    pdl_trigger();
-    constexpr int V = D / 32;            // elements a lane holds
-    constexpr int kShare = W / Q;   // warps of one query head
-    const int q = blockIdx.y % (G / Q) * Q + warp / kShare, sub = warp % kShare;
-    const int col = tok % M * G + q;
-    uint32_t *out = reinterpret_cast<uint32_t *>(p.o + (((int64_t)blockIdx.x * p.hkv + head) * G + q) * D + lane * V);
-    if (tiles == 0) {
-        if (sub == 0)
-#pragma unroll
-            for (int v = 0; v < V; v += 2) out[v / 2] = 0u;
-        return;
-    }
-    const Cut cut(n * p.groups, p.ranges);
-    const int64_t first = (int64_t)(head / p.hg) * n + before;
-    const int32_t i0 = cut.range_of(first), i1 = cut.range_of(first + tiles - 1);
-    if (i0 == i1) return;
+// One query head's records i0 .. i1 into its row; `on`: there are any for this warp's head.
+template <int D, int W, int S>
+PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, int32_t i0, int32_t i1, int hl, int col,
+                         float (&s_acc)[W][D], float4 (&s_ml)[W]) {
+    constexpr int V = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % S;
+    if (!on) i1 = i0 - 1;
     float top = -INFINITY, L = 0.f, E = 0.f, O[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) O[v] = 0.f;
-    // folds in a record (or another warp's sums)
-    auto join = [&](const float4 &x, const float *a) {
-        if (x.x > top) {
-            const float f = ex2(top - x.x);
-            L *= ex2(top - x.x + (x.z - E));
-#pragma unroll
-            for (int v = 0; v < V; ++v) O[v] *= f;
-            top = x.x;
-            E = x.z;
-        }
-        if (x.x == -INFINITY) return;
-        const float w = ex2(x.x - top);
-        L += x.y * ex2(x.x - top - (x.z - E));
-#pragma unroll
-        for (int v = 0; v < V; ++v) O[v] += a[v] * w;
-    };
-    constexpr int kBatch = 4;
-    for (int32_t i = i0 + sub; i <= i1; i += kShare * kBatch) {
+    for (int32_t i = i0 + sub; i <= i1; i += S * kBatch) {
         float4 ml[kBatch];
         float a[kBatch][V];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int32_t k = i + b * kShare;
+            const int32_t k = i + b * S;
             ml[b] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[b][v] = 0.f;
             if (k > i1) continue;
-            // a stream's first range ends inside it (slot 1); the others begin inside it (slot 0)
-            const int64_t rec = (((int64_t)k * 2 + (k == i0 && first >= cut.start(i0) ? 1 : 0)) * p.hg + head % p.hg) * 8 + col;
+            // a stream's first range ends inside it (record 1), the others begin inside it (record 0)
+            const int64_t rec = (((int64_t)k * 2 + (k == i0)) * p.hg + hl) * 8 + col;
             ml[b] = *reinterpret_cast<const float4 *>(p.rec_ml + rec * 4);
             if constexpr (V == 4) {
                 const float4 y = *reinterpret_cast<const float4 *>(p.rec + rec * D + lane * V);
@@ -679,23 +615,139 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
                 a[b][1] = y.y;
             }
         }
+        // the batch's reference first, so that its terms add independently
+        const float was = top, was_e = E;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) join(ml[b], a[b]);
+        for (int b = 0; b < kBatch; ++b)
+            if (ml[b].x > top) {
+                top = ml[b].x;
+                E = ml[b].z;
+            }
+        if (top == -INFINITY) continue;
+        const float f = ex2(was - top);
+        L *= ex2(was - top + (E - was_e));
+#pragma unroll
+        for (int v = 0; v < V; ++v) O[v] *= f;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const float w = ex2(ml[b].x - top);
+            L += ml[b].y * ex2(ml[b].x - top + (E - ml[b].z));
+#pragma unroll
+            for (int v = 0; v < V; ++v) O[v] += a[b][v] * w;
+        }
     }
+    if constexpr (S > 1) {
+        __syncthreads();  // the combining warp of the head before has read
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = O[v];
-    if (lane == 0) s_ml[warp] = make_float4(top, L, E, 0.f);
-    __syncthreads();
-    if (sub != 0) return;
-    for (int w = 1; w < kShare; ++w) {
-        float a[V];
+        for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = O[v];
+        if (lane == 0) s_ml[warp] = make_float4(top, L, E, 0.f);
+        __syncthreads();
+        if (sub != 0) return;
+        // the warps' sums the same way: lane w takes warp w's reference, sum and factor
+        const float4 x = lane < S ? s_ml[warp + lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        top = x.x;
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[v] = s_acc[warp + w][lane * V + v];
-        join(s_ml[warp + w], a);
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float m = top == -INFINITY ? 0.f : top;
+        E = __shfl_sync(0xffffffffu, x.z, __ffs(__ballot_sync(0xffffffffu, x.x == top)) - 1);
+        const float f = ex2(x.x - m);
+        L = x.x == -INFINITY ? 0.f : x.y * ex2(x.x - m + (E - x.z));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+#pragma unroll
+        for (int v = 0; v < V; ++v) O[v] = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < S; ++w) {
+            const float fw = __shfl_sync(0xffffffffu, f, w);
+#pragma unroll
+            for (int v = 0; v < V; ++v) O[v] += s_acc[warp + w][lane * V + v] * fw;
+        }
     }
+    if (!on) return;
     const float inv = row_scale(L, E);
 #pragma unroll
-    for (int v = 0; v < V; v += 2) out[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
+    for (int v = 0; v < V; v += 2)
+        reinterpret_cast<uint32_t *>(out + lane * V)[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
+}
+
+// Joins the records of the streams that cross ranges and clears the rows of empty requests.  A CTA
+// takes a query row and every gridDim.y-th (W / S) query heads, S warps a head: they share the
+// head's records, four in flight a warp, and combine through shared memory.  S grows with the
+// records of a stream: 1 for a few, 32 for a request alone in the batch, which may have one of every
+// range (100,001 keys: 24 us with 8 warps a head, 6 with 32).
+template <int D, int G, int W, int S>
+__global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodeParams p) {
+    __shared__ int64_t warp_sums[2 * W];
+    __shared__ float s_acc[W][D];
+    __shared__ float4 s_ml[W];
+    __shared__ int32_t s_req;
+    constexpr int32_t M = 8 / G;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t r = blockIdx.x, tok = 0;
+    if (p.indptr) {  // the request of this query row
+        if (tid == 0) s_req = -1;
+        __syncthreads();
+        for (int i = tid; i < p.batch; i += 32 * W)
+            if (__ldg(p.indptr + i) <= r && r < __ldg(p.indptr + i + 1)) s_req = i;
+        __syncthreads();
+        tok = s_req < 0 ? 0 : r - __ldg(p.indptr + s_req);
+        r = s_req;
+    }
+    int64_t before = 0, all = 0;
+    for (int i = tid; i < p.batch; i += 32 * W) {
+        const int64_t t = request_tiles(p, i, M, false);
+        all += t;
+        if (i < r) before += t;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, d);
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+    }
+    if (lane == 0) {
+        warp_sums[warp] = all;
+        warp_sums[W + warp] = before;
+    }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        all += warp_sums[w];
+        before += warp_sums[W + w];
+    }
+    const int32_t n = line_length(p, all, false);
+    const int32_t len = r < 0 || n == 0 ? 0 : checked_len(p, r, false);
+    int32_t tiles = tiles_of(len);
+    if (p.indptr && len > 0) {
+        const int32_t ext = query_rows(p, r, len).y, s = tok / M;
+        for (int32_t i = 0; i < s; ++i) before += tiles_of(stream_len(len, ext, i, M));
+        tiles = tok < ext ? tiles_of(stream_len(len, ext, s, M)) : 0;
+    }
+    constexpr int V = D / 32;  // elements a lane holds
+    const int sub = warp % S;
+    const Cut cut(max(n * p.groups, 1), p.ranges);
+    int32_t grp = -1, i0 = 0, i1 = 0;
+    pdl_wait();  // the records
+    pdl_trigger();
+    const int hq = p.hkv * G, step = W / S * gridDim.y;
+    for (int h0 = W / S * blockIdx.y; h0 < hq; h0 += step) {
+        const int qh = h0 + warp / S;
+        const bool on = qh < hq;
+        const int head = on ? qh / G : 0, q = qh % G;
+        uint16_t *out = p.o + ((int64_t)blockIdx.x * hq + qh) * D;
+        if (tiles == 0) {
+            if (on && sub == 0)
+                for (int d = lane; d < D / 2; d += 32) reinterpret_cast<uint32_t *>(out)[d] = 0u;
+            continue;
+        }
+        if (head / p.hg != grp) {
+            grp = head / p.hg;
+            const int32_t first = grp * n + (int32_t)before;
+            i0 = cut.range_of(first);
+            i1 = cut.range_of(first + tiles - 1);
+        }
+        merge_head<D, W, S>(p, out, on && i0 < i1, i0, i1, head % p.hg, tok % M * G + q, s_acc, s_ml);
+    }
 }
 
 static int head_group(int32_t hkv) {
@@ -722,9 +774,14 @@ static int launch(const BlockDecodeParams &p, const CUtensorMap &kmap, const CUt
     if (launch_pdl(block_decode_kernel<D, G>, dim3((p.ranges + per_cta - 1) / per_cta), dim3(kThreads), smem, s, true, p, kmap,
                    vmap) != cudaSuccess)
         return PKV_E_CUDA;
-    const bool few = q_rows * p.hkv < 2 * num_sms();
-    auto merge = few ? block_merge_kernel<D, G, 1, 32> : block_merge_kernel<D, G, G, kWarps>;
-    return launch_pdl(merge, dim3((unsigned)q_rows, p.hkv * (few ? G : 1)), dim3(few ? 1024 : 32 * kWarps), 0, s, true, p) == cudaSuccess
+    // records of a stream, about, and CTAs for a few waves of the GPU's
+    const int64_t each = p.ranges / std::max<int64_t>(q_rows * p.groups, 1), hq = p.hkv * G;
+    auto merge = each > 64 ? block_merge_kernel<D, G, 32, 32> : each > 4 ? block_merge_kernel<D, G, kWarps, kWarps>
+                                                                         : block_merge_kernel<D, G, kWarps, 1>;
+    const int64_t heads = each > 4 ? 1 : kWarps;  // a CTA's at a time
+    const int64_t y = std::min<int64_t>((hq + heads - 1) / heads, std::max<int64_t>(1, 4 * (int64_t)num_sms() / q_rows));
+    return launch_pdl(merge, dim3((unsigned)q_rows, (unsigned)y), dim3(each > 64 ? 1024 : 32 * kWarps), 0, s, true, p) ==
+                   cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
 }
