@@ -59,6 +59,7 @@ struct BlockDecodeParams {
     uint16_t *o;
     float scale_log2;
     int32_t ranges;  // at most
+    const int32_t *share;  // decode: tiles that the requests of a stream have in common, NULL: none
     float *rec;      // [range][2][hg][8 columns][D], then (R, l, ea, -) [range][2][hg][8][4]
     float *rec_ml;
     int32_t *err;
@@ -125,11 +126,27 @@ PKV_DEV int2 query_rows(const BlockDecodeParams &p, int r, int32_t len) {
 // Keys that the last token of stream s of a request sees (streams of M = 8 / G tokens).
 PKV_DEV int32_t stream_len(int32_t len, int32_t ext, int32_t s, int32_t M) { return len - ext + min(ext, (s + 1) * M); }
 
-PKV_DEV int64_t request_tiles(const BlockDecodeParams &p, int r, int32_t M, bool report) {
-    const int32_t len = checked_len(p, r, report);
-    if (!p.indptr) return tiles_of(len);
+// Decode: stream i is requests i M .. i M + M - 1, whose first shared_tiles are the same pages.  Its
+// tiles: those, seen by every column, then each request's others, seen by its own.
+PKV_DEV int32_t shared_tiles(const BlockDecodeParams &p, int i) { return p.share ? p.share[i] : 0; }
+
+template <int32_t M>
+PKV_DEV int64_t stream_tiles(const BlockDecodeParams &p, int i, bool report) {
+    const int32_t share = shared_tiles(p, i);
+    int64_t n = share;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (i * M + m < p.batch) n += tiles_of(checked_len(p, i * M + m, report)) - share;
+    return n;
+}
+// What a chunk of the line is counted in: streams (decode), or requests with all their streams.
+template <int32_t M>
+PKV_DEV int32_t num_units(const BlockDecodeParams &p) { return p.indptr ? p.batch : (p.batch + M - 1) / M; }
+template <int32_t M>
+PKV_DEV int64_t unit_tiles(const BlockDecodeParams &p, int i, bool report) {
+    if (!p.indptr) return stream_tiles<M>(p, i, report);
+    const int32_t len = checked_len(p, i, report), ext = query_rows(p, i, len).y;
     int64_t n = 0;
-    const int32_t ext = query_rows(p, r, len).y;
     for (int32_t s = 0; s * M < ext; ++s) n += tiles_of(stream_len(len, ext, s, M));
     return n;
 }
@@ -338,43 +355,72 @@ PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_
     }
 }
 
-// A place on the line: stream s of request r for one group of heads, whose first tile is tile `first`
-// of the line.
+// A place on the line: segment s of a stream, whose first tile is tile `first` of the line, for one
+// group of heads.  A segment is a run of tiles of one request that the same columns see.
 template <int G>
 struct Walk {
     static constexpr int32_t M = 8 / G;
-    int32_t grp, r, s, len, ext, q0, first, tiles;
+    int32_t grp, r, s;             // r: the stream's (first) request
+    int32_t len, ext, q0;          // of the segment's request: length; query tokens and first row (decode: of r)
+    int32_t first, tiles, key0;    // the segment's tiles; its first tile's number in the request
+    int32_t from, all;             // the stream's first tile on the line and its tiles
+    int32_t share;                 // decode: tiles that the stream's requests have in common
 
+    // The request whose pages the segment reads, and the one member whose columns see it (-1: all).
+    PKV_DEV int32_t member(const BlockDecodeParams &p) const { return p.indptr || s == 0 ? -1 : s - 1; }
+    PKV_DEV int32_t request(const BlockDecodeParams &p) const { return r + max(member(p), 0); }
+
+    // The stream that begins at tile `from`.
     PKV_DEV void load(const BlockDecodeParams &p) {
-        len = checked_len(p, r, false);
-        const int2 qr = query_rows(p, r, len);
-        q0 = qr.x;
-        ext = qr.y;
-        s = 0;
-        size(p);
+        first = from;
+        if (p.indptr) {
+            len = checked_len(p, r, false);
+            const int2 qr = query_rows(p, r, len);
+            q0 = qr.x;
+            ext = qr.y;
+            share = 0;
+            all = tiles = s * M < ext ? tiles_of(stream_len(len, ext, s, M)) : 0;
+            key0 = 0;
+        } else {
+            q0 = r;
+            ext = min(M, p.batch - r);
+            share = shared_tiles(p, r / M);
+            all = (int32_t)stream_tiles<M>(p, r / M, false);
+            s = 0;
+            len = share * kTile;
+            tiles = share;
+            key0 = 0;
+        }
     }
-    PKV_DEV void size(const BlockDecodeParams &p) {
-        tiles = s * M < ext ? tiles_of(p.indptr ? stream_len(len, ext, s, M) : len) : 0;
-    }
-    // To the stream that holds tile `at` of the line, from one at or before it.  False when there is
+    // To the segment that holds tile `at` of the line, from one at or before it.  False when there is
     // none (the lengths changed under the call).
     PKV_DEV bool seek(const BlockDecodeParams &p, int32_t at) {
         while (at - first >= tiles) {
             first += tiles;
-            if ((s + 1) * M < ext) {
+            if (!p.indptr && s < ext) {  // the next member's own tiles
                 ++s;
-                size(p);
+                len = checked_len(p, r + s - 1, false);
+                tiles = tiles_of(len) - share;
+                key0 = share;
                 continue;
             }
-            if (++r >= p.batch) {
-                r = 0;
-                if (++grp >= p.groups) return false;
+            from = first;
+            if (p.indptr && (s + 1) * M < ext) {
+                ++s;
+            } else {
+                s = 0;
+                r += p.indptr ? 1 : M;
+                if (r >= p.batch) {
+                    r = 0;
+                    if (++grp >= p.groups) return false;
+                }
             }
             load(p);
         }
         return true;
     }
-    // base: tiles before each of the 256 chunks of requests; n tiles in a group of heads
+    // base: tiles before each of the 256 chunks of requests (decode: of streams); n tiles in a group
+    // of heads
     PKV_DEV bool start(const BlockDecodeParams &p, const int32_t *base, int chunk, int32_t n, int32_t at) {
         grp = p.groups == 1 ? 0 : at / n;
         int lo = 0, hi = 32 * kWarps;
@@ -382,12 +428,51 @@ struct Walk {
             const int mid = (lo + hi) >> 1;
             if (base[mid] <= at - grp * n) lo = mid; else hi = mid;
         }
-        r = lo * chunk;
-        first = grp * n + base[lo];
+        r = lo * chunk * (p.indptr ? 1 : M);
+        s = 0;
+        from = grp * n + base[lo];
         load(p);
         return seek(p, at);
     }
 };
+
+// Tiles that the M requests of each decode stream have in common: whole pages, counted from the
+// front while every request's table names the same one.  A CTA a stream.
+template <int M>
+__global__ void __launch_bounds__(kThreads) block_share_kernel(const BlockDecodeParams p, int32_t *share) {
+    __shared__ int32_t s_first;
+    pdl_wait();
+    pdl_trigger();
+    const int r0 = blockIdx.x * M, members = min(M, p.batch - r0);
+    const int32_t *rows[M];
+    int32_t pages = 0x7FFFFFFF;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int r = r0 + min(m, members - 1);
+        const int32_t len = checked_len(p, r, false);
+        pages = min(pages, len >> p.shift);
+        rows[m] = p.table + (int64_t)(len > 0 ? __ldg(p.rows + r) : 0) * p.stride;
+    }
+    if (members < M) pages = 0;  // the last stream, when it is not full
+    if (threadIdx.x == 0) s_first = pages;
+    __syncthreads();
+    for (int32_t j0 = 0; j0 < pages; j0 += 2 * kThreads) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t j = j0 + u * kThreads + threadIdx.x;
+            if (j >= pages) continue;
+            bool same = true;
+            const int32_t first = __ldg(rows[0] + j);
+#pragma unroll
+            for (int m = 1; m < M; ++m) same &= __ldg(rows[m] + j) == first;
+            if (!same) atomicMin(&s_first, j);
+        }
+        __syncthreads();
+        if (s_first < j0 + 2 * kThreads) break;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) share[blockIdx.x] = s_first << (p.shift - 4);
+}
 
 // A bounded wait for a tile (see WaitPolicy).
 PKV_DEV bool tile_wait(uint64_t *bar, uint32_t parity, const BlockDecodeParams &p) {
@@ -415,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     using R = Ring<D>;
     extern __shared__ uint8_t dyn[];
     __shared__ int64_t warp_sums[kWarps];
-    __shared__ int32_t base[kThreads + 1];  // tiles before each thread's chunk of requests
+    __shared__ int32_t base[kThreads + 1];  // tiles before each thread's chunk
     __shared__ uint64_t full[kWarps][R::kStages];
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -427,9 +512,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     pdl_wait();
     pdl_trigger();
-    const int chunk = (p.batch + kThreads - 1) / kThreads;
+    const int32_t units = num_units<M>(p);
+    const int chunk = (units + kThreads - 1) / kThreads;
     int64_t mine = 0;
-    for (int r = tid * chunk; r < min((tid + 1) * chunk, p.batch); ++r) mine += request_tiles(p, r, M, blockIdx.x == 0);
+    for (int i = tid * chunk; i < min((tid + 1) * chunk, units); ++i) mine += unit_tiles<M>(p, i, blockIdx.x == 0);
     int64_t scan = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -481,16 +567,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 end = ask_at;
                 return;
             }
-            ask_row = p.table + (int64_t)__ldg(p.rows + ask.r) * p.stride;
+            ask_row = p.table + (int64_t)__ldg(p.rows + ask.request(p)) * p.stride;
         }
-        ask_page = __ldg(ask_row + ((ask_at - ask.first) >> tpp));
+        ask_page = __ldg(ask_row + ((ask.key0 + ask_at - ask.first) >> tpp));
     };
     auto ask_tile = [&](uint32_t st) {
         if (ask_at >= end) return;
         // a page outside the pool: rows past the maps' last, which read as zeros
         const bool in = (uint32_t)ask_page < (uint64_t)p.num_pages;
         bad |= !in;
-        const int32_t key = (ask_at - ask.first) * kTile;
+        const int32_t key = (ask.key0 + ask_at - ask.first) * kTile;
         const int32_t slot = in ? (ask_page << p.shift) + (key & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
         if (lane == 0) {
             mbar_arrive_expect_tx(&bars[st], 2 * R::kBox);
@@ -506,11 +592,46 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     uint32_t sg = 0, phase = 0;
     int32_t at = begin;
-    bool ok = true;
+    bool ok = true, fresh = true;  // fresh: a stream begins
+    uint32_t qb[D / 16][2];
+    float cs[2];
+    int32_t out[2];  // query rows of this lane's columns, -1: none
+    DecodeState<D> st;
     while (at < end && cur.seek(p, at)) {
-        const int32_t j0 = at - cur.first, j1 = min(cur.tiles, end - cur.first);
         const int kv_head = cur.grp * p.hg + hl;
-        const int32_t *row = p.table + (int64_t)__ldg(p.rows + cur.r) * p.stride;
+        if (fresh) {
+            // columns: query row col / G of the stream's M, head col % G of the group
+            const int32_t t0 = p.indptr ? cur.s * M : 0;
+            const int32_t row = t0 + g / G;
+            const int e = load_query<D>(
+                g / G < M && row < cur.ext ? p.q + ((int64_t)(cur.q0 + row) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
+                const int32_t t = t0 + (2 * c + h) / G;
+                out[h] = (2 * c + h) / G < M && t < cur.ext ? cur.q0 + t : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
+            st.m[0] = st.m[1] = -INFINITY;
+            st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
+            fresh = false;
+        }
+        // what the columns see of this segment
+        int32_t sees[2], last = cur.len, all_see;
+        if (p.indptr) {
+            last = stream_len(cur.len, cur.ext, cur.s, M);
+            all_see = cur.len - cur.ext + cur.s * M + 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sees[h] = out[h] < 0 ? last : cur.len - cur.ext + (out[h] - cur.q0) + 1;
+        } else {
+            const int32_t m = cur.member(p);
+            all_see = m < 0 || M == 1 ? last : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sees[h] = m < 0 || (2 * c + h) / G == m ? last : 0;
+        }
+        const int32_t j0 = cur.key0 + at - cur.first, j1 = cur.key0 + min(cur.tiles, end - cur.first);
+        const int32_t *row = p.table + (int64_t)__ldg(p.rows + cur.request(p)) * p.stride;
         auto page_exp = [&](const uint8_t *e, int32_t page) {
             return (uint32_t)page < (uint64_t)p.num_pages ? (int)__ldg(e + (int64_t)page * p.hkv + kv_head) : 127;
         };
@@ -518,28 +639,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         int32_t page = __ldg(row + (j0 >> tpp));
         int ek = page_exp(p.k_exp, page), ev = page_exp(p.v_exp, page);
         page = __ldg(row + (min(j0 + 1, j1 - 1) >> tpp));
-        // columns: token s M + col / G of the request, head col % G of the group
-        const int32_t tok = cur.s * M + g / G;
-        uint32_t qb[D / 16][2];
-        const int e = load_query<D>(
-            g / G < M && tok < cur.ext ? p.q + ((int64_t)(cur.q0 + tok) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
-        float cs[2];
-        int32_t sees[2], out[2];
-        const int32_t last = p.indptr ? stream_len(cur.len, cur.ext, cur.s, M) : cur.len;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
-            const int32_t tk = cur.s * M + (2 * c + h) / G;
-            const bool on = (2 * c + h) / G < M && tk < cur.ext;
-            out[h] = on ? cur.q0 + tk : -1;
-            sees[h] = on ? cur.len - cur.ext + tk + 1 : last;
-        }
-        const int32_t all_see = cur.len - cur.ext + cur.s * M + 1;  // keys that every column sees
-        DecodeState<D> st;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
-        st.m[0] = st.m[1] = -INFINITY;
-        st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
         int32_t j = j0;
 #pragma unroll 1
         for (; j < j1; ++j) {
@@ -564,10 +663,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             ek = next_ek;
             ev = next_ev;
         }
-        at = cur.first + j;
+        at = cur.first + j - cur.key0;
         if (!ok) break;
-        const bool whole = j0 == 0 && j1 == cur.tiles;
-        write_piece<D, G>(p, st, kv_head, out, whole ? -1 : 2 * range + (cur.first < begin ? 0 : 1), hl);
+        if (at == end || at == cur.from + cur.all) {
+            const bool whole = cur.from >= begin && at == cur.from + cur.all;
+            write_piece<D, G>(p, st, kv_head, out, whole ? -1 : 2 * range + (cur.from < begin ? 0 : 1), hl);
+            fresh = true;
+        }
     }
     if (bad && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
     // after a wait that gave up: what was asked for lands before the CTA ends
@@ -683,19 +785,19 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
     __shared__ int32_t s_req;
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int32_t r = blockIdx.x, tok = 0;
-    if (p.indptr) {  // the request of this query row
+    int32_t r = blockIdx.x / M, tok = blockIdx.x % M;  // decode: the stream and the row's place in it
+    if (p.indptr) {  // the request of this query row, the row's place in it
         if (tid == 0) s_req = -1;
         __syncthreads();
         for (int i = tid; i < p.batch; i += 32 * W)
-            if (__ldg(p.indptr + i) <= r && r < __ldg(p.indptr + i + 1)) s_req = i;
+            if (__ldg(p.indptr + i) <= blockIdx.x && blockIdx.x < __ldg(p.indptr + i + 1)) s_req = i;
         __syncthreads();
-        tok = s_req < 0 ? 0 : r - __ldg(p.indptr + s_req);
         r = s_req;
+        tok = r < 0 ? 0 : blockIdx.x - __ldg(p.indptr + r);
     }
     int64_t before = 0, all = 0;
-    for (int i = tid; i < p.batch; i += 32 * W) {
-        const int64_t t = request_tiles(p, i, M, false);
+    for (int i = tid; i < num_units<M>(p); i += 32 * W) {
+        const int64_t t = unit_tiles<M>(p, i, false);
         all += t;
         if (i < r) before += t;
     }
@@ -716,12 +818,13 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
         before += warp_sums[W + w];
     }
     const int32_t n = line_length(p, all, false);
-    const int32_t len = r < 0 || n == 0 ? 0 : checked_len(p, r, false);
-    int32_t tiles = tiles_of(len);
-    if (p.indptr && len > 0) {
-        const int32_t ext = query_rows(p, r, len).y, s = tok / M;
+    int32_t tiles = 0;  // of the row's stream; 0: the row sees no key
+    if (n > 0 && !p.indptr) {
+        if (checked_len(p, blockIdx.x, false) > 0) tiles = (int32_t)stream_tiles<M>(p, r, false);
+    } else if (n > 0 && r >= 0) {
+        const int32_t len = checked_len(p, r, false), ext = query_rows(p, r, len).y, s = tok / M;
         for (int32_t i = 0; i < s; ++i) before += tiles_of(stream_len(len, ext, i, M));
-        tiles = tok < ext ? tiles_of(stream_len(len, ext, s, M)) : 0;
+        if (tok < ext) tiles = tiles_of(stream_len(len, ext, s, M));
     }
     constexpr int V = D / 32;  // elements a lane holds
     const int sub = warp % S;
@@ -760,17 +863,30 @@ static int decode_ctas() { return 2 * num_sms(); }
 // Bytes of a range's two records.
 static size_t range_bytes(int hg, int32_t d) { return 2 * (size_t)hg * 8 * (d + 4) * sizeof(float); }
 
+// Requests of rows shorter than this are not looked through: the look costs about 2 us.
+constexpr int64_t kMinShared = 1024;
+constexpr int kMaxShared = 16384;  // streams whose requests are looked through for shared pages
+
 static size_t decode_workspace(int32_t hkv, int32_t d) {
     const int hg = head_group(hkv);
-    return kWorkspaceHeader + (size_t)decode_ctas() * (kWarps / hg) * range_bytes(hg, d);
+    return kWorkspaceHeader + kMaxShared * sizeof(int32_t) + (size_t)decode_ctas() * (kWarps / hg) * range_bytes(hg, d);
 }
 
 template <int D, int G>
-static int launch(const BlockDecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows, cudaStream_t s) {
+static int launch(BlockDecodeParams p, int32_t *share, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows, cudaStream_t s) {
     constexpr int smem = Ring<D>::kSmem;
     if (cudaFuncSetAttribute(block_decode_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return PKV_E_CUDA;
     const int per_cta = kWarps / p.hg;
+    constexpr int M = 8 / G;
+    if constexpr (M > 1) {
+        const int64_t streams = (p.batch + M - 1) / M;
+        if (share && p.batch > 1 && streams <= kMaxShared && (p.stride << p.shift) >= kMinShared) {
+            if (launch_pdl(block_share_kernel<M>, dim3((unsigned)streams), dim3(kThreads), 0, s, true, p, share) != cudaSuccess)
+                return PKV_E_CUDA;
+            p.share = share;
+        }
+    }
     if (launch_pdl(block_decode_kernel<D, G>, dim3((p.ranges + per_cta - 1) / per_cta), dim3(kThreads), smem, s, true, p, kmap,
                    vmap) != cudaSuccess)
         return PKV_E_CUDA;
@@ -787,13 +903,13 @@ static int launch(const BlockDecodeParams &p, const CUtensorMap &kmap, const CUt
 }
 
 template <int D>
-static int launch_group(int G, const BlockDecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows,
+static int launch_group(int G, const BlockDecodeParams &p, int32_t *share, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows,
                         cudaStream_t s) {
     switch (G) {
-        case 1: return launch<D, 1>(p, kmap, vmap, q_rows, s);
-        case 2: return launch<D, 2>(p, kmap, vmap, q_rows, s);
-        case 4: return launch<D, 4>(p, kmap, vmap, q_rows, s);
-        default: return launch<D, 8>(p, kmap, vmap, q_rows, s);
+        case 1: return launch<D, 1>(p, share, kmap, vmap, q_rows, s);
+        case 2: return launch<D, 2>(p, share, kmap, vmap, q_rows, s);
+        case 4: return launch<D, 4>(p, share, kmap, vmap, q_rows, s);
+        default: return launch<D, 8>(p, share, kmap, vmap, q_rows, s);
     }
 }
 
@@ -837,19 +953,23 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     p.q = static_cast<const uint16_t *>(q);
     p.o = static_cast<uint16_t *>(o);
     p.scale_log2 = sm_scale * kLog2eB;
-    const size_t room = ws_bytes < kWorkspaceHeader ? 0 : (ws_bytes - kWorkspaceHeader) / range_bytes(p.hg, D);
+    // workspace: header | decode: tiles shared by each stream | records
+    const size_t head = kWorkspaceHeader + (indptr ? 0 : kMaxShared * sizeof(int32_t));
+    const size_t room = ws_bytes < head ? 0 : (ws_bytes - head) / range_bytes(p.hg, D);
     p.ranges = (int32_t)std::min<size_t>((size_t)decode_ctas() * (kWarps / p.hg), room);
     if (p.ranges < 1) return PKV_E_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.err = reinterpret_cast<int32_t *>(ws);
-    p.rec = reinterpret_cast<float *>(ws + kWorkspaceHeader);
+    int32_t *share = indptr ? nullptr : reinterpret_cast<int32_t *>(ws + kWorkspaceHeader);
+    p.share = nullptr;
+    p.rec = reinterpret_cast<float *>(ws + head);
     p.rec_ml = p.rec + (size_t)p.ranges * 2 * p.hg * 8 * D;
     p.wait = wait_policy(wait_limit_ns());
     CUtensorMap kmap, vmap;
     int rc = code_map(&kmap, pool, pool->k);
     if (!rc) rc = code_map(&vmap, pool, pool->v);
     if (rc) return rc;
-    return D == 128 ? launch_group<128>(G, p, kmap, vmap, q_rows, s) : launch_group<64>(G, p, kmap, vmap, q_rows, s);
+    return D == 128 ? launch_group<128>(G, p, share, kmap, vmap, q_rows, s) : launch_group<64>(G, p, share, kmap, vmap, q_rows, s);
 }
 
 }  // namespace pkv

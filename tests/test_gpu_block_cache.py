@@ -335,6 +335,33 @@ def test_decode_batches(pkv, b, length):
     assert error(pkv, ws) == 0 and torch.isfinite(o).all()
 
 
+@pytest.mark.parametrize("g,hkv,d,page", [(1, 8, 64, 16), (2, 3, 128, 32), (4, 8, 128, 16), (4, 2, 64, 64), (8, 4, 128, 16)])
+@pytest.mark.parametrize("b", [2, 9, 70])
+def test_decode_with_shared_pages(pkv, g, hkv, d, page, b):
+    """Requests behind a common prefix (attended once for neighbours), some shorter than it, some
+    empty, some that leave it early, some that meet again behind a difference, and a page of it
+    that is outside the pool."""
+    rng = np.random.default_rng(b + g)
+    shared = 640 // page
+    lens = rng.integers(640, 1500, b)
+    lens[0] = 1400            # (the table is long enough to be looked through)
+    if b > 2:
+        lens[3], lens[4], lens[6] = 90, 0, 640
+    pages = int((-(-lens // page)).sum()) + shared
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    table, rows, _ = paged_batch(pkv, rng, lens.tolist(), page, pages, shared)
+    kill_tails(pool, was, table, rows, [n if n > 640 else 0 for n in lens], page)
+    if b > 2:
+        table[rows[8], 2] = table[rows[8], shared]     # another page in place of the third
+        table[rows[1], 0] = table[rows[1], shared]     # the first differs, the rest is common
+    only = range(b) if b < 10 else [0, 1, 2, 3, 4, 5, 6, 7, 8, 9, b - 2, b - 1]
+    o, ws = check_decode(pkv, pool, was, table, rows, lens.tolist(), page, hkv * g, d ** -0.5, only=only)
+    assert error(pkv, ws) == 0
+    table[rows, 1] = pages
+    o, ws = check_decode(pkv, pool, was, table, rows, lens.tolist(), page, hkv * g, d ** -0.5, only=only)
+    assert error(pkv, ws) == 0x100
+
+
 @pytest.mark.parametrize("hkv,d", [(8, 128), (2, 64)])
 def test_decode_exponents_far_apart(pkv, hkv, d):
     """Pages whose V exponents differ by up to 40 binades, K logits of several hundred, queries of
