@@ -23,8 +23,8 @@
 //     are d x 8.  V's bytes are paired by key with byte permutes on their way to f16.
 //   * mma.sync m16n8k16 in f16: an e4m3 code is an f16 value, and so is a query element over a
 //     power of two that brings its row's largest to [2^14, 2^15) (elements below 2^-31 of it
-//     round, far under the fp32 sum's own rounding).  Weights are f16 times 2^15: 11 bits down to
-//     2^-29 of the largest, against bf16's 8.
+//     round, far under the fp32 sum's own rounding).  Weights are f16 times 2^6: 11 bits down to
+//     2^-20 of the largest and a step of 2^-30 of it below, against bf16's 8 bits.
 // A request may also have several query tokens (the last ext[r] positions of its context): each
 // block of 8 / G of them is a *stream* of its own over the same keys, which only the first finds in
 // HBM.
@@ -41,8 +41,9 @@ constexpr int kWarps = 8;
 constexpr int kRingBytes = 96 * 1024;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 4;         // records a merging warp has in flight
-constexpr float kBias = 15.f;     // weights carry 2^15
-constexpr float kUnbias = 1.f / (1 << 15);
+constexpr float kBias = 6.f;      // weights carry 2^6 over their reference, which may lag the
+constexpr float kSlack = 8.f;     // largest by 2^8: they stay below 2^15 in f16
+constexpr float kUnbias = 1.f / (1 << 6);
 constexpr float kLog2eB = 1.4426950408889634f;
 
 struct BlockDecodeParams {
@@ -234,7 +235,7 @@ PKV_DEV void tile_scores(float (&t)[4], const uint32_t (&qb)[D / 16][2], const u
 // V rows of MMA k 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 bytes each.  Rows at or past `valid` read as
 // zeros: a weight of 0 does not undo a NaN or an infinity.
 template <int D>
-PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off)[2], int valid) {
+PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off)[2], bool ragged, int valid) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint8_t *row = at + off[i & 1] + (i >> 1) * 8 * D;
@@ -250,7 +251,7 @@ PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off
             v[i][1] = y.y;
         }
     }
-    if (valid < kTile) {
+    if (ragged) {
         const int c = threadIdx.x & 3;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -260,36 +261,37 @@ PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off
     }
 }
 
-// Folds the tile's weights (as B fragments b0, b1) and its maximum into the running state.
+// Folds the tile's weights (as B fragments b0, b1) and its maximum into the running state.  exps: the
+// tile's exponent bytes, K's low, V's above it.  hide[h]: -inf where column 2c + h does not see the
+// segment, else 0.  ragged: some column does not see the whole tile, but the keys before sees[h].
+// The reference moves, and the state is rescaled, only when a key is more than 2^8 above it: then
+// the lanes agree on the column's maximum.
 template <int D>
-PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int ek, int ev_byte, int key,
-                          const int32_t (&sees)[2], int32_t full, uint32_t &b0, uint32_t &b1) {
-    const float kf = exp_value(clamp_exp(ek)), ev = (float)(clamp_exp(ev_byte) - 127);
+PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int exps, const float (&hide)[2],
+                          bool ragged, int key, const int32_t (&sees)[2], uint32_t &b0, uint32_t &b1) {
+    const float kf = exp_value(exps & 0xFF);
+    // (a whole number below 2^23 as a float: its bits under those of 2^23)
+    const float ev = __uint_as_float(0x4B000000u | (uint32_t)(exps >> 8)) - (8388608.f + 127.f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + ev;
-    if (key + kTile > full) {  // some column does not see the whole tile
+    for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + (ev + hide[e & 1]);
+    if (ragged) {
         const int mine = key + key_of<D>((threadIdx.x & 31) >> 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (mine + 8 * (e >> 1) >= sees[e & 1]) t[e] = -INFINITY;
     }
-    float mn[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float y = fmaxf(t[h], t[2 + h]);
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-        mn[h] = fmaxf(st.m[h], y);
-    }
-    if (__any_sync(0xffffffffu, mn[0] > st.m[0] || mn[1] > st.m[1])) {
+    if (__any_sync(0xffffffffu, fmaxf(t[0], t[2]) > st.m[0] + kSlack || fmaxf(t[1], t[3]) > st.m[1] + kSlack)) {
         float al[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            float y = fmaxf(t[h], t[2 + h]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
             al[h] = 1.f;
-            if (mn[h] > st.m[h]) {
-                al[h] = ex2(st.m[h] - mn[h]);
-                st.l[h] *= ex2(st.m[h] - mn[h] + (ev - st.ea[h]));
-                st.m[h] = mn[h];
+            if (y > st.m[h]) {
+                al[h] = ex2(st.m[h] - y);
+                st.l[h] *= ex2(st.m[h] - y + (ev - st.ea[h]));
+                st.m[h] = y;
                 st.ea[h] = ev;
             }
         }
@@ -298,11 +300,10 @@ PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2
 #pragma unroll
             for (int e = 0; e < 4; ++e) st.acc[i][e] *= al[e & 1];
     }
-    float w[4];
-    float rw[2], rl[2];
+    float w[4], rw[2], rl[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float m = mn[h] == -INFINITY ? 0.f : mn[h];  // a column that has seen no key yet
+        const float m = st.m[h] == -INFINITY ? 0.f : st.m[h];  // a column that has seen no key yet
         rw[h] = m - kBias;
         rl[h] = m + (ev - st.ea[h]);
     }
@@ -502,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ int64_t warp_sums[kWarps];
     __shared__ int32_t base[kThreads + 1];  // tiles before each thread's chunk
     __shared__ uint64_t full[kWarps][R::kStages];
+    __shared__ Walk<G> walks[kWarps];  // where each warp asks: read and written at a segment's end only
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -554,40 +556,57 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // The asking side runs up to kStages tiles ahead, over the ends of streams; the page of the
     // tile that it asks for next is already there or on its way.
-    Walk<G> ask, cur;
-    if (!ask.start(p, base, chunk, n, begin)) return;
-    cur = ask;
-    int32_t ask_at = begin, ask_page = 0;
-    const int32_t *ask_row = nullptr;
+    Walk<G> cur;
+    if (!cur.start(p, base, chunk, n, begin)) return;
+    if (lane == 0) walks[warp] = cur;
+    __syncwarp();
+    // The lanes hold the first slots of 32 tiles from tile ask_b of the line on, and of the 32 after
+    // them; ask_end is the segment's end, ask_lim the first tile that these 32 do not cover.
+    int32_t ask_at = begin, ask_b = begin, ask_end = begin, ask_lim = begin, ask_slot = 0, ask_next = 0, ask_head = 0;
     bool bad = false;
-    auto next_page = [&] {
+    auto slots_from = [&](const Walk<G> &w, int32_t b) {
+        const int32_t j = w.key0 + min(b + lane - w.first, w.tiles - 1);
+        const int32_t page = __ldg(p.table + (int64_t)__ldg(p.rows + w.request(p)) * p.stride + (j >> tpp));
+        // a page outside the pool: rows past the maps' last, which read as zeros
+        const bool in = (uint32_t)page < (uint64_t)p.num_pages;
+        bad |= !in;
+        return in ? (page << p.shift) + ((j * kTile) & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
+    };
+    auto next_slots = [&] {  // at ask_lim
         if (ask_at >= end) return;
-        if (ask_row == nullptr || ask_at - ask.first >= ask.tiles) {
-            if (!ask.seek(p, ask_at)) {  // no such tile: what was asked for is all there is
+        if (ask_at == ask_end) {
+            Walk<G> w = walks[warp];
+            if (!w.seek(p, ask_at)) {  // no such tile: what was asked for is all there is
                 end = ask_at;
                 return;
             }
-            ask_row = p.table + (int64_t)__ldg(p.rows + ask.request(p)) * p.stride;
+            __syncwarp();
+            if (lane == 0) walks[warp] = w;
+            __syncwarp();
+            ask_b = ask_at;
+            ask_end = w.first + w.tiles;
+            ask_head = w.grp * p.hg + hl;
+            ask_slot = slots_from(w, ask_b);
+            ask_next = slots_from(w, ask_b + 32);
+        } else {
+            ask_b += 32;
+            ask_slot = ask_next;
+            ask_next = slots_from(walks[warp], ask_b + 32);
         }
-        ask_page = __ldg(ask_row + ((ask.key0 + ask_at - ask.first) >> tpp));
+        ask_lim = min(min(ask_end, ask_b + 32), end);
     };
     auto ask_tile = [&](uint32_t st) {
-        if (ask_at >= end) return;
-        // a page outside the pool: rows past the maps' last, which read as zeros
-        const bool in = (uint32_t)ask_page < (uint64_t)p.num_pages;
-        bad |= !in;
-        const int32_t key = (ask.key0 + ask_at - ask.first) * kTile;
-        const int32_t slot = in ? (ask_page << p.shift) + (key & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
+        if (ask_at >= ask_lim) return;
+        const int32_t slot = __shfl_sync(0xffffffffu, ask_slot, ask_at - ask_b);
         if (lane == 0) {
             mbar_arrive_expect_tx(&bars[st], 2 * R::kBox);
             const uint32_t dst = smem_u32(ring + st * 2 * R::kBox);
-            tma_load_3d(dst, &kmap, 0, ask.grp * p.hg + hl, slot, &bars[st]);
-            tma_load_3d(dst + R::kBox, &vmap, 0, ask.grp * p.hg + hl, slot, &bars[st]);
+            tma_load_3d(dst, &kmap, 0, ask_head, slot, &bars[st]);
+            tma_load_3d(dst + R::kBox, &vmap, 0, ask_head, slot, &bars[st]);
         }
-        ++ask_at;
-        next_page();
+        if (++ask_at == ask_lim) next_slots();
     };
-    next_page();
+    next_slots();
     for (uint32_t st = 0; st < R::kStages; ++st) ask_tile(st);
 
     uint32_t sg = 0, phase = 0;
@@ -618,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             fresh = false;
         }
         // what the columns see of this segment
-        int32_t sees[2], last = cur.len, all_see;
+        int32_t sees[2], last = cur.len, all_see = cur.len;
+        float hide[2] = {0.f, 0.f};
         if (p.indptr) {
             last = stream_len(cur.len, cur.ext, cur.s, M);
             all_see = cur.len - cur.ext + cur.s * M + 1;
@@ -626,31 +646,42 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int h = 0; h < 2; ++h) sees[h] = out[h] < 0 ? last : cur.len - cur.ext + (out[h] - cur.q0) + 1;
         } else {
             const int32_t m = cur.member(p);
-            all_see = m < 0 || M == 1 ? last : 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) sees[h] = m < 0 || (2 * c + h) / G == m ? last : 0;
+            for (int h = 0; h < 2; ++h) {
+                sees[h] = last;
+                if (m >= 0 && (2 * c + h) / G != m) hide[h] = -INFINITY;
+            }
         }
         const int32_t j0 = cur.key0 + at - cur.first, j1 = cur.key0 + min(cur.tiles, end - cur.first);
         const int32_t *row = p.table + (int64_t)__ldg(p.rows + cur.request(p)) * p.stride;
-        auto page_exp = [&](const uint8_t *e, int32_t page) {
-            return (uint32_t)page < (uint64_t)p.num_pages ? (int)__ldg(e + (int64_t)page * p.hkv + kv_head) : 127;
+        // The lanes hold the exponents of 32 tiles (K's byte low, V's above it) and of the 32 after
+        // them, and the pages of the 32 after those.
+        auto pages_from = [&](int32_t b) { return __ldg(row + (min(b + lane, j1 - 1) >> tpp)); };
+        auto exps_of = [&](int32_t page) {
+            if ((uint32_t)page >= (uint64_t)p.num_pages) return 127 | 127 << 8;
+            const int64_t at = (int64_t)page * p.hkv + kv_head;
+            return clamp_exp(__ldg(p.k_exp + at)) | clamp_exp(__ldg(p.v_exp + at)) << 8;
         };
-        // exponents come a tile ahead, the page they are read by two tiles ahead
-        int32_t page = __ldg(row + (j0 >> tpp));
-        int ek = page_exp(p.k_exp, page), ev = page_exp(p.v_exp, page);
-        page = __ldg(row + (min(j0 + 1, j1 - 1) >> tpp));
+        int exps = exps_of(pages_from(j0)), exps_next = exps_of(pages_from(j0 + 32));
+        int32_t pages = pages_from(j0 + 64), jb = j0;
         int32_t j = j0;
 #pragma unroll 1
         for (; j < j1; ++j) {
-            const int next_ek = page_exp(p.k_exp, page), next_ev = page_exp(p.v_exp, page);
-            page = __ldg(row + (min(j + 2, j1 - 1) >> tpp));
+            if (j - jb == 32) {
+                jb = j;
+                exps = exps_next;
+                exps_next = exps_of(pages);
+                pages = pages_from(j + 64);
+            }
+            const int e = __shfl_sync(0xffffffffu, exps, j - jb);
             ok = __all_sync(0xffffffffu, tile_wait(&bars[sg], phase, p));
             if (!ok) break;
             const uint8_t *tile = ring + sg * 2 * R::kBox;
             float w[4];
             tile_scores<D>(w, qb, tile, k_off);
             uint32_t v[4][D / 32];
-            read_v<D>(v, tile + R::kBox, v_off, last - j * kTile);
+            const bool ragged = (j + 1) * kTile > all_see;
+            read_v<D>(v, tile + R::kBox, v_off, ragged, last - j * kTile);
             __syncwarp();  // every lane has read the stage: ask for the tile kStages ahead
             ask_tile(sg);
             if (++sg == R::kStages) {
@@ -658,10 +689,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 phase ^= 1;
             }
             uint32_t b0, b1;
-            tile_weights<D>(st, w, cs, ek, ev, j * kTile, sees, all_see, b0, b1);
+            tile_weights<D>(st, w, cs, e, hide, ragged, j * kTile, sees, b0, b1);
             tile_product<D>(st, v, b0, b1);
-            ek = next_ek;
-            ev = next_ev;
         }
         at = cur.first + j - cur.key0;
         if (!ok) break;
@@ -671,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             fresh = true;
         }
     }
-    if (bad && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+    if (bad) set_error(p.err, DERR_SLOT_RANGE);
     // after a wait that gave up: what was asked for lands before the CTA ends
     for (int32_t left = ask_at - at; left > 0; --left) {
         mbar_wait(&bars[sg], phase);

@@ -94,13 +94,15 @@ def attend(q, k, v, scale, positions, weight_eps, log_weight_eps=0.0, v_exp=None
     The kernel's errors: (1) its output's rounding, half a bf16 step, 2^-8 of the result;
     (2) each weight w_j carries a relative error of weight_eps plus log_weight_eps |ln(w_j / w_max)|
     (rounding the weight, and rounding the exponent it is computed from), which moves the result by
-    at most sum_j p_j err_j |v_j - o|, the normalisation included; (3) a logit, an fp32 sum of d
+    at most sum_j p_j err_j |v_j - o|, the normalisation included, where the sum takes the same weights,
+    and sum_j p_j err_j |v_j| where it takes them unrounded (the kernels that v_exp is given for:
+    d(sum w v / l) = sum dw v / l with l as it is; a lone key's weight is then not cancelled); (3) a logit, an fp32 sum of d
     products, is off by at most (d + 4) 2^-24 sum |q_i k_i| times the scale, and so is ln w_j, with
     the fp32 exponential's 2^-22 beside it; (4) the fp32 sum over the keys: L 2^-24 sum p |v|;
-    (5) where v_exp [L, hkv] (V's exponents) is given, weights are f16: 2^15 2^(s_j + e_j - R) with
-    R = max (s_j + e_j), s in log2 units, times the code v_j 2^-e_j.  f16's smallest step is 2^-24, so
-    such a weight is also off by up to 2^-25, whatever its size, which moves the result by
-    2^-40 2^R / sum 2^s_j times sum |code_j|."""
+    (5) where v_exp [L, hkv] (V's exponents) is given, weights are f16: 2^6 2^(s_j + e_j - R) with
+    R <= max (s_j + e_j), s in log2 units, times the code v_j 2^-e_j.  f16's smallest step is 2^-24, so
+    such a weight is also off by up to 2^-25, whatever its size, which moves the result by at most
+    2^-31 2^R / sum 2^s_j times sum |code_j|, largest for the largest R."""
     n, hq, d = q.shape
     length, hkv = k.shape[:2]
     o, bound = np.zeros((n, hq, d)), np.zeros((n, hq, d))
@@ -117,10 +119,10 @@ def attend(q, k, v, scale, positions, weight_eps, log_weight_eps=0.0, v_exp=None
             o[i, h] = p @ vv
             logit = (d + 4) * 2.0 ** -24 * (np.abs(kk) @ np.abs(q[i, h])) * abs(scale)
             err = weight_eps + log_weight_eps * (top - s) + 2 * logit.max() + 2.0 ** -21
-            bound[i, h] = (2.0 ** -8 * np.abs(o[i, h]) + (p * err) @ np.abs(vv - o[i, h])
+            bound[i, h] = (2.0 ** -8 * np.abs(o[i, h]) + (p * err) @ np.abs(vv - (o[i, h] if v_exp is None else 0.0))
                            + m * 2.0 ** -24 * (p @ np.abs(vv)) + 1e-37)
             if v_exp is not None:
                 e = v_exp[:m, h * hkv // hq].astype(np.float64)
                 log2p = (s - top) / np.log(2.0) - np.log2(w.sum())
-                bound[i, h] += 2.0 ** -40 * 2.0 ** (log2p + e).max() * np.abs(vv * 2.0 ** -e[:, None]).sum(0)
+                bound[i, h] += 2.0 ** -31 * 2.0 ** (log2p + e).max() * np.abs(vv * 2.0 ** -e[:, None]).sum(0)
     return o, bound
