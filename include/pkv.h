@@ -390,7 +390,8 @@ int pkv_build_block_tables(const pkv_batch *batch, const int32_t *new_lens, cons
  * rescales the page's earlier rows.  Codes are x * 2^-e rounded to nearest even, saturating;
  * infinities saturate, NaN is stored as NaN (0x7F).
  *   out_cache_loc  -1 is padding and skipped; another slot outside the pool is skipped and sets
- *                  PKV_DERR_SLOT_RANGE in the workspace's error word (workspace may be NULL) */
+ *                  PKV_DERR_SLOT_RANGE in the workspace's error word (workspace may be NULL).  A
+ *                  skipped token leaves its row out of the run around it */
 int pkv_kv_store_block(const pkv_block_pool *pool, const void *k_new, const void *v_new,
                        const int32_t *out_cache_loc, int64_t n, void *workspace, void *stream);
 

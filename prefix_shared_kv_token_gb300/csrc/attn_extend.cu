@@ -152,23 +152,18 @@ struct GatherParams {
 
 // One CTA per unit of <= 32 keys: thread t moves 16-byte pieces of the units' slot rows
 // (Hkv * D elements, contiguous in the pool and in the output).
-// What the pool holds: bf16 rows, e4m3 codes under a scale of the whole pool (converted as they
-// are, the scale applied to the logits and the output), or codes under an exponent per page and KV
-// head (converted to the values they stand for, which are bf16 values).
-enum class Rows { kBf16, kFp8, kBlock };
-
-template <int D, Rows R>
+template <int D, bool FP8>
 PKV_DEV void gather_body(const GatherParams &p);
 
-template <int D, Rows R>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
     if (p.pdl_wait_start) pdl_wait();  // the pool rows and tables may come from the preceding kernel
     pdl_trigger();
-    gather_body<D, R>(p);
+    gather_body<D, FP8>(p);
     if (!p.pdl_wait_start) pdl_wait();  // complete only after the preceding kernel
 }
 
-template <int D, Rows R>
+template <int D, bool FP8>
 PKV_DEV void gather_body(const GatherParams &p) {
     if ((int)blockIdx.x >= p.nunits) {  // a query row
         const int i = blockIdx.x - p.nunits, r = __ldg(p.q_rows + i);
@@ -217,7 +212,7 @@ PKV_DEV void gather_body(const GatherParams &p) {
             const int32_t slot = s_slot[key];
             if (slot < 0) continue;
             const uint8_t *pool = tensor ? p.v_pool : p.k_pool;
-            if constexpr (R == Rows::kBf16) {
+            if constexpr (!FP8) {
                 y[k] = __ldg(reinterpret_cast<const uint4 *>(pool + (int64_t)slot * p.slot_bytes) + v);
             } else {
                 const uint2 x = __ldg(reinterpret_cast<const uint2 *>(pool + (int64_t)slot * p.slot_bytes) + v);
@@ -225,15 +220,6 @@ PKV_DEV void gather_body(const GatherParams &p) {
                 y[k].y = e4m3x2_to_bf16x2((uint16_t)(x.x >> 16));
                 y[k].z = e4m3x2_to_bf16x2((uint16_t)(x.y & 0xFFFFu));
                 y[k].w = e4m3x2_to_bf16x2((uint16_t)(x.y >> 16));
-                if constexpr (R == Rows::kBlock) {
-                    const uint8_t *exps = tensor ? p.v_exp : p.k_exp;
-                    const uint32_t e = clamp_exp(__ldg(exps + (int64_t)(slot >> p.block_shift) * p.hkv + v / (D / 8)));
-                    const uint32_t f = (e << 7) | (e << 23);  // 2^(e - 127), twice
-                    y[k].x = mul_bf16x2(y[k].x, f);
-                    y[k].y = mul_bf16x2(y[k].y, f);
-                    y[k].z = mul_bf16x2(y[k].z, f);
-                    y[k].w = mul_bf16x2(y[k].w, f);
-                }
             }
         }
 #pragma unroll
@@ -247,6 +233,68 @@ PKV_DEV void gather_body(const GatherParams &p) {
             reinterpret_cast<uint4 *>(out + (int64_t)(u.key0 + key) * elems)[v] = y[k];
         }
     }
+}
+
+// The same copy out of a block-scaled pool: codes become the bf16 values they stand for, exactly
+// (a code times a power of two is a bf16 value).  A thread turns 16 codes, half a head's row or a
+// quarter, into 32 bytes, four such loads and their exponents in flight.
+template <int D>
+__global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p) {
+    __shared__ int32_t s_slot[32];
+    if (p.pdl_wait_start) pdl_wait();
+    pdl_trigger();
+    const GatherUnit u = p.units[blockIdx.x];
+    const int row = __ldg(p.req_pool_indices + u.src);
+    if (row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift)) {
+        if (threadIdx.x == 0) set_error(p.err, DERR_POSITION);
+        return;
+    }
+    if (threadIdx.x < u.len) {
+        const int32_t slot = table_slot(p.req_to_token + (int64_t)row * p.rt_stride, u.pos0 + threadIdx.x, p.page_shift, p.num_slots);
+        if (slot < 0) set_error(p.err, DERR_SLOT_RANGE);  // a zero row
+        s_slot[threadIdx.x] = slot;
+    }
+    __syncthreads();
+    const int vecs = p.hkv * (D / 16), per = u.len * vecs;  // 16-code pieces of a row, of a tensor
+    const bool pow2 = (vecs & (vecs - 1)) == 0;
+    const int vshift = 31 - __clz(vecs);
+    constexpr int kInFlight = 4;
+    for (int base = threadIdx.x; base < 2 * per; base += kInFlight * blockDim.x) {
+        uint4 x[kInFlight];
+        uint32_t f[kInFlight];
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int i = base + k * blockDim.x;
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            f[k] = 0u;
+            if (i >= 2 * per) continue;
+            const bool v = i >= per;
+            const int rem = v ? i - per : i, key = pow2 ? rem >> vshift : rem / vecs, piece = rem - key * vecs;
+            const int32_t slot = s_slot[key];
+            if (slot < 0) continue;
+            x[k] = __ldg(reinterpret_cast<const uint4 *>((v ? p.v_pool : p.k_pool) + (int64_t)slot * p.slot_bytes) + piece);
+            f[k] = __ldg((v ? p.v_exp : p.k_exp) + (int64_t)(slot >> p.block_shift) * p.hkv + piece / (D / 16));
+        }
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int i = base + k * blockDim.x;
+            if (i >= 2 * per) continue;
+            const bool v = i >= per;
+            const int rem = v ? i - per : i, key = pow2 ? rem >> vshift : rem / vecs, piece = rem - key * vecs;
+            const uint32_t e = clamp_exp(f[k]), f2 = (e << 7) | (e << 23);  // 2^(e - 127), twice
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                y[2 * q] = mul_bf16x2(e4m3x2_to_bf16x2((uint16_t)(w[q] & 0xFFFFu)), f2);
+                y[2 * q + 1] = mul_bf16x2(e4m3x2_to_bf16x2((uint16_t)(w[q] >> 16)), f2);
+            }
+            uint4 *out = reinterpret_cast<uint4 *>((v ? p.v_out : p.k_out) + (int64_t)(u.key0 + key) * p.hkv * D) + 2 * piece;
+            out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+    }
+    if (!p.pdl_wait_start) pdl_wait();  // complete only after the preceding kernel
 }
 
 // p = 2^(s * scale - m) for the 128 scores of one row (masked scores are -inf and give 0),
@@ -846,7 +894,7 @@ static int dispatch_extend(int G, const ExtendParams &p, const XMaps &mp, int n,
 
 template <int D>
 static int launch_gather(const GatherParams &p, bool fp8, int nunits, cudaStream_t s) {
-    auto kern = !fp8 ? gather_kernel<D, Rows::kBf16> : p.k_exp ? gather_kernel<D, Rows::kBlock> : gather_kernel<D, Rows::kFp8>;
+    auto kern = p.k_exp ? block_gather_kernel<D> : fp8 ? gather_kernel<D, true> : gather_kernel<D, false>;
     return launch_pdl(kern, dim3(nunits), dim3(256), 0, s, true, p) ==
                    cudaSuccess
                ? PKV_OK

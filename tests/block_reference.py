@@ -29,18 +29,25 @@ def page_exponent(x):
 
 
 def store(codes, exps, x, loc, page):
-    """In place: rows x [n, heads, d] (float64) into the slots loc; runs of consecutive slots."""
-    n, i = len(loc), 0
-    while i < n:
-        if loc[i] < 0 or loc[i] >= len(codes):
-            i += 1
+    """In place: rows x [n, heads, d] (float64) into the slots loc.  A run is tokens at consecutive
+    slots of a page; a token with no slot of the pool is skipped and leaves its row out of the run."""
+    ok = [0 <= s < len(codes) for s in loc]
+    done = [False] * len(loc)
+    for i in range(len(loc)):
+        if not ok[i] or done[i]:
             continue
-        j = i + 1
-        while j < n and loc[j] == loc[j - 1] + 1 and loc[j] % page:
-            j += 1
         block, off = loc[i] // page, loc[i] % page
+        run = [i]
+        for j in range(i + 1, min(i + page - off, len(loc))):
+            if ok[j] and loc[j] != loc[i] + j - i:
+                break
+            if ok[j]:
+                run.append(j)
+        for j in run:
+            done[j] = True
+        slots = [loc[j] for j in run]
         for h in range(codes.shape[1]):
-            e = page_exponent(x[i:j, h])
+            e = page_exponent(x[run, h])
             old = int(np.clip(exps[block, h], 10, 245)) - 127
             if off and old >= e:
                 e = old
@@ -48,9 +55,8 @@ def store(codes, exps, x, loc, page):
                 rows = slice(loc[i] - off, loc[i])
                 codes[rows, h] = e4m3_encode(e4m3_decode(codes[rows, h]) * 2.0 ** (old - e))
             exps[block, h] = e + 127
-            y = np.clip(x[i:j, h] * 2.0 ** -e, -1024.0, 1024.0)   # past 448 it saturates (infinities too)
-            codes[loc[i]:loc[i] + j - i, h] = e4m3_encode(y)
-        i = j
+            # past 448 it saturates (infinities too)
+            codes[slots, h] = e4m3_encode(np.clip(x[run, h] * 2.0 ** -e, -1024.0, 1024.0))
 
 
 def rows_of(codes, exps, table_row, length, page):
