@@ -360,11 +360,25 @@ def attn_extend_ctx(pool: Pool, q, o, sm_scale, k_new, v_new, out_cache_loc, ctx
 # the block-scaled 8-bit pool
 
 
-def _current():
-    """(index, stream handle) of the current CUDA device."""
+_torch = None      # torch, loaded by the first call that takes tensors
+_raw_stream = None
+
+
+def _load_torch():
+    global _torch, _raw_stream
     import torch
+    # the handle without a Stream object around it, where torch offers it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _where(stream):
+    """(torch, index of the current CUDA device, stream handle)."""
+    torch = _torch or _load_torch()
     device = torch.cuda.current_device()
-    return device, torch.cuda.current_stream(device).cuda_stream
+    return torch, device, _raw_stream(device) if stream is None else _stream(stream)
 
 
 def _space(workspace, device):
@@ -373,9 +387,8 @@ def _space(workspace, device):
     return at, workspace.numel() * workspace.element_size()
 
 
-def _block_batch(batch: Batch, device) -> PkvBatch:
-    import torch
-    table, rows, i32 = batch.req_to_token, batch.req_pool_indices, torch.int32
+def _block_batch(batch: Batch, device, i32) -> PkvBatch:
+    table, rows = batch.req_to_token, batch.req_pool_indices
     at, rows_at = _fits("req_to_token", table, i32, device, 2), _fits("req_pool_indices", rows, i32, device, 1)
     n, stride = table.shape
     return PkvBatch(at, stride, n, rows_at, _fits("seq_lens", batch.seq_lens, i32, device, rows.shape), rows.shape[0],
@@ -387,10 +400,9 @@ def build_block_tables(req_to_token, req_pool_indices, seq_lens, new_lens, free_
     """Page table entries, slots, positions and query offsets of a step from its lengths (see
     pkv_build_block_tables); every argument is an int32 tensor on the GPU, req_to_token is written
     in place."""
-    import torch
+    torch, device, stream = _where(stream)
     i32 = torch.int32
-    device, current = _current()
-    b = _block_batch(Batch(req_to_token, req_pool_indices, seq_lens, int(page_size)), device)
+    b = _block_batch(Batch(req_to_token, req_pool_indices, seq_lens, int(page_size)), device, i32)
     ws, size = _space(workspace, device)
     free = _fits("free_pages", free_pages, i32, device, 1)
     loc = _fits("out_cache_loc", out_cache_loc, i32, device, 1)
@@ -399,21 +411,20 @@ def build_block_tables(req_to_token, req_pool_indices, seq_lens, new_lens, free_
         _fits("free_head", free_head, i32, device, (1,)), _fits("free_head_out", free_head_out, i32, device, (1,)), loc,
         _fits("positions", positions, i32, device, out_cache_loc.shape), out_cache_loc.shape[0],
         _fits("qo_indptr", qo_indptr, i32, device, (b.batch + 1,)), ws, size,
-        current if stream is None else _stream(stream)))
+        stream))
 
 
 def kv_store_block(pool: BlockPool, k_new, v_new, out_cache_loc, workspace=None, stream=None) -> None:
     """Quantises k_new, v_new (bf16 [n, heads, head_dim]) into the slots out_cache_loc; tokens of
     one page are neighbours at consecutive slots, -1 is padding (see pkv_kv_store_block)."""
-    import torch
-    device, current = _current()
+    torch, device, stream = _where(stream)
     p = pool.c(device)
     loc = _fits("out_cache_loc", out_cache_loc, torch.int32, device, 1)
     n = out_cache_loc.shape[0]
     rows = (n, p.num_kv_heads, p.head_dim)
     check("pkv_kv_store_block", lib.pkv_kv_store_block(
         p, _fits("k_new", k_new, torch.bfloat16, device, rows), _fits("v_new", v_new, torch.bfloat16, device, rows), loc,
-        n, None if workspace is None else _space(workspace, device)[0], current if stream is None else _stream(stream)))
+        n, None if workspace is None else _space(workspace, device)[0], stream))
 
 
 def decode_block_workspace(pool: BlockPool, num_q_heads: int) -> int:
@@ -426,22 +437,20 @@ def decode_block_workspace(pool: BlockPool, num_q_heads: int) -> int:
 def attn_decode_block(pool: BlockPool, batch: Batch, q, o, sm_scale, workspace, stream=None) -> None:
     """One query per request (q, o bf16 [batch, num_q_heads, head_dim]) over its pages; no plan, and
     a request of length 0 gets zeros (see pkv_attn_decode_block)."""
-    import torch
-    device, current = _current()
-    p, b = pool.c(device), _block_batch(batch, device)
+    torch, device, stream = _where(stream)
+    p, b = pool.c(device), _block_batch(batch, device, torch.int32)
     rows = (b.batch, q.shape[1] if q.dim() == 3 else 0, p.head_dim)
     ws, size = _space(workspace, device)
     check("pkv_attn_decode_block", lib.pkv_attn_decode_block(
         p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), rows[1], sm_scale,
-        ws, size, current if stream is None else _stream(stream)))
+        ws, size, stream))
 
 
 def attn_extend_block(pool: BlockPool, batch: Batch, q, o, sm_scale, plan: Plan, plan_dev, workspace,
                       stream=None) -> None:
     """attn_extend over a block-scaled pool (the same plans and workspace)."""
-    import torch
-    device, current = _current()
-    p, b, info = pool.c(device), _block_batch(batch, device), plan.info
+    torch, device, stream = _where(stream)
+    p, b, info = pool.c(device), _block_batch(batch, device, torch.int32), plan.info
     rows = (info.total_q, info.num_q_heads, p.head_dim)
     at = _fits("plan_dev", plan_dev, torch.uint8, device, 1)
     if plan_dev.shape[0] < info.plan_bytes:
@@ -449,7 +458,7 @@ def attn_extend_block(pool: BlockPool, batch: Batch, q, o, sm_scale, plan: Plan,
     ws, size = _space(workspace, device)
     check("pkv_attn_extend_block", lib.pkv_attn_extend_block(
         p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), sm_scale, info, at,
-        ws, size, current if stream is None else _stream(stream)))
+        ws, size, stream))
 
 
 def get_device_error(workspace, stream=None) -> int:

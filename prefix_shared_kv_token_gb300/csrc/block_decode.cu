@@ -30,6 +30,7 @@
 // HBM.
 
 #include <algorithm>
+#include <atomic>
 
 #include "block.cuh"
 
@@ -904,8 +905,14 @@ static size_t decode_workspace(int32_t hkv, int32_t d) {
 template <int D, int G>
 static int launch(BlockDecodeParams p, int32_t *share, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t q_rows, cudaStream_t s) {
     constexpr int smem = Ring<D>::kSmem;
-    if (cudaFuncSetAttribute(block_decode_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return PKV_E_CUDA;
+    static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_E_CUDA;
+    if (dev >= 64 || !((allowed.load(std::memory_order_relaxed) >> dev) & 1)) {
+        if (cudaFuncSetAttribute(block_decode_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return PKV_E_CUDA;
+        if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
     const int per_cta = kWarps / p.hg;
     constexpr int M = 8 / G;
     if constexpr (M > 1) {

@@ -106,7 +106,7 @@ int64_t extend_item_cost(const ExtendItem &x, int32_t tq, const std::vector<Pack
 // rates measured on GB300: streams take 0.036 ns a key and KV head (the decode kernel's own work, at
 // d = 128), the gather moves 6 bytes a code at 4.6 TB/s, an extend item costs 0.38 a unit of
 // extend_item_cost; each way starts in about 10.  (4 requests of 5 tokens after 9,000: 142 by the
-// gather, REPLACE by streams; 64 of 200 after 1,800: 440 against 5,000.)
+// gather, 41 by streams; 64 of 200 after 1,800: 440 by the gather.)
 bool few_tokens_are_streams(int32_t batch, const int32_t *seq_lens, const int32_t *extend_lens, int32_t hq, int32_t hkv,
                             int32_t d, int64_t gathered, const std::vector<ExtendItem> &items,
                             const std::vector<PackInfo> &packs, int32_t num_sms) {

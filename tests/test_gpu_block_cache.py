@@ -551,6 +551,46 @@ def test_extend_streams_over_many_ranges(pkv, b, old, new):
         want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, d ** -0.5, np.arange(old[r], lens[r]), DECODE_EPS, v_exp=e)
         assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
 
+@pytest.mark.parametrize("what", ["decode", "streams"])
+def test_a_short_wait_limit_gives_up_and_the_next_call_is_right(pkv, what):
+    """Only the limit is cut: waits for tiles that are on their way give up, every copy lands, the
+    error word says so, and the same call with the default limit is right."""
+    rng = np.random.default_rng(12)
+    page, hkv, d, lens = 16, 8, 128, [900, 300, 200000, 17]   # 410 MB of codes: tiles have to be waited for
+    pages = sum(-(-n // page) for n in lens)
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    table, rows, batch = paged_batch(pkv, rng, lens, page, pages)
+    ext = [1] * 4 if what == "decode" else [3, 2, 5, 1]
+    qo = np.concatenate([[0], np.cumsum(ext)])
+    plan = pkv.plan_extend(lens, ext, qo, hkv * 4, hkv, d)
+    plan.info.offsets[18] = 1
+    q, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * 4, d)))
+    o = torch.zeros_like(q)
+    ws = words(max(pkv.decode_block_workspace(pool, hkv * 4), plan.info.workspace_bytes) // 4 + 1)
+    blob = dev(plan.blob, np.uint8)
+
+    def call():
+        if what == "decode":
+            pkv.attn_decode_block(pool, batch, q, o, 0.1, ws)
+        else:
+            pkv.attn_extend_block(pool, batch, q, o, 0.1, plan, blob, ws)
+    try:
+        pkv.set_wait_limit_ns(1)
+        for _ in range(3):
+            call()
+        assert error(pkv, ws) & 0x200
+    finally:
+        pkv.set_wait_limit_ns(0)
+    ws.zero_()
+    call()
+    assert error(pkv, ws) == 0 and torch.isfinite(o).all()
+    for r in (0, 1, 3):
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(lens[r] - ext[r], lens[r]), DECODE_EPS, v_exp=e)
+        assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound)
+
+
 def test_python_calls_check_their_tensors(pkv):
     rng = np.random.default_rng(0)
     pool, _ = random_pool(pkv, rng, 4, 16, 2, 64)
