@@ -50,7 +50,8 @@ constexpr float kLog2eB = 1.4426950408889634f;
 struct BlockDecodeParams {
     const uint8_t *k_exp, *v_exp;
     int64_t num_pages;
-    int32_t shift, hkv, hg, groups;  // hg KV heads read side by side, `groups` times
+    int32_t shift, hkv, hg, groups;  // hg (a power of two) KV heads read side by side, `groups` times
+    int32_t hg_shift;
     const int32_t *table;
     int64_t stride;
     int32_t num_rows, batch;
@@ -62,7 +63,8 @@ struct BlockDecodeParams {
     float scale_log2;
     int32_t ranges;  // at most
     const int32_t *share;  // decode: tiles that the requests of a stream have in common, NULL: none
-    float *rec;      // [range][2][hg][8 columns][D], then (R, l, ea, -) [range][2][hg][8][4]
+    float *rec;      // [range][2][hg][8 columns][D] (d in the order that merge_head says), then
+                     // (R, l, ea, -) [range][2][hg][8][4]
     float *rec_ml;
     int32_t *err;
     WaitPolicy wait;
@@ -262,17 +264,17 @@ PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off
     }
 }
 
-// Folds the tile's weights (as B fragments b0, b1) and its maximum into the running state.  exps: the
-// tile's exponent bytes, K's low, V's above it.  hide[h]: -inf where column 2c + h does not see the
+// Folds the tile's weights (as B fragments b0, b1) and its maximum into the running state.  ek, ev_byte:
+// the tile's exponent bytes.  hide[h]: -inf where column 2c + h does not see the
 // segment, else 0.  ragged: some column does not see the whole tile, but the keys before sees[h].
 // The reference moves, and the state is rescaled, only when a key is more than 2^8 above it: then
 // the lanes agree on the column's maximum.
 template <int D>
-PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int exps, const float (&hide)[2],
-                          bool ragged, int key, const int32_t (&sees)[2], uint32_t &b0, uint32_t &b1) {
-    const float kf = exp_value(exps & 0xFF);
+PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int ek, int ev_byte,
+                          const float (&hide)[2], bool ragged, int key, const int32_t (&sees)[2], uint32_t &b0, uint32_t &b1) {
+    const float kf = exp_value(clamp_exp(ek));
     // (a whole number below 2^23 as a float: its bits under those of 2^23)
-    const float ev = __uint_as_float(0x4B000000u | (uint32_t)(exps >> 8)) - (8388608.f + 127.f);
+    const float ev = __uint_as_float(0x4B000000u | (uint32_t)clamp_exp(ev_byte)) - (8388608.f + 127.f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + (ev + hide[e & 1]);
     if (ragged) {
@@ -344,14 +346,20 @@ PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_
         if (row[h] < 0) continue;
         if (rec < 0) {
             const float inv = row_scale(st.l[h], st.ea[h]);
-            uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + ((int64_t)row[h] * p.hkv * G + kv_head * G + col % G) * D + g * (D / 8));
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((int64_t)row[h] * p.hkv * G + kv_head * G + col % G) * D + g * (D / 8));
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) dst[i] = pack_bf16x2(st.acc[i][h] * inv, st.acc[i][2 + h] * inv);
+            for (int i = 0; i < D / 16; i += 4)
+                dst[i / 4] = make_uint4(pack_bf16x2(st.acc[i][h] * inv, st.acc[i][2 + h] * inv),
+                                        pack_bf16x2(st.acc[i + 1][h] * inv, st.acc[i + 1][2 + h] * inv),
+                                        pack_bf16x2(st.acc[i + 2][h] * inv, st.acc[i + 2][2 + h] * inv),
+                                        pack_bf16x2(st.acc[i + 3][h] * inv, st.acc[i + 3][2 + h] * inv));
         } else {
             const int64_t at = ((int64_t)rec * p.hg + hl) * 8 + col;
-            float2 *dst = reinterpret_cast<float2 *>(p.rec + at * D + g * (D / 8));
+            // piece i / 2 of lane g's run of d next to its neighbours' (see merge_head)
+            float4 *dst = reinterpret_cast<float4 *>(p.rec + at * D) + g;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) dst[i] = make_float2(st.acc[i][h], st.acc[i][2 + h]);
+            for (int i = 0; i < D / 16; i += 2)
+                dst[4 * i] = make_float4(st.acc[i][h], st.acc[i][2 + h], st.acc[i + 1][h], st.acc[i + 1][2 + h]);
             if (g == 0) *reinterpret_cast<float4 *>(p.rec_ml + at * 4) = make_float4(st.m[h], st.l[h], st.ea[h], 0.f);
         }
     }
@@ -425,11 +433,11 @@ struct Walk {
     // of heads
     PKV_DEV bool start(const BlockDecodeParams &p, const int32_t *base, int chunk, int32_t n, int32_t at) {
         grp = p.groups == 1 ? 0 : at / n;
-        int lo = 0, hi = 32 * kWarps;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (base[mid] <= at - grp * n) lo = mid; else hi = mid;
-        }
+        // the last chunk that begins at or before the tile: first of every 8, then of the 8
+        const int lane = threadIdx.x & 31;
+        const int32_t x = at - grp * n;
+        int lo = 8 * (31 - __clz(__ballot_sync(0xffffffffu, base[8 * lane] <= x)));
+        lo += 31 - __clz(__ballot_sync(0xffffffffu, lane < 8 && base[lo + lane] <= x));
         r = lo * chunk * (p.indptr ? 1 : M);
         s = 0;
         from = grp * n + base[lo];
@@ -476,6 +484,23 @@ __global__ void __launch_bounds__(kThreads) block_share_kernel(const BlockDecode
     if (threadIdx.x == 0) share[blockIdx.x] = s_first << (p.shift - 4);
 }
 
+// A batch of tiles to ask for: up to tile `lim` of the line, of one KV head.
+struct Ahead {
+    int32_t at, lim, head;
+};
+
+// Touches a stream's query rows for one KV head, so that they are in L1 when the stream begins.
+template <int D, int G>
+PKV_DEV void warm_query(const BlockDecodeParams &p, const Walk<G> &w, int hl) {
+    constexpr int32_t M = 8 / G, kLines = G * D * 2 / 128;  // 128-byte lines of a query row's group
+    const int lane = threadIdx.x & 31, t = (p.indptr ? w.s * M : 0) + lane / kLines;
+    if (lane < M * kLines && t < w.ext) {
+        const uint16_t *at = p.q + ((int64_t)(w.q0 + t) * p.hkv * G + (w.grp * p.hg + hl) * G) * D + lane % kLines * 64;
+        uint32_t x;
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(at));
+    }
+}
+
 // A bounded wait for a tile (see WaitPolicy).
 PKV_DEV bool tile_wait(uint64_t *bar, uint32_t parity, const BlockDecodeParams &p) {
     if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
@@ -504,6 +529,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ int64_t warp_sums[kWarps];
     __shared__ int32_t base[kThreads + 1];  // tiles before each thread's chunk
     __shared__ uint64_t full[kWarps][R::kStages];
+    __shared__ uint32_t exps[kWarps][R::kStages];  // of each tile in the ring: K's exponent byte, V's above it
+    __shared__ Ahead ahead[kWarps][2];
     __shared__ Walk<G> walks[kWarps];  // where each warp asks: read and written at a segment's end only
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -540,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     const Cut cut(n * p.groups, p.ranges);
     const int tpp = p.shift - 4;  // log2 of the tiles in a page
-    const int hl = warp % p.hg;
-    const int32_t range = blockIdx.x * (kWarps / p.hg) + warp / p.hg;
+    const int hl = warp & (p.hg - 1);
+    const int32_t range = blockIdx.x * (kWarps >> p.hg_shift) + (warp >> p.hg_shift);
     if (range >= cut.n) return;
     const int32_t begin = cut.start(range);
     int32_t end = cut.start(range + 1);
@@ -555,59 +582,80 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t *ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023) + warp * R::kStages * 2 * R::kBox;
     uint64_t *bars = full[warp];
 
-    // The asking side runs up to kStages tiles ahead, over the ends of streams; the page of the
-    // tile that it asks for next is already there or on its way.
+    // The asking side runs up to kStages tiles ahead, over the ends of streams, in batches of up to 32
+    // tiles of a segment: the lanes hold the first slots and exponents of the batch that is asked for
+    // (tiles ask_b on, up to ask_lim), the same of the next, whose exponents are on their way, and the
+    // slots of the one after, on their way too.  So no load is waited for where batches follow.
     Walk<G> cur;
     if (!cur.start(p, base, chunk, n, begin)) return;
     if (lane == 0) walks[warp] = cur;
     __syncwarp();
-    // The lanes hold the first slots of 32 tiles from tile ask_b of the line on, and of the 32 after
-    // them; ask_end is the segment's end, ask_lim the first tile that these 32 do not cover.
-    int32_t ask_at = begin, ask_b = begin, ask_end = begin, ask_lim = begin, ask_slot = 0, ask_next = 0, ask_head = 0;
+    const int32_t num_slots = (int32_t)(p.num_pages << p.shift);
+    int32_t line_at = begin;  // the first tile that is in no batch yet
     bool bad = false;
-    auto slots_from = [&](const Walk<G> &w, int32_t b) {
-        const int32_t j = w.key0 + min(b + lane - w.first, w.tiles - 1);
-        const int32_t page = __ldg(p.table + (int64_t)__ldg(p.rows + w.request(p)) * p.stride + (j >> tpp));
-        // a page outside the pool: rows past the maps' last, which read as zeros
-        const bool in = (uint32_t)page < (uint64_t)p.num_pages;
-        bad |= !in;
-        return in ? (page << p.shift) + ((j * kTile) & ((1 << p.shift) - 1)) : (int32_t)(p.num_pages << p.shift);
-    };
-    auto next_slots = [&] {  // at ask_lim
-        if (ask_at >= end) return;
-        if (ask_at == ask_end) {
+    auto take_batch = [&](Ahead &to) {
+        int32_t slot = num_slots;
+        Ahead x = {line_at, line_at, 0};
+        if (line_at < end) {
             Walk<G> w = walks[warp];
-            if (!w.seek(p, ask_at)) {  // no such tile: what was asked for is all there is
-                end = ask_at;
-                return;
+            const int32_t was = w.from;
+            if (w.seek(p, line_at)) {
+                __syncwarp();
+                if (lane == 0) walks[warp] = w;
+                if (w.from != was || line_at == begin) warm_query<D, G>(p, w, hl);
+                x.lim = min(min(w.first + w.tiles, line_at + 32), end);
+                x.head = w.grp * p.hg + hl;
+                const int32_t j = w.key0 + min(line_at + lane, x.lim - 1) - w.first;
+                const int32_t page = __ldg(p.table + (int64_t)__ldg(p.rows + w.request(p)) * p.stride + (j >> tpp));
+                // a page outside the pool: rows past the maps' last, which read as zeros
+                const bool in = (uint32_t)page < (uint64_t)p.num_pages;
+                bad |= !in;
+                if (in) slot = (page << p.shift) + ((j * kTile) & ((1 << p.shift) - 1));
+                line_at = x.lim;
+            } else {
+                end = line_at;  // no such tile: what was taken is all there is
             }
-            __syncwarp();
-            if (lane == 0) walks[warp] = w;
-            __syncwarp();
-            ask_b = ask_at;
-            ask_end = w.first + w.tiles;
-            ask_head = w.grp * p.hg + hl;
-            ask_slot = slots_from(w, ask_b);
-            ask_next = slots_from(w, ask_b + 32);
-        } else {
-            ask_b += 32;
-            ask_slot = ask_next;
-            ask_next = slots_from(walks[warp], ask_b + 32);
         }
-        ask_lim = min(min(ask_end, ask_b + 32), end);
+        __syncwarp();
+        if (lane == 0) to = x;
+        __syncwarp();
+        return slot;
     };
+    auto exps_of = [&](int32_t slot, int32_t head) {
+        const int64_t at = (int64_t)(slot < num_slots ? slot >> p.shift : 0) * p.hkv + head;
+        return (uint32_t)__ldg(p.k_exp + at) | (uint32_t)__ldg(p.v_exp + at) << 8;
+    };
+    Ahead *next = ahead[warp], *after = next + 1;
+    int32_t slot_c = take_batch(*next);
+    int32_t ask_at = begin, ask_b = begin, ask_lim = next->lim, ask_head = next->head;
+    int32_t slot_n = take_batch(*next), slot_m = take_batch(*after);
+    uint32_t exps_c = exps_of(slot_c, ask_head), exps_n = exps_of(slot_n, next->head);
     auto ask_tile = [&](uint32_t st) {
         if (ask_at >= ask_lim) return;
-        const int32_t slot = __shfl_sync(0xffffffffu, ask_slot, ask_at - ask_b);
+        const int32_t slot = __shfl_sync(0xffffffffu, slot_c, ask_at - ask_b);
+        const uint32_t e = __shfl_sync(0xffffffffu, exps_c, ask_at - ask_b);
         if (lane == 0) {
+            exps[warp][st] = e;
             mbar_arrive_expect_tx(&bars[st], 2 * R::kBox);
             const uint32_t dst = smem_u32(ring + st * 2 * R::kBox);
             tma_load_3d(dst, &kmap, 0, ask_head, slot, &bars[st]);
             tma_load_3d(dst + R::kBox, &vmap, 0, ask_head, slot, &bars[st]);
         }
-        if (++ask_at == ask_lim) next_slots();
+        if (++ask_at == ask_lim) {
+            ask_b = ask_at;
+            ask_lim = next->lim;
+            ask_head = next->head;
+            slot_c = slot_n;
+            exps_c = exps_n;
+            slot_n = slot_m;
+            exps_n = exps_of(slot_n, after->head);
+            Ahead *x = next;
+            next = after;
+            after = x;
+            slot_m = take_batch(*after);
+        }
     };
-    next_slots();
+#pragma unroll 1
     for (uint32_t st = 0; st < R::kStages; ++st) ask_tile(st);
 
     uint32_t sg = 0, phase = 0;
@@ -654,30 +702,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         const int32_t j0 = cur.key0 + at - cur.first, j1 = cur.key0 + min(cur.tiles, end - cur.first);
-        const int32_t *row = p.table + (int64_t)__ldg(p.rows + cur.request(p)) * p.stride;
-        // The lanes hold the exponents of 32 tiles (K's byte low, V's above it) and of the 32 after
-        // them, and the pages of the 32 after those.
-        auto pages_from = [&](int32_t b) { return __ldg(row + (min(b + lane, j1 - 1) >> tpp)); };
-        auto exps_of = [&](int32_t page) {
-            if ((uint32_t)page >= (uint64_t)p.num_pages) return 127 | 127 << 8;
-            const int64_t at = (int64_t)page * p.hkv + kv_head;
-            return clamp_exp(__ldg(p.k_exp + at)) | clamp_exp(__ldg(p.v_exp + at)) << 8;
-        };
-        int exps = exps_of(pages_from(j0)), exps_next = exps_of(pages_from(j0 + 32));
-        int32_t pages = pages_from(j0 + 64), jb = j0;
         int32_t j = j0;
 #pragma unroll 1
         for (; j < j1; ++j) {
-            if (j - jb == 32) {
-                jb = j;
-                exps = exps_next;
-                exps_next = exps_of(pages);
-                pages = pages_from(j + 64);
-            }
-            const int e = __shfl_sync(0xffffffffu, exps, j - jb);
             ok = __all_sync(0xffffffffu, tile_wait(&bars[sg], phase, p));
             if (!ok) break;
             const uint8_t *tile = ring + sg * 2 * R::kBox;
+            const uint32_t e = exps[warp][sg];
             float w[4];
             tile_scores<D>(w, qb, tile, k_off);
             uint32_t v[4][D / 32];
@@ -690,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 phase ^= 1;
             }
             uint32_t b0, b1;
-            tile_weights<D>(st, w, cs, e, hide, ragged, j * kTile, sees, b0, b1);
+            tile_weights<D>(st, w, cs, e & 0xFF, e >> 8, hide, ragged, j * kTile, sees, b0, b1);
             tile_product<D>(st, v, b0, b1);
         }
         at = cur.first + j - cur.key0;
@@ -797,9 +828,11 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, int3
     }
     if (!on) return;
     const float inv = row_scale(L, E);
+    // a record's 16-byte piece 8 i + g is d = (D / 8) g + 4 i + {0 .. 3}
+    const int piece = lane * V / 4, d = D / 8 * (piece % 8) + 4 * (piece / 8) + lane * V % 4;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
-        reinterpret_cast<uint32_t *>(out + lane * V)[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
+        reinterpret_cast<uint32_t *>(out + d)[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
 }
 
 // Joins the records of the streams that cross ranges and clears the rows of empty requests.  A CTA
@@ -926,12 +959,12 @@ static int launch(BlockDecodeParams p, int32_t *share, const CUtensorMap &kmap, 
     if (launch_pdl(block_decode_kernel<D, G>, dim3((p.ranges + per_cta - 1) / per_cta), dim3(kThreads), smem, s, true, p, kmap,
                    vmap) != cudaSuccess)
         return PKV_E_CUDA;
-    // records of a stream, about, and CTAs for a few waves of the GPU's
-    const int64_t each = p.ranges / std::max<int64_t>(q_rows * p.groups, 1), hq = p.hkv * G;
+    // records of a stream, at most, in a batch like this one
+    const int64_t each = p.ranges / std::max<int64_t>((q_rows + M - 1) / M * p.groups, 1), hq = p.hkv * G;
     auto merge = each > 64 ? block_merge_kernel<D, G, 32, 32> : each > 4 ? block_merge_kernel<D, G, kWarps, kWarps>
                                                                          : block_merge_kernel<D, G, kWarps, 1>;
     const int64_t heads = each > 4 ? 1 : kWarps;  // a CTA's at a time
-    const int64_t y = std::min<int64_t>((hq + heads - 1) / heads, std::max<int64_t>(1, 4 * (int64_t)num_sms() / q_rows));
+    const int64_t y = std::min<int64_t>((hq + heads - 1) / heads, std::max<int64_t>(1, 8 * (int64_t)num_sms() / q_rows));
     return launch_pdl(merge, dim3((unsigned)q_rows, (unsigned)y), dim3(each > 64 ? 1024 : 32 * kWarps), 0, s, true, p) ==
                    cudaSuccess
                ? PKV_OK
@@ -979,6 +1012,7 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     p.hkv = hkv;
     p.hg = head_group(hkv);
     p.groups = hkv / p.hg;
+    p.hg_shift = log2_of(p.hg);
     p.table = batch->req_to_token;
     p.stride = batch->stride;
     p.num_rows = batch->num_rows;
@@ -992,7 +1026,11 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     // workspace: header | decode: tiles shared by each stream | records
     const size_t head = kWorkspaceHeader + (indptr ? 0 : kMaxShared * sizeof(int32_t));
     const size_t room = ws_bytes < head ? 0 : (ws_bytes - head) / range_bytes(p.hg, D);
-    p.ranges = (int32_t)std::min<size_t>((size_t)decode_ctas() * (kWarps / p.hg), room);
+    // no more ranges than the tables have room for tiles of
+    const int64_t M = 8 / G, tiles = (std::min<int64_t>(batch->stride, ((int64_t)1 << 31) >> p.shift) << p.shift) / kTile;
+    const int64_t line = (indptr ? (q_rows + M - 1) / M + batch->batch : batch->batch) * tiles * p.groups;
+    p.ranges = (int32_t)std::min<int64_t>({(int64_t)decode_ctas() * (kWarps / p.hg), (int64_t)room,
+                                           std::max<int64_t>(1, line / kMinTiles)});
     if (p.ranges < 1) return PKV_E_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.err = reinterpret_cast<int32_t *>(ws);

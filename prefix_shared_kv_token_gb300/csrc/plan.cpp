@@ -19,6 +19,7 @@
 // the rest of the context causally; one record per (query token, part), merged per token.
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <numeric>
@@ -103,24 +104,34 @@ int64_t extend_item_cost(const ExtendItem &x, int32_t tq, const std::vector<Pack
 // An extend call over a block-scaled pool has two ways: gather every key run as bf16 rows, then the
 // tensor-core kernel; or the decode kernel, 8 / G query tokens of a request at a time, each such
 // stream reading the codes again (from L2 after the first).  The estimates, in microseconds, use
-// rates measured on GB300: streams take 0.036 ns a key and KV head (the decode kernel's own work, at
-// d = 128), the gather moves 6 bytes a code at 4.6 TB/s, an extend item costs 0.38 a unit of
-// extend_item_cost; each way starts in about 10.  (4 requests of 5 tokens after 9,000: 142 by the
-// gather, 41 by streams; 64 of 200 after 1,800: 440 by the gather.)
+// rates measured on GB300.  Streams: 0.036 ns a key and KV head (the decode kernel's own work at
+// d = 128), but no less than a range's tiles and streams one after the other, 0.8 and 1.5 each -- the
+// ranges are as many as the call's workspace has records for -- and 8 to start.  The gather: 6 bytes a
+// code at 4.6 TB/s; an extend item: 0.38 a unit of extend_item_cost; 9 to start.  (4 requests of 5
+// tokens after 9,000: 142 by the gather, 41 by streams; 64 of 200 after 1,800: 440 by the gather.)
 bool few_tokens_are_streams(int32_t batch, const int32_t *seq_lens, const int32_t *extend_lens, int32_t hq, int32_t hkv,
                             int32_t d, int64_t gathered, const std::vector<ExtendItem> &items,
-                            const std::vector<PackInfo> &packs, int32_t num_sms) {
+                            const std::vector<PackInfo> &packs, int32_t num_sms, size_t ws_bytes) {
     const int32_t G = hq / hkv, M = 8 / G;
-    double keys = 0.0;
-    for (int32_t r = 0; r < batch; ++r) keys += (double)((extend_lens[r] + M - 1) / M) * seq_lens[r];
-    const double streams = keys * hkv * (d == 128 ? 0.036e-3 : 0.024e-3) + 10.0;
+    int32_t hg = 8;
+    while (hkv % hg) hg /= 2;
+    double keys = 0.0, streams = 0.0;
+    for (int32_t r = 0; r < batch; ++r) {
+        const int32_t n = (extend_lens[r] + M - 1) / M;
+        keys += (double)n * seq_lens[r];
+        streams += n;
+    }
+    const double tiles = keys / 16.0 * (hkv / hg), room = (double)ws_bytes / (2.0 * hg * 8 * (d + 4) * 4);
+    const double ranges = std::max(1.0, std::min({tiles / 2.0, room, 2.0 * num_sms * (8 / hg)}));
+    const double few = std::max(keys * hkv * (d == 128 ? 0.036e-3 : 0.024e-3),
+                                0.8 * std::ceil(tiles / ranges) + 1.5 * std::ceil(streams * (hkv / hg) / ranges)) + 8.0;
     double sum = 0.0, longest = 0.0;
     for (const ExtendItem &x : items) {
         const double c = 0.38 * (double)extend_item_cost(x, 128 / G, &packs);
         sum += c;
         longest = std::max(longest, c);
     }
-    return streams < (double)gathered * hkv * d * 6.0 / 4.6e6 + std::max(sum / num_sms, longest) + 10.0;
+    return few < (double)gathered * hkv * d * 6.0 / 4.6e6 + std::max(sum / num_sms, longest) + 9.0;
 }
 
 // Keys per gather unit (one CTA each): up to 32, fewer when the gather is small, so that it
@@ -832,8 +843,9 @@ static int plan_extend_impl(int32_t batch, const int32_t *seq_lens, const int32_
     // better attended as decode streams (see few_tokens_are_streams)
     std::vector<int32_t> rows(qo_indptr, qo_indptr + batch + 1);
     info->offsets[17] = (int64_t)off; off = align16(off + rows.size() * sizeof(int32_t));
+    const size_t gather_bytes = ctx ? 0 : 2 * (size_t)nkeys * num_kv_heads * head_dim * 2;
     info->offsets[18] = !ctx && !fuse && few_tokens_are_streams(batch, seq_lens, extend_lens, num_q_heads, num_kv_heads, head_dim,
-                                                                nkeys, items, packs, num_sms);
+                                                                nkeys, items, packs, num_sms, gather_bytes);
     std::vector<uint8_t> blob(std::max<size_t>(off, 16), 0);
     put(blob, (size_t)info->offsets[17], rows);
     put(blob, (size_t)info->offsets[0], placed);
@@ -845,7 +857,7 @@ static int plan_extend_impl(int32_t batch, const int32_t *seq_lens, const int32_
     put(blob, (size_t)info->offsets[15], tok_row);
     const size_t rec_bytes = (size_t)info->num_records * num_q_heads * (head_dim + 2) * 4;
     info->workspace_bytes = kHeader + ((rec_bytes + 255) & ~size_t(255)) +
-                            (ctx ? 0 : 2 * (size_t)nkeys * num_kv_heads * head_dim * 2);
+                            gather_bytes;
     return emit(blob, plan, plan_cap, info);
 }
 
