@@ -62,6 +62,8 @@ struct BlockDecodeParams {
     uint16_t *o;
     float scale_log2;
     int32_t ranges;  // at most
+    int32_t *before;  // decode: tiles before each unit, written by the first kernel for the second where
+                      // there are too many units to add them up again; NULL: none
     const int32_t *share;  // decode: tiles that the requests of a stream have in common, NULL: none
     float *rec;      // [range][2][hg][8 columns][D] (d in the order that merge_head says), then
                      // (R, l, ea, -) [range][2][hg][8][4]
@@ -220,11 +222,13 @@ PKV_DEV float row_scale(float l, float ea) { return l == 0.f ? 0.f : kUnbias / l
 // Logits of a tile's 16 keys: this lane's MMA rows g and g + 8 of columns 2c and 2c + 1.  The rows
 // g + 8 are 8 D bytes behind the rows g, under the same swizzle.
 template <int D>
-PKV_DEV void tile_scores(float (&t)[4], const uint32_t (&qb)[D / 16][2], const uint8_t *k, const int (&off)[D / 64]) {
+PKV_DEV void tile_scores(float (&t)[4], const uint32_t (&qb)[D / 16][2], const uint8_t *k, int off) {
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains of MMAs
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(k + off[u]), y = *reinterpret_cast<const uint4 *>(k + off[u] + 8 * D);
+        // (piece 4 + c is piece c with that bit changed, under the swizzle too)
+        const uint8_t *at = k + (off ^ 64 * u);
+        const uint4 x = *reinterpret_cast<const uint4 *>(at), y = *reinterpret_cast<const uint4 *>(at + 8 * D);
         const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -238,10 +242,11 @@ PKV_DEV void tile_scores(float (&t)[4], const uint32_t (&qb)[D / 16][2], const u
 // V rows of MMA k 2c, 2c + 1, 2c + 8, 2c + 9: D / 8 bytes each.  Rows at or past `valid` read as
 // zeros: a weight of 0 does not undo a NaN or an infinity.
 template <int D>
-PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off)[2], bool ragged, int valid) {
+PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, int off, bool ragged, int valid) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint8_t *row = at + off[i & 1] + (i >> 1) * 8 * D;
+        // (the key of MMA row 2c + 1 is that of 2c with one bit changed: 4 at d = 128, 1 at d = 64)
+        const uint8_t *row = at + (i & 1 ? off ^ (D == 128 ? 4 * 128 | 4 << 4 : 64) : off) + (i >> 1) * 8 * D;
         if constexpr (D == 128) {
             const uint4 y = *reinterpret_cast<const uint4 *>(row);
             v[i][0] = y.x;
@@ -265,23 +270,30 @@ PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, const int (&off
 }
 
 // Folds the tile's weights (as B fragments b0, b1) and its maximum into the running state.  ek, ev_byte:
-// the tile's exponent bytes.  hide[h]: -inf where column 2c + h does not see the
-// segment, else 0.  ragged: some column does not see the whole tile, but the keys before sees[h].
+// the tile's exponent bytes.  Columns are G heads each of the stream's requests or tokens: only the
+// `only`-th sees the tile (-1: all do); ragged: the i-th sees of it the keys before sees + i step.
+// (A logit that is not seen may be NaN: it is replaced.)
 // The reference moves, and the state is rescaled, only when a key is more than 2^8 above it: then
 // the lanes agree on the column's maximum.
-template <int D>
+template <int D, int G>
 PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int ek, int ev_byte,
-                          const float (&hide)[2], bool ragged, int key, const int32_t (&sees)[2], uint32_t &b0, uint32_t &b1) {
+                          int only, bool ragged, int sees, int step, uint32_t &b0, uint32_t &b1) {
     const float kf = exp_value(clamp_exp(ek));
     // (a whole number below 2^23 as a float: its bits under those of 2^23)
     const float ev = __uint_as_float(0x4B000000u | (uint32_t)clamp_exp(ev_byte)) - (8388608.f + 127.f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + (ev + hide[e & 1]);
-    if (ragged) {
-        const int mine = key + key_of<D>((threadIdx.x & 31) >> 2);
+    for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + ev;
+    const int col = 2 * (threadIdx.x & 3);
+    if (only >= 0) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (mine + 8 * (e >> 1) >= sees[e & 1]) t[e] = -INFINITY;
+            if ((col + (e & 1)) / G != only) t[e] = -INFINITY;
+    }
+    if (ragged) {
+        const int row = key_of<D>((threadIdx.x & 31) >> 2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (row + 8 * (e >> 1) >= sees + (col + (e & 1)) / G * step) t[e] = -INFINITY;
     }
     if (__any_sync(0xffffffffu, fmaxf(t[0], t[2]) > st.m[0] + kSlack || fmaxf(t[1], t[3]) > st.m[1] + kSlack)) {
         float al[2];
@@ -319,6 +331,7 @@ PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2
     b1 = transpose_8x8(pack_f16x2(w[2], w[3]));
 }
 
+// O^T += V^T P^T.
 template <int D>
 PKV_DEV void tile_product(DecodeState<D> &st, const uint32_t (&v)[4][D / 32], uint32_t b0, uint32_t b1) {
 #pragma unroll
@@ -331,6 +344,37 @@ PKV_DEV void tile_product(DecodeState<D> &st, const uint32_t (&v)[4][D / 32], ui
             mma_f16_16816(st.acc[2 * j + u], e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
                           e4m3x2_hi_to_f16x2(hi), b0, b1);
         }
+}
+
+// A weight of 0 does not undo a NaN in a V row that a column does not see.  Where there may be one
+// (a segment of one of several requests; a tile that tokens see in part), the columns that did not
+// see it get back what they had.
+template <int D>
+struct Kept {
+    volatile float acc[D / 4];
+    PKV_DEV void take(const DecodeState<D> &st) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[4 * i + e] = st.acc[i][e];
+    }
+    PKV_DEV void give_back(DecodeState<D> &st, const bool (&mine)[2]) const {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!mine[e & 1]) st.acc[i][e] = acc[4 * i + e];
+    }
+};
+// Whether a column outside `mine` has become NaN (or infinite).
+template <int D>
+PKV_DEV bool poisoned(const DecodeState<D> &st, const bool (&mine)[2]) {
+    float x[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e & 1] += st.acc[i][e] * 0.f;
+    return (!mine[0] && x[0] != 0.f) || (!mine[1] && x[1] != 0.f);
 }
 
 // The result (rec < 0) or record of a stream's piece.  Column 2c + h of this lane belongs to query
@@ -486,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) block_share_kernel(const BlockDecode
 
 // A batch of tiles to ask for: up to tile `lim` of the line, of one KV head.
 struct Ahead {
-    int32_t at, lim, head;
+    int32_t lim, head;
 };
 
 // Touches a stream's query rows for one KV head, so that they are in L1 when the stream begins.
@@ -531,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ uint64_t full[kWarps][R::kStages];
     __shared__ uint32_t exps[kWarps][R::kStages];  // of each tile in the ring: K's exponent byte, V's above it
     __shared__ Ahead ahead[kWarps][2];
-    __shared__ Walk<G> walks[kWarps];  // where each warp asks: read and written at a segment's end only
+    // where each warp asks and where it attends: read and written at a segment's end only
+    __shared__ Walk<G> walks[kWarps], curs[kWarps];
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -562,6 +607,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int32_t n = line_length(p, all, blockIdx.x == 0 && tid == 0);
     base[tid] = (int32_t)(before + scan - mine);
     if (tid == 0) base[kThreads] = n;
+    if (p.before && blockIdx.x == 0) {
+        int32_t at = base[tid];
+        for (int i = tid * chunk; i < min((tid + 1) * chunk, units); ++i) {
+            p.before[i] = at;
+            at += (int32_t)unit_tiles<M>(p, i, false);
+        }
+        if (tid == 0) p.before[units] = n;
+    }
     __syncthreads();
     if (n == 0) return;
 
@@ -573,12 +626,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int32_t begin = cut.start(range);
     int32_t end = cut.start(range + 1);
     const int g = lane >> 2, c = lane & 3;
-    int k_off[D / 64], v_off[2];
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u) k_off[u] = piece_at<D>(key_of<D>(g), 4 * u + c);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        v_off[i] = D == 128 ? piece_at<D>(key_of<D>(2 * c + i), g) : piece_at<D>(key_of<D>(2 * c + i), g >> 1) + 8 * (g & 1);
+    // this lane's first K piece and V bytes in a tile (see tile_scores and read_v for the others)
+    const int k_off = piece_at<D>(key_of<D>(g), c);
+    const int v_off = D == 128 ? piece_at<D>(key_of<D>(2 * c), g) : piece_at<D>(key_of<D>(2 * c), g >> 1) + 8 * (g & 1);
     uint8_t *ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023) + warp * R::kStages * 2 * R::kBox;
     uint64_t *bars = full[warp];
 
@@ -586,34 +636,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     // tiles of a segment: the lanes hold the first slots and exponents of the batch that is asked for
     // (tiles ask_b on, up to ask_lim), the same of the next, whose exponents are on their way, and the
     // slots of the one after, on their way too.  So no load is waited for where batches follow.
-    Walk<G> cur;
-    if (!cur.start(p, base, chunk, n, begin)) return;
-    if (lane == 0) walks[warp] = cur;
-    __syncwarp();
     const int32_t num_slots = (int32_t)(p.num_pages << p.shift);
-    int32_t line_at = begin;  // the first tile that is in no batch yet
     bool bad = false;
-    auto take_batch = [&](Ahead &to) {
+    // The batch that begins at tile `from` of the line; `warm`: its stream's queries have not been seen.
+    auto take_batch = [&](int32_t from, Ahead &to, bool warm) {
         int32_t slot = num_slots;
-        Ahead x = {line_at, line_at, 0};
-        if (line_at < end) {
+        Ahead x = {from, 0};
+        if (from < end) {
             Walk<G> w = walks[warp];
-            const int32_t was = w.from;
-            if (w.seek(p, line_at)) {
+            if (w.seek(p, from)) {
                 __syncwarp();
                 if (lane == 0) walks[warp] = w;
-                if (w.from != was || line_at == begin) warm_query<D, G>(p, w, hl);
-                x.lim = min(min(w.first + w.tiles, line_at + 32), end);
+                if (from == w.from || warm) warm_query<D, G>(p, w, hl);
+                x.lim = min(min(w.first + w.tiles, from + 32), end);
                 x.head = w.grp * p.hg + hl;
-                const int32_t j = w.key0 + min(line_at + lane, x.lim - 1) - w.first;
+                const int32_t j = w.key0 + min(from + lane, x.lim - 1) - w.first;
                 const int32_t page = __ldg(p.table + (int64_t)__ldg(p.rows + w.request(p)) * p.stride + (j >> tpp));
                 // a page outside the pool: rows past the maps' last, which read as zeros
                 const bool in = (uint32_t)page < (uint64_t)p.num_pages;
                 bad |= !in;
                 if (in) slot = (page << p.shift) + ((j * kTile) & ((1 << p.shift) - 1));
-                line_at = x.lim;
             } else {
-                end = line_at;  // no such tile: what was taken is all there is
+                end = from;  // no such tile: what was taken is all there is
             }
         }
         __syncwarp();
@@ -625,11 +669,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int64_t at = (int64_t)(slot < num_slots ? slot >> p.shift : 0) * p.hkv + head;
         return (uint32_t)__ldg(p.k_exp + at) | (uint32_t)__ldg(p.v_exp + at) << 8;
     };
-    Ahead *next = ahead[warp], *after = next + 1;
-    int32_t slot_c = take_batch(*next);
-    int32_t ask_at = begin, ask_b = begin, ask_lim = next->lim, ask_head = next->head;
-    int32_t slot_n = take_batch(*next), slot_m = take_batch(*after);
-    uint32_t exps_c = exps_of(slot_c, ask_head), exps_n = exps_of(slot_n, next->head);
+    int32_t slot_c, slot_n, slot_m, ask_at, ask_b, ask_lim, ask_head;
+    uint32_t exps_c, exps_n, turn = 0;  // ahead[warp][turn] is the next batch, the other the one after it
     auto ask_tile = [&](uint32_t st) {
         if (ask_at >= ask_lim) return;
         const int32_t slot = __shfl_sync(0xffffffffu, slot_c, ask_at - ask_b);
@@ -642,67 +683,83 @@ __global__ void __launch_bounds__(kThreads, 2)
             tma_load_3d(dst + R::kBox, &vmap, 0, ask_head, slot, &bars[st]);
         }
         if (++ask_at == ask_lim) {
+            const Ahead next = ahead[warp][turn], after = ahead[warp][turn ^ 1];
             ask_b = ask_at;
-            ask_lim = next->lim;
-            ask_head = next->head;
+            ask_lim = next.lim;
+            ask_head = next.head;
             slot_c = slot_n;
             exps_c = exps_n;
             slot_n = slot_m;
-            exps_n = exps_of(slot_n, after->head);
-            Ahead *x = next;
-            next = after;
-            after = x;
-            slot_m = take_batch(*after);
+            exps_n = exps_of(slot_n, after.head);
+            slot_m = take_batch(after.lim, ahead[warp][turn], false);
+            turn ^= 1;
         }
     };
-#pragma unroll 1
-    for (uint32_t st = 0; st < R::kStages; ++st) ask_tile(st);
-
     uint32_t sg = 0, phase = 0;
-    int32_t at = begin;
-    bool ok = true, fresh = true;  // fresh: a stream begins
+    int32_t at = begin, piece = begin;  // the tile to attend next; the first tile of its piece
+    bool careful = false;               // NaN were met: see poisoned
+again:
+    // from the piece's first tile, with nothing asked for
+    at = ask_at = ask_b = piece;
+    {
+        Walk<G> w;
+        if (!w.start(p, base, chunk, n, at)) return;
+        if (lane == 0) walks[warp] = curs[warp] = w;
+        __syncwarp();
+    }
+    slot_c = take_batch(at, ahead[warp][0], true);
+    ask_lim = ahead[warp][0].lim;
+    ask_head = ahead[warp][0].head;
+    __syncwarp();
+    slot_n = take_batch(ask_lim, ahead[warp][0], false);
+    slot_m = take_batch(ahead[warp][0].lim, ahead[warp][1], false);
+    turn = 0;
+    exps_c = exps_of(slot_c, ask_head);
+    exps_n = exps_of(slot_n, ahead[warp][0].head);
+#pragma unroll 1
+    for (uint32_t i = 0; i < R::kStages; ++i) ask_tile(sg + i < R::kStages ? sg + i : sg + i - R::kStages);
+
+    bool ok = true, fresh = true, nan = false;  // fresh: a piece begins
     uint32_t qb[D / 16][2];
     float cs[2];
-    int32_t out[2];  // query rows of this lane's columns, -1: none
     DecodeState<D> st;
-    while (at < end && cur.seek(p, at)) {
-        const int kv_head = cur.grp * p.hg + hl;
-        if (fresh) {
-            // columns: query row col / G of the stream's M, head col % G of the group
-            const int32_t t0 = p.indptr ? cur.s * M : 0;
-            const int32_t row = t0 + g / G;
-            const int e = load_query<D>(
-                g / G < M && row < cur.ext ? p.q + ((int64_t)(cur.q0 + row) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
+    while (at < end) {
+        // last, all_see: keys of the segment's request that some column and every column see; only: the
+        // one request or token whose columns do, -1: all
+        int32_t last, all_see, only = -1, shift, j, j1;
+        {
+            Walk<G> w = curs[warp];
+            if (!w.seek(p, at)) break;
+            __syncwarp();
+            if (lane == 0) curs[warp] = w;
+            __syncwarp();
+            if (fresh) {
+                // columns: query row col / G of the stream's M, head col % G of the group
+                const int32_t row = (p.indptr ? w.s * M : 0) + g / G, kv_head = w.grp * p.hg + hl;
+                const int e = load_query<D>(
+                    g / G < M && row < w.ext ? p.q + ((int64_t)(w.q0 + row) * p.hkv * G + kv_head * G + g % G) * D : nullptr, qb);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
-                const int32_t t = t0 + (2 * c + h) / G;
-                out[h] = (2 * c + h) / G < M && t < cur.ext ? cur.q0 + t : -1;
+                for (int h = 0; h < 2; ++h) cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
+                st.m[0] = st.m[1] = -INFINITY;
+                st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
+                fresh = false;
             }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
-            st.m[0] = st.m[1] = -INFINITY;
-            st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
-            fresh = false;
-        }
-        // what the columns see of this segment
-        int32_t sees[2], last = cur.len, all_see = cur.len;
-        float hide[2] = {0.f, 0.f};
-        if (p.indptr) {
-            last = stream_len(cur.len, cur.ext, cur.s, M);
-            all_see = cur.len - cur.ext + cur.s * M + 1;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) sees[h] = out[h] < 0 ? last : cur.len - cur.ext + (out[h] - cur.q0) + 1;
-        } else {
-            const int32_t m = cur.member(p);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sees[h] = last;
-                if (m >= 0 && (2 * c + h) / G != m) hide[h] = -INFINITY;
+            last = all_see = w.len;
+            if (p.indptr) {
+                last = stream_len(w.len, w.ext, w.s, M);
+                all_see = w.len - w.ext + w.s * M + 1;
+            } else if (M > 1 && w.ext > 1) {
+                only = w.member(p);
             }
+            shift = w.first - w.key0;
+            j = at - shift;
+            j1 = min(w.first + w.tiles, end) - shift;
         }
-        const int32_t j0 = cur.key0 + at - cur.first, j1 = cur.key0 + min(cur.tiles, end - cur.first);
-        int32_t j = j0;
+        Kept<D> had;
+        const bool mine[2] = {2 * c / G == only, (2 * c + 1) / G == only};
+        if (M > 1 && only >= 0 && careful) had.take(st);
 #pragma unroll 1
         for (; j < j1; ++j) {
             ok = __all_sync(0xffffffffu, tile_wait(&bars[sg], phase, p));
@@ -721,19 +778,51 @@ __global__ void __launch_bounds__(kThreads, 2)
                 phase ^= 1;
             }
             uint32_t b0, b1;
-            tile_weights<D>(st, w, cs, e & 0xFF, e >> 8, hide, ragged, j * kTile, sees, b0, b1);
-            tile_product<D>(st, v, b0, b1);
+            tile_weights<D, G>(st, w, cs, e & 0xFF, e >> 8, M > 1 ? only : -1, ragged, all_see - j * kTile, M > 1 && p.indptr ? 1 : 0,
+                               b0, b1);
+            // where tokens see different keys of the tile, one token at a time, from the one that sees
+            // most: V's rows past each one's last key become zeros
+            int t = M > 1 && ragged && p.indptr ? M - 1 : -1;
+            do {
+                if (M > 1 && t >= 0) {
+                    had.take(st);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j * kTile + key_of<D>(2 * c + (i & 1) + 8 * (i >> 1)) >= all_see + t)
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k) v[i][k] = 0u;
+                }
+                tile_product<D>(st, v, b0, b1);
+                if (M > 1 && t >= 0) {
+                    const bool its[2] = {2 * c / G == t, (2 * c + 1) / G == t};
+                    had.give_back(st, its);
+                }
+            } while (M > 1 && --t >= 0);
         }
-        at = cur.first + j - cur.key0;
+        at = shift + j;
         if (!ok) break;
-        if (at == end || at == cur.from + cur.all) {
-            const bool whole = cur.from >= begin && at == cur.from + cur.all;
-            write_piece<D, G>(p, st, kv_head, out, whole ? -1 : 2 * range + (cur.from < begin ? 0 : 1), hl);
+        if (M > 1 && only >= 0) {
+            if (careful) had.give_back(st, mine);
+            else nan = nan || __any_sync(0xffffffffu, poisoned(st, mine));
+        }
+        const Walk<G> w = curs[warp];
+        if (at == end || at == w.from + w.all) {
+            // a NaN of one request reached another's columns: once more, keeping them apart segment
+            // by segment (which costs 8 % where it is not needed)
+            if (nan) break;
+            int32_t out[2];  // query rows of this lane's columns, -1: none
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t i = (2 * c + h) / G, row = (p.indptr ? w.s * M : 0) + i;
+                out[h] = i < M && row < w.ext ? w.q0 + row : -1;
+            }
+            const bool whole = w.from >= begin && at == w.from + w.all;
+            write_piece<D, G>(p, st, w.grp * p.hg + hl, out, whole ? -1 : 2 * range + (w.from < begin ? 0 : 1), hl);
             fresh = true;
+            piece = at;
         }
     }
-    if (bad) set_error(p.err, DERR_SLOT_RANGE);
-    // after a wait that gave up: what was asked for lands before the CTA ends
+    // what was asked for and not attended lands before the warp goes on or ends (a wait gave up, or NaN)
     for (int32_t left = ask_at - at; left > 0; --left) {
         mbar_wait(&bars[sg], phase);
         if (++sg == R::kStages) {
@@ -741,6 +830,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             phase ^= 1;
         }
     }
+    if (nan && ok) {
+        careful = true;
+        goto again;
+    }
+    if (bad) set_error(p.err, DERR_SLOT_RANGE);
 }
 
 // One query head's records i0 .. i1 into its row; `on`: there are any for this warp's head.
@@ -859,26 +953,32 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
         tok = r < 0 ? 0 : blockIdx.x - __ldg(p.indptr + r);
     }
     int64_t before = 0, all = 0;
-    for (int i = tid; i < num_units<M>(p); i += 32 * W) {
-        const int64_t t = unit_tiles<M>(p, i, false);
-        all += t;
-        if (i < r) before += t;
-    }
+    if (p.before) {
+        pdl_wait();
+        before = p.before[r];
+        all = p.before[num_units<M>(p)];
+    } else {
+        for (int i = tid; i < num_units<M>(p); i += 32 * W) {
+            const int64_t t = unit_tiles<M>(p, i, false);
+            all += t;
+            if (i < r) before += t;
+        }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, d);
-        before += __shfl_xor_sync(0xffffffffu, before, d);
-    }
-    if (lane == 0) {
-        warp_sums[warp] = all;
-        warp_sums[W + warp] = before;
-    }
-    __syncthreads();
-    all = before = 0;
+        for (int d = 16; d > 0; d >>= 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, d);
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+        }
+        if (lane == 0) {
+            warp_sums[warp] = all;
+            warp_sums[W + warp] = before;
+        }
+        __syncthreads();
+        all = before = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        all += warp_sums[w];
-        before += warp_sums[W + w];
+        for (int w = 0; w < W; ++w) {
+            all += warp_sums[w];
+            before += warp_sums[W + w];
+        }
     }
     const int32_t n = line_length(p, all, false);
     int32_t tiles = 0;  // of the row's stream; 0: the row sees no key
@@ -928,11 +1028,15 @@ static size_t range_bytes(int hg, int32_t d) { return 2 * (size_t)hg * 8 * (d + 
 
 // Requests of rows shorter than this are not looked through: the look costs about 2 us.
 constexpr int64_t kMinShared = 1024;
+constexpr size_t kListBytes = 2 * 65536 + 256;  // share and before
+// Batches of more units than this have the tiles before each written down: adding them up in every
+// CTA of the second kernel would grow with the square of the batch.
+constexpr int kManyUnits = 512;
 constexpr int kMaxShared = 16384;  // streams whose requests are looked through for shared pages
 
 static size_t decode_workspace(int32_t hkv, int32_t d) {
     const int hg = head_group(hkv);
-    return kWorkspaceHeader + kMaxShared * sizeof(int32_t) + (size_t)decode_ctas() * (kWarps / hg) * range_bytes(hg, d);
+    return kWorkspaceHeader + kListBytes + (size_t)decode_ctas() * (kWarps / hg) * range_bytes(hg, d);
 }
 
 template <int D, int G>
@@ -1023,8 +1127,8 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     p.q = static_cast<const uint16_t *>(q);
     p.o = static_cast<uint16_t *>(o);
     p.scale_log2 = sm_scale * kLog2eB;
-    // workspace: header | decode: tiles shared by each stream | records
-    const size_t head = kWorkspaceHeader + (indptr ? 0 : kMaxShared * sizeof(int32_t));
+    // workspace: header | decode: tiles shared by each stream, tiles before each | records
+    const size_t head = kWorkspaceHeader + (indptr ? 0 : kListBytes);
     const size_t room = ws_bytes < head ? 0 : (ws_bytes - head) / range_bytes(p.hg, D);
     // no more ranges than the tables have room for tiles of
     const int64_t M = 8 / G, tiles = (std::min<int64_t>(batch->stride, ((int64_t)1 << 31) >> p.shift) << p.shift) / kTile;
@@ -1036,6 +1140,8 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     p.err = reinterpret_cast<int32_t *>(ws);
     int32_t *share = indptr ? nullptr : reinterpret_cast<int32_t *>(ws + kWorkspaceHeader);
     p.share = nullptr;
+    const int64_t streams = (batch->batch + M - 1) / M;
+    p.before = !indptr && streams > kManyUnits && streams <= kMaxShared ? share + kMaxShared : nullptr;
     p.rec = reinterpret_cast<float *>(ws + head);
     p.rec_ml = p.rec + (size_t)p.ranges * 2 * p.hg * 8 * D;
     p.wait = wait_policy(wait_limit_ns());

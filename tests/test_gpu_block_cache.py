@@ -320,7 +320,7 @@ def test_decode(pkv, g, hkv, d, page, layout):
     assert torch.all(o[0] == 0) and torch.all(o[14] == 0)
 
 
-@pytest.mark.parametrize("b,length", [(1, 1), (1, 100), (1, 70000), (3, 9001), (40, 2300), (700, 40), (4100, 3)])
+@pytest.mark.parametrize("b,length", [(1, 1), (1, 100), (1, 70000), (3, 9001), (40, 2300), (700, 40), (4100, 3), (9000, 30)])
 def test_decode_batches(pkv, b, length):
     """One long request split over the GPU, and more requests than warps."""
     rng = np.random.default_rng(b)
@@ -360,6 +360,60 @@ def test_decode_with_shared_pages(pkv, g, hkv, d, page, b):
     table[rows, 1] = pages
     o, ws = check_decode(pkv, pool, was, table, rows, lens.tolist(), page, hkv * g, d ** -0.5, only=only)
     assert error(pkv, ws) == 0x100
+
+
+@pytest.mark.parametrize("g,hkv,d", [(1, 2, 64), (4, 8, 128), (2, 1, 128), (8, 2, 64)])
+@pytest.mark.parametrize("shared", [0, 64])
+def test_decode_keeps_a_nan_to_its_request(pkv, g, hkv, d, shared):
+    """NaN codes among one request's keys or values: its rows are NaN where the definition's are, and
+    the requests attended beside it are not touched."""
+    rng = np.random.default_rng(d)
+    page, lens = 16, [1100, 1090, 1300, 70, 1200, 1024, 1111, 1040, 1500]
+    pages = sum(-(-n // page) for n in lens) + shared
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    table, rows, _ = paged_batch(pkv, rng, lens, page, pages, shared)
+    for r, codes, t in ((1, was[0], pool.k), (4, was[2], pool.v), (6, was[2], pool.v), (6, was[0], pool.k)):
+        slot = int(table[rows[r], (lens[r] - 7) // page]) * page + (lens[r] - 7) % page
+        codes[slot, 0, 3] = 0xFF
+        t[slot, 0, 3] = 0xFF
+    q, qv = bf16(rng.standard_normal((len(lens), hkv * g, d)))
+    o, ws = decode(pkv, pool, pkv.Batch(dev(table), dev(rows), dev(lens), page), q, hkv * g, d ** -0.5)
+    got = values(o)
+    for r in range(len(lens)):
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+        with np.errstate(invalid="ignore"):
+            want, bound = ref.attend(qv[r:r + 1], k, v, d ** -0.5, [lens[r] - 1], DECODE_EPS, v_exp=e)
+        assert np.array_equal(np.isnan(got[r:r + 1]), np.isnan(want)), r
+        fine = np.isfinite(want)
+        assert np.all(np.abs(got[r:r + 1] - want)[fine] <= np.where(np.isfinite(bound), bound, np.inf)[fine]), r
+    assert np.isfinite(got[[0, 2, 3, 5, 7, 8]]).all()
+
+
+def test_extend_streams_keep_a_later_nan_from_earlier_tokens(pkv):
+    """A NaN in a new token's row reaches the tokens that see it, not those before it."""
+    rng = np.random.default_rng(0)
+    page, hkv, g, d, lens, ext = 16, 2, 2, 64, [75, 40], [6, 3]
+    pool, was = random_pool(pkv, rng, 9, page, hkv, d)
+    table, rows, batch = paged_batch(pkv, rng, lens, page, 9)
+    for codes, t in ((was[0], pool.k), (was[2], pool.v)):
+        slot = int(table[rows[0], 72 // page]) * page + 72 % page     # token 3 of 6
+        codes[slot] = 0x7F
+        t[slot] = 0x7F
+    qo = np.array([0, 6, 9])
+    plan = pkv.plan_extend(lens, ext, qo, hkv * g, hkv, d)
+    plan.info.offsets[18] = 1
+    q, qv = bf16(rng.standard_normal((9, hkv * g, d)))
+    o, ws = torch.empty_like(q), words(plan.info.workspace_bytes // 4 + 1)
+    pkv.attn_extend_block(pool, batch, q, o, 0.1, plan, dev(plan.blob, np.uint8), ws)
+    got = values(o)
+    assert np.isnan(got[3:6]).all()
+    for r, rows_ in ((0, range(3)), (1, range(6, 9))):
+        k, v = (np.nan_to_num(ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page)) for j in (0, 2))
+        e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+        for i in rows_:
+            want, bound = ref.attend(qv[i:i + 1], k, v, 0.1, [lens[r] - ext[r] + i - qo[r]], DECODE_EPS, v_exp=e)
+            assert np.all(np.abs(got[i:i + 1] - want) <= bound)
 
 
 @pytest.mark.parametrize("hkv,d", [(8, 128), (2, 64)])
