@@ -442,7 +442,7 @@ def attn_decode_block(pool: BlockPool, batch: Batch, q, o, sm_scale, workspace, 
     rows = (b.batch, q.shape[1] if q.dim() == 3 else 0, p.head_dim)
     ws, size = _space(workspace, device)
     check("pkv_attn_decode_block", lib.pkv_attn_decode_block(
-        p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), rows[1], sm_scale,
+        p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), rows[1], float(sm_scale),
         ws, size, stream))
 
 
@@ -457,7 +457,7 @@ def attn_extend_block(pool: BlockPool, batch: Batch, q, o, sm_scale, plan: Plan,
         raise ValueError("plan_dev is shorter than the plan")
     ws, size = _space(workspace, device)
     check("pkv_attn_extend_block", lib.pkv_attn_extend_block(
-        p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), sm_scale, info, at,
+        p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), float(sm_scale), info, at,
         ws, size, stream))
 
 

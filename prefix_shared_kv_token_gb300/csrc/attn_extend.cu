@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p)
     if (p.pdl_wait_start) pdl_wait();
     pdl_trigger();
     const GatherUnit u = p.units[blockIdx.x];
-    const int row = __ldg(p.req_pool_indices + u.src);
+    const int row = ld(p.req_pool_indices + u.src);
     if (row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift)) {
         if (threadIdx.x == 0) set_error(p.err, DERR_POSITION);
         return;
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p)
             const int rem = v ? i - per : i, key = pow2 ? rem >> vshift : rem / vecs, piece = rem - key * vecs;
             const int32_t slot = s_slot[key];
             if (slot < 0) continue;
-            x[k] = __ldg(reinterpret_cast<const uint4 *>((v ? p.v_pool : p.k_pool) + (int64_t)slot * p.slot_bytes) + piece);
-            f[k] = __ldg((v ? p.v_exp : p.k_exp) + (int64_t)(slot >> p.block_shift) * p.hkv + piece / (D / 16));
+            x[k] = ld(reinterpret_cast<const uint4 *>((v ? p.v_pool : p.k_pool) + (int64_t)slot * p.slot_bytes) + piece);
+            f[k] = ld((v ? p.v_exp : p.k_exp) + (int64_t)(slot >> p.block_shift) * p.hkv + piece / (D / 16));
         }
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) {

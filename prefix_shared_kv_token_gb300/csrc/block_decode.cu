@@ -74,7 +74,7 @@ struct BlockDecodeParams {
 
 // A request's length as the kernels use it: 0 where its row or length is out of range.
 PKV_DEV int32_t checked_len(const BlockDecodeParams &p, int r, bool report) {
-    const int32_t len = __ldg(p.lens + r), row = __ldg(p.rows + r);
+    const int32_t len = ld(p.lens + r), row = ld(p.rows + r);
     if (len == 0) return 0;
     if (len < 0 || row < 0 || row >= p.num_rows || (int64_t)len > (p.stride << p.shift)) {
         if (report) set_error(p.err, DERR_POSITION);
@@ -126,7 +126,7 @@ PKV_DEV uint32_t pack_f16x2(float lo, float hi) {
 // Query tokens of request r: (first row of q, how many), and of them the streams.
 PKV_DEV int2 query_rows(const BlockDecodeParams &p, int r, int32_t len) {
     if (!p.indptr) return make_int2(r, 1);
-    const int32_t a = __ldg(p.indptr + r), n = __ldg(p.indptr + r + 1) - a;
+    const int32_t a = ld(p.indptr + r), n = ld(p.indptr + r + 1) - a;
     return make_int2(a, min(n, len));
 }
 // Keys that the last token of stream s of a request sees (streams of M = 8 / G tokens).
@@ -169,7 +169,7 @@ PKV_DEV int load_query(const uint16_t *row, uint32_t (&qb)[D / 16][2]) {
     for (int h = 0; h < D / 64; ++h)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint4 x = row ? __ldg(reinterpret_cast<const uint4 *>(row + 64 * h + 16 * c) + u) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x = row ? ld(reinterpret_cast<const uint4 *>(row + 64 * h + 16 * c) + u) : make_uint4(0u, 0u, 0u, 0u);
             w[8 * h + 4 * u] = x.x;
             w[8 * h + 4 * u + 1] = x.y;
             w[8 * h + 4 * u + 2] = x.z;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) block_share_kernel(const BlockDecode
         const int r = r0 + min(m, members - 1);
         const int32_t len = checked_len(p, r, false);
         pages = min(pages, len >> p.shift);
-        rows[m] = p.table + (int64_t)(len > 0 ? __ldg(p.rows + r) : 0) * p.stride;
+        rows[m] = p.table + (int64_t)(len > 0 ? ld(p.rows + r) : 0) * p.stride;
     }
     if (members < M) pages = 0;  // the last stream, when it is not full
     if (threadIdx.x == 0) s_first = pages;
@@ -516,9 +516,9 @@ __global__ void __launch_bounds__(kThreads) block_share_kernel(const BlockDecode
             const int32_t j = j0 + u * kThreads + threadIdx.x;
             if (j >= pages) continue;
             bool same = true;
-            const int32_t first = __ldg(rows[0] + j);
+            const int32_t first = ld(rows[0] + j);
 #pragma unroll
-            for (int m = 1; m < M; ++m) same &= __ldg(rows[m] + j) == first;
+            for (int m = 1; m < M; ++m) same &= ld(rows[m] + j) == first;
             if (!same) atomicMin(&s_first, j);
         }
         __syncthreads();
@@ -541,7 +541,7 @@ PKV_DEV void warm_query(const BlockDecodeParams &p, const Walk<G> &w, int hl) {
     if (lane < M * kLines && t < w.ext) {
         const uint16_t *at = p.q + ((int64_t)(w.q0 + t) * p.hkv * G + (w.grp * p.hg + hl) * G) * D + lane % kLines * 64;
         uint32_t x;
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(at));
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(at));
     }
 }
 
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 x.lim = min(min(w.first + w.tiles, from + 32), end);
                 x.head = w.grp * p.hg + hl;
                 const int32_t j = w.key0 + min(from + lane, x.lim - 1) - w.first;
-                const int32_t page = __ldg(p.table + (int64_t)__ldg(p.rows + w.request(p)) * p.stride + (j >> tpp));
+                const int32_t page = ld(p.table + (int64_t)ld(p.rows + w.request(p)) * p.stride + (j >> tpp));
                 // a page outside the pool: rows past the maps' last, which read as zeros
                 const bool in = (uint32_t)page < (uint64_t)p.num_pages;
                 bad |= !in;
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     auto exps_of = [&](int32_t slot, int32_t head) {
         const int64_t at = (int64_t)(slot < num_slots ? slot >> p.shift : 0) * p.hkv + head;
-        return (uint32_t)__ldg(p.k_exp + at) | (uint32_t)__ldg(p.v_exp + at) << 8;
+        return (uint32_t)ld(p.k_exp + at) | (uint32_t)ld(p.v_exp + at) << 8;
     };
     int32_t slot_c, slot_n, slot_m, ask_at, ask_b, ask_lim, ask_head;
     uint32_t exps_c, exps_n, turn = 0;  // ahead[warp][turn] is the next batch, the other the one after it
@@ -947,10 +947,10 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
         if (tid == 0) s_req = -1;
         __syncthreads();
         for (int i = tid; i < p.batch; i += 32 * W)
-            if (__ldg(p.indptr + i) <= blockIdx.x && blockIdx.x < __ldg(p.indptr + i + 1)) s_req = i;
+            if (ld(p.indptr + i) <= blockIdx.x && blockIdx.x < ld(p.indptr + i + 1)) s_req = i;
         __syncthreads();
         r = s_req;
-        tok = r < 0 ? 0 : blockIdx.x - __ldg(p.indptr + r);
+        tok = r < 0 ? 0 : blockIdx.x - ld(p.indptr + r);
     }
     int64_t before = 0, all = 0;
     if (p.before) {

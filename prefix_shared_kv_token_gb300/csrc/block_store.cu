@@ -60,7 +60,7 @@ PKV_DEV bool is_slot(const BlockStoreParams &p, int32_t s) { return s >= 0 && (i
 PKV_DEV bool begins_run(const BlockStoreParams &p, int64_t i, int32_t slot) {
     const int off = slot & ((1 << p.shift) - 1);
     for (int d = 1; d <= off && d <= i; ++d) {
-        const int32_t s = __ldg(p.loc + i - d);
+        const int32_t s = ld(p.loc + i - d);
         if (is_slot(p, s)) return s != slot - d;
     }
     return true;
@@ -75,7 +75,7 @@ PKV_DEV int run_length(const BlockStoreParams &p, int64_t i, int32_t slot, bool 
     holes = false;
     while (len < most) {
         const int j = len + lane;
-        const int32_t s = j < most ? __ldg(p.loc + i + j) : -1;
+        const int32_t s = j < most ? ld(p.loc + i + j) : -1;
         const bool here = s == slot + j, out = j < most && !is_slot(p, s);
         const uint32_t stop = ~__ballot_sync(0xffffffffu, here || out), skip = __ballot_sync(0xffffffffu, out);
         const int more = stop ? __ffs(stop) - 1 : 32;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256) block_store_kernel(const BlockStoreParams
             const int64_t i = w0 + t + lane;
             bool begins = false;
             if (t + lane < p.window && i < p.n) {
-                const int32_t slot = __ldg(p.loc + i);
+                const int32_t slot = ld(p.loc + i);
                 begins = is_slot(p, slot) && begins_run(p, i, slot);
                 if (slot != -1 && !is_slot(p, slot) && blockIdx.y == 0) set_error(p.err, DERR_SLOT_RANGE);
             }
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(256) block_store_kernel(const BlockStoreParams
             if (begins) {
                 const int k = count + __popc(who & ((1u << lane) - 1));
                 runs[k] = t + lane;
-                slots[k] = __ldg(p.loc + i);
+                slots[k] = ld(p.loc + i);
             }
             count += __popc(who);
         }
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(256) block_store_kernel(const BlockStoreParams
         const int off = slot & mask;
         const int len = abs(lens[run]);
         const bool holes = lens[run] < 0;
-        auto stored = [&](int j) { return j < len && (!holes || __ldg(p.loc + i + j) == slot + j); };
+        auto stored = [&](int j) { return j < len && (!holes || ld(p.loc + i + j) == slot + j); };
         const int old = off > 0 ? clamp_exp(*page_exp) : 0;
         const bool held = len <= share * kChunk;  // the group's registers hold the run
         uint4 x[kLoads];
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) block_store_kernel(const BlockStoreParams
             for (int u = 0; u < kLoads; ++u) {
                 const int j = c + u * kRows + row_in;
                 if (!stored(j)) continue;
-                if (!held) x[u] = __ldg(reinterpret_cast<const uint4 *>(src + j * src_row));
+                if (!held) x[u] = ld(reinterpret_cast<const uint4 *>(src + j * src_row));
                 *reinterpret_cast<uint2 *>(codes + (int64_t)(slot + j) * p.slot_bytes + col) =
                     make_uint2(__byte_perm(quantise2(x[u].x, f), quantise2(x[u].y, f), 0x5410),
                                __byte_perm(quantise2(x[u].z, f), quantise2(x[u].w, f), 0x5410));

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablePa
     int64_t my_tok = 0, my_pg = 0;  // 64 bits: a bad step may ask for more than 2^31
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
-        const int32_t seq = __ldg(p.seq + r), n = __ldg(p.fresh + r), row = __ldg(p.rows + r);
+        const int32_t seq = ld(p.seq + r), n = ld(p.fresh + r), row = ld(p.rows + r);
         const bool ok = n >= 0 && seq >= n && (int64_t)seq <= (p.stride << p.shift) && row >= 0 && row < p.num_rows;
         bad |= !ok;
         if (ok) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablePa
     } else {
         int64_t at_tok = base_tok + scan_tok - my_tok, at_pg = base_pg + scan_pg - my_pg;
         for (int r = r0; r < r1; ++r) {
-            const int32_t seq = __ldg(p.seq + r), n = __ldg(p.fresh + r);
+            const int32_t seq = ld(p.seq + r), n = ld(p.fresh + r);
             tok[r] = (int32_t)at_tok;
             pg[r] = (int32_t)at_pg;
             at_tok += n;
@@ -130,11 +130,11 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablePa
         int32_t slot = -1, t = -1;
         if (!refuse && i < tokens) {
             const int r = last_at_most(tok, p.batch, (int32_t)i);
-            const int32_t old = __ldg(p.seq + r) - __ldg(p.fresh + r);
+            const int32_t old = ld(p.seq + r) - ld(p.fresh + r);
             t = old + (int32_t)(i - tok[r]);
             const int32_t had = pages_of(old, p.shift), b = t >> p.shift;
-            const int32_t page = b < had ? p.table[(int64_t)__ldg(p.rows + r) * p.stride + b]
-                                         : __ldg(p.free_pages + head + pg[r] + (b - had));
+            const int32_t page = b < had ? p.table[(int64_t)ld(p.rows + r) * p.stride + b]
+                                         : ld(p.free_pages + head + pg[r] + (b - had));
             slot = (int32_t)((uint32_t)page << p.shift) + (t & mask);
         }
         p.loc[i] = slot;
@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablePa
     if (!refuse) {
         for (int64_t i = first; i < pages; i += step) {
             const int r = last_at_most(pg, p.batch, (int32_t)i);
-            const int32_t old = __ldg(p.seq + r) - __ldg(p.fresh + r);
+            const int32_t old = ld(p.seq + r) - ld(p.fresh + r);
             const int64_t b = pages_of(old, p.shift) + (i - pg[r]);
-            p.table[(int64_t)__ldg(p.rows + r) * p.stride + b] = __ldg(p.free_pages + head + i);
+            p.table[(int64_t)ld(p.rows + r) * p.stride + b] = ld(p.free_pages + head + i);
         }
     }
     // every CTA has read the head before it draws its ticket; the counter wraps to 0 by itself

@@ -473,6 +473,22 @@ def test_decode_reports_bad_pages_rows_and_lengths(pkv):
             assert np.all(np.abs(values(o[r:r + 1]) - want) <= bound)
 
 
+@pytest.mark.parametrize("g,hkv,d", [(1, 64, 64), (4, 8, 128), (8, 1, 128)])
+def test_decode_of_the_same_row_more_than_once(pkv, g, hkv, d):
+    """Several queries of one row (samples of one prompt) at the same and at different lengths, and
+    rows that fill their table to its last position."""
+    rng = np.random.default_rng(g)
+    page = 32
+    lens = [40 * page, 40 * page, 1000, 40 * page, 999, 1, 40 * page]
+    pool, was = random_pool(pkv, rng, 80, page, hkv, d)
+    table = rng.permutation(80).reshape(2, 40)
+    rows = [0, 0, 0, 1, 0, 1, 1]
+    q = rng.standard_normal((len(lens), hkv * g, d))
+    q[1] = q[0]
+    o, ws = check_decode(pkv, pool, was, table, rows, lens, page, hkv * g, d ** -0.5, q=q)
+    assert error(pkv, ws) == 0
+
+
 def test_decode_is_the_same_every_time_and_on_any_stream(pkv):
     rng = np.random.default_rng(8)
     page, hkv, d, lens = 32, 8, 128, [5000, 1, 777, 2048]
