@@ -44,6 +44,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 4;         // records a merging warp has in flight
 constexpr float kBias = 6.f;      // weights carry 2^6 over their reference, which may lag the
 constexpr float kSlack = 8.f;     // largest by 2^8: they stay below 2^15 in f16
+constexpr float kNoKey = -3.402823466e38f;  // the reference of a column that has seen no key: the least finite,
+                                            // so that a logit of -inf less it is -inf
 constexpr float kUnbias = 1.f / (1 << 6);
 constexpr float kLog2eB = 1.4426950408889634f;
 
@@ -278,9 +280,9 @@ PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, int off, bool r
 template <int D, int G>
 PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int ek, int ev_byte,
                           int only, bool ragged, int sees, int step, uint32_t &b0, uint32_t &b1) {
-    const float kf = exp_value(clamp_exp(ek));
+    const float kf = exp_value(ek);
     // (a whole number below 2^23 as a float: its bits under those of 2^23)
-    const float ev = __uint_as_float(0x4B000000u | (uint32_t)clamp_exp(ev_byte)) - (8388608.f + 127.f);
+    const float ev = __uint_as_float(0x4B000000u | (uint32_t)ev_byte) - (8388608.f + 127.f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) t[e] = t[e] * (cs[e & 1] * kf) + ev;
     const int col = 2 * (threadIdx.x & 3);
@@ -318,9 +320,8 @@ PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2
     float w[4], rw[2], rl[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float m = st.m[h] == -INFINITY ? 0.f : st.m[h];  // a column that has seen no key yet
-        rw[h] = m - kBias;
-        rl[h] = m + (ev - st.ea[h]);
+        rw[h] = st.m[h] - kBias;
+        rl[h] = st.m[h] + (ev - st.ea[h]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     auto exps_of = [&](int32_t slot, int32_t head) {
         const int64_t at = (int64_t)(slot < num_slots ? slot >> p.shift : 0) * p.hkv + head;
-        return (uint32_t)ld(p.k_exp + at) | (uint32_t)ld(p.v_exp + at) << 8;
+        return (uint32_t)clamp_exp(ld(p.k_exp + at)) | (uint32_t)clamp_exp(ld(p.v_exp + at)) << 8;
     };
     int32_t slot_c, slot_n, slot_m, ask_at, ask_b, ask_lim, ask_head;
     uint32_t exps_c, exps_n, turn = 0;  // ahead[warp][turn] is the next batch, the other the one after it
@@ -742,7 +743,7 @@ again:
                 for (int h = 0; h < 2; ++h) cs[h] = ldexpf(p.scale_log2, __shfl_sync(0xffffffffu, e, 8 * c + 4 * h));
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
-                st.m[0] = st.m[1] = -INFINITY;
+                st.m[0] = st.m[1] = kNoKey;
                 st.l[0] = st.l[1] = st.ea[0] = st.ea[1] = 0.f;
                 fresh = false;
             }
