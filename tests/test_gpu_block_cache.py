@@ -594,6 +594,31 @@ def test_extend_chooses_by_the_tokens(pkv):
     assert few.info.offsets[18] == 1 and many.info.offsets[18] == 0
 
 
+@pytest.mark.parametrize("hkv,g,d", [(1, 1, 64), (8, 4, 128), (3, 8, 64), (16, 2, 128)])
+@pytest.mark.parametrize("old,new", [([0], [1]), ([1], [1]), ([0, 3], [5, 1]), ([15] * 7, [1] * 7)])
+def test_extend_of_short_contexts(pkv, hkv, g, d, old, new):
+    """A few keys in all, by the way that the plan chooses in the workspace that it asks for."""
+    rng = np.random.default_rng(hkv + len(old))
+    page, lens = 16, [a + b for a, b in zip(old, new)]
+    pool, was = random_pool(pkv, rng, 12, page, hkv, d)
+    table, rows, batch = paged_batch(pkv, rng, lens, page, 12)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d)
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
+    o = torch.full_like(qt, float("nan"))
+    ws = words((plan.info.workspace_bytes + 3) // 4)
+    pkv.attn_extend_block(pool, batch, qt, o, 0.1, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0
+    got = values(o)
+    for r in range(len(old)):
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(old[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
+        if plan.info.offsets[18]:
+            e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+            want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(old[r], lens[r]), DECODE_EPS, v_exp=e)
+        assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
+
+
 @pytest.mark.parametrize("b,old,new", [(2, 20000, 3), (60, 700, 9), (300, 1, 2)])
 def test_extend_streams_over_many_ranges(pkv, b, old, new):
     """Streams cut into many ranges, and more streams than ranges."""

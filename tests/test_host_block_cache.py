@@ -99,6 +99,21 @@ def test_extend_refusals():
     assert lib.pkv_attn_extend_block(C.byref(p), None, P, P, 0.1, C.byref(plan.info), P, P, 1 << 40, None) == INVALID
 
 
+@pytest.mark.parametrize("hkv,g,d", [(1, 1, 64), (1, 8, 128), (2, 4, 64), (3, 2, 128), (8, 1, 128), (16, 4, 64)])
+def test_extend_streams_fit_the_plans_workspace(hkv, g, d):
+    """Short contexts, whose gathered rows are smaller than one range's two records of 8 columns for a
+    group of up to 8 heads: such a plan gathers."""
+    hg = max(x for x in (8, 4, 2, 1) if hkv % x == 0)
+    streams = 0
+    for b in (1, 2, 7, 40):
+        for seq, ext in ((1, 1), (2, 1), (5, 5), (17, 3), (130, 2), (1000, 1)):
+            plan = pkv.plan_extend([seq] * b, [ext] * b, [i * ext for i in range(b + 1)], hkv * g, hkv, d)
+            if plan.info.offsets[18]:
+                streams += 1
+                assert plan.info.workspace_bytes - 256 >= 2 * hg * 8 * (d + 4) * 4
+    assert streams
+
+
 def test_table_refusals():
     def call(new=P, free=P, num_free=5, head=P, head_out=P, loc=P, pos=P, cap=4, indptr=P, ws=P, size=256, **kw):
         b = batch(**kw)
