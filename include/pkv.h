@@ -375,7 +375,9 @@ typedef struct pkv_block_pool {
  *                  that may overlap on the GPU need a workspace each.
  * A step that has a request with lengths or a row out of range, or more than cap new tokens
  * (PKV_DERR_POSITION), or too few free pages (PKV_DERR_NO_PAGES), is refused whole: no table
- * entry is written, the maps hold -1 everywhere, qo_indptr 0, and the head stays. */
+ * entry is written, the maps hold -1 everywhere, qo_indptr 0, and the head stays.  A page id below
+ * 0 or with slots past 2^31, in the table or the list, sets PKV_DERR_SLOT_RANGE and gives its
+ * tokens the slot -1. */
 int pkv_build_block_tables(const pkv_batch *batch, const int32_t *new_lens, const int32_t *free_pages,
                            int64_t num_free, const int32_t *free_head, int32_t *free_head_out,
                            int32_t *out_cache_loc, int32_t *positions, int64_t cap, int32_t *qo_indptr,

@@ -8,6 +8,7 @@
 // and its new token i (position t = seq - new + i, query row indptr[r] + i) goes to slot
 // table[row[r]][t / P] * P + t mod P.
 //
+// A page id that no pool can have (negative, or its slots past 2^31) is flagged, its tokens' slots are -1.
 // A step with a bad request (or more pages than the list has, or more tokens than the maps
 // hold) is refused whole: the error word is set, no table entry is written, every map entry is
 // -1 and the list's head stays.
@@ -135,7 +136,10 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TablePa
             const int32_t had = pages_of(old, p.shift), b = t >> p.shift;
             const int32_t page = b < had ? p.table[(int64_t)ld(p.rows + r) * p.stride + b]
                                          : ld(p.free_pages + head + pg[r] + (b - had));
-            slot = (int32_t)((uint32_t)page << p.shift) + (t & mask);
+            if ((uint32_t)page <= (uint32_t)0x7FFFFFFF >> p.shift)
+                slot = (page << p.shift) + (t & mask);
+            else
+                set_error(p.err, DERR_SLOT_RANGE);  // no page: its slots do not fit
         }
         p.loc[i] = slot;
         p.pos[i] = t;

@@ -131,6 +131,31 @@ def test_tables_refuse_a_bad_step_whole(pkv, case, code, b):
     assert np.all(got[3] == 0) and got[4].tolist() == [head]
 
 
+@pytest.mark.parametrize("page", [1, 16, 4096])
+def test_tables_flag_pages_that_no_pool_has(pkv, page):
+    """Page ids whose slots do not fit 32 bits, where they are read: in a row and in the free list."""
+    last = 2**31 // page - 1    # the last that fits
+    for bad in (-1, 2**31 // page, 2**31 - 1, -2**31):
+        if bad == last or bad >= 2**31:
+            continue
+        table = np.array([[last, 7], [bad, 8]])
+        half = max(page // 2, 1)
+        # request 0: the rest of page `last`, then a bad page; request 1: the rest of a bad page (a page of
+        # one token leaves no rest)
+        old = half if page > 1 else 0
+        seq, new = [page + 1, page], [page + 1 - old, page - old]
+        if page == 1:
+            table[:] = -5
+        free = [last, bad, bad] if page == 1 else [bad]
+        got, ws = build(pkv, page, seq, new, [0, 1], table, free, 0, sum(new))
+        assert error(pkv, ws) == 0x100
+        ok = new[0] - 1
+        assert got[0][0, 1] == bad and got[4].tolist() == [len(free)]
+        assert got[0][1, 0] == bad
+        assert np.array_equal(got[2], [*range(old, page + 1), *range(old, page)])
+        assert np.array_equal(got[1], [last * page + old + i for i in range(ok)] + [-1] * (1 + new[1]))
+
+
 # ----------------------------------------------------------------------------------------
 # the pool and its store
 
