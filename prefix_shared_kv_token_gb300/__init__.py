@@ -383,7 +383,7 @@ def _where(stream):
 
 def _space(workspace, device):
     """(address, bytes) of a workspace."""
-    at = _fits("workspace", workspace, workspace.dtype, device, workspace.shape)
+    at = _fits("workspace", workspace, getattr(workspace, "dtype", None), device, getattr(workspace, "shape", None))
     return at, workspace.numel() * workspace.element_size()
 
 
@@ -439,7 +439,7 @@ def attn_decode_block(pool: BlockPool, batch: Batch, q, o, sm_scale, workspace, 
     a request of length 0 gets zeros (see pkv_attn_decode_block)."""
     torch, device, stream = _where(stream)
     p, b = pool.c(device), _block_batch(batch, device, torch.int32)
-    rows = (b.batch, q.shape[1] if q.dim() == 3 else 0, p.head_dim)
+    rows = (b.batch, q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0, p.head_dim)
     ws, size = _space(workspace, device)
     check("pkv_attn_decode_block", lib.pkv_attn_decode_block(
         p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), rows[1], float(sm_scale),

@@ -934,7 +934,8 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, int3
 // takes a query row and every gridDim.y-th (W / S) query heads, S warps a head: they share the
 // head's records, four in flight a warp, and combine through shared memory.  S grows with the
 // records of a stream: 1 for a few, 32 for a request alone in the batch, which may have one of every
-// range (100,001 keys: 24 us with 8 warps a head, 6 with 32).
+// range (100,001 keys: 24 us with 8 warps a head, 6 with 32).  Lengths, rows and shared tiles are read
+// before the wait: the decode kernel lets this one start only after its own wait for what wrote them.
 template <int D, int G, int W, int S>
 __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodeParams p) {
     __shared__ int64_t warp_sums[2 * W];
