@@ -412,7 +412,7 @@ int pkv_attn_decode_block(const pkv_block_pool *pool, const pkv_batch *batch, co
                           int32_t num_q_heads, float sm_scale, void *workspace, size_t ws_bytes, void *stream);
 
 /* pkv_attn_extend over a block-scaled pool: the same plans (pkv_plan_extend, cascade included,
- * without fuse_store), workspace and errors.  Each key run is turned once into the bf16 values its
+ * without fuse_store), workspace and errors; sm_scale must be positive.  Each key run is turned once into the bf16 values its
  * codes stand for. */
 int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o, float sm_scale,
                           const pkv_plan_info *info, const void *plan_dev, void *workspace, size_t ws_bytes,

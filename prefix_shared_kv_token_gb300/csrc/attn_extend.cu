@@ -40,6 +40,7 @@
 //      freed.
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/pkv.h"
 #include "block.cuh"
@@ -1198,6 +1199,8 @@ extern "C" int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch
     const int rc = validate_block_pool(pool);
     if (rc) return rc;
     if (!batch || batch->page_size != pool->page_size) return PKV_E_INVALID;
+    // the extend kernel takes a row's maximum before the scale, and masks with -inf
+    if (!(sm_scale > 0.f) || std::isinf(sm_scale)) return PKV_E_INVALID;
     pkv_pool rows{};
     rows.k = pool->k;
     rows.v = pool->v;

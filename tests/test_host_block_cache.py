@@ -99,6 +99,15 @@ def test_extend_refusals():
     assert lib.pkv_attn_extend_block(C.byref(p), None, P, P, 0.1, C.byref(plan.info), P, P, 1 << 40, None) == INVALID
 
 
+def test_extend_refuses_a_scale_that_is_not_positive():
+    p, b = pool(), batch(batch=1)
+    for tokens, seq in ((8, 40), (1, 9000)):      # gathered, streams
+        plan = pkv.plan_extend([seq], [tokens], [0, tokens], 32, 8, 128)
+        for scale in (0.0, -0.1, float("nan"), float("inf")):
+            assert lib.pkv_attn_extend_block(C.byref(p), C.byref(b), P, P, scale, C.byref(plan.info), P, P, 1 << 40,
+                                             None) == INVALID
+
+
 @pytest.mark.parametrize("hkv,g,d", [(1, 1, 64), (1, 8, 128), (2, 4, 64), (3, 2, 128), (8, 1, 128), (16, 4, 64)])
 def test_extend_streams_fit_the_plans_workspace(hkv, g, d):
     """Short contexts, whose gathered rows are smaller than one range's two records of 8 columns for a
