@@ -412,8 +412,10 @@ int pkv_attn_decode_block(const pkv_block_pool *pool, const pkv_batch *batch, co
                           int32_t num_q_heads, float sm_scale, void *workspace, size_t ws_bytes, void *stream);
 
 /* pkv_attn_extend over a block-scaled pool: the same plans (pkv_plan_extend, cascade included,
- * without fuse_store), workspace and errors; sm_scale must be positive.  Each key run is turned once into the bf16 values its
- * codes stand for. */
+ * without fuse_store), workspace and errors; sm_scale must be positive.  Each key run is turned once
+ * into the bf16 values its codes stand for, and attended with pkv_attn_extend's arithmetic (bf16
+ * weights); where the plan finds few tokens a request, they are attended over the pages with
+ * pkv_attn_decode_block's.  A NaN code reaches the query rows that see it and no others. */
 int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o, float sm_scale,
                           const pkv_plan_info *info, const void *plan_dev, void *workspace, size_t ws_bytes,
                           void *stream);

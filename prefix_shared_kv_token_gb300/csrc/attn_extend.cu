@@ -146,6 +146,7 @@ struct GatherParams {
     const uint8_t *k_exp;
     const uint8_t *v_exp;
     int32_t block_shift;
+    uint32_t *nans;  // of the workspace header: kNanMark where a gathered V row holds a NaN, then a count
     int32_t *err;
     int32_t pdl_wait_start;  // 1: wait for the preceding kernel first; 0: it wrote nothing this
                              // gather reads, wait for it only before exiting
@@ -238,7 +239,11 @@ PKV_DEV void gather_body(const GatherParams &p) {
 
 // The same copy out of a block-scaled pool: codes become the bf16 values they stand for, exactly
 // (a code times a power of two is a bf16 value).  A thread turns 16 codes, half a head's row or a
-// quarter, into 32 bytes, four such loads and their exponents in flight.
+// quarter, into 32 bytes, four such loads and their exponents in flight.  NaN codes of V are looked
+// for on the way (see block_mend_kernel).
+constexpr uint32_t kNanMark = 0x4E614E21u;
+constexpr int kNanWord = 20;  // of the workspace header
+
 template <int D>
 __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p) {
     __shared__ int32_t s_slot[32];
@@ -260,6 +265,7 @@ __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p)
     const bool pow2 = (vecs & (vecs - 1)) == 0;
     const int vshift = 31 - __clz(vecs);
     constexpr int kInFlight = 4;
+    uint32_t nans = 0;
     for (int base = threadIdx.x; base < 2 * per; base += kInFlight * blockDim.x) {
         uint4 x[kInFlight];
         uint32_t f[kInFlight];
@@ -289,13 +295,143 @@ __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p)
             for (int q = 0; q < 4; ++q) {
                 y[2 * q] = mul_bf16x2(e4m3x2_to_bf16x2((uint16_t)(w[q] & 0xFFFFu)), f2);
                 y[2 * q + 1] = mul_bf16x2(e4m3x2_to_bf16x2((uint16_t)(w[q] >> 16)), f2);
+                // (a byte of 0x7F and one more has its top bit set, no other has)
+                if (v) nans |= (w[q] & 0x7F7F7F7Fu) + 0x01010101u;
             }
             uint4 *out = reinterpret_cast<uint4 *>((v ? p.v_out : p.k_out) + (int64_t)(u.key0 + key) * p.hkv * D) + 2 * piece;
             out[0] = make_uint4(y[0], y[1], y[2], y[3]);
             out[1] = make_uint4(y[4], y[5], y[6], y[7]);
         }
     }
+    if (nans & 0x80808080u) {
+        p.nans[0] = kNanMark;
+        p.nans[1] = 0u;
+    }
     if (!p.pdl_wait_start) pdl_wait();  // complete only after the preceding kernel
+}
+
+struct MendParams {
+    const uint8_t *k, *v, *k_exp, *v_exp;
+    int64_t slot_bytes, num_pages;
+    int32_t shift, hkv, hq;
+    const int32_t *table;
+    int64_t stride;
+    int32_t num_rows, batch;
+    const int32_t *rows, *lens, *indptr;
+    const uint16_t *q;
+    uint16_t *o;
+    int32_t total_q;
+    float scale_log2;
+    uint32_t *nans;
+};
+
+// The attention kernel gives keys that a row does not see a weight of 0, which a NaN in such a key's V
+// row turns into a NaN: a later token's, or, where the gathered rows of two requests meet in a 128-key
+// tile, another request's.  When the gather met a NaN (only then), the rows that came out with one
+// are computed again, over the keys that they see and no others.  A warp a row and head; a lane a key
+// for the logits, D / 32 elements of the row for the sums, all in fp32 straight from the codes.  What
+// bounds it does not matter where it works; where it does not, the launch does not show in a call of 440 us.
+template <int D>
+__global__ void __launch_bounds__(256) block_mend_kernel(const MendParams p) {
+    __shared__ float s_q[8][D];
+    pdl_wait();
+    pdl_trigger();
+    if (__ldcg(p.nans) != kNanMark) return;
+    constexpr int V = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t units = (int64_t)p.total_q * p.hq;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + warp; u < units; u += (int64_t)gridDim.x * 8) {
+        uint32_t *out = reinterpret_cast<uint32_t *>(p.o + u * D) + lane * (V / 2);
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) nan |= (out[i] & 0x7FFFu) > 0x7F80u || ((out[i] >> 16) & 0x7FFFu) > 0x7F80u;
+        if (!__any_sync(0xffffffffu, nan)) continue;
+        const int32_t t = (int32_t)(u / p.hq), h = (int32_t)(u - (int64_t)t * p.hq), kv = h / (p.hq / p.hkv);
+        int lo = 0, hi = p.batch;  // the last request that begins at or before row t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ld(p.indptr + mid) <= t) lo = mid; else hi = mid;
+        }
+        const int32_t row = ld(p.rows + lo);
+        const int64_t keys = (int64_t)ld(p.lens + lo) - (ld(p.indptr + lo + 1) - t) + 1;
+        if (row < 0 || row >= p.num_rows || keys > (p.stride << p.shift)) continue;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const uint32_t x = reinterpret_cast<const uint32_t *>(p.q + u * D)[lane * (V / 2) + i];
+            s_q[warp][lane * V + 2 * i] = bf16_lo(x);
+            s_q[warp][lane * V + 2 * i + 1] = bf16_hi(x);
+        }
+        __syncwarp();
+        float m = -INFINITY, l = 0.f, acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int64_t j0 = 0; j0 < keys; j0 += 32) {
+            const int n = (int)min((int64_t)32, keys - j0);
+            // a lane's key: its slot (-1: a page outside the pool, whose rows are zeros) and logit
+            int32_t slot = -1;
+            float s = -INFINITY, ev = 0.f;
+            if (lane < n) {
+                const int64_t j = j0 + lane;
+                const int32_t page = ld(p.table + (int64_t)row * p.stride + (j >> p.shift));
+                s = 0.f;
+                if (page >= 0 && page < p.num_pages) {
+                    slot = (page << p.shift) + (int32_t)(j & ((1 << p.shift) - 1));
+                    const uint4 *at = reinterpret_cast<const uint4 *>(p.k + (int64_t)slot * p.slot_bytes + kv * D);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint4 x = ld(at + i);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t a = e4m3x2_to_f16x2(w[k]), b = e4m3x2_hi_to_f16x2(w[k]);
+                            const float2 x0 = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+                            const float2 x1 = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+                            const float *q = &s_q[warp][16 * i + 4 * k];
+                            s = fmaf(q[0], x0.x, fmaf(q[1], x0.y, fmaf(q[2], x1.x, fmaf(q[3], x1.y, s))));
+                        }
+                    }
+                    s *= exp_value(clamp_exp(ld(p.k_exp + (int64_t)page * p.hkv + kv))) * p.scale_log2;
+                    ev = exp_value(clamp_exp(ld(p.v_exp + (int64_t)page * p.hkv + kv)));
+                }
+            }
+            float top = s;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, m);
+            const float ref = top == -INFINITY ? 0.f : top, f = ex2(m - ref), w = lane < n ? ex2(s - ref) : 0.f;
+            m = top;
+            l = l * f + w;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] *= f;
+            for (int j = 0; j < n; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j), ej = __shfl_sync(0xffffffffu, ev, j);
+                const int32_t at = __shfl_sync(0xffffffffu, slot, j);
+                if (at < 0) continue;
+                const uint8_t *src = p.v + (int64_t)at * p.slot_bytes + kv * D + lane * V;
+                uint32_t code;
+                if constexpr (V == 4) code = *reinterpret_cast<const uint32_t *>(src);
+                else code = *reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const uint32_t a = i ? e4m3x2_hi_to_f16x2(code) : e4m3x2_to_f16x2(code);
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+                    acc[i] = fmaf(wj, x.x * ej, acc[i]);
+                    acc[i + 1] = fmaf(wj, x.y * ej, acc[i + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) out[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    }
+    // the last CTA to get here, when all have read the mark, takes it away
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(p.nans + 1, 1u) == gridDim.x - 1) p.nans[0] = 0u;
+    }
 }
 
 // p = 2^(s * scale - m) for the 128 scores of one row (masked scores are -inf and give 0),
@@ -979,6 +1115,7 @@ int decode_span_gather(const pkv_pool *pool, const pkv_batch *batch, const void 
     gp.v_out = b.vg;
     gp.k_exp = gp.v_exp = nullptr;
     gp.block_shift = 0;
+    gp.nans = nullptr;
     gp.err = reinterpret_cast<int32_t *>(ws);
     gp.pdl_wait_start = 1;
     // one launch: the span keys, then the member query rows
@@ -1149,6 +1286,7 @@ static int extend_call(const pkv_pool *pool, const pkv_batch *batch, const void 
     gp.k_exp = block ? block->k_exp : nullptr;
     gp.v_exp = block ? block->v_exp : nullptr;
     gp.block_shift = block ? log2_of(block->page_size) : 0;
+    gp.nans = reinterpret_cast<uint32_t *>(ws) + kNanWord;
     gp.err = reinterpret_cast<int32_t *>(ws);
     gp.pdl_wait_start = 1;
     const int nunits = (int)info->offsets[5];
@@ -1220,8 +1358,37 @@ extern "C" int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch
         return block_attend_few(pool, batch, indptr, info->total_q, q, o, info->num_q_heads, sm_scale, workspace, ws_bytes,
                                 reinterpret_cast<cudaStream_t>(stream));
     }
-    return extend_call(&rows, batch, q, o, sm_scale, nullptr, nullptr, nullptr, false, info, plan_dev, workspace, ws_bytes,
-                       stream, pool);
+    const int err = extend_call(&rows, batch, q, o, sm_scale, nullptr, nullptr, nullptr, false, info, plan_dev, workspace,
+                                ws_bytes, stream, pool);
+    if (err || info->num_items == 0) return err;
+    MendParams p;
+    p.k = static_cast<const uint8_t *>(pool->k);
+    p.v = static_cast<const uint8_t *>(pool->v);
+    p.k_exp = pool->k_exp;
+    p.v_exp = pool->v_exp;
+    p.slot_bytes = block_slot_bytes(pool);
+    p.num_pages = pool->num_pages;
+    p.shift = log2_of(pool->page_size);
+    p.hkv = pool->num_kv_heads;
+    p.hq = info->num_q_heads;
+    p.table = batch->req_to_token;
+    p.stride = batch->stride;
+    p.num_rows = batch->num_rows;
+    p.batch = batch->batch;
+    p.rows = batch->req_pool_indices;
+    p.lens = batch->seq_lens;
+    p.indptr = reinterpret_cast<const int32_t *>(static_cast<const uint8_t *>(plan_dev) + info->offsets[17]);
+    p.q = static_cast<const uint16_t *>(q);
+    p.o = static_cast<uint16_t *>(o);
+    p.total_q = info->total_q;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    p.nans = static_cast<uint32_t *>(workspace) + kNanWord;
+    const int64_t want = ((int64_t)p.total_q * p.hq + 7) / 8;
+    return launch_pdl(pool->head_dim == 128 ? block_mend_kernel<128> : block_mend_kernel<64>,
+                      dim3((unsigned)std::min<int64_t>(want, 4 * num_sms())), dim3(256), 0,
+                      reinterpret_cast<cudaStream_t>(stream), true, p) == cudaSuccess
+               ? PKV_OK
+               : PKV_E_CUDA;
 }
 
 extern "C" int pkv_attn_extend_store(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o,

@@ -619,6 +619,52 @@ def test_extend_chooses_by_the_tokens(pkv):
     assert few.info.offsets[18] == 1 and many.info.offsets[18] == 0
 
 
+@pytest.mark.parametrize("hkv,g,d,page", [(2, 4, 128, 16), (3, 8, 64, 32), (8, 1, 128, 64)])
+def test_gathered_extend_keeps_a_nan_to_the_rows_that_see_it(pkv, hkv, g, d, page):
+    """Requests whose gathered rows meet in a 128-key tile, later tokens of the same request, and a
+    prefix that two share: a NaN code of K or V reaches what sees it, element by element."""
+    rng = np.random.default_rng(hkv + d)
+    old, new = [30, 0, 260, 256, 7], [20, 40, 33, 50, 1]
+    lens = [a + b for a, b in zip(old, new)]
+    pages = sum(-(-n // page) for n in lens) + 1
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    table, rows, batch = paged_batch(pkv, rng, lens, page, pages)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d)
+    plan.info.offsets[18] = 0
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
+    ws = words((plan.info.workspace_bytes + 3) // 4)
+    blob = dev(plan.blob, np.uint8)
+
+    def slot(r, j):
+        return int(table[rows[r], j // page]) * page + j % page
+    # (tensor, request, position, head, element): in order of how many rows see it
+    plants = [None, (2, 1, 0, 0, 3), (2, 0, 45, hkv - 1, d - 1), (0, 3, 280, 0, 0), (2, 2, 0, hkv - 1, 17), (2, 4, 7, 0, 1), None]
+    last = None
+    for plant in plants:
+        if last is not None:   # what was there before the last one
+            (pool.k, None, pool.v)[last[0]][last[1]] = int(last[2])
+            was[last[0]][last[1]] = last[2]
+        last = None
+        if plant is not None:
+            t, r, j, h, i = plant
+            at = (slot(r, j), h, i)
+            last = (t, at, was[t][at])
+            (pool.k, None, pool.v)[t][at] = 0xFF
+            was[t][at] = 0xFF
+        o = torch.full_like(qt, 5.0)
+        pkv.attn_extend_block(pool, batch, qt, o, 0.1, plan, blob, ws)
+        assert error(pkv, ws) == 0 and int(ws[20]) == 0
+        got = values(o)
+        for r in range(len(old)):
+            k, v = (ref.rows_of(was[x], was[x + 1], table[rows[r]], lens[r], page) for x in (0, 2))
+            with np.errstate(invalid="ignore"):
+                want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(old[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
+            mine = got[qo[r]:qo[r + 1]]
+            assert np.array_equal(np.isnan(mine), np.isnan(want)), (plant, r)
+            assert np.all((np.abs(mine - want) <= bound) | np.isnan(want)), (plant, r)
+
+
 @pytest.mark.parametrize("hkv,g,d", [(1, 1, 64), (8, 4, 128), (3, 8, 64), (16, 2, 128)])
 @pytest.mark.parametrize("old,new", [([0], [1]), ([1], [1]), ([0, 3], [5, 1]), ([15] * 7, [1] * 7)])
 def test_extend_of_short_contexts(pkv, hkv, g, d, old, new):
