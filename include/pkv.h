@@ -384,8 +384,11 @@ int pkv_build_block_tables(const pkv_batch *batch, const int32_t *new_lens, cons
                            void *workspace, size_t ws_bytes, void *stream);
 
 /* Quantises new K/V rows into their slots.  Arguments as pkv_kv_store, and: tokens of one page
- * stand next to each other in the call, at consecutive slots (the order pkv_build_block_tables
- * gives), and a page's rows are filled from its offset 0 on.  Per KV head and tensor, the run of
+ * stand next to each other in the call, each in the slot behind the one before it (the order
+ * pkv_build_block_tables gives; a skipped token between two of them stands for the row between
+ * them), and a page's rows are filled from its offset 0 on.  What a
+ * page holds after a call that names it in two places, or one of its slots twice, is not
+ * specified.  Per KV head and tensor, the run of
  * a page's new tokens needs the smallest exponent e with max |x| <= 448 * 2^e over its finite
  * values.  A run that starts its page (offset 0) sets that exponent; what the page held before
  * is dead.  A later run keeps the page's exponent if that is as large, else raises it and
