@@ -873,3 +873,55 @@ def test_a_serving_run_in_a_graph(pkv):
             check(o[at], qv[at], lens, [(r, int(lens[r]) - 1) for r in at])
     pages = sum(-(-int(n) // page) for n in lens)
     assert int(head) == pages and len(set(host(table)[host(table) >= 0].tolist())) == pages
+
+
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("captured", [False, True])
+def test_tables_feed_the_calls_over_a_plain_pool(pkv, page, captured):
+    """The step's tables and slots are any pool's: steps of tables, kv_store and attn_extend over a bf16
+    pool, one behind the other with nothing in between that waits, also in one graph."""
+    rng = np.random.default_rng(page)
+    b, hkv, d, steps, grow = 120, 2, 64, 12, 3
+    stride = -(-steps * grow // page)
+    slots = b * stride * page
+    pool = pkv.Pool(*(torch.zeros((slots, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    free, head = dev(rng.permutation(b * stride)), dev([0])
+    table, rows, new = torch.full((b, stride), -1, dtype=torch.int32, device="cuda"), dev(rng.permutation(b)), dev([grow] * b)
+    loc, pos, qo, ws = words(b * grow), words(b * grow), words(b + 1), words()
+    qo_host = np.arange(b + 1) * grow
+    xs, outs, calls = [], [], []
+    for s in range(steps):
+        lens = [(s + 1) * grow] * b
+        plan = pkv.plan_extend(lens, [grow] * b, qo_host, hkv * 4, hkv, d)
+        x = [bf16(rng.standard_normal((b * grow, n, d)))[0] for n in (hkv, hkv, hkv * 4)]
+        calls.append((dev(lens), plan, dev(plan.blob, np.uint8), words((plan.info.workspace_bytes + 3) // 4)))
+        xs.append(x)
+        outs.append(torch.zeros_like(x[2]))
+    torch.cuda.synchronize()
+
+    def run():
+        for (k, v, q), o, (lens, plan, blob, space) in zip(xs, outs, calls):
+            pkv.build_block_tables(table, rows, lens, new, free, head, head, loc, pos, qo, page, ws)
+            pkv.kv_store(pool, k, v, loc, ws)
+            pkv.attn_extend(pool, pkv.Batch(table, rows, lens, page), q, o, 0.2, plan, blob, space)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        graph.replay()
+    else:
+        run()
+    assert error(pkv, ws) == 0 and int(head[0]) == b * stride
+    # what request r should hold is what its steps gave it, in order
+    k, v = (np.concatenate([values(x[i]).reshape(b, grow, hkv, d) for x in xs], 1) for i in (0, 1))
+    t = host(table)[host(rows)]
+    at = np.arange(steps * grow)
+    assert np.array_equal(values(pool.k)[t[:, at // page] * page + at % page], k)
+    assert np.array_equal(values(pool.v)[t[:, at // page] * page + at % page], v)
+    for s in (0, 5, steps - 1):
+        assert error(pkv, calls[s][3]) == 0
+        q, got = values(xs[s][2]).reshape(b, grow, -1, d), values(outs[s]).reshape(b, grow, -1, d)
+        for r in range(0, b, 17):
+            n = (s + 1) * grow
+            want, bound = ref.attend(q[r], k[r, :n], v[r, :n], 0.2, np.arange(n - grow, n), EXTEND_EPS, EXTEND_LOG_EPS)
+            assert np.all(np.abs(got[r] - want) <= bound)
