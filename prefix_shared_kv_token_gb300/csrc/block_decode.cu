@@ -1030,11 +1030,12 @@ static size_t range_bytes(int hg, int32_t d) { return 2 * (size_t)hg * 8 * (d + 
 
 // Requests of rows shorter than this are not looked through: the look costs about 2 us.
 constexpr int64_t kMinShared = 1024;
-constexpr size_t kListBytes = 2 * 65536 + 256;  // share and before
+constexpr int kMaxListed = 65536;  // streams that have a place in the lists: share, and before with its end
+constexpr size_t kListBytes = 2 * kMaxListed * sizeof(int32_t) + 256;
 // Batches of more units than this have the tiles before each written down: adding them up in every
-// CTA of the second kernel would grow with the square of the batch.
+// CTA of the second kernel would grow with the square of the batch (65,536 requests of 100 keys: 9.6 ms, with
+// the list 2.9).
 constexpr int kManyUnits = 512;
-constexpr int kMaxShared = 16384;  // streams whose requests are looked through for shared pages
 
 static size_t decode_workspace(int32_t hkv, int32_t d) {
     const int hg = head_group(hkv);
@@ -1056,7 +1057,7 @@ static int launch(BlockDecodeParams p, int32_t *share, const CUtensorMap &kmap, 
     constexpr int M = 8 / G;
     if constexpr (M > 1) {
         const int64_t streams = (p.batch + M - 1) / M;
-        if (share && p.batch > 1 && streams <= kMaxShared && (p.stride << p.shift) >= kMinShared) {
+        if (share && p.batch > 1 && streams <= kMaxListed && (p.stride << p.shift) >= kMinShared) {
             if (launch_pdl(block_share_kernel<M>, dim3((unsigned)streams), dim3(kThreads), 0, s, true, p, share) != cudaSuccess)
                 return PKV_E_CUDA;
             p.share = share;
@@ -1143,7 +1144,7 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     int32_t *share = indptr ? nullptr : reinterpret_cast<int32_t *>(ws + kWorkspaceHeader);
     p.share = nullptr;
     const int64_t streams = (batch->batch + M - 1) / M;
-    p.before = !indptr && streams > kManyUnits && streams <= kMaxShared ? share + kMaxShared : nullptr;
+    p.before = !indptr && streams > kManyUnits && streams <= kMaxListed ? share + kMaxListed : nullptr;
     p.rec = reinterpret_cast<float *>(ws + head);
     p.rec_ml = p.rec + (size_t)p.ranges * 2 * p.hg * 8 * D;
     p.wait = wait_policy(wait_limit_ns());

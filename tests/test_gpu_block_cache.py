@@ -360,6 +360,24 @@ def test_decode_batches(pkv, b, length):
     assert error(pkv, ws) == 0 and torch.isfinite(o).all()
 
 
+@pytest.mark.parametrize("b,g,hkv", [(16385, 8, 1), (65536, 8, 1), (65537, 8, 1), (40000, 4, 2), (131073, 4, 1)])
+def test_decode_of_very_many_requests(pkv, b, g, hkv):
+    """Batches around the most whose shared pages and tile sums are kept (65,536 streams), rows of the
+    same table many times."""
+    rng = np.random.default_rng(b)
+    page, d, n = 16, 64, 500
+    pool, was = random_pool(pkv, rng, 3 * n, page, hkv, d)
+    table, rows = rng.permutation(3 * n).reshape(n, 3), rng.integers(0, n, b)
+    lens = rng.integers(0, 49, b)
+    lens[-1] = 48
+    only = [0, b - 1, *rng.permutation(b)[:10]]
+    q = np.zeros((b, hkv * g, d), np.float32)
+    q[:] = rng.standard_normal((1, hkv * g, d))
+    o, ws = check_decode(pkv, pool, was, table, rows, lens.tolist(), page, hkv * g, 0.1, q=q, only=only)
+    assert error(pkv, ws) == 0 and torch.isfinite(o).all()
+    assert torch.equal((o == 0).all(2).all(1).cpu(), torch.from_numpy(lens == 0))
+
+
 @pytest.mark.parametrize("g,hkv,d,page", [(1, 8, 64, 16), (2, 3, 128, 32), (4, 8, 128, 16), (4, 2, 64, 64), (8, 4, 128, 16)])
 @pytest.mark.parametrize("b", [2, 9, 70])
 def test_decode_with_shared_pages(pkv, g, hkv, d, page, b):
