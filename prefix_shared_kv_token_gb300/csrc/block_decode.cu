@@ -33,6 +33,7 @@
 #include <atomic>
 
 #include "block.cuh"
+#include "block_plan.h"
 
 namespace pkv {
 
@@ -64,8 +65,8 @@ struct BlockDecodeParams {
     uint16_t *o;
     float scale_log2;
     int32_t ranges;  // at most
-    int32_t *before;  // decode: tiles before each unit, written by the first kernel for the second where
-                      // there are too many units to add them up again; NULL: none
+    int32_t *before;  // tiles before each unit, written by the first kernel for the second where there are
+                      // too many units to add them up again; NULL: none
     const int32_t *share;  // decode: tiles that the requests of a stream have in common, NULL: none
     float *rec;      // [range][2][hg][8 columns][D] (d in the order that merge_head says), then
                      // (R, l, ea, -) [range][2][hg][8][4]
@@ -946,10 +947,18 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t r = blockIdx.x / M, tok = blockIdx.x % M;  // decode: the stream and the row's place in it
     if (p.indptr) {  // the request of this query row, the row's place in it
-        if (tid == 0) s_req = -1;
-        __syncthreads();
-        for (int i = tid; i < p.batch; i += 32 * W)
-            if (ld(p.indptr + i) <= blockIdx.x && blockIdx.x < ld(p.indptr + i + 1)) s_req = i;
+        if (warp == 0) {
+            // the last request that begins at or before the row, each step among 32 times fewer
+            int lo = 0;
+            for (int left = p.batch; left > 1;) {
+                const int step = (left + 31) / 32, at = lo + lane * step;
+                const bool on = lane * step < left && ld(p.indptr + at) <= (int32_t)blockIdx.x;
+                const int skip = step * (31 - __clz(__ballot_sync(0xffffffffu, on) | 1u));
+                lo += skip;
+                left = min(step, left - skip);
+            }
+            if (lane == 0) s_req = (int32_t)blockIdx.x < ld(p.indptr + lo + 1) ? lo : -1;
+        }
         __syncthreads();
         r = s_req;
         tok = r < 0 ? 0 : blockIdx.x - ld(p.indptr + r);
@@ -957,7 +966,7 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
     int64_t before = 0, all = 0;
     if (p.before) {
         pdl_wait();
-        before = p.before[r];
+        before = p.before[max(r, 0)];
         all = p.before[num_units<M>(p)];
     } else {
         for (int i = tid; i < num_units<M>(p); i += 32 * W) {
@@ -1032,10 +1041,6 @@ static size_t range_bytes(int hg, int32_t d) { return 2 * (size_t)hg * 8 * (d + 
 constexpr int64_t kMinShared = 1024;
 constexpr int kMaxListed = 65536;  // streams that have a place in the lists: share, and before with its end
 constexpr size_t kListBytes = 2 * kMaxListed * sizeof(int32_t) + 256;
-// Batches of more units than this have the tiles before each written down: adding them up in every
-// CTA of the second kernel would grow with the square of the batch (65,536 requests of 100 keys: 9.6 ms, with
-// the list 2.9).
-constexpr int kManyUnits = 512;
 
 static size_t decode_workspace(int32_t hkv, int32_t d) {
     const int hg = head_group(hkv);
@@ -1130,8 +1135,9 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     p.q = static_cast<const uint16_t *>(q);
     p.o = static_cast<uint16_t *>(o);
     p.scale_log2 = sm_scale * kLog2eB;
-    // workspace: header | decode: tiles shared by each stream, tiles before each | records
-    const size_t head = kWorkspaceHeader + (indptr ? 0 : kListBytes);
+    // workspace: header | decode: tiles shared by each stream, tiles before each; else, of many requests, tiles
+    // before each | records
+    const size_t list = block_list_bytes(batch->batch), head = kWorkspaceHeader + (indptr ? list : kListBytes);
     const size_t room = ws_bytes < head ? 0 : (ws_bytes - head) / range_bytes(p.hg, D);
     // no more ranges than the tables have room for tiles of
     const int64_t M = 8 / G, tiles = (std::min<int64_t>(batch->stride, ((int64_t)1 << 31) >> p.shift) << p.shift) / kTile;
@@ -1144,7 +1150,8 @@ int block_attend_few(const pkv_block_pool *pool, const pkv_batch *batch, const i
     int32_t *share = indptr ? nullptr : reinterpret_cast<int32_t *>(ws + kWorkspaceHeader);
     p.share = nullptr;
     const int64_t streams = (batch->batch + M - 1) / M;
-    p.before = !indptr && streams > kManyUnits && streams <= kMaxListed ? share + kMaxListed : nullptr;
+    if (indptr) p.before = list ? reinterpret_cast<int32_t *>(ws + kWorkspaceHeader) : nullptr;
+    else p.before = streams > kManyUnits && streams <= kMaxListed ? share + kMaxListed : nullptr;
     p.rec = reinterpret_cast<float *>(ws + head);
     p.rec_ml = p.rec + (size_t)p.ranges * 2 * p.hg * 8 * D;
     p.wait = wait_policy(wait_limit_ns());

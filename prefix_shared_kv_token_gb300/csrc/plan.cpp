@@ -28,6 +28,7 @@
 #include <vector>
 
 #include "../../include/pkv.h"
+#include "block_plan.h"
 
 namespace {
 
@@ -121,7 +122,8 @@ bool few_tokens_are_streams(int32_t batch, const int32_t *seq_lens, const int32_
         keys += (double)n * seq_lens[r];
         streams += n;
     }
-    const double tiles = keys / 16.0 * (hkv / hg), room = (double)ws_bytes / (2.0 * hg * 8 * (d + 4) * 4);
+    const double tiles = keys / 16.0 * (hkv / hg);
+    const double room = ((double)ws_bytes - (double)pkv::block_list_bytes(batch)) / (2.0 * hg * 8 * (d + 4) * 4);
     if (room < 1.0) return false;  // a few keys, whose gathered rows are less than one range's records
     const double ranges = std::max(1.0, std::min({tiles / 2.0, room, 2.0 * num_sms * (8 / hg)}));
     const double few = std::max(keys * hkv * (d == 128 ? 0.036e-3 : 0.024e-3),

@@ -683,6 +683,32 @@ def test_gathered_extend_keeps_a_nan_to_the_rows_that_see_it(pkv, hkv, g, d, pag
             assert np.all((np.abs(mine - want) <= bound) | np.isnan(want)), (plant, r)
 
 
+@pytest.mark.parametrize("b,g,hkv", [(512, 4, 2), (513, 8, 2), (1025, 2, 3), (3000, 4, 1)])
+def test_extend_streams_of_many_requests(pkv, b, g, hkv):
+    """Around the batch from which the tiles before each request are written down (512)."""
+    rng = np.random.default_rng(b)
+    page, d, n = 16, 64, 400
+    new, old = rng.integers(1, 5, b), rng.integers(0, 60, b)
+    old[-1], new[-1] = 59, 4
+    lens = old + new
+    pool, was = random_pool(pkv, rng, 4 * n, page, hkv, d)
+    table, rows = rng.permutation(4 * n).reshape(n, 4), rng.integers(0, n, b)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d)
+    plan.info.offsets[18] = 1
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
+    o, ws = torch.full_like(qt, float("nan")), words((plan.info.workspace_bytes + 3) // 4)
+    batch = pkv.Batch(dev(table), dev(rows), dev(lens), page)
+    pkv.attn_extend_block(pool, batch, qt, o, 0.1, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0 and torch.isfinite(o).all()
+    got = values(o)
+    for r in [0, 1, 510, 511, b - 2, b - 1, *rng.permutation(b)[:10]]:
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(old[r], lens[r]), DECODE_EPS, v_exp=e)
+        assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
+
+
 @pytest.mark.parametrize("hkv,g,d", [(1, 1, 64), (8, 4, 128), (3, 8, 64), (16, 2, 128)])
 @pytest.mark.parametrize("old,new", [([0], [1]), ([1], [1]), ([0, 3], [5, 1]), ([15] * 7, [1] * 7)])
 def test_extend_of_short_contexts(pkv, hkv, g, d, old, new):
