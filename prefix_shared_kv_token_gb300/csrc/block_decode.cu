@@ -148,6 +148,26 @@ PKV_DEV int64_t stream_tiles(const BlockDecodeParams &p, int i, bool report) {
         if (i * M + m < p.batch) n += tiles_of(checked_len(p, i * M + m, report)) - share;
     return n;
 }
+// Member i's own tiles of a decode stream that begins at tile `from` and shares `share`: where they
+// begin and end.
+template <int32_t M>
+PKV_DEV int2 own_tiles(const BlockDecodeParams &p, int32_t r, int i, int32_t from, int32_t share) {
+    int32_t a = from + share, b = a;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (m <= i && r + m < p.batch) {
+            a = b;
+            b += tiles_of(checked_len(p, r + m, false)) - share;
+        }
+    return make_int2(a, b);
+}
+// Whether a request's columns get results and records by its own tiles and not by its stream's: a request that
+// shares no pages with the others of its stream then has no more records than it has ranges.  With 8 or 4
+// requests a stream that is worth its bookkeeping (237 requests of up to 93 keys, 16 heads x 64, G = 1: 34 to
+// 26 us), with 2 it is not (64 of up to 40 keys, 8 heads x 128, G = 4: 13.3 to 14.4).
+template <int32_t M>
+constexpr bool kApart = M >= 4;
+
 // What a chunk of the line is counted in: streams (decode), or requests with all their streams.
 template <int32_t M>
 PKV_DEV int32_t num_units(const BlockDecodeParams &p) { return p.indptr ? p.batch : (p.batch + M - 1) / M; }
@@ -379,10 +399,10 @@ PKV_DEV bool poisoned(const DecodeState<D> &st, const bool (&mine)[2]) {
     return (!mine[0] && x[0] != 0.f) || (!mine[1] && x[1] != 0.f);
 }
 
-// The result (rec < 0) or record of a stream's piece.  Column 2c + h of this lane belongs to query
-// row `row[h]` (-1: none) and head `hd[h]` of the group.
+// The results and records of a stream's piece.  Column 2c + h of this lane belongs to query row `row[h]`:
+// a result where rec[h] < 0, that record elsewhere (row < 0: neither).
 template <int D, int G>
-PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_head, const int32_t (&row)[2], int32_t rec, int hl) {
+PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_head, const int32_t (&row)[2], const int32_t (&rec)[2], int hl) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -390,7 +410,7 @@ PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_
         for (int d = 4; d < 32; d <<= 1) st.l[h] += __shfl_xor_sync(0xffffffffu, st.l[h], d);
         const int col = 2 * c + h;
         if (row[h] < 0) continue;
-        if (rec < 0) {
+        if (rec[h] < 0) {
             const float inv = row_scale(st.l[h], st.ea[h]);
             uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((int64_t)row[h] * p.hkv * G + kv_head * G + col % G) * D + g * (D / 8));
 #pragma unroll
@@ -400,7 +420,7 @@ PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_
                                         pack_bf16x2(st.acc[i + 2][h] * inv, st.acc[i + 2][2 + h] * inv),
                                         pack_bf16x2(st.acc[i + 3][h] * inv, st.acc[i + 3][2 + h] * inv));
         } else {
-            const int64_t at = ((int64_t)rec * p.hg + hl) * 8 + col;
+            const int64_t at = ((int64_t)rec[h] * p.hg + hl) * 8 + col;
             // piece i / 2 of lane g's run of d next to its neighbours' (see merge_head)
             float4 *dst = reinterpret_cast<float4 *>(p.rec + at * D) + g;
 #pragma unroll
@@ -812,14 +832,23 @@ again:
             // a NaN of one request reached another's columns: once more, keeping them apart segment
             // by segment (which costs 8 % where it is not needed)
             if (nan) break;
-            int32_t out[2];  // query rows of this lane's columns, -1: none
+            // this lane's columns: a result where the range holds every tile that they see, a record
+            // where it holds some
+            const bool whole = w.from >= begin && at == w.from + w.all;
+            int32_t out[2], rec[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int32_t i = (2 * c + h) / G, row = (p.indptr ? w.s * M : 0) + i;
                 out[h] = i < M && row < w.ext ? w.q0 + row : -1;
+                rec[h] = whole ? -1 : 2 * range + (w.from < begin ? 0 : 1);
+                if (kApart<M> && !p.indptr && !whole && w.ext > 1) {
+                    const int2 own = own_tiles<M>(p, w.r, i, w.from, w.share);
+                    const int32_t first = w.share == 0 ? own.x : w.from, past = own.y > own.x ? own.y : w.from + w.share;
+                    if (first >= begin && past <= at) rec[h] = -1;
+                    if (piece >= w.from + w.share && max(own.x, piece) >= min(own.y, at)) out[h] = -1;
+                }
             }
-            const bool whole = w.from >= begin && at == w.from + w.all;
-            write_piece<D, G>(p, st, w.grp * p.hg + hl, out, whole ? -1 : 2 * range + (w.from < begin ? 0 : 1), hl);
+            write_piece<D, G>(p, st, w.grp * p.hg + hl, out, rec, hl);
             fresh = true;
             piece = at;
         }
@@ -839,28 +868,33 @@ again:
     if (bad) set_error(p.err, DERR_SLOT_RANGE);
 }
 
-// One query head's records i0 .. i1 into its row; `on`: there are any for this warp's head.
-template <int D, int W, int S>
-PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, int32_t i0, int32_t i1, int hl, int col,
+// A query row's records: those of n1 ranges from i0 on and of the others, up to n, from j0 on.  They are
+// the second ones in the range in which their stream begins.
+struct Records {
+    int32_t i0, n1, j0, n, stream;
+};
+
+// One query head's records into its row; `on`: there are any for this warp's head.
+template <int D, int W, int S, bool kTwo, class Where>
+PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, const Where &from, int hl, int col,
                          float (&s_acc)[W][D], float4 (&s_ml)[W]) {
     constexpr int V = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % S;
-    if (!on) i1 = i0 - 1;
+    const int32_t n = on ? from.n : 0;
     float top = -INFINITY, L = 0.f, E = 0.f, O[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) O[v] = 0.f;
-    for (int32_t i = i0 + sub; i <= i1; i += S * kBatch) {
+    for (int32_t i = sub; i < n; i += S * kBatch) {
         float4 ml[kBatch];
         float a[kBatch][V];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int32_t k = i + b * S;
+            const int32_t at = i + b * S, k = !kTwo || at < from.n1 ? from.i0 + at : from.j0 + at - from.n1;
             ml[b] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[b][v] = 0.f;
-            if (k > i1) continue;
-            // a stream's first range ends inside it (record 1), the others begin inside it (record 0)
-            const int64_t rec = (((int64_t)k * 2 + (k == i0)) * p.hg + hl) * 8 + col;
+            if (at >= n) continue;
+            const int64_t rec = (((int64_t)k * 2 + (k == (kTwo ? from.stream : from.i0))) * p.hg + hl) * 8 + col;
             ml[b] = *reinterpret_cast<const float4 *>(p.rec_ml + rec * 4);
             if constexpr (V == 4) {
                 const float4 y = *reinterpret_cast<const float4 *>(p.rec + rec * D + lane * V);
@@ -938,11 +972,12 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, int3
 // range (100,001 keys: 24 us with 8 warps a head, 6 with 32).  Lengths, rows and shared tiles are read
 // before the wait: the decode kernel lets this one start only after its own wait for what wrote them.
 template <int D, int G, int W, int S>
-__global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodeParams p) {
+__global__ void __launch_bounds__(32 * W, 32 / W) block_merge_kernel(const BlockDecodeParams p) {
     __shared__ int64_t warp_sums[2 * W];
     __shared__ float s_acc[W][D];
     __shared__ float4 s_ml[W];
     __shared__ int32_t s_req;
+    __shared__ Records s_from[kApart<8 / G> ? W : 1];  // (registers are short)
     constexpr int32_t M = 8 / G;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t r = blockIdx.x / M, tok = blockIdx.x % M;  // decode: the stream and the row's place in it
@@ -992,21 +1027,52 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
         }
     }
     const int32_t n = line_length(p, all, false);
-    int32_t tiles = 0;  // of the row's stream; 0: the row sees no key
+    // the row's tiles on the line of a group of heads: `share` from `before` on and own.x .. own.y (or the
+    // stream's); tiles: how many (0: the row sees no key)
+    int32_t tiles = 0, share = 0;
+    int2 own = make_int2(0, 0);
     if (n > 0 && !p.indptr) {
-        if (checked_len(p, blockIdx.x, false) > 0) tiles = (int32_t)stream_tiles<M>(p, r, false);
+        if (kApart<M>) {
+            share = shared_tiles(p, r);
+            own = own_tiles<M>(p, r * M, tok, (int32_t)before, share);
+        } else {
+            own = make_int2((int32_t)before, (int32_t)(before + stream_tiles<M>(p, r, false)));
+        }
+        if (checked_len(p, blockIdx.x, false) > 0) tiles = share + own.y - own.x;
     } else if (n > 0 && r >= 0) {
         const int32_t len = checked_len(p, r, false), ext = query_rows(p, r, len).y, s = tok / M;
         for (int32_t i = 0; i < s; ++i) before += tiles_of(stream_len(len, ext, i, M));
         if (tok < ext) tiles = tiles_of(stream_len(len, ext, s, M));
+        own = make_int2((int32_t)before, (int32_t)before + tiles);
     }
     constexpr int V = D / 32;  // elements a lane holds
     const int sub = warp % S;
     const Cut cut(max(n * p.groups, 1), p.ranges);
-    int32_t grp = -1, i0 = 0, i1 = 0;
+    const int hq = p.hkv * G, step = W / S * gridDim.y;
+    int32_t grp = -1;
+    Records from{};
+    // where the records of a group of heads are, for this warp
+    auto locate = [&](int32_t of) {
+        grp = of;
+        const int32_t base = grp * n;
+        const bool shares = kApart<M> && share > 0;
+        Records &x = from;
+        x.stream = cut.range_of(base + (int32_t)before);
+        x.i0 = shares ? x.stream : cut.range_of(base + own.x);
+        x.n = x.n1 = cut.range_of(base + (shares ? (int32_t)before + share : own.y) - 1) - x.i0 + 1;
+        if (shares && own.y > own.x) {  // (a range that holds tiles of both has one record)
+            x.j0 = max(cut.range_of(base + own.x), x.i0 + x.n1);
+            x.n += max(cut.range_of(base + own.y - 1) - x.j0 + 1, 0);
+        }
+        if constexpr (kApart<M>) {
+            __syncwarp();
+            if (lane == 0) s_from[warp] = x;
+            __syncwarp();
+        }
+    };
+    if (kApart<M> && tiles > 0) locate(min(W / S * (int)blockIdx.y + warp / S, hq - 1) / G / p.hg);
     pdl_wait();  // the records
     pdl_trigger();
-    const int hq = p.hkv * G, step = W / S * gridDim.y;
     for (int h0 = W / S * blockIdx.y; h0 < hq; h0 += step) {
         const int qh = h0 + warp / S;
         const bool on = qh < hq;
@@ -1017,13 +1083,13 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
                 for (int d = lane; d < D / 2; d += 32) reinterpret_cast<uint32_t *>(out)[d] = 0u;
             continue;
         }
-        if (head / p.hg != grp) {
-            grp = head / p.hg;
-            const int32_t first = grp * n + (int32_t)before;
-            i0 = cut.range_of(first);
-            i1 = cut.range_of(first + tiles - 1);
+        if (head / p.hg != grp) locate(head / p.hg);
+        if constexpr (kApart<M>) {
+            const volatile Records &where = s_from[warp];
+            merge_head<D, W, S, true>(p, out, on && where.n > 1, where, head % p.hg, tok % M * G + q, s_acc, s_ml);
+        } else {
+            merge_head<D, W, S, false>(p, out, on && from.n > 1, from, head % p.hg, tok % M * G + q, s_acc, s_ml);
         }
-        merge_head<D, W, S>(p, out, on && i0 < i1, i0, i1, head % p.hg, tok % M * G + q, s_acc, s_ml);
     }
 }
 
@@ -1071,8 +1137,10 @@ static int launch(BlockDecodeParams p, int32_t *share, const CUtensorMap &kmap, 
     if (launch_pdl(block_decode_kernel<D, G>, dim3((p.ranges + per_cta - 1) / per_cta), dim3(kThreads), smem, s, true, p, kmap,
                    vmap) != cudaSuccess)
         return PKV_E_CUDA;
-    // records of a stream, at most, in a batch like this one
-    const int64_t each = p.ranges / std::max<int64_t>((q_rows + M - 1) / M * p.groups, 1), hq = p.hkv * G;
+    // records of a row, at most, in a batch like this one (a request that shares no pages has those of its own
+    // tiles)
+    const int64_t parts = p.indptr || p.share || !kApart<M> ? (q_rows + M - 1) / M : q_rows;
+    const int64_t each = p.ranges / std::max<int64_t>(parts * p.groups, 1), hq = p.hkv * G;
     auto merge = each > 64 ? block_merge_kernel<D, G, 32, 32> : each > 4 ? block_merge_kernel<D, G, kWarps, kWarps>
                                                                          : block_merge_kernel<D, G, kWarps, 1>;
     const int64_t heads = each > 4 ? 1 : kWarps;  // a CTA's at a time
