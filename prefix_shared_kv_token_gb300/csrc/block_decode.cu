@@ -880,21 +880,22 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, cons
                          float (&s_acc)[W][D], float4 (&s_ml)[W]) {
     constexpr int V = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % S;
-    const int32_t n = on ? from.n : 0;
+    // the records one after the other (kTwo), or the ranges themselves
+    const int32_t i0 = kTwo ? 0 : from.i0, past = on ? i0 + from.n : i0;
     float top = -INFINITY, L = 0.f, E = 0.f, O[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) O[v] = 0.f;
-    for (int32_t i = sub; i < n; i += S * kBatch) {
+    for (int32_t i = i0 + sub; i < past; i += S * kBatch) {
         float4 ml[kBatch];
         float a[kBatch][V];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int32_t at = i + b * S, k = !kTwo || at < from.n1 ? from.i0 + at : from.j0 + at - from.n1;
+            const int32_t at = i + b * S, k = !kTwo ? at : at < from.n1 ? from.i0 + at : from.j0 + at - from.n1;
             ml[b] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) a[b][v] = 0.f;
-            if (at >= n) continue;
-            const int64_t rec = (((int64_t)k * 2 + (k == (kTwo ? from.stream : from.i0))) * p.hg + hl) * 8 + col;
+            if (at >= past) continue;
+            const int64_t rec = (((int64_t)k * 2 + (k == (kTwo ? from.stream : i0))) * p.hg + hl) * 8 + col;
             ml[b] = *reinterpret_cast<const float4 *>(p.rec_ml + rec * 4);
             if constexpr (V == 4) {
                 const float4 y = *reinterpret_cast<const float4 *>(p.rec + rec * D + lane * V);
@@ -1036,9 +1037,10 @@ __global__ void __launch_bounds__(32 * W, 32 / W) block_merge_kernel(const Block
             share = shared_tiles(p, r);
             own = own_tiles<M>(p, r * M, tok, (int32_t)before, share);
         } else {
-            own = make_int2((int32_t)before, (int32_t)(before + stream_tiles<M>(p, r, false)));
+            tiles = (int32_t)stream_tiles<M>(p, r, false);
         }
-        if (checked_len(p, blockIdx.x, false) > 0) tiles = share + own.y - own.x;
+        if (checked_len(p, blockIdx.x, false) == 0) tiles = 0;
+        else if (kApart<M>) tiles = share + own.y - own.x;
     } else if (n > 0 && r >= 0) {
         const int32_t len = checked_len(p, r, false), ext = query_rows(p, r, len).y, s = tok / M;
         for (int32_t i = 0; i < s; ++i) before += tiles_of(stream_len(len, ext, i, M));
@@ -1054,20 +1056,24 @@ __global__ void __launch_bounds__(32 * W, 32 / W) block_merge_kernel(const Block
     // where the records of a group of heads are, for this warp
     auto locate = [&](int32_t of) {
         grp = of;
-        const int32_t base = grp * n;
-        const bool shares = kApart<M> && share > 0;
-        Records &x = from;
-        x.stream = cut.range_of(base + (int32_t)before);
-        x.i0 = shares ? x.stream : cut.range_of(base + own.x);
-        x.n = x.n1 = cut.range_of(base + (shares ? (int32_t)before + share : own.y) - 1) - x.i0 + 1;
-        if (shares && own.y > own.x) {  // (a range that holds tiles of both has one record)
-            x.j0 = max(cut.range_of(base + own.x), x.i0 + x.n1);
-            x.n += max(cut.range_of(base + own.y - 1) - x.j0 + 1, 0);
-        }
+        const int32_t first = grp * n + (int32_t)before;
         if constexpr (kApart<M>) {
+            const int32_t base = grp * n;
+            const bool shares = share > 0;
+            Records x{};
+            x.stream = cut.range_of(first);
+            x.i0 = shares ? x.stream : cut.range_of(base + own.x);
+            x.n = x.n1 = cut.range_of((shares ? first + share : base + own.y) - 1) - x.i0 + 1;
+            if (shares && own.y > own.x) {  // (a range that holds tiles of both has one record)
+                x.j0 = max(cut.range_of(base + own.x), x.i0 + x.n1);
+                x.n += max(cut.range_of(base + own.y - 1) - x.j0 + 1, 0);
+            }
             __syncwarp();
             if (lane == 0) s_from[warp] = x;
             __syncwarp();
+        } else {
+            from.i0 = cut.range_of(first);
+            from.n = cut.range_of(first + tiles - 1) - from.i0 + 1;
         }
     };
     if (kApart<M> && tiles > 0) locate(min(W / S * (int)blockIdx.y + warp / S, hq - 1) / G / p.hg);
