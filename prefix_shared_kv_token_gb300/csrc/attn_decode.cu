@@ -161,7 +161,7 @@ PKV_DEV void load_rows(const DecodeParams &p, int item, int w, ItemRows<D, G> &x
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = r + 8 * h;
-        x.req[h] = i < it.nreq * G ? __ldg(p.row_req + it.row_off + i / G) : -1;
+        x.req[h] = i < it.nreq * G ? ld(p.row_req + it.row_off + i / G) : -1;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -170,7 +170,7 @@ PKV_DEV void load_rows(const DecodeParams &p, int item, int w, ItemRows<D, G> &x
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             uint2 v = make_uint2(0u, 0u);
-            if (x.req[h] >= 0) v = __ldg(reinterpret_cast<const uint2 *>(qrow + ks * 16));
+            if (x.req[h] >= 0) v = ld(reinterpret_cast<const uint2 *>(qrow + ks * 16));
             x.qf[ks][h] = v.x;       // k-slots 2c, 2c+1
             x.qf[ks][2 + h] = v.y;   // k-slots 2c+8, 2c+9
         }
@@ -312,8 +312,8 @@ PKV_DEV TileSlot next_tile(const DecodeParams &p, TileCursor &cur, int c1, int k
         }
         ++cur.i;
         const DecodeItem it = p.items[cur.i];
-        const int row = __ldg(p.req_pool_indices + it.src);
-        const int k1 = it.k1 < 0 ? __ldg(p.seq_lens + it.src) : it.k1;
+        const int row = ld(p.req_pool_indices + it.src);
+        const int k1 = it.k1 < 0 ? ld(p.seq_lens + it.src) : it.k1;
         if (row < 0 || row >= p.rt_rows || it.k0 < 0 || k1 > (p.rt_stride << p.page_shift) || k1 <= it.k0) {
             if ((threadIdx.x & 31) == 0) set_error(p.err, DERR_POSITION);
             continue;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__((D == 64 ? 288 : 320), (D == 64 ? 2 : 1)) deco
         pdl_wait();     // the query tokens' K/V were stored just before
         pdl_trigger();  // the span pass may take SMs as this kernel's CTAs finish
     }
-    const int c0 = __ldg(p.cta_off + blockIdx.x), c1 = __ldg(p.cta_off + blockIdx.x + 1);
+    const int c0 = ld(p.cta_off + blockIdx.x), c1 = ld(p.cta_off + blockIdx.x + 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__((D == 64 ? 288 : 320), (D == 64 ? 2 : 1)) deco
                 load_rows<D, G>(p, ti.item, w, cur);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                rec[h] = cur.req[h] >= 0 ? __ldg(p.row_rec + cur.row_off + (r + 8 * h) / G) : -1;
+                rec[h] = cur.req[h] >= 0 ? ld(p.row_rec + cur.row_off + (r + 8 * h) / G) : -1;
                 st.m[h] = -INFINITY;
                 st.l[h] = 0.f;
             }
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__((D == 64 ? 288 : 320), (D == 64 ? 2 : 1)) deco
 // four at a time with all their loads in flight, rescaling the running sums when the
 // maximum grows.
 template <int D>
-__global__ void __launch_bounds__(256) merge_kernel(const MergeItem *__restrict__ merges, const float *__restrict__ rec_acc,
-                                                    const float *__restrict__ rec_ml, uint16_t *__restrict__ o, int hq) {
+__global__ void __launch_bounds__(256) merge_kernel(const MergeItem *merges, const float *rec_acc, const float *rec_ml,
+                                                    uint16_t *o, int hq) {
     // the merge list is plan data, complete before the call: read it while the kernel before
     // is still running, then wait for the records
     const MergeItem mi = merges[blockIdx.x];
@@ -555,15 +555,15 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeItem *__restrict_
             for (int v = 0; v < V; ++v) a[j][v] = 0.f;
             if (k0 + j < mi.nrec) {
                 const int64_t rb = (int64_t)(mi.rec0 + (k0 + j) * mi.rec_stride) * hq + h;
-                ml[j] = __ldg(reinterpret_cast<const float2 *>(rec_ml + rb * 2));
+                ml[j] = ld(reinterpret_cast<const float2 *>(rec_ml + rb * 2));
                 if constexpr (V == 4) {
-                    const float4 x = __ldg(reinterpret_cast<const float4 *>(rec_acc + rb * D + lane * 4));
+                    const float4 x = ld(reinterpret_cast<const float4 *>(rec_acc + rb * D + lane * 4));
                     a[j][0] = x.x;
                     a[j][1] = x.y;
                     a[j][2] = x.z;
                     a[j][3] = x.w;
                 } else {
-                    const float2 x = __ldg(reinterpret_cast<const float2 *>(rec_acc + rb * D + lane * 2));
+                    const float2 x = ld(reinterpret_cast<const float2 *>(rec_acc + rb * D + lane * 2));
                     a[j][0] = x.x;
                     a[j][1] = x.y;
                 }

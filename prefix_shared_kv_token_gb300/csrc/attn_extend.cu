@@ -168,17 +168,17 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
 template <int D, bool FP8>
 PKV_DEV void gather_body(const GatherParams &p) {
     if ((int)blockIdx.x >= p.nunits) {  // a query row
-        const int i = blockIdx.x - p.nunits, r = __ldg(p.q_rows + i);
+        const int i = blockIdx.x - p.nunits, r = ld(p.q_rows + i);
         if (r < 0 || r >= p.q_batch) {
             if (threadIdx.x == 0) set_error(p.err, DERR_POSITION);
             return;
         }
         for (int v = threadIdx.x; v < p.q_row_vecs; v += blockDim.x)
-            p.q_out[(int64_t)i * p.q_row_vecs + v] = __ldg(p.q_src + (int64_t)r * p.q_row_vecs + v);
+            p.q_out[(int64_t)i * p.q_row_vecs + v] = ld(p.q_src + (int64_t)r * p.q_row_vecs + v);
         return;
     }
     const GatherUnit u = p.units[blockIdx.x];
-    const int row = __ldg(p.req_pool_indices + u.src);
+    const int row = ld(p.req_pool_indices + u.src);
     if (row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift)) {
         if (threadIdx.x == 0) set_error(p.err, DERR_POSITION);
         return;
@@ -215,9 +215,9 @@ PKV_DEV void gather_body(const GatherParams &p) {
             if (slot < 0) continue;
             const uint8_t *pool = tensor ? p.v_pool : p.k_pool;
             if constexpr (!FP8) {
-                y[k] = __ldg(reinterpret_cast<const uint4 *>(pool + (int64_t)slot * p.slot_bytes) + v);
+                y[k] = ld(reinterpret_cast<const uint4 *>(pool + (int64_t)slot * p.slot_bytes) + v);
             } else {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(pool + (int64_t)slot * p.slot_bytes) + v);
+                const uint2 x = ld(reinterpret_cast<const uint2 *>(pool + (int64_t)slot * p.slot_bytes) + v);
                 y[k].x = e4m3x2_to_bf16x2((uint16_t)(x.x & 0xFFFFu));
                 y[k].y = e4m3x2_to_bf16x2((uint16_t)(x.x >> 16));
                 y[k].z = e4m3x2_to_bf16x2((uint16_t)(x.y & 0xFFFFu));
@@ -544,7 +544,7 @@ PKV_DEV void write_out(const ExtendParams &p, const XItem &it, int t, int tok, i
             dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
-        const int64_t rb = (int64_t)(p.rec_list ? __ldg(p.rec_list + it.rec + t) : it.rec + t) * p.hq + head;
+        const int64_t rb = (int64_t)(p.rec_list ? ld(p.rec_list + it.rec + t) : it.rec + t) * p.hq + head;
         float4 *dst = reinterpret_cast<float4 *>(p.rec_acc + rb * D + c4 * 32);
 #pragma unroll
         for (int v = 0; v < 8; ++v)
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(384, 1)
     if (p.pdl_wait_start) pdl_wait();
     pdl_trigger();
     // the plan is read only from here on: with pdl_wait_start it may come from the kernel before
-    const int i0 = __ldg(p.cta_off + blockIdx.x), i1 = __ldg(p.cta_off + blockIdx.x + 1);
+    const int i0 = ld(p.cta_off + blockIdx.x), i1 = ld(p.cta_off + blockIdx.x + 1);
     // once any CTA of this launch gave up on a wait, the rest exit instead of waiting too
     __shared__ int32_t s_skip;
     __shared__ float2 s_ml[2][kBM];  // split items: each warpgroup's running (max, sum) per row

@@ -16,12 +16,6 @@
 
 namespace pkv {
 
-// A load of what the kernel before may have written.  (Not the read-only path: a kernel launched
-// programmatically is already running while that is written, and read-only loads may be moved
-// above the wait for it.)
-template <class T>
-PKV_DEV T ld(const T *p) { return *p; }
-
 // Exponent bytes a page may have: 2^-117 keeps the smallest code (2^-9) a normal bf16 value,
 // 2^118 keeps the largest (448) finite in bf16.
 constexpr int kExpMin = 10, kExpMax = 245;

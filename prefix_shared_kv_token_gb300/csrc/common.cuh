@@ -57,12 +57,19 @@ PKV_DEV void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::
 PKV_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 PKV_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A load of what the kernel before may have written: tables, slots, lengths, rows, records, the plan.
+// Not the read-only path (__ldg, or a const __restrict__ parameter): a kernel launched
+// programmatically is already running while they are written, and the compiler may move read-only
+// loads above the wait for that.  An ordinary load stays behind pdl_wait.
+template <class T>
+PKV_DEV T ld(const T *p) { return *p; }
+
 // Slot of context position t from a row of the batch table: the token table's entry, or
 // with pages of 2^shift slots, the position's page times the page size plus its offset.
 // A page outside the pool gives -1 (the callers flag it and read zeros).
 PKV_DEV int32_t table_slot(const int32_t *row, int t, int shift, int64_t num_slots) {
-    if (shift == 0) return __ldg(row + t);
-    const int32_t pg = __ldg(row + (t >> shift));
+    if (shift == 0) return ld(row + t);
+    const int32_t pg = ld(row + (t >> shift));
     const int64_t slot = ((int64_t)pg << shift) + (t & ((1 << shift) - 1));
     return (pg < 0 || slot >= num_slots) ? -1 : (int32_t)slot;
 }

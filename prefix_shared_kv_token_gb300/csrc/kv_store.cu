@@ -24,13 +24,10 @@ namespace pkv {
 // (ctx_rows rows; a row outside them records DERR_POSITION with the token and the row, and
 // that copy is skipped).
 template <bool FP8, bool CTX>
-__global__ void __launch_bounds__(256) kv_store_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-                                                       const int32_t *__restrict__ loc, int64_t n, int32_t vec_per_row,
-                                                       int64_t slot_bytes, uint8_t *__restrict__ k_pool,
-                                                       uint8_t *__restrict__ v_pool,
-                                                       int64_t num_slots, float k_scale, float v_scale,
-                                                       int32_t *__restrict__ err, uint4 *__restrict__ ctx_k,
-                                                       uint4 *__restrict__ ctx_v, const int32_t *__restrict__ ctx_row,
+__global__ void __launch_bounds__(256) kv_store_kernel(const uint4 *k_new, const uint4 *v_new, const int32_t *loc, int64_t n,
+                                                       int32_t vec_per_row, int64_t slot_bytes, uint8_t *k_pool,
+                                                       uint8_t *v_pool, int64_t num_slots, float k_scale, float v_scale,
+                                                       int32_t *err, uint4 *ctx_k, uint4 *ctx_v, const int32_t *ctx_row,
                                                        int64_t ctx_rows) {
     // one warp per token row (K rows of tokens 0..n-1, then their V rows), grid-strided; the
     // row's slot is read once and the lanes stride its vec_per_row 16-byte source vectors,
@@ -42,7 +39,7 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const uint4 *__restrict__
     for (int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < 2 * n; row += nwarps) {
         const bool is_v = row >= n;
         const int64_t tok = is_v ? row - n : row;
-        const int32_t slot = __ldg(loc + tok);
+        const int32_t slot = ld(loc + tok);
         if (slot < 0 || (int64_t)slot >= num_slots) {
             if (lane == 0) set_error(err, DERR_SLOT_RANGE);
             continue;
@@ -52,7 +49,7 @@ __global__ void __launch_bounds__(256) kv_store_kernel(const uint4 *__restrict__
         const float s = is_v ? v_scale : k_scale;
         uint4 *cdst = nullptr;
         if constexpr (CTX) {
-            const int32_t r = __ldg(ctx_row + tok);
+            const int32_t r = ld(ctx_row + tok);
             if (r < 0 || (int64_t)r >= ctx_rows) {
                 if (lane == 0) set_error_where(err, DERR_POSITION, (int32_t)tok, r, 0);
             } else {
