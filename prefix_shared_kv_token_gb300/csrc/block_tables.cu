@@ -20,6 +20,7 @@
 // written by the CTA that finishes last, so that it may be read and written in place.
 
 #include <algorithm>
+#include <atomic>
 
 #include "block.cuh"
 
@@ -203,9 +204,18 @@ extern "C" int pkv_build_block_tables(const pkv_batch *batch, const int32_t *new
     const int64_t want = (std::max<int64_t>(cap, batch->batch + 1) + kTabThreads - 1) / kTabThreads;
     const int grid = (int)std::min<int64_t>(want, num_sms());
     const size_t smem = 2 * ((size_t)batch->batch + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess)
-        return PKV_E_CUDA;
+    // Leave for the largest batch's sums, given once a device and never lowered: a size of this call's own could be
+    // taken back by another thread's smaller call before the launch.  (The 48 KB a kernel may use without it
+    // count its static shared memory too.)
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_E_CUDA;
+    if (dev >= 64 || !((allowed.load(std::memory_order_relaxed) >> dev) & 1)) {
+        constexpr int most = 2 * (kMaxTableBatch + 1) * (int)sizeof(int32_t);
+        if (cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+            return PKV_E_CUDA;
+        if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
     return launch_pdl(block_tables_kernel, dim3(grid), dim3(kTabThreads), smem, reinterpret_cast<cudaStream_t>(stream),
                       true, p) == cudaSuccess
                ? PKV_OK

@@ -1,0 +1,90 @@
+"""Edges of the block-scaled cache's calls: batches at a launch limit, workspaces with old contents, exponents
+and logits at their ends, pools at any 16-byte address, large batches of few-head groups."""
+
+import os
+import subprocess
+import sys
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+from test_gpu_block_cache import (DECODE_EPS, EXTEND_EPS, EXTEND_LOG_EPS, bf16, check_decode, check_store, dev,
+                                  error, host, paged_batch, random_pool, table_inputs, values, words)
+
+pytestmark = pytest.mark.gpu
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    import prefix_shared_kv_token_gb300 as m
+    return m
+
+
+# ----------------------------------------------------------------------------------------
+# tables
+
+RISING = """
+import numpy as np
+import block_reference as ref
+import prefix_shared_kv_token_gb300 as pkv
+from test_gpu_block_cache import build, error, table_inputs
+for b in (6111, 6112, 6143, 6144, 16384, 7000):
+    seq, new, rows, table, free = table_inputs(np.random.default_rng(b), b, 16, 100, 2)
+    cap = int(new.sum()) + 5
+    got, ws = build(pkv, 16, seq, new, rows, table, free, 0, cap)
+    assert error(pkv, ws) == 0, b
+    for g, w in zip(got, ref.tables(table, rows, seq, new, free, 0, 16, cap)):
+        assert np.array_equal(g.reshape(-1), np.asarray(w).reshape(-1)), b
+print("done")
+"""
+
+
+def test_tables_of_rising_batches_in_a_process_of_their_own():
+    """8 bytes a request and one more in shared memory, and 256 bytes beside them: 6,112 requests are
+    the first to pass 48 KB with both, 6,144 without those."""
+    path = os.pathsep.join([HERE, os.path.dirname(HERE), os.environ.get("PYTHONPATH", "")])
+    run = subprocess.run([sys.executable, "-c", RISING], env={**os.environ, "PYTHONPATH": path}, capture_output=True, text=True)
+    assert run.returncode == 0 and run.stdout.strip() == "done", run.stderr[-2000:]
+
+
+def test_tables_of_different_batches_from_two_threads(pkv):
+    """Two host threads, each with its own stream and workspace: a small batch's launch takes nothing
+    from a large one's."""
+    def inputs(b):
+        seq, new, rows, table, free = table_inputs(np.random.default_rng(b), b, 16, 100, 2)
+        cap = int(new.sum())
+        out = [words(cap), words(cap), words(b + 1), words(1)]
+        want = ref.tables(table, rows, seq, new, free, 0, 16, cap)
+        return [dev(x) for x in (table, rows, seq, new, free, [0])], out, words(), torch.cuda.Stream(), want
+    sets, failed = [inputs(16384), inputs(7000)], []
+    torch.cuda.synchronize()
+
+    def calls(args, out, ws, stream, want):
+        try:
+            table, rows, seq, new, free, head = args
+            loc, pos, qo, head_out = out
+            for _ in range(400):
+                pkv.build_block_tables(table, rows, seq, new, free, head, head_out, loc, pos, qo, 16, ws, stream=stream)
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+    threads = [threading.Thread(target=calls, args=s) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for (table, *_), (loc, pos, qo, head), ws, _, want in sets:
+        assert error(pkv, ws) == 0
+        for g, w in zip((table, loc, pos, qo, head), want):
+            assert np.array_equal(host(g).reshape(-1), np.asarray(w).reshape(-1))
