@@ -251,13 +251,16 @@ __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p)
     pdl_trigger();
     const GatherUnit u = p.units[blockIdx.x];
     const int row = ld(p.req_pool_indices + u.src);
-    if (row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift)) {
-        if (threadIdx.x == 0) set_error(p.err, DERR_POSITION);
-        return;
-    }
+    // A unit whose row or positions are out of range is zero rows too: its neighbours' 128-key tiles may reach into
+    // it, and what the workspace held may be a NaN, which a weight of 0 does not undo.
+    const bool refused = row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift);
+    if (refused && threadIdx.x == 0) set_error(p.err, DERR_POSITION);
     if (threadIdx.x < u.len) {
-        const int32_t slot = table_slot(p.req_to_token + (int64_t)row * p.rt_stride, u.pos0 + threadIdx.x, p.page_shift, p.num_slots);
-        if (slot < 0) set_error(p.err, DERR_SLOT_RANGE);  // a zero row
+        int32_t slot = -1;
+        if (!refused) {
+            slot = table_slot(p.req_to_token + (int64_t)row * p.rt_stride, u.pos0 + threadIdx.x, p.page_shift, p.num_slots);
+            if (slot < 0) set_error(p.err, DERR_SLOT_RANGE);  // a zero row
+        }
         s_slot[threadIdx.x] = slot;
     }
     __syncthreads();

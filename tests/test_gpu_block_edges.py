@@ -88,3 +88,50 @@ def test_tables_of_different_batches_from_two_threads(pkv):
         assert error(pkv, ws) == 0
         for g, w in zip((table, loc, pos, qo, head), want):
             assert np.array_equal(host(g).reshape(-1), np.asarray(w).reshape(-1))
+
+
+# ----------------------------------------------------------------------------------------
+# gathered extend: what a refused request leaves in the workspace
+
+OLD_NAN = 0x7FC07FC0    # two bf16 NaN
+
+
+def bad_neighbours(rng, pages_a_row=40):
+    """(lengths, new tokens, their offsets, table, rows): requests of which several meet in a 128-key tile."""
+    lens, new = [30, 40, 300, 20], [10, 12, 40, 20]
+    return lens, new, np.concatenate([[0], np.cumsum(new)]), rng.permutation(5 * pages_a_row).reshape(5, pages_a_row), rng.permutation(5)[:4]
+
+
+@pytest.mark.parametrize("change", ["row", "negative row", "position"])
+@pytest.mark.parametrize("bad", [1, 3])
+def test_gathered_extend_beside_a_refused_request(pkv, change, bad):
+    """A request whose row or positions are out of range gets an error; the keys it would have gathered are
+    zeros and not what the workspace held, which a neighbour in the same tile would see as NaN."""
+    rng = np.random.default_rng(bad)
+    page, hkv, g, d = 16, 2, 4, 64
+    lens, new, qo, table, rows = bad_neighbours(rng)
+    pool, was = random_pool(pkv, rng, table.size, page, hkv, d)
+    rr, t = rows.copy(), table
+    if change == "position":
+        t = table[:, :2] if bad == 1 else table[:, :1]    # too short for request 1, and for 2; or for all but the last
+        lens = [30, 40, 28, 20] if bad == 1 else [10, 12, 16, 20]
+        new = [10, 12, 8, 20] if bad == 1 else [5, 6, 8, 20]
+        qo = np.concatenate([[0], np.cumsum(new)])
+    else:
+        rr[bad] = len(table) if change == "row" else -1
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d)
+    plan.info.offsets[18] = 0
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
+    o = torch.full_like(qt, float("nan"))
+    ws = words((plan.info.workspace_bytes + 3) // 4)
+    ws[64:] = OLD_NAN
+    pkv.attn_extend_block(pool, pkv.Batch(dev(t), dev(rr), dev(lens), page), qt, o, 0.1, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0x400
+    got = values(o)
+    assert np.isfinite(got).all()
+    for r in range(4):
+        if r == bad:
+            continue
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(lens[r] - new[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
+        assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
