@@ -179,18 +179,20 @@ PKV_DEV void gather_body(const GatherParams &p) {
     }
     const GatherUnit u = p.units[blockIdx.x];
     const int row = ld(p.req_pool_indices + u.src);
-    if (row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift)) {
-        if (threadIdx.x == 0) set_error(p.err, DERR_POSITION);
-        return;
-    }
+    // a unit whose row or positions are out of range is zero rows (see block_gather_kernel)
+    const bool refused = row < 0 || row >= p.rt_rows || u.pos0 < 0 || u.pos0 + u.len > (p.rt_stride << p.page_shift);
+    if (refused && threadIdx.x == 0) set_error(p.err, DERR_POSITION);
     // the unit's slots, checked once
     __shared__ int32_t s_slot[32];
     if (threadIdx.x < u.len) {
-        int32_t slot = table_slot(p.req_to_token + (int64_t)row * p.rt_stride, u.pos0 + threadIdx.x, p.page_shift,
-                                  p.num_slots);
-        if (slot < 0 || (int64_t)slot >= p.num_slots) {
-            set_error(p.err, DERR_SLOT_RANGE);
-            slot = -1;  // zero row
+        int32_t slot = -1;
+        if (!refused) {
+            slot = table_slot(p.req_to_token + (int64_t)row * p.rt_stride, u.pos0 + threadIdx.x, p.page_shift,
+                              p.num_slots);
+            if (slot < 0 || (int64_t)slot >= p.num_slots) {
+                set_error(p.err, DERR_SLOT_RANGE);
+                slot = -1;  // zero row
+            }
         }
         s_slot[threadIdx.x] = slot;
     }

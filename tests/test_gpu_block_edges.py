@@ -135,3 +135,37 @@ def test_gathered_extend_beside_a_refused_request(pkv, change, bad):
         k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
         want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, 0.1, np.arange(lens[r] - new[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
         assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [1, 16])
+def test_extend_of_a_plain_pool_beside_a_refused_request(pkv, fp8, page):
+    """The same over the pools without block scales."""
+    rng = np.random.default_rng(page)
+    hkv, g, d = 2, 4, 64
+    lens, new, qo, table, rows = bad_neighbours(rng, 320 if page == 1 else 40)
+    x = [rng.standard_normal((table.size * page, hkv, d)) for _ in range(2)]
+    t = [bf16(a)[0] for a in x]
+    if fp8:
+        t = [a.to(torch.float8_e4m3fn) for a in t]
+        pool = pkv.Pool(*(a.view(torch.uint8) for a in t), "fp8_e4m3")
+    else:
+        pool = pkv.Pool(*t)
+    kv = [values(a) for a in t]
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d)
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), hkv * g, d)))
+    o = torch.full_like(qt, float("nan"))
+    ws = words((plan.info.workspace_bytes + 3) // 4)
+    ws[64:] = OLD_NAN
+    rr = rows.copy()
+    rr[1] = len(table)
+    pkv.attn_extend(pool, pkv.Batch(dev(table), dev(rr), dev(lens), page), qt, o, 0.1, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0x400
+    got = values(o)
+    assert np.isfinite(got).all()
+    for r in (0, 2, 3):
+        at = np.arange(lens[r])
+        slots = table[rows[r]][at // page] * page + at % page
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], kv[0][slots], kv[1][slots], 0.1, np.arange(lens[r] - new[r], lens[r]),
+                                 EXTEND_EPS, EXTEND_LOG_EPS)
+        assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
