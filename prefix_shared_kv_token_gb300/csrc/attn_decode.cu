@@ -627,10 +627,9 @@ int launch_merge(const pkv_plan_info *info, const void *plan_dev, const float *r
     return e == cudaSuccess ? PKV_OK : PKV_E_CUDA;
 }
 
-int check_call(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o, const pkv_plan_info *info,
+// The arguments of a planned call beside its pool, which is valid.
+int check_args(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o, const pkv_plan_info *info,
                const void *plan_dev, void *workspace, size_t ws_bytes, int op) {
-    int rc = validate_pool(pool);
-    if (rc) return rc;
     if (!batch || !q || !o || !info || !plan_dev || !workspace) return PKV_E_INVALID;
     if (!batch->req_to_token || !batch->req_pool_indices || !batch->seq_lens) return PKV_E_INVALID;
     if (page_shift_of(batch) < 0) return PKV_E_INVALID;
@@ -641,6 +640,12 @@ int check_call(const pkv_pool *pool, const pkv_batch *batch, const void *q, void
         return PKV_E_INVALID;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o)) & 15) return PKV_E_INVALID;
     return PKV_OK;
+}
+
+int check_call(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o, const pkv_plan_info *info,
+               const void *plan_dev, void *workspace, size_t ws_bytes, int op) {
+    const int rc = validate_pool(pool);
+    return rc ? rc : check_args(pool, batch, q, o, info, plan_dev, workspace, ws_bytes, op);
 }
 
 }  // namespace pkv

@@ -1043,6 +1043,8 @@ static int launch_gather(const GatherParams &p, bool fp8, int nunits, cudaStream
                : PKV_E_CUDA;
 }
 
+int check_args(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o, const pkv_plan_info *info,
+               const void *plan_dev, void *workspace, size_t ws_bytes, int op);
 int check_call(const pkv_pool *pool, const pkv_batch *batch, const void *q, void *o, const pkv_plan_info *info,
                const void *plan_dev, void *workspace, size_t ws_bytes, int op);
 int launch_merge(const pkv_plan_info *info, const void *plan_dev, const float *rec_acc, const float *rec_ml,
@@ -1254,7 +1256,8 @@ static int extend_call(const pkv_pool *pool, const pkv_batch *batch, const void 
                        const void *k_new, const void *v_new, const int32_t *out_cache_loc, bool store,
                        const pkv_plan_info *info, const void *plan_dev, void *workspace, size_t ws_bytes,
                        void *stream, const pkv_block_pool *block = nullptr) {
-    int rc = check_call(pool, batch, q, o, info, plan_dev, workspace, ws_bytes, 2);
+    // (a block-scaled pool has had checks of its own: its arrays begin at any 16-byte address)
+    int rc = (block ? check_args : check_call)(pool, batch, q, o, info, plan_dev, workspace, ws_bytes, 2);
     if (rc) return rc;
     if (info->offsets[16] != (store ? 2 : 0)) return PKV_E_PLAN;
     if (store) {
@@ -1354,7 +1357,7 @@ extern "C" int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch
     rows.k_scale = rows.v_scale = 1.f;
     rows.slot_stride = pool->slot_stride;
     if (info && info->op == 2 && info->offsets[16] == 0 && info->offsets[18] != 0) {
-        const int err = check_call(&rows, batch, q, o, info, plan_dev, workspace, ws_bytes, 2);
+        const int err = check_args(&rows, batch, q, o, info, plan_dev, workspace, ws_bytes, 2);
         if (err) return err;
         if (batch->stride < 0 || batch->stride >= ((int64_t)1 << 31) || batch->num_rows < 0) return PKV_E_INVALID;
         if (info->total_q == 0) return PKV_OK;

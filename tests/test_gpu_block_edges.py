@@ -169,3 +169,47 @@ def test_extend_of_a_plain_pool_beside_a_refused_request(pkv, fp8, page):
         want, bound = ref.attend(qv[qo[r]:qo[r + 1]], kv[0][slots], kv[1][slots], 0.1, np.arange(lens[r] - new[r], lens[r]),
                                  EXTEND_EPS, EXTEND_LOG_EPS)
         assert np.all(np.abs(got[qo[r]:qo[r + 1]] - want) <= bound), r
+
+
+# ----------------------------------------------------------------------------------------
+# a pool's address
+
+
+@pytest.mark.parametrize("g,d,layer", [(4, 64, 1), (8, 64, 2), (1, 128, 1)])
+def test_a_layer_of_a_cache_of_many(pkv, g, d, layer):
+    """K and V are a layer's view of [slots, layers, 1, d]: rows 16-byte aligned, one behind the other at
+    the stride of all layers.  Store, decode and both ways of extend."""
+    rng = np.random.default_rng(d + g)
+    page, layers, pages = 16, 3, 40
+    was_pool, was = random_pool(pkv, rng, pages, page, 1, d)
+    k, v = (torch.full((pages * page, layers, 1, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+    k[:, layer], v[:, layer] = was_pool.k, was_pool.v
+    pool = pkv.BlockPool(k[:, layer], v[:, layer], was_pool.k_exp, was_pool.v_exp, page)
+    assert d == 128 or layer % 2 == 0 or pool.k.data_ptr() % 128 == 64
+    lens, new = [200, 33, 300], [5, 33, 2]
+    table, rows, batch = paged_batch(pkv, rng, lens, page, pages)
+    loc = np.concatenate([[int(table[rows[r], t // page]) * page + t % page for t in range(n - e, n)]
+                          for r, (n, e) in enumerate(zip(lens, new))])
+    x = [rng.standard_normal((len(loc), 1, d)) for _ in range(2)]
+    ws = words()
+    check_store(pkv, pool, was, *x, loc, page, ws)
+    assert error(pkv, ws) == 0
+    o, ws = check_decode(pkv, pool, was, table, rows, lens, page, g, d ** -0.5)
+    assert error(pkv, ws) == 0
+    qo = np.concatenate([[0], np.cumsum(new)])
+    qt, qv = bf16(rng.standard_normal((int(qo[-1]), g, d)))
+    for streams in (0, 1):
+        plan = pkv.plan_extend(lens, new, qo, g, 1, d)
+        plan.info.offsets[18] = streams
+        o, ws = torch.full_like(qt, float("nan")), words((plan.info.workspace_bytes + 3) // 4)
+        pkv.attn_extend_block(pool, batch, qt, o, 0.1, plan, dev(plan.blob, np.uint8), ws)
+        assert error(pkv, ws) == 0
+        for r in range(3):
+            kk, vv = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+            e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+            at = np.arange(lens[r] - new[r], lens[r])
+            want, bound = ref.attend(qv[qo[r]:qo[r + 1]], kk, vv, 0.1, at, *((DECODE_EPS, 0.0, e) if streams else
+                                                                             (EXTEND_EPS, EXTEND_LOG_EPS)))
+            assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound), (streams, r)
+    for t in (k, v):    # the other layers are as they were
+        assert torch.all(t[:, [i for i in range(layers) if i != layer]] == 0x7F)

@@ -174,3 +174,19 @@ def test_block_pool_struct_matches_the_header(tmp_path):
                    check=True)
     got = subprocess.run([str(tmp_path / "layout")], check=True, capture_output=True, text=True).stdout.split()
     assert [int(x) for x in got] == [C.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+
+
+@pytest.mark.parametrize("offset", [16, 64, 112])
+def test_a_pool_at_any_16_byte_address_is_taken_by_every_call(offset):
+    """Each call gets past the pool to the refusal of what comes after it."""
+    p, b = pool(k=P + offset, v=P + offset, num_kv_heads=8), batch(batch=1)
+    assert lib.pkv_kv_store_block(C.byref(p), P + 2, P, P, 4, None, None) == INVALID
+    assert lib.pkv_kv_store_block(C.byref(p), None, None, None, 0, None, None) == 0
+    need = C.c_size_t(0)
+    assert lib.pkv_decode_block_workspace(C.byref(p), 32, C.byref(need)) == 0
+    assert lib.pkv_attn_decode_block(C.byref(p), C.byref(b), P, P, 32, 0.1, P, need.value - 1, None) == WORKSPACE
+    for tokens, seq in ((8, 40), (1, 9000)):      # gathered, streams
+        plan = pkv.plan_extend([seq], [tokens], [0, tokens], 32, 8, 128)
+        assert plan.info.offsets[18] == (tokens == 1)
+        assert lib.pkv_attn_extend_block(C.byref(p), C.byref(b), P, P, 0.1, C.byref(plan.info), P, P,
+                                         plan.info.workspace_bytes - 1, None) == WORKSPACE
