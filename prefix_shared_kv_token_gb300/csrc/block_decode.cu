@@ -7,8 +7,11 @@
 // With s_j the logits in log2 units, R = max_j (s_j + ev_j) and w_j = 2^(s_j + ev_j - R), the sum
 // is  sum w_j code_j / sum 2^(s_j - R):  V's exponents move into the weights, so the codes enter
 // the product as they are, and a weight is at most 1 however far the pages' exponents differ.  The
-// sum below is kept as l = sum 2^(s_j - R + ea), ea = ev of the key that set R, so that it too is of
-// size 1 whatever the pages' exponents; the result is acc / l * 2^ea.
+// sum below is kept as l = sum 2^(s_j - R + ea), ea = ev of the key that set R, and the result is
+// acc / l * 2^ea: that key counts 1 in l whatever its page's exponent.  A key of a far smaller ev may stand far
+// above it in s_j alone and pass fp32's range in l (ev 127 or more below, s_j as much above).  Where l
+// passes 2^100 the piece is attended once more with l's own reference R - ea moved up with max s_j; the
+// joining kernel always takes the largest of its records' R - ea.
 //
 // Design.  The work is a stream of codes, so what counts is bytes in flight:
 //   * 16-key tiles of all requests, laid end to end, are cut into equal contiguous ranges (each CTA
@@ -48,6 +51,7 @@ constexpr float kSlack = 8.f;     // largest by 2^8: they stay below 2^15 in f16
 constexpr float kNoKey = -3.402823466e38f;  // the reference of a column that has seen no key: the least finite,
                                             // so that a logit of -inf less it is -inf
 constexpr float kUnbias = 1.f / (1 << 6);
+constexpr float kFarSum = 1.2676506e30f;  // 2^100: see careful
 constexpr float kLog2eB = 1.4426950408889634f;
 
 struct BlockDecodeParams {
@@ -240,7 +244,7 @@ struct DecodeState {
 };
 
 // The result of a row from its sums.
-PKV_DEV float row_scale(float l, float ea) { return l == 0.f ? 0.f : kUnbias / l * exp_value((int)ea + 127); }
+PKV_DEV float row_scale(float l, float ea) { return l == 0.f ? 0.f : kUnbias / l * ex2(ea); }
 
 // Logits of a tile's 16 keys: this lane's MMA rows g and g + 8 of columns 2c and 2c + 1.  The rows
 // g + 8 are 8 D bytes behind the rows g, under the same swizzle.
@@ -297,10 +301,11 @@ PKV_DEV void read_v(uint32_t (&v)[4][D / 32], const uint8_t *at, int off, bool r
 // `only`-th sees the tile (-1: all do); ragged: the i-th sees of it the keys before sees + i step.
 // (A logit that is not seen may be NaN: it is replaced.)
 // The reference moves, and the state is rescaled, only when a key is more than 2^8 above it: then
-// the lanes agree on the column's maximum.
+// the lanes agree on the column's maximum.  careful: with every tile, and l's reference moves to the largest s
+// too (a key's s is at most R - ea).
 template <int D, int G>
 PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2], int ek, int ev_byte,
-                          int only, bool ragged, int sees, int step, uint32_t &b0, uint32_t &b1) {
+                          int only, bool ragged, int sees, int step, bool careful, uint32_t &b0, uint32_t &b1) {
     const float kf = exp_value(ek);
     // (a whole number below 2^23 as a float: its bits under those of 2^23)
     const float ev = __uint_as_float(0x4B000000u | (uint32_t)ev_byte) - (8388608.f + 127.f);
@@ -318,7 +323,7 @@ PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2
         for (int e = 0; e < 4; ++e)
             if (row + 8 * (e >> 1) >= sees + (col + (e & 1)) / G * step) t[e] = -INFINITY;
     }
-    if (__any_sync(0xffffffffu, fmaxf(t[0], t[2]) > st.m[0] + kSlack || fmaxf(t[1], t[3]) > st.m[1] + kSlack)) {
+    if (careful || __any_sync(0xffffffffu, fmaxf(t[0], t[2]) > st.m[0] + kSlack || fmaxf(t[1], t[3]) > st.m[1] + kSlack)) {
         float al[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -326,11 +331,12 @@ PKV_DEV void tile_weights(DecodeState<D> &st, float (&t)[4], const float (&cs)[2
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
             al[h] = 1.f;
-            if (y > st.m[h]) {
-                al[h] = ex2(st.m[h] - y);
-                st.l[h] *= ex2(st.m[h] - y + (ev - st.ea[h]));
-                st.m[h] = y;
-                st.ea[h] = ev;
+            if (y > st.m[h] || careful) {
+                const float top = fmaxf(y, st.m[h]), ea = careful ? fminf(st.ea[h] + (top - st.m[h]), ev + (top - y)) : ev;
+                al[h] = ex2(st.m[h] - top);
+                st.l[h] *= ex2(st.m[h] - top + (ea - st.ea[h]));
+                st.m[h] = top;
+                st.ea[h] = ea;
             }
         }
 #pragma unroll
@@ -719,7 +725,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     uint32_t sg = 0, phase = 0;
     int32_t at = begin, piece = begin;  // the tile to attend next; the first tile of its piece
-    bool careful = false;               // NaN were met: see poisoned
+    // A piece is attended once more where a NaN was met (see poisoned; then columns are kept apart segment by
+    // segment, which costs 8 % where it is not needed) or l passed 2^100 (its reference then moves with every tile).
+    bool careful = false;
 again:
     // from the piece's first tile, with nothing asked for
     at = ask_at = ask_b = piece;
@@ -801,7 +809,7 @@ again:
             }
             uint32_t b0, b1;
             tile_weights<D, G>(st, w, cs, e & 0xFF, e >> 8, M > 1 ? only : -1, ragged, all_see - j * kTile, M > 1 && p.indptr ? 1 : 0,
-                               b0, b1);
+                               careful, b0, b1);
             // where tokens see different keys of the tile, one token at a time, from the one that sees
             // most: V's rows past each one's last key become zeros
             int t = M > 1 && ragged && p.indptr ? M - 1 : -1;
@@ -829,8 +837,11 @@ again:
         }
         const Walk<G> w = curs[warp];
         if (at == end || at == w.from + w.all) {
-            // a NaN of one request reached another's columns: once more, keeping them apart segment
-            // by segment (which costs 8 % where it is not needed)
+            bool far = false;  // (a column without a query row may see what nobody does)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                far |= (p.indptr ? w.s * M : 0) + (2 * c + h) / G < w.ext && !(st.l[h] <= kFarSum);
+            nan = nan || (!careful && __any_sync(0xffffffffu, far));
             if (nan) break;
             // this lane's columns: a result where the range holds every tile that they see, a record
             // where it holds some
@@ -874,7 +885,8 @@ struct Records {
     int32_t i0, n1, j0, n, stream;
 };
 
-// One query head's records into its row; `on`: there are any for this warp's head.
+// One query head's records into its row; `on`: there are any for this warp's head.  E is R - (l's reference):
+// the least of ea_k + (R - R_k), so that no record's l counts more than once in L.
 template <int D, int W, int S, bool kTwo, class Where>
 PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, const Where &from, int hl, int col,
                          float (&s_acc)[W][D], float4 (&s_ml)[W]) {
@@ -882,7 +894,7 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % S;
     // the records one after the other (kTwo), or the ranges themselves
     const int32_t i0 = kTwo ? 0 : from.i0, past = on ? i0 + from.n : i0;
-    float top = -INFINITY, L = 0.f, E = 0.f, O[V];
+    float top = -INFINITY, L = 0.f, E = INFINITY, O[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) O[v] = 0.f;
     for (int32_t i = i0 + sub; i < past; i += S * kBatch) {
@@ -912,12 +924,11 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, cons
         // the batch's reference first, so that its terms add independently
         const float was = top, was_e = E;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (ml[b].x > top) {
-                top = ml[b].x;
-                E = ml[b].z;
-            }
+        for (int b = 0; b < kBatch; ++b) top = fmaxf(top, ml[b].x);
         if (top == -INFINITY) continue;
+        E += top - was;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) E = fminf(E, ml[b].z + (top - ml[b].x));
         const float f = ex2(was - top);
         L *= ex2(was - top + (E - was_e));
 #pragma unroll
@@ -943,7 +954,9 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, cons
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float m = top == -INFINITY ? 0.f : top;
-        E = __shfl_sync(0xffffffffu, x.z, __ffs(__ballot_sync(0xffffffffu, x.x == top)) - 1);
+        E = x.z + (m - x.x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) E = fminf(E, __shfl_xor_sync(0xffffffffu, E, d));
         const float f = ex2(x.x - m);
         L = x.x == -INFINITY ? 0.f : x.y * ex2(x.x - m + (E - x.z));
 #pragma unroll

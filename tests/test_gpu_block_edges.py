@@ -213,3 +213,80 @@ def test_a_layer_of_a_cache_of_many(pkv, g, d, layer):
             assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound), (streams, r)
     for t in (k, v):    # the other layers are as they were
         assert torch.all(t[:, [i for i in range(layers) if i != layer]] == 0x7F)
+
+
+# ----------------------------------------------------------------------------------------
+# exponents and logits at their ends
+
+
+def steep_keys(pool, was, rng, page, top):
+    """K rows whose logits (for queries of whole numbers over d) are up to `top` apart in log2 units, page
+    by page; V pages at the ends of the exponents and between."""
+    pages, hkv = was[1].shape
+    level = rng.choice([0.0, 0.03125, 0.25, 0.75, 1.0], (pages * page, hkv, 1)) * np.where(rng.random((pages * page, hkv, 1)) < 0.2, 1, 0)
+    codes = np.broadcast_to(ref.e4m3_encode(level), was[0].shape).astype(np.uint8).copy()
+    was[0][:], was[1][:] = codes, 127
+    was[3][:] = rng.choice([10, 60, 127, 190, 245], (pages, hkv))
+    for t, w in zip((pool.k, pool.k_exp, pool.v_exp), (was[0], was[1], was[3])):
+        t.copy_(dev(w, np.uint8))
+    return top * np.log(2.0)
+
+
+@pytest.mark.parametrize("g,hkv,d", [(1, 3, 64), (2, 8, 128), (4, 2, 64), (8, 1, 128), (8, 4, 64)])
+@pytest.mark.parametrize("top", [100, 300, 1000])
+@pytest.mark.parametrize("lens", [[900, 33, 5000, 16, 1, 130, 2600, 64], [30000], [40] * 9])
+def test_decode_sums_of_steep_logits_over_far_exponents(pkv, g, hkv, d, top, lens):
+    """A key far above the others in logit may lie far below them in s + e (V's exponent 235 lower): the
+    sum of the weights without V's exponents then passes fp32's range over the reference of the others."""
+    rng = np.random.default_rng(top + d + len(lens))
+    page = 16
+    pages = sum(-(-n // page) for n in lens) + 64
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    scale = steep_keys(pool, was, rng, page, top)
+    table, rows, _ = paged_batch(pkv, rng, lens, page, pages, 2 if len(lens) == 8 else 0)
+    q = np.broadcast_to(rng.choice([1.0, 0.5, -1.0], (len(lens), hkv * g, 1)), (len(lens), hkv * g, d)) / d
+    o, ws = check_decode(pkv, pool, was, table, rows, lens, page, hkv * g, scale, q=q)
+    assert error(pkv, ws) == 0
+
+
+@pytest.mark.parametrize("first", ["near", "far"])
+@pytest.mark.parametrize("gap", [119, 126, 127, 128, 140, 200, 235])
+def test_decode_of_two_pages_far_apart(pkv, first, gap):
+    """One page whose V exponent is `gap` binades above the other's; the other's keys are `gap` - 1 above it in
+    logits, so that both reach the result, or far more, so that only they do."""
+    page, hkv, g, d = 16, 1, 8, 64
+    rng = np.random.default_rng(gap)
+    pool, was = random_pool(pkv, rng, 4, page, hkv, d)
+    lo, hi = (245 - gap, 245) if gap > 200 else (127 - gap // 2, 127 - gap // 2 + gap)
+    order = [0, 1] if first == "near" else [1, 0]
+    was[0][:page], was[0][page:2 * page] = 0, 0x38          # logits 0 and q * 64 scale
+    was[1][:], was[3][0], was[3][1] = 127, hi, lo
+    for t, w in zip((pool.k, pool.k_exp, pool.v_exp), (was[0], was[1], was[3])):
+        t.copy_(dev(w, np.uint8))
+    table = np.array([order + [0, 0]])
+    q = np.broadcast_to(np.array([1.0, 0.5, 2.0, 4.0, 0.25, -1.0, 1.5, 0.75])[None, :, None], (1, 8, d)) / d
+    o, ws = check_decode(pkv, pool, was, table, [0], [2 * page], page, 8, (gap - 1) * np.log(2.0), q=q)
+    assert error(pkv, ws) == 0
+
+
+@pytest.mark.parametrize("hkv,g,d", [(2, 4, 64), (1, 8, 128), (8, 1, 64)])
+def test_extend_streams_of_steep_logits_over_far_exponents(pkv, hkv, g, d):
+    rng = np.random.default_rng(d + g)
+    page, lens, new = 16, [700, 20, 3000, 5], [5, 20, 3, 1]
+    pages = sum(-(-n // page) for n in lens) + 1
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    scale = steep_keys(pool, was, rng, page, 300)
+    table, rows, batch = paged_batch(pkv, rng, lens, page, pages)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d)
+    plan.info.offsets[18] = 1
+    n = int(qo[-1])
+    qt, qv = bf16(np.broadcast_to(rng.choice([1.0, 0.5, -1.0], (n, hkv * g, 1)), (n, hkv * g, d)) / d)
+    o, ws = torch.full_like(qt, float("nan")), words((plan.info.workspace_bytes + 3) // 4)
+    pkv.attn_extend_block(pool, batch, qt, o, scale, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0
+    for r in range(len(lens)):
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, np.arange(lens[r] - new[r], lens[r]), DECODE_EPS, v_exp=e)
+        assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound), r
