@@ -243,8 +243,10 @@ struct DecodeState {
     float m[2], l[2], ea[2];
 };
 
-// The result of a row from its sums.
-PKV_DEV float row_scale(float l, float ea) { return l == 0.f ? 0.f : kUnbias / l * ex2(ea); }
+// The result of a row from its sums: acc times the first factor, then times the second.  (Their product may
+// lie below fp32's normal numbers where the result does not: 2^-117 over the weights of a million keys.)
+PKV_DEV float2 row_scale(float l, float ea) { return make_float2(l == 0.f ? 0.f : kUnbias / l, l == 0.f ? 0.f : ex2(ea)); }
+PKV_DEV uint32_t pack_result(float a, float b, float2 f) { return pack_bf16x2(a * f.x * f.y, b * f.x * f.y); }
 
 // Logits of a tile's 16 keys: this lane's MMA rows g and g + 8 of columns 2c and 2c + 1.  The rows
 // g + 8 are 8 D bytes behind the rows g, under the same swizzle.
@@ -417,14 +419,14 @@ PKV_DEV void write_piece(const BlockDecodeParams &p, DecodeState<D> &st, int kv_
         const int col = 2 * c + h;
         if (row[h] < 0) continue;
         if (rec[h] < 0) {
-            const float inv = row_scale(st.l[h], st.ea[h]);
+            const float2 f = row_scale(st.l[h], st.ea[h]);
             uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((int64_t)row[h] * p.hkv * G + kv_head * G + col % G) * D + g * (D / 8));
 #pragma unroll
             for (int i = 0; i < D / 16; i += 4)
-                dst[i / 4] = make_uint4(pack_bf16x2(st.acc[i][h] * inv, st.acc[i][2 + h] * inv),
-                                        pack_bf16x2(st.acc[i + 1][h] * inv, st.acc[i + 1][2 + h] * inv),
-                                        pack_bf16x2(st.acc[i + 2][h] * inv, st.acc[i + 2][2 + h] * inv),
-                                        pack_bf16x2(st.acc[i + 3][h] * inv, st.acc[i + 3][2 + h] * inv));
+                dst[i / 4] = make_uint4(pack_result(st.acc[i][h], st.acc[i][2 + h], f),
+                                        pack_result(st.acc[i + 1][h], st.acc[i + 1][2 + h], f),
+                                        pack_result(st.acc[i + 2][h], st.acc[i + 2][2 + h], f),
+                                        pack_result(st.acc[i + 3][h], st.acc[i + 3][2 + h], f));
         } else {
             const int64_t at = ((int64_t)rec[h] * p.hg + hl) * 8 + col;
             // piece i / 2 of lane g's run of d next to its neighbours' (see merge_head)
@@ -971,12 +973,12 @@ PKV_DEV void merge_head(const BlockDecodeParams &p, uint16_t *out, bool on, cons
         }
     }
     if (!on) return;
-    const float inv = row_scale(L, E);
+    const float2 f = row_scale(L, E);
     // a record's 16-byte piece 8 i + g is d = (D / 8) g + 4 i + {0 .. 3}
     const int piece = lane * V / 4, d = D / 8 * (piece % 8) + 4 * (piece / 8) + lane * V % 4;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
-        reinterpret_cast<uint32_t *>(out + d)[v / 2] = pack_bf16x2(O[v] * inv, O[v + 1] * inv);
+        reinterpret_cast<uint32_t *>(out + d)[v / 2] = pack_result(O[v], O[v + 1], f);
 }
 
 // Joins the records of the streams that cross ranges and clears the rows of empty requests.  A CTA

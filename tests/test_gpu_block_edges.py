@@ -290,3 +290,27 @@ def test_extend_streams_of_steep_logits_over_far_exponents(pkv, hkv, g, d):
         e = ref.exponents_of(was[3], table[rows[r]], lens[r], page)
         want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, np.arange(lens[r] - new[r], lens[r]), DECODE_EPS, v_exp=e)
         assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound), r
+
+
+@pytest.mark.parametrize("g,hkv", [(8, 1), (2, 2)])
+@pytest.mark.parametrize("length,listed", [(1109248, 70000), (100016, 16 * 6251)])
+def test_decode_of_the_smallest_values_over_long_contexts(pkv, g, hkv, length, listed):
+    """Equal weights over one page named many times, a power of two in each column of V: every sum is a whole
+    number of that power, below 2^24, so that the result is the value itself, at the smallest exponent too.  Only the
+    output's rounding and five fp32 roundings are left: the weights' sum, its reciprocal (2 ulp), two factors."""
+    page, d = 16, 64
+    pool = pkv.BlockPool.allocate(2, page, hkv, d)
+    codes = np.broadcast_to(0x50 + 8 * (np.arange(d) % 6), (page, hkv, d)).astype(np.uint8)     # 8 to 256
+    pool.v[page:] = dev(codes, np.uint8)
+    pool.v_exp.fill_(10)
+    blocks = -(-length // page)
+    table = torch.ones((1, blocks), dtype=torch.int32, device="cuda")
+    q, _ = bf16(np.ones((1, hkv * g, d)))
+    o = torch.full_like(q, float("nan"))
+    ws = words(pkv.decode_block_workspace(pool, hkv * g) // 4)
+    for n in (length, length - 5, listed):
+        pkv.attn_decode_block(pool, pkv.Batch(table, dev([0]), dev([n]), page), q, o, 0.1, ws)
+        assert error(pkv, ws) == 0
+        want = ref.e4m3_decode(codes[:1]) * 2.0 ** -117
+        got = values(o).reshape(1, hkv, g, d)
+        assert np.all(np.abs(got - want[:, :, None]) <= (2.0 ** -8 + 5 * 2.0 ** -24) * want[:, :, None])
