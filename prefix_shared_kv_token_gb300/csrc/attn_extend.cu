@@ -146,7 +146,7 @@ struct GatherParams {
     const uint8_t *k_exp;
     const uint8_t *v_exp;
     int32_t block_shift;
-    uint32_t *nans;  // of the workspace header: kNanMark where a gathered V row holds a NaN, then a count
+    uint32_t *nans;  // of the workspace header: kNanMark where a gathered V row asks for block_mend_kernel, then a count
     int32_t *err;
     int32_t pdl_wait_start;  // 1: wait for the preceding kernel first; 0: it wrote nothing this
                              // gather reads, wait for it only before exiting
@@ -241,9 +241,12 @@ PKV_DEV void gather_body(const GatherParams &p) {
 
 // The same copy out of a block-scaled pool: codes become the bf16 values they stand for, exactly
 // (a code times a power of two is a bf16 value).  A thread turns 16 codes, half a head's row or a
-// quarter, into 32 bytes, four such loads and their exponents in flight.  NaN codes of V are looked
-// for on the way (see block_mend_kernel).
+// quarter, into 32 bytes, four such loads and their exponents in flight.  NaN codes of V, and values so large that
+// a sum of them may pass fp32's range, are looked for on the way (see block_mend_kernel).
 constexpr uint32_t kNanMark = 0x4E614E21u;
+// Exponent bytes of V up to this one are safe to sum: codes below 2^9 under it times weights of up to 2^8 (the extend
+// kernel's reference lags by as much) stay below 2^128 for 2^31 keys.
+constexpr uint32_t kExpSafe = 127 + 80;
 constexpr int kNanWord = 20;  // of the workspace header
 
 template <int D>
@@ -303,6 +306,7 @@ __global__ void __launch_bounds__(256) block_gather_kernel(const GatherParams p)
                 // (a byte of 0x7F and one more has its top bit set, no other has)
                 if (v) nans |= (w[q] & 0x7F7F7F7Fu) + 0x01010101u;
             }
+            if (v && f[k] > kExpSafe) nans = 0x80808080u;
             uint4 *out = reinterpret_cast<uint4 *>((v ? p.v_out : p.k_out) + (int64_t)(u.key0 + key) * p.hkv * D) + 2 * piece;
             out[0] = make_uint4(y[0], y[1], y[2], y[3]);
             out[1] = make_uint4(y[4], y[5], y[6], y[7]);
@@ -332,10 +336,14 @@ struct MendParams {
 
 // The attention kernel gives keys that a row does not see a weight of 0, which a NaN in such a key's V
 // row turns into a NaN: a later token's, or, where the gathered rows of two requests meet in a 128-key
-// tile, another request's.  When the gather met a NaN (only then), the rows that came out with one
-// are computed again, over the keys that they see and no others.  A warp a row and head; a lane a key
-// for the logits, D / 32 elements of the row for the sums, all in fp32 straight from the codes.  What
-// bounds it does not matter where it works; where it does not, the launch does not show in a call of 440 us.
+// tile, another request's.  And it divides by the weights' sum at the end, before which a sum of V values
+// near bf16's largest may pass fp32's range.  When the gather met such a value (only then), the rows that came
+// out with a NaN or an infinity are computed again, over the keys that they see and no others.  A warp a row and
+// head; a lane a key for the logits, D / 32 elements of the row for the running mean (it is divided as it
+// goes, so it never passes the largest value), all in fp32 straight from the codes.  A lane a key is slow, 0.44 ns
+// a key and row with the whole GPU: 64 prompts of 200 tokens behind 1,792 shared keys take 443 us, 1.39 ms with a
+// NaN in a last token (4 rows see it) and 46 ms with one in the prefix (51,652 rows).  Where there is none the launch does
+// not show.
 template <int D>
 __global__ void __launch_bounds__(256) block_mend_kernel(const MendParams p) {
     __shared__ float s_q[8][D];
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(256) block_mend_kernel(const MendParams p) {
         uint32_t *out = reinterpret_cast<uint32_t *>(p.o + u * D) + lane * (V / 2);
         bool nan = false;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) nan |= (out[i] & 0x7FFFu) > 0x7F80u || ((out[i] >> 16) & 0x7FFFu) > 0x7F80u;
+        for (int i = 0; i < V / 2; ++i) nan |= (out[i] & 0x7FFFu) >= 0x7F80u || ((out[i] >> 16) & 0x7FFFu) >= 0x7F80u;
         if (!__any_sync(0xffffffffu, nan)) continue;
         const int32_t t = (int32_t)(u / p.hq), h = (int32_t)(u - (int64_t)t * p.hq), kv = h / (p.hq / p.hkv);
         int lo = 0, hi = p.batch;  // the last request that begins at or before row t
@@ -403,11 +411,16 @@ __global__ void __launch_bounds__(256) block_mend_kernel(const MendParams p) {
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             top = fmaxf(top, m);
-            const float ref = top == -INFINITY ? 0.f : top, f = ex2(m - ref), w = lane < n ? ex2(s - ref) : 0.f;
-            m = top;
-            l = l * f + w;
+            const float ref = top == -INFINITY ? 0.f : top;
+            float w = lane < n ? ex2(s - ref) : 0.f, sum = w;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] *= f;
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const float had = l * ex2(m - ref), all = had + sum, inv = all == 0.f ? 0.f : 1.f / all;
+            m = top;
+            l = all;
+            w *= inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] *= had * inv;
             for (int j = 0; j < n; ++j) {
                 const float wj = __shfl_sync(0xffffffffu, w, j), ej = __shfl_sync(0xffffffffu, ev, j);
                 const int32_t at = __shfl_sync(0xffffffffu, slot, j);
@@ -426,10 +439,7 @@ __global__ void __launch_bounds__(256) block_mend_kernel(const MendParams p) {
             }
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) out[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+        for (int i = 0; i < V / 2; ++i) out[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
     }
     // the last CTA to get here, when all have read the mark, takes it away
     __syncthreads();

@@ -314,3 +314,40 @@ def test_decode_of_the_smallest_values_over_long_contexts(pkv, g, hkv, length, l
         want = ref.e4m3_decode(codes[:1]) * 2.0 ** -117
         got = values(o).reshape(1, hkv, g, d)
         assert np.all(np.abs(got - want[:, :, None]) <= (2.0 ** -8 + 5 * 2.0 ** -24) * want[:, :, None])
+
+
+@pytest.mark.parametrize("choice", [[10], [245], [10, 127, 245], [205, 215, 225]])
+@pytest.mark.parametrize("hkv,g,d,shared", [(2, 4, 64, 0), (1, 8, 128, 128), (8, 1, 128, 0)])
+def test_gathered_extend_at_the_ends_of_the_exponents(pkv, choice, hkv, g, d, shared):
+    """V pages at the smallest exponent, the largest and both.  Values of one sign, so that a sum of the largest
+    ones passes fp32's range where their mean does not; none so small that a product with its weight
+    (2^-12 or more) would be below fp32's normal numbers."""
+    rng = np.random.default_rng(len(choice) + d)
+    page, old, new = 16, [0, 900, 130, 300], [60, 30, 200, 3]
+    lens = [a + b for a, b in zip(old, new)]
+    if shared:
+        old[0], lens[0] = 200, 260
+    pages = sum(-(-n // page) for n in lens) + 1
+    pool, was = random_pool(pkv, rng, pages, page, hkv, d)
+    was[2][:] = rng.integers(0x50, 0x7F, was[2].shape)    # 8 to 448
+    was[3][:] = rng.choice(choice, was[3].shape)
+    pool.v.copy_(dev(was[2], np.uint8))
+    pool.v_exp.copy_(dev(was[3], np.uint8))
+    table, rows, batch = paged_batch(pkv, rng, lens, page, pages, shared // page)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    cascade = None
+    if shared:
+        cascade = pkv.Cascade(*(np.asarray(a, np.int32) for a in ([0], [0], [shared], [0, 4], range(4))))
+    plan = pkv.plan_extend(lens, new, qo, hkv * g, hkv, d, cascade)
+    plan.info.offsets[18] = 0
+    x = rng.standard_normal((int(qo[-1]), hkv * g, d))
+    qt, qv = bf16(x)
+    scale = 0.01
+    o, ws = torch.full_like(qt, float("nan")), words((plan.info.workspace_bytes + 3) // 4)
+    for _ in range(2):
+        pkv.attn_extend_block(pool, batch, qt, o, scale, plan, dev(plan.blob, np.uint8), ws)
+    assert error(pkv, ws) == 0 and int(ws[20]) == 0
+    for r in range(len(lens)):
+        k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
+        want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, np.arange(lens[r] - new[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
+        assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound), r
