@@ -351,3 +351,72 @@ def test_gathered_extend_at_the_ends_of_the_exponents(pkv, choice, hkv, g, d, sh
         k, v = (ref.rows_of(was[j], was[j + 1], table[rows[r]], lens[r], page) for j in (0, 2))
         want, bound = ref.attend(qv[qo[r]:qo[r + 1]], k, v, scale, np.arange(lens[r] - new[r], lens[r]), EXTEND_EPS, EXTEND_LOG_EPS)
         assert np.all(np.abs(values(o[qo[r]:qo[r + 1]]) - want) <= bound), r
+
+
+# ----------------------------------------------------------------------------------------
+# large batches of few-head groups
+
+
+@pytest.mark.parametrize("b,g,hkv,stride", [(4097, 1, 2, 4), (5000, 1, 1, 70), (2049, 2, 3, 70), (9000, 2, 1, 4)])
+def test_decode_of_many_requests_of_own_tiles(pkv, b, g, hkv, stride):
+    """With 4 or 8 requests a stream results and records go by a request's own tiles; past 512 streams the
+    tiles before each are written down.  Both at once, with and without shared pages (rows long enough to
+    be looked through), lengths that cross ranges, and empty requests."""
+    rng = np.random.default_rng(b)
+    page, d, n = 16, 64, 100
+    pool, was = random_pool(pkv, rng, stride * n, page, hkv, d)
+    table, rows = rng.permutation(stride * n).reshape(n, stride), np.repeat(rng.integers(0, n, b), 3)[:b]
+    if stride > 4:
+        table[50:, :40] = table[0, :40]     # a prefix of half of the rows
+    lens = rng.integers(0, stride * page + 1, b)
+    lens[rng.random(b) < 0.1] = 0
+    lens[-1] = stride * page
+    q = np.zeros((b, hkv * g, d), np.float32)
+    q[:] = rng.standard_normal((1, hkv * g, d))
+    only = [0, 1, b // 2, b - 1, *rng.permutation(b)[:16]]
+    o, ws = check_decode(pkv, pool, was, table, rows, lens.tolist(), page, hkv * g, 0.1, q=q, only=only)
+    assert error(pkv, ws) == 0 and torch.isfinite(o).all()
+    assert torch.equal((o == 0).all(2).all(1).cpu(), torch.from_numpy(lens == 0))
+
+
+@pytest.mark.parametrize("g", [1, 4, 8])
+def test_a_captured_step_holds_decodes_own_bound(pkv, g):
+    """Tables, store and decode in one graph, replayed as lengths grow, with attention held to decode's bound."""
+    rng = np.random.default_rng(g)
+    page, hkv, d, b, scale = 16, 2, 64, 9, 0.125
+    hq = hkv * g
+    pool = pkv.BlockPool.allocate(80, page, hkv, d)
+    free, head, table = dev(rng.permutation(80)), words(1), torch.full((b, 6), -1, dtype=torch.int32, device="cuda")
+    rows, seq, new = dev(rng.permutation(b)), words(b), words(b)
+    most = 30
+    loc, pos, qo = words(b * most), words(b * most), words(b + 1)
+    k, v = (torch.zeros((b * most, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, o = (torch.zeros((b, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws, space = words(), words(pkv.decode_block_workspace(pool, hq) // 4)
+
+    def step():
+        pkv.build_block_tables(table, rows, seq, new, free, head, head, loc, pos, qo, page, ws)
+        pkv.kv_store_block(pool, k, v, loc, ws)
+        pkv.attn_decode_block(pool, pkv.Batch(table, rows, seq, page), q, o, scale, space)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    lens = np.zeros(b, np.int64)
+    for i in range(4):
+        add = rng.integers(0, most + 1, b) if i == 0 else rng.integers(0, 2, b)
+        lens += add
+        for t, a in zip((seq, new), (lens, add)):
+            t.copy_(dev(a))
+        for t in (k, v):
+            t.copy_(bf16(rng.standard_normal(t.shape) * 2.0 ** rng.integers(-2, 3, (b * most, hkv, 1)))[0])
+        qt, qv = bf16(rng.standard_normal((b, hq, d)))
+        q.copy_(qt)
+        graph.replay()
+        assert error(pkv, ws) == 0 and error(pkv, space) == 0
+        codes, t = [host(x) for x in (pool.k, pool.k_exp, pool.v, pool.v_exp)], host(table)[host(rows)]
+        for r in range(b):
+            kk, vv = (ref.rows_of(codes[j], codes[j + 1], t[r], lens[r], page) for j in (0, 2))
+            e = ref.exponents_of(codes[3], t[r], lens[r], page)
+            want, bound = ref.attend(qv[r:r + 1], kk, vv, scale, [lens[r] - 1], DECODE_EPS, v_exp=e)
+            assert np.all(np.abs(values(o[r:r + 1]) - want) <= bound), (i, r)
