@@ -422,9 +422,12 @@ def kv_store_block(pool: BlockPool, k_new, v_new, out_cache_loc, workspace=None,
     loc = _fits("out_cache_loc", out_cache_loc, torch.int32, device, 1)
     n = out_cache_loc.shape[0]
     rows = (n, p.num_kv_heads, p.head_dim)
+    ws, size = (None, 4) if workspace is None else _space(workspace, device)
+    if size < 4:
+        raise ValueError("workspace must hold the error word (4 bytes)")
     check("pkv_kv_store_block", lib.pkv_kv_store_block(
         p, _fits("k_new", k_new, torch.bfloat16, device, rows), _fits("v_new", v_new, torch.bfloat16, device, rows), loc,
-        n, None if workspace is None else _space(workspace, device)[0], stream))
+        n, ws, stream))
 
 
 def decode_block_workspace(pool: BlockPool, num_q_heads: int) -> int:

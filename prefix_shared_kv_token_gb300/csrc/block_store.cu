@@ -223,6 +223,7 @@ extern "C" int pkv_kv_store_block(const pkv_block_pool *pool, const void *k_new,
     if (n == 0) return PKV_OK;
     if (!k_new || !v_new || !out_cache_loc) return PKV_E_INVALID;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return PKV_E_INVALID;
+    if (reinterpret_cast<uintptr_t>(workspace) & 3) return PKV_E_INVALID;  // (its error word is changed atomically)
     BlockStoreParams p;
     p.k_new = static_cast<const uint16_t *>(k_new);
     p.v_new = static_cast<const uint16_t *>(v_new);

@@ -420,3 +420,23 @@ def test_a_captured_step_holds_decodes_own_bound(pkv, g):
             e = ref.exponents_of(codes[3], t[r], lens[r], page)
             want, bound = ref.attend(qv[r:r + 1], kk, vv, scale, [lens[r] - 1], DECODE_EPS, v_exp=e)
             assert np.all(np.abs(values(o[r:r + 1]) - want) <= bound), (i, r)
+
+
+# ----------------------------------------------------------------------------------------
+# the store's error word
+
+
+def test_store_refuses_a_workspace_without_an_error_word(pkv):
+    pool, was = random_pool(pkv, np.random.default_rng(0), 4, 16, 2, 64)
+    x, _ = bf16(np.ones((3, 2, 64)))
+    raw = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    for ws in (raw[:0], raw[:3]):
+        with pytest.raises(ValueError):
+            pkv.kv_store_block(pool, x, x, dev([0, 1, 2]), ws)
+    for at in (1, 2, 3):
+        with pytest.raises(pkv.PkvError):
+            pkv.kv_store_block(pool, x, x, dev([0, 1, 2]), raw[at:])
+    for t, w in zip((pool.k, pool.k_exp, pool.v, pool.v_exp), was):
+        assert np.array_equal(host(t), w)
+    pkv.kv_store_block(pool, x, x, dev([0, 1, -2]), raw[4:])
+    assert error(pkv, raw[4:]) == 0x100 and torch.all(raw[8:] == 0) and torch.all(raw[:4] == 0)

@@ -190,3 +190,9 @@ def test_a_pool_at_any_16_byte_address_is_taken_by_every_call(offset):
         assert plan.info.offsets[18] == (tokens == 1)
         assert lib.pkv_attn_extend_block(C.byref(p), C.byref(b), P, P, 0.1, C.byref(plan.info), P, P,
                                          plan.info.workspace_bytes - 1, None) == WORKSPACE
+
+
+def test_store_refuses_an_error_word_that_is_not_aligned():
+    p = pool()
+    for at in (1, 2, 3):
+        assert lib.pkv_kv_store_block(C.byref(p), P, P, P, 4, P + at, None) == INVALID
