@@ -338,6 +338,11 @@ int pkv_get_noalloc_device_error(void *stream, int32_t *raw);
 /* stored code is one rounding of its value, and a page whose scale has to grow is rescaled */
 /* without a second rounding (but for e4m3's subnormals).  Bytes are in [10, 245]; another  */
 /* one is read as the nearer end of that range.                                            */
+/* A store that raises a page's exponent rewrites the codes that the page already held (the   */
+/* other pools' stores write new slots only).  So attention over a page must not run beside a */
+/* store into that page: put both on one stream, or order them.                              */
+/* Logits are sums in fp32 (K's exponent and the query's size together have to leave them     */
+/* there); V may use the whole range of exponents.                                          */
 /* The four calls below make a step: tables and slots from the requests' lengths, the store  */
 /* of the new rows, attention over the pages.  Page ids are pkv_batch's (page_size > 1):     */
 /* position t of a request is slot req_to_token[row][t / P] * P + t % P.                     */
@@ -357,7 +362,10 @@ typedef struct pkv_block_pool {
 } pkv_block_pool;
 
 /* A step's tables from the requests' lengths, on the device (pkv_fill_batch_table and the slot
- * allocator do this on the host).  Request r has seq_lens[r] positions after the step, the last
+ * allocator do this on the host).  The list only shrinks here: when a request leaves, its pages, the
+ * first ceil(len / P) entries of its row, are the caller's to give back between steps, by writing them
+ * below free_pages[*free_head] and lowering the head by as many, or to the host's allocator of pages where
+ * they came from one.  A page that other rows name, a shared prefix, stays.  Request r has seq_lens[r] positions after the step, the last
  * new_lens[r] of them new (0 <= new_lens[r] <= seq_lens[r]).  With had = ceil((seq - new) / P)
  * and has = ceil(seq / P), its table entries [had, has) receive the next has - had pages of the
  * free list, in request order.  Query row qo_indptr[r] + i is new token i of request r:
@@ -395,8 +403,8 @@ int pkv_build_block_tables(const pkv_batch *batch, const int32_t *new_lens, cons
  * rescales the page's earlier rows.  Codes are x * 2^-e rounded to nearest even, saturating;
  * infinities saturate, NaN is stored as NaN (0x7F).
  *   out_cache_loc  -1 is padding and skipped; another slot outside the pool is skipped and sets
- *                  PKV_DERR_SLOT_RANGE in the workspace's error word (workspace may be NULL).  A
- *                  skipped token leaves its row out of the run around it */
+ *                  PKV_DERR_SLOT_RANGE in the workspace's error word (workspace may be NULL, else
+ *                  4-byte aligned).  A skipped token leaves its row out of the run around it */
 int pkv_kv_store_block(const pkv_block_pool *pool, const void *k_new, const void *v_new,
                        const int32_t *out_cache_loc, int64_t n, void *workspace, void *stream);
 
@@ -406,8 +414,10 @@ int pkv_kv_store_block(const pkv_block_pool *pool, const void *k_new, const void
  * lengths, rows and tables that change between replays.  A request of length 0 gets zeros (a
  * padded batch), and so does one whose row or length is out of range, which also sets
  * PKV_DERR_POSITION; a page outside the pool reads as zero rows and sets PKV_DERR_SLOT_RANGE.
- * num_q_heads / num_kv_heads is 1, 2, 4 or 8.  Accumulation is fp32; weights enter the product
- * as f16 (11 bits), codes exactly.
+ * num_q_heads / num_kv_heads is 1, 2, 4 or 8 (G).  Accumulation is fp32; weights enter the product
+ * as f16 (11 bits), codes exactly.  Up to 65,536 groups of 8 / G neighbouring requests, the time grows with
+ * the work; past that it also grows with the square of the batch and shared pages are not looked for, so a
+ * larger batch is better cut into calls.
  *   workspace  device, 256-byte aligned, >= pkv_decode_block_workspace bytes (whatever the
  *              batch), first word zeroed once.  Calls that may overlap on the GPU need one each. */
 int pkv_decode_block_workspace(const pkv_block_pool *pool, int32_t num_q_heads, size_t *bytes);
@@ -418,7 +428,10 @@ int pkv_attn_decode_block(const pkv_block_pool *pool, const pkv_batch *batch, co
  * without fuse_store), workspace and errors; sm_scale must be positive.  Each key run is turned once
  * into the bf16 values its codes stand for, and attended with pkv_attn_extend's arithmetic (bf16
  * weights); where the plan finds few tokens a request, they are attended over the pages with
- * pkv_attn_decode_block's.  A NaN code reaches the query rows that see it and no others. */
+ * pkv_attn_decode_block's.  A NaN code reaches the query rows that see it and no others.  That costs a
+ * gathered call time where it meets one in V, as do sums of V values past fp32's range (pages with exponent bytes above
+ * 207): each row that such a value reached is computed again, key by key.  A NaN that every row of a large prefill
+ * sees makes it some 100 times as long (64 prompts of 200 tokens behind 1,792: 0.44 and 46 ms). */
 int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, const void *q, void *o, float sm_scale,
                           const pkv_plan_info *info, const void *plan_dev, void *workspace, size_t ws_bytes,
                           void *stream);

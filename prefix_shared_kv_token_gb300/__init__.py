@@ -416,7 +416,8 @@ def build_block_tables(req_to_token, req_pool_indices, seq_lens, new_lens, free_
 
 def kv_store_block(pool: BlockPool, k_new, v_new, out_cache_loc, workspace=None, stream=None) -> None:
     """Quantises k_new, v_new (bf16 [n, heads, head_dim]) into the slots out_cache_loc; tokens of
-    one page are neighbours at consecutive slots, -1 is padding (see pkv_kv_store_block)."""
+    one page are neighbours at consecutive slots, -1 is padding (see pkv_kv_store_block).  A page whose
+    exponent grows has its earlier rows rewritten: nothing may read it on another stream meanwhile."""
     torch, device, stream = _where(stream)
     p = pool.c(device)
     loc = _fits("out_cache_loc", out_cache_loc, torch.int32, device, 1)

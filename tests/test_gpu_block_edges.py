@@ -440,3 +440,29 @@ def test_store_refuses_a_workspace_without_an_error_word(pkv):
         assert np.array_equal(host(t), w)
     pkv.kv_store_block(pool, x, x, dev([0, 1, -2]), raw[4:])
     assert error(pkv, raw[4:]) == 0x100 and torch.all(raw[8:] == 0) and torch.all(raw[:4] == 0)
+
+
+# ----------------------------------------------------------------------------------------
+# pages given back
+
+
+def test_pages_given_back_are_taken_again(pkv):
+    """A request that left has its row's pages written below the list's head, which drops by as many; the next
+    step takes them first, and the other requests' pages stay theirs."""
+    page, b = 16, 3
+    free, head = dev(np.arange(20, 40)), words(1)
+    table = torch.full((b, 8), -1, dtype=torch.int32, device="cuda")
+    loc, pos, qo, ws = words(200), words(200), words(b + 1), words()
+
+    def step(seq, new):
+        pkv.build_block_tables(table, dev([0, 1, 2]), dev(seq), dev(new), free, head, head, loc, pos, qo, page, ws)
+        assert error(pkv, ws) == 0
+        return host(table), host(loc), int(head)
+    t, _, h = step([33, 20, 0], [33, 20, 0])
+    assert t[0, :3].tolist() == [20, 21, 22] and t[1, :2].tolist() == [23, 24] and h == 5
+    free[h - 3:h] = table[0, :3]
+    head -= 3
+    t, slots, h = step([0, 33, 20], [0, 13, 20])     # request 1 grows into a third page, request 2 arrives
+    assert t[1, :3].tolist() == [23, 24, 20] and t[2, :2].tolist() == [21, 22] and h == 5
+    want = [24 * 16 + i for i in range(4, 16)] + [20 * 16] + [21 * 16 + i for i in range(16)] + [22 * 16 + i for i in range(4)]
+    assert slots[:33].tolist() == want and np.all(slots[33:] == -1)
