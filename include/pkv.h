@@ -437,6 +437,104 @@ int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, co
                           void *stream);
 
 /* ------------------------------------------------------------------------------------ */
+/* rotary positions                                                                       */
+/*                                                                                      */
+/* The first rotary_dim elements of a head turn with the token's position p: pair i,        */
+/* (x1, x2), at frequency f_i by the angle p f_i,                                           */
+/*     y1 = magnitude (x1 cos - x2 sin),  y2 = magnitude (x2 cos + x1 sin).                 */
+/* Pair i is elements (i, i + rotary_dim / 2), or interleaved (2i, 2i + 1).  The elements     */
+/* behind rotary_dim are copied.  Arithmetic is fp32, rounded once; the angle's error is       */
+/* below 2^-22 of a radian at any int32 position (also a negative one).                      */
+
+typedef struct pkv_rope_spec {
+    const uint64_t *phases;  /* device, [rotary_dim / 2]: 2^64ths of a turn a position         */
+                             /* (pkv_rope_phases), 8-byte aligned                              */
+    int32_t rotary_dim;      /* a multiple of 16, at most the head's                          */
+    int32_t interleaved;     /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1)         */
+    float   magnitude;       /* of a rotated pair (1, or a long context's factor)              */
+} pkv_rope_spec;
+
+/* Frequencies in radians a position (host, finite) to phases (host). */
+int pkv_rope_phases(const double *inv_freq, int32_t n, uint64_t *phases);
+
+/* Rotates n tokens of num_heads heads of dim elements, bf16, dim a multiple of 8 up to 512.  Head h of
+ * token i is at element i * token_stride + h * head_stride of x and of out; strides are multiples of 8,
+ * addresses 16-byte aligned.  out may be x with x's strides (in place); otherwise they may not overlap.
+ *   positions  device int32 [n] */
+int pkv_rope(const pkv_rope_spec *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+             int64_t out_token_stride, int64_t out_head_stride, int32_t num_heads, int32_t dim,
+             const int32_t *positions, int64_t n, void *stream);
+
+/* pkv_rope of q and of k_new, and pkv_kv_store of the rotated k and of v_new, in one pass: rows of a fused
+ * projection go to q_out and to the pool.  Strides are in elements as above; heads of k_new and v_new are
+ * dense (head_dim elements apart).  rope->rotary_dim is at most pool->head_dim.
+ *   q, q_out       bf16, num_q_heads heads of pool->head_dim elements; q_out may be q.  num_q_heads 0: none
+ *   out_cache_loc  device int32 [n], as pkv_kv_store, and: -1 is a padded token, of which nothing is read
+ *                  or written, its row of q_out included.  Another slot outside the pool sets
+ *                  PKV_DERR_SLOT_RANGE in workspace (4 bytes, 4-aligned, or NULL), and its q alone is rotated
+ * An fp8 pool gets e4m3_rn_satfinite(x / scale) of the fp32 rotated value: one rounding, where pkv_rope and
+ * pkv_kv_store after it make two. */
+int pkv_rope_store(const pkv_pool *pool, const pkv_rope_spec *rope, const void *q, int64_t q_token_stride,
+                   int64_t q_head_stride, void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                   int32_t num_q_heads, const void *k_new, int64_t k_token_stride, const void *v_new,
+                   int64_t v_token_stride, const int32_t *positions, const int32_t *out_cache_loc, int64_t n,
+                   void *workspace, void *stream);
+
+/* ------------------------------------------------------------------------------------ */
+/* the latent pool: keys and values of all heads from one vector a token                  */
+/*                                                                                      */
+/* A slot's row is the token's latent (latent_dim elements) and behind it a rotary key        */
+/* (rope_dim) that all heads share.  In the absorbed form a query head is latent_dim +        */
+/* rope_dim elements, its part for the latent already multiplied by the head's key             */
+/* projection, and what attention returns, latent_dim elements a head, is multiplied by the     */
+/* head's value projection afterwards; both are the caller's matrix products.  Slots, tables      */
+/* and the radix tree are the other pools'.                                                */
+
+typedef struct pkv_latent_pool {
+    void    *rows;         /* device, bf16, slot s's row at element s * slot_stride; 16-byte aligned */
+    int64_t  num_slots;    /* < 2^31                                                        */
+    int32_t  latent_dim;   /* 256 or 512                                                    */
+    int32_t  rope_dim;     /* 64                                                            */
+    int64_t  slot_stride;  /* elements, a multiple of 8; 0 means latent_dim + rope_dim           */
+} pkv_latent_pool;
+
+/* Writes new tokens' rows into their slots: the latent, normalised, and the rotated rotary key.
+ *     row = [ c * norm_weight / sqrt(mean(c^2) + eps), rope(pe) ]      fp32, rounded once
+ *   c_new, pe_new  bf16 [n][latent_dim] and [n][rope_dim], rows token_stride elements apart (a multiple of
+ *                  8; slices of one projection's rows); 16-byte aligned
+ *   norm_weight    bf16 [latent_dim], 16-byte aligned, or NULL: the latent is copied as it is
+ *   rope           rotary_dim must be rope_dim
+ *   out_cache_loc  device int32 [n], distinct; -1 is padding and skipped, another slot outside the pool is
+ *                  skipped and sets PKV_DERR_SLOT_RANGE in workspace (4 bytes, 4-aligned, or NULL) */
+int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec *rope, const void *c_new, int64_t c_token_stride,
+                     const void *pe_new, int64_t pe_token_stride, const void *norm_weight, float eps,
+                     const int32_t *positions, const int32_t *out_cache_loc, int64_t n, void *workspace, void *stream);
+
+/* Attention of each request's newest tokens over its rows of a latent pool.  Request r's new tokens are
+ * rows qo_indptr[r] .. qo_indptr[r + 1] of q (bf16 [total_q][num_heads][latent_dim + rope_dim]) and o
+ * (bf16 [total_q][num_heads][latent_dim]), the last ones of its seq_lens[r] positions; each sees the
+ * positions up to its own:
+ *     o[t, h] = sum_j softmax_j(sm_scale * q[t, h] . row_j) * latent_j.
+ * qo_indptr NULL: one token a request, in batch order (decode; total_q is the batch).  There is no plan:
+ * the work is divided on the device from seq_lens and qo_indptr, so a captured graph follows lengths,
+ * rows, tables and offsets that change between replays.  Rows of o outside every request are left as they
+ * are.  A token that sees no position (length 0, or more new tokens than positions) gets zeros, and so do the
+ * tokens of a request whose row or length is out of range, which also sets PKV_DERR_POSITION; a request whose offsets are
+ * out of range is left out and sets it too.  A slot outside the pool reads as a zero row and sets PKV_DERR_SLOT_RANGE.
+ * Logits and sums are fp32, weights bf16 (their sum, which divides, is of the rounded ones).  A NaN or an
+ * infinity in a row reaches the tokens that see it and no others.  Latents times 2^8 times the context's
+ * length have to stay in fp32's range.
+ * Past some 170 new tokens a request, multiplying the latents out into per-head keys and values costs
+ * fewer operations than this form; pkv_attn_extend serves those.
+ *   num_heads  1 to 1024; total_q * num_heads < 2^31
+ *   workspace  device, 256-byte aligned, >= pkv_latent_workspace bytes (whatever the batch), first word
+ *              zeroed once.  Calls that may overlap on the GPU need one each. */
+int pkv_latent_workspace(const pkv_latent_pool *pool, int32_t num_heads, size_t *bytes);
+int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *batch, const void *q, void *o, int64_t total_q,
+                    const int32_t *qo_indptr, int32_t num_heads, float sm_scale, void *workspace, size_t ws_bytes,
+                    void *stream);
+
+/* ------------------------------------------------------------------------------------ */
 /* host radix tree ([RC]): token ids -> pool slots, with LRU eviction and lock_ref       */
 /*                                                                                      */
 /* Page size 1: children are keyed by the first token of their key.  Time is a logical   */

@@ -21,6 +21,12 @@ memory -- and forwards to the library.  Names follow the C entry points without 
     build_block_tables  page table entries, slots and positions of a step from its lengths
     kv_store_block  scatter new K/V rows into pages, raising a page's exponent where they need it
     attn_decode_block / attn_extend_block  the two attention calls over such a pool
+    Rope          rotary positions: layout, rotated part of a head, scaling for long contexts
+    rope          rotates the heads of a tensor by their tokens' positions
+    rope_store    rotates q and k and stores k and v into pool slots in one pass
+    LatentPool    a pool of one latent vector and one shared rotary key a token
+    latent_store  norms new latents, rotates their rotary keys and stores both into slots
+    attn_latent   attention of each request's newest tokens over such a pool, no host plan
     RadixTree     host radix tree: match_prefix (with split), insert, LRU evict, lock_ref,
                   cascade extraction
     Allocator     token-slot free list
@@ -31,17 +37,19 @@ There is no CPU or eager fallback: importing the package loads the library or ra
 from __future__ import annotations
 
 import ctypes as C
+import math
 from dataclasses import dataclass
 
 import numpy as np
 
-from ._lib import (PKV_BF16, PKV_FP8_E4M3, PkvBatch, PkvBlockPool, PkvCascade, PkvError, PkvPlanInfo, PkvPlanOpts, PkvPool,
-                   check, lib)
+from ._lib import (PKV_BF16, PKV_FP8_E4M3, PkvBatch, PkvBlockPool, PkvCascade, PkvError, PkvLatentPool, PkvPlanInfo,
+                   PkvPlanOpts, PkvPool, PkvRopeSpec, check, lib)
 
 __all__ = ["Pool", "Batch", "Plan", "Cascade", "kv_store", "check_out_cache_loc", "plan_decode", "plan_extend",
            "plan_extend_ctx", "attn_decode", "attn_extend", "attn_extend_store", "attn_extend_ctx", "get_device_error", "get_noalloc_device_error", "set_kernel_events",
            "set_wait_limit_ns", "get_wait_limit_ns", "fill_batch_table", "BlockPool", "build_block_tables",
            "kv_store_block", "decode_block_workspace", "attn_decode_block", "attn_extend_block",
+           "Rope", "rope", "rope_store", "LatentPool", "latent_store", "latent_workspace", "attn_latent",
            "RadixTree", "Allocator", "PkvError", "version"]
 
 
@@ -463,6 +471,241 @@ def attn_extend_block(pool: BlockPool, batch: Batch, q, o, sm_scale, plan: Plan,
     check("pkv_attn_extend_block", lib.pkv_attn_extend_block(
         p, b, _fits("q", q, torch.bfloat16, device, rows), _fits("o", o, torch.bfloat16, device, rows), float(sm_scale), info, at,
         ws, size, stream))
+
+
+# ----------------------------------------------------------------------------------------
+# rotary positions, the latent pool
+
+
+class Rope:
+    """Rotary positions of the first ``rotary_dim`` elements of a head (a multiple of 16).
+
+    layout   "half": pairs (i, i + rotary_dim / 2); "interleaved": pairs (2i, 2i + 1)
+    base     pair i turns by base^(-2i / rotary_dim) radians a position
+    scaling  None, or for contexts beyond the trained one a dict with a "kind":
+             "linear" (factor): every frequency divided by factor;
+             "ntk" (factor): a base under which the slowest pair's frequency is divided by factor;
+             "yarn" (factor, original; beta_fast 32, beta_slow 1, magnitude 0.1 ln factor + 1): pairs that turn
+             more than beta_fast times within the original context keep their frequency, those below
+             beta_slow have it divided by factor, a ramp between them
+    inv_freq frequencies of the caller's own (float64 [rotary_dim / 2]), instead of base and scaling
+    magnitude  factor on the rotated elements (default 1, or the scaling's)
+
+    ``inv_freq`` and ``magnitude`` hold what came out, ``phases`` its device form."""
+
+    def __init__(self, rotary_dim, base=10000.0, layout="half", scaling=None, inv_freq=None, magnitude=None, device="cuda"):
+        import torch
+        self.rotary_dim = int(rotary_dim)
+        if self.rotary_dim <= 0 or self.rotary_dim % 16:
+            raise ValueError("rotary_dim must be a positive multiple of 16")
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"unknown rotary layout {layout!r}")
+        self.layout = layout
+        if inv_freq is None:
+            self.inv_freq, own = self._frequencies(self.rotary_dim, float(base), scaling)
+        else:
+            if scaling is not None:
+                raise ValueError("inv_freq are final: give no scaling with them")
+            self.inv_freq, own = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64)), 1.0
+        if self.inv_freq.shape != (self.rotary_dim // 2,) or not np.all(np.isfinite(self.inv_freq)):
+            raise ValueError("inv_freq must be rotary_dim / 2 finite numbers")
+        self.magnitude = float(own if magnitude is None else magnitude)
+        if not math.isfinite(self.magnitude):
+            raise ValueError("magnitude must be finite")
+        phases = np.zeros(self.rotary_dim // 2, dtype=np.uint64)
+        check("pkv_rope_phases", lib.pkv_rope_phases(_ptr(self.inv_freq), len(phases), _ptr(phases)))
+        self.phases = torch.from_numpy(phases.view(np.int64)).to(device)
+        self._device = self.phases.get_device()
+        self._c = PkvRopeSpec(_ptr(self.phases), self.rotary_dim, int(layout == "interleaved"), self.magnitude)
+
+    @staticmethod
+    def _frequencies(dim, base, scaling):
+        if not (math.isfinite(base) and base > 1):
+            raise ValueError("base must be a finite number above 1")
+        i = np.arange(0, dim, 2, dtype=np.float64)
+        freq = base ** (-i / dim)
+        if scaling is None:
+            return freq, 1.0
+        opts = dict(scaling)
+        kind, factor = opts.pop("kind", None), float(opts.pop("factor", 0))
+        if kind not in ("linear", "ntk", "yarn"):
+            raise ValueError(f"unknown rotary scaling {kind!r}")
+        if not (math.isfinite(factor) and factor >= 1):
+            raise ValueError("a scaling's factor must be a finite number of at least 1")
+        magnitude = 1.0
+        if kind == "linear":
+            freq = freq / factor
+        elif kind == "ntk":
+            freq = (base * factor ** (dim / max(dim - 2, 1))) ** (-i / dim)
+        else:
+            original = float(opts.pop("original", 0))
+            fast, slow = float(opts.pop("beta_fast", 32.0)), float(opts.pop("beta_slow", 1.0))
+            if not (original > 0 and fast > slow > 0):
+                raise ValueError("yarn scaling needs the original context length and beta_fast above beta_slow above 0")
+            # the pair (fractional) that turns `turns` times within the original context
+            pair = lambda turns: dim * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+            lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), dim - 1)
+            ramp = np.clip((np.arange(dim // 2) - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+            freq = freq * (1 - ramp) + freq / factor * ramp
+            magnitude = float(opts.pop("magnitude", 0.1 * math.log(factor) + 1.0))
+        if opts:
+            raise ValueError(f"unknown options of {kind} scaling: {sorted(opts)}")
+        return freq, magnitude
+
+    def c(self, device) -> PkvRopeSpec:
+        if self._device != device:
+            raise ValueError("Rope is not on the current CUDA device")
+        return self._c
+
+
+def _rows(name, t, device, shape) -> tuple:
+    """(address, strides) of a bf16 tensor of this shape whose last dimension is dense."""
+    if _torch is not None and isinstance(t, _torch.Tensor) and t.get_device() == device and t.dtype is _torch.bfloat16 \
+            and t.dim() == len(shape) and t.shape == shape and (t.stride(-1) == 1 or shape[-1] == 1):
+        return t.data_ptr(), t.stride()
+    if not isinstance(t, _torch.Tensor) or t.get_device() != device:
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    if t.dtype is not _torch.bfloat16 or t.dim() != len(shape) or t.shape != shape:
+        raise ValueError(f"{name} must be bfloat16 of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    raise ValueError(f"{name} must be dense in its last dimension")
+
+
+def _heads(name, t) -> tuple:
+    if not isinstance(t, _torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, dim] tensor")
+    return tuple(t.shape)
+
+
+def _apart(name, t) -> None:
+    """Refuses an output whose elements share memory (an expanded tensor)."""
+    if t.numel() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must have a place for each of its elements")
+
+
+def rope(x, positions, rope, out=None, stream=None):
+    """Rotates x (bf16 [n, heads, dim], any strides of 8 elements' multiple, the last dimension dense) by the
+    tokens' positions (int32 [n]) into ``out``, a new tensor by default; out may be x (in place).  Returns out
+    (see pkv_rope)."""
+    torch, device, stream = _where(stream)
+    n, heads, dim = shape = _heads("x", x)
+    spec = rope.c(device)
+    at, s = _rows("x", x, device, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    to, so = _rows("out", out, device, shape)
+    _apart("out", out)
+    check("pkv_rope", lib.pkv_rope(spec, at, s[0], s[1], to, so[0], so[1], heads, dim,
+                                   _fits("positions", positions, torch.int32, device, (n,)), n, stream))
+    return out
+
+
+def rope_store(pool: Pool, q, k_new, v_new, positions, out_cache_loc, rope, q_out=None, workspace=None, stream=None):
+    """Rotates q [n, num_q_heads, head_dim] and k_new [n, heads, head_dim] and stores the rotated k and v_new into
+    the slots out_cache_loc, in one pass; the tensors may be slices of one projection's rows.  Returns q_out, a new
+    tensor by default; it may be q.  A token whose slot is -1 is padding: nothing of it is touched (see pkv_rope_store)."""
+    torch, device, stream = _where(stream)
+    if not isinstance(pool.k, torch.Tensor) or pool.k.get_device() != device or pool.v.get_device() != device:
+        raise ValueError("Pool is not on the current CUDA device")
+    p, spec = pool.c(), rope.c(device)
+    n, hq, _ = _heads("q", q)
+    shape, rows = (n, hq, p.head_dim), (n, p.num_kv_heads, p.head_dim)
+    at, s = _rows("q", q, device, shape)
+    k, sk = _rows("k_new", k_new, device, rows)
+    v, sv = _rows("v_new", v_new, device, rows)
+    for name, st in (("k_new", sk), ("v_new", sv)):
+        if p.num_kv_heads > 1 and st[1] != p.head_dim:
+            raise ValueError(f"{name} must have its heads side by side")
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    to, so = _rows("q_out", q_out, device, shape)
+    _apart("q_out", q_out)
+    ws, size = (None, 4) if workspace is None else _space(workspace, device)
+    if size < 4:
+        raise ValueError("workspace must hold the error word (4 bytes)")
+    check("pkv_rope_store", lib.pkv_rope_store(
+        p, spec, at, s[0], s[1], to, so[0], so[1], hq, k, sk[0], v, sv[0],
+        _fits("positions", positions, torch.int32, device, (n,)), _fits("out_cache_loc", out_cache_loc, torch.int32, device, (n,)),
+        n, ws, stream))
+    return q_out
+
+
+@dataclass(frozen=True)
+class LatentPool:
+    """Pool of latents: rows bf16 [num_slots, latent_dim + 64], a token's latent and its rotary key.  Rows may be
+    further apart than they are long."""
+    rows: object
+    latent_dim: int
+
+    @classmethod
+    def allocate(cls, num_slots, latent_dim=512, rope_dim=64, device="cuda"):
+        import torch
+        return cls(torch.zeros((num_slots, latent_dim + rope_dim), dtype=torch.bfloat16, device=device), int(latent_dim))
+
+    def __post_init__(self):
+        import torch
+        rows = self.rows
+        if not isinstance(rows, torch.Tensor) or rows.dtype != torch.bfloat16 or rows.dim() != 2 or rows.stride(1) != 1:
+            raise ValueError("LatentPool.rows must be a bfloat16 tensor [slots, latent_dim + rope_dim] with dense rows")
+        if rows.shape[0] > 1 and rows.stride(0) < rows.shape[1]:
+            raise ValueError("LatentPool.rows must not overlap")
+        stride = int(rows.stride(0)) if rows.shape[0] > 1 else rows.shape[1]
+        object.__setattr__(self, "_c", PkvLatentPool(_ptr(rows), rows.shape[0], int(self.latent_dim),
+                                                     rows.shape[1] - int(self.latent_dim), stride))
+        object.__setattr__(self, "_device", rows.get_device())
+
+    @property
+    def num_slots(self):
+        return self.rows.shape[0]
+
+    @property
+    def rope_dim(self):
+        return self.rows.shape[1] - self.latent_dim
+
+    def c(self, device) -> PkvLatentPool:
+        if self._device != device:
+            raise ValueError("LatentPool is not on the current CUDA device")
+        return self._c
+
+
+def latent_store(pool: LatentPool, c_new, pe_new, positions, out_cache_loc, rope, norm_weight=None, eps=1e-6, workspace=None,
+                 stream=None) -> None:
+    """Stores new tokens' rows into the slots out_cache_loc: c_new [n, latent_dim] under an RMS norm with
+    norm_weight [latent_dim] (None: as it is), pe_new [n, rope_dim] rotated; bf16, slices of one projection's
+    rows.  -1 is padding (see pkv_latent_store)."""
+    torch, device, stream = _where(stream)
+    p, spec = pool.c(device), rope.c(device)
+    loc = _fits("out_cache_loc", out_cache_loc, torch.int32, device, 1)
+    n = out_cache_loc.shape[0]
+    at, s = _rows("c_new", c_new, device, (n, p.latent_dim))
+    pe, sp = _rows("pe_new", pe_new, device, (n, p.rope_dim))
+    w = None if norm_weight is None else _fits("norm_weight", norm_weight, torch.bfloat16, device, (p.latent_dim,))
+    ws, size = (None, 4) if workspace is None else _space(workspace, device)
+    if size < 4:
+        raise ValueError("workspace must hold the error word (4 bytes)")
+    check("pkv_latent_store", lib.pkv_latent_store(
+        p, spec, at, s[0], pe, sp[0], w, float(eps), _fits("positions", positions, torch.int32, device, (n,)), loc, n, ws,
+        stream))
+
+
+def latent_workspace(pool: LatentPool, num_heads: int) -> int:
+    """Bytes of attn_latent's workspace (whatever the batch)."""
+    n = C.c_size_t(0)
+    check("pkv_latent_workspace", lib.pkv_latent_workspace(pool._c, int(num_heads), C.byref(n)))
+    return n.value
+
+
+def attn_latent(pool: LatentPool, batch: Batch, q, o, sm_scale, workspace, qo_indptr=None, stream=None) -> None:
+    """Attention of each request's newest tokens, rows qo_indptr[r] .. qo_indptr[r + 1] of q (bf16 [tokens, heads,
+    latent_dim + rope_dim]) and o ([tokens, heads, latent_dim]), over its rows of the pool; without
+    qo_indptr (int32 [batch + 1], on the GPU) one token a request.  No plan (see pkv_attn_latent)."""
+    torch, device, stream = _where(stream)
+    p, b = pool.c(device), _block_batch(batch, device, torch.int32)
+    n, heads, _ = _heads("q", q)
+    ws, size = _space(workspace, device)
+    qo = None if qo_indptr is None else _fits("qo_indptr", qo_indptr, torch.int32, device, (b.batch + 1,))
+    check("pkv_attn_latent", lib.pkv_attn_latent(
+        p, b, _fits("q", q, torch.bfloat16, device, (n, heads, p.latent_dim + p.rope_dim)),
+        _fits("o", o, torch.bfloat16, device, (n, heads, p.latent_dim)), n, qo, heads, float(sm_scale), ws, size, stream))
 
 
 def get_device_error(workspace, stream=None) -> int:

@@ -35,6 +35,15 @@ class PkvBlockPool(C.Structure):
                 ("head_dim", C.c_int32), ("slot_stride", C.c_int64)]
 
 
+class PkvLatentPool(C.Structure):
+    _fields_ = [("rows", C.c_void_p), ("num_slots", C.c_int64), ("latent_dim", C.c_int32), ("rope_dim", C.c_int32),
+                ("slot_stride", C.c_int64)]
+
+
+class PkvRopeSpec(C.Structure):
+    _fields_ = [("phases", C.c_void_p), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32), ("magnitude", C.c_float)]
+
+
 class PkvBatch(C.Structure):
     _fields_ = [("req_to_token", C.c_void_p), ("stride", C.c_int64), ("num_rows", C.c_int32),
                 ("req_pool_indices", C.c_void_p), ("seq_lens", C.c_void_p), ("batch", C.c_int32),
@@ -91,6 +100,15 @@ SIGNATURES = {
     "pkv_attn_decode_block": (C.c_int, [C.POINTER(PkvBlockPool), C.POINTER(PkvBatch), _P, _P, _I32, _F, _P, _SZ, _P]),
     "pkv_attn_extend_block": (C.c_int, [C.POINTER(PkvBlockPool), C.POINTER(PkvBatch), _P, _P, _F,
                                         C.POINTER(PkvPlanInfo), _P, _P, _SZ, _P]),
+    "pkv_rope_phases": (C.c_int, [_P, _I32, _P]),
+    "pkv_rope": (C.c_int, [C.POINTER(PkvRopeSpec), _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _P]),
+    "pkv_rope_store": (C.c_int, [C.POINTER(PkvPool), C.POINTER(PkvRopeSpec), _P, _I64, _I64, _P, _I64, _I64, _I32, _P,
+                                 _I64, _P, _I64, _P, _P, _I64, _P, _P]),
+    "pkv_latent_store": (C.c_int, [C.POINTER(PkvLatentPool), C.POINTER(PkvRopeSpec), _P, _I64, _P, _I64, _P, _F, _P, _P,
+                                   _I64, _P, _P]),
+    "pkv_latent_workspace": (C.c_int, [C.POINTER(PkvLatentPool), _I32, C.POINTER(_SZ)]),
+    "pkv_attn_latent": (C.c_int, [C.POINTER(PkvLatentPool), C.POINTER(PkvBatch), _P, _P, _I64, _P, _I32, _F, _P, _SZ,
+                                  _P]),
     "pkv_get_device_error": (C.c_int, [_P, _P, _PI32]),
     "pkv_set_kernel_events": (C.c_int, [_P, _P]),
     "pkv_set_wait_limit_ns": (C.c_int, [C.c_uint64]),

@@ -1,0 +1,959 @@
+// attn_latent: attention of each request's newest tokens over a latent pool (the absorbed form).
+// A pool row is a token's latent c (R elements) and its rotary key (64); every head's key is the
+// whole row, every head's value the latent:
+//     o[t, h] = sum_{j <= position of t} softmax_j(sm_scale * q[t, h] . row_j) * c_j.
+//
+// One row of 2 (R + 64) bytes serves all heads, so the product is far denser than attention over
+// K/V heads: 2 (2 R + 64) flops a head and key.  With 16 heads the row's bytes bound the call, with
+// 128 the tensor cores do as much.
+//
+// Both products run transposed, keys and latent elements in the M rows of tcgen05.mma and query
+// rows (token x head) in its N columns:
+//     S^T [64 keys x N] = rows Q^T           (A: the tile as it lies in shared memory, K-major)
+//     O^T [R x N]      += c^T P^T            (A: the same tile, MN-major, R / 128 products of M 128)
+// So one copy of a tile feeds both; the accumulator takes R / 128 * N columns of tensor memory,
+// where O itself would take all 512 for any M and leave no room for S; and N may be as small as the
+// rows there are (16, 32 or 64), with M still full.  A tile of 64 keys is 72 KB at R = 512: two of
+// them, Q and P fill the 227 KB.
+//
+// A CTA of 12 warps:
+//   warp 0      gathers the tile's rows by TMA (tile::gather4, four slots a copy, a lane a few of them)
+//   warp 1      issues the products, whichever of the next S and the next P V has its operands first
+//   warps 4-11  softmax: S^T from tensor memory (16x32bx2: the 16 lanes that an M of 64 fills, columns split
+//               between the half-warps), a thread one key and N / 4 columns; P back through shared memory
+// The softmax needs a column's maximum, which lies across lanes.  A running reference stands in for it: weights
+// are 2^(s - ref), and only where a logit passes ref by more than 8 (a vote a tile) is the tile's maximum
+// reduced, ref raised and O^T rescaled: once at a range's start, seldom after.  Weights stay below 2^8, in
+// bf16 (their own sum is what they are divided by).  Sums are fp32.
+//
+// Work is divided on the device, from seq_lens: tiles of all requests in a line, an equal range of them a
+// CTA (or pair, below), so a captured graph follows the lengths.  A request's rows beyond N are further units of the
+// line; with more than 64 rows two CTAs take the same range, 64 rows each, so that the second one's tiles
+// come from L2.  A range's first and last unit may be shared with its neighbours: their partial sums go to records
+// in the workspace, which merge_kernel joins.
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "../../include/pkv.h"
+#include "common.cuh"
+#include "latent.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+constexpr int kLTile = 64;              // keys a tile
+constexpr int kLThreads = 384;
+constexpr int kLSoftmax = 256;          // threads of the softmax warps
+constexpr int kLBarVote = 1;            // named barrier of the softmax warps
+constexpr int kLMinTiles = 2;           // a range's tiles at least
+constexpr float kLog2eL = 1.4426950408889634f;
+constexpr float kLagL = 8.0f;           // log2 units by which a logit may pass its reference
+
+struct LatentParams {
+    const int32_t *table;
+    int64_t stride;
+    int32_t num_rows, shift;
+    const int32_t *rows, *lens, *indptr;  // indptr NULL: one token a request
+    int32_t batch, heads;
+    int64_t total_q, num_slots;
+    uint16_t *o;
+    float scale_log2;
+    int32_t gs, ranges;                   // CTAs that share a range; ranges
+    float *rec;                           // [range][2][gs][N][R]
+    float *rec_ml;                        // [range][2][gs][N][2]
+    int32_t *units;                       // [range][8]: first unit (request, set, ends there), last unit (request, set)
+    int32_t *err;
+    WaitPolicy wait;
+};
+
+template <int R, int N>
+struct LCfg {
+    static constexpr int kBlocks = R / 64 + 1;                   // 64-column blocks of a row
+    static constexpr int kBlk = kLTile * 128;
+    static constexpr int kStage = kBlocks * kBlk;
+    static constexpr int kStages = R == 512 ? 2 : 4;
+    static constexpr int kQBlk = N * 128;
+    static constexpr int kQOff = kStages * kStage;
+    static constexpr int kPOff = kQOff + kBlocks * kQBlk;
+    static constexpr int kMiscOff = kPOff + kLTile * 128;
+    static constexpr int kSmem = kMiscOff + 2560;
+    static constexpr int kCols = N / 4;                          // columns a softmax thread
+    static constexpr uint32_t kColO = 128;                       // O^T block b at kColO + b * N
+};
+
+struct LMisc {
+    uint64_t full[4], empty[4];
+    uint64_t qfull, qempty, sfull[2], pfull, pvdone, ofull, drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t start_r;      // the range's first request, and the tiles of it that earlier ranges have
+    int32_t pad;
+    int64_t start_off, left;
+    int64_t scan[12];
+    float colmax[4][64];  // a quarter's column maxima; sums at the end
+    float alpha[64];
+    int32_t lim[64];      // keys that each row sees
+};
+static_assert(sizeof(LMisc) <= 2560, "LMisc");
+
+// ------------------------------------------------------------------------------------------
+// the line of tiles
+
+struct LReq {
+    int32_t len, e, row, sets, tiles;  // tiles: what a unit of the request counts in the line
+    int64_t q0;
+};
+
+PKV_DEV LReq load_req(const LatentParams &p, int r, int rps, bool report) {
+    LReq q;
+    q.len = ld(p.lens + r);
+    q.row = ld(p.rows + r);
+    if (p.indptr) {
+        q.q0 = ld(p.indptr + r);
+        q.e = ld(p.indptr + r + 1) - (int32_t)q.q0;
+    } else {
+        q.q0 = r;
+        q.e = 1;
+    }
+    bool bad = false;
+    if (q.q0 < 0 || q.e < 0 || q.q0 + q.e > p.total_q) {
+        bad = true;
+        q.e = 0;
+    }
+    if (q.row < 0 || q.row >= p.num_rows || q.len < 0 || (int64_t)q.len > (p.stride << p.shift)) {
+        bad = true;
+        q.len = 0;
+    }
+    if (bad && report) set_error(p.err, DERR_POSITION);
+    q.sets = (int32_t)(((int64_t)q.e * p.heads + rps - 1) / rps);
+    q.tiles = max(1, (q.len + kLTile - 1) / kLTile);
+    return q;
+}
+
+// A piece of one unit: this CTA's rows against tiles [t0, t1).
+struct LSeg {
+    int32_t r, set, row, vis;     // vis: keys that the unit's last row sees
+    int32_t t0, t1, nrows;        // nrows: this CTA's rows of the unit (0: none)
+    int64_t q_row0;               // first of them, in rows of q
+    int32_t vis0;                 // keys that their first token sees (0 or less: none), that is before its later tokens'
+    int32_t row_lo;               // first of them, in rows of the request
+    bool whole, first, ends;      // all of the unit is in this range; the range begins inside it; it ends in this range
+};
+
+struct LCursor {
+    int32_t r, j, t;
+    int64_t left;
+    bool loaded;
+    LReq q;
+};
+
+PKV_DEV LCursor cursor_at(const LatentParams &p, int r, int64_t off, int64_t left, int rps) {
+    LCursor c{r, 0, 0, left, false, {}};
+    if (left > 0) {
+        c.q = load_req(p, r, rps, false);
+        c.loaded = true;
+        c.j = (int32_t)(off / c.q.tiles);
+        c.t = (int32_t)(off - (int64_t)c.j * c.q.tiles);
+    }
+    return c;
+}
+
+template <int N>
+PKV_DEV bool next_seg(const LatentParams &p, LCursor &c, LSeg &s, int g) {
+    const int rps = N * p.gs;
+    if (c.left <= 0) return false;
+    while (!c.loaded) {
+        if (c.r >= p.batch) return false;
+        c.q = load_req(p, c.r, rps, false);
+        if (c.q.sets > 0) {
+            c.loaded = true;
+            c.j = c.t = 0;
+        } else {
+            ++c.r;
+        }
+    }
+    // A request's units in the order first, last, second, last but one, ..: the earlier ones see fewer keys of the
+    // new tokens than they count for, and so any stretch of the line has about its share of the work.
+    s.set = c.j & 1 ? c.q.sets - 1 - (c.j >> 1) : c.j >> 1;
+    s.r = c.r;
+    s.row = c.q.row;
+    const int32_t n = (int32_t)min((int64_t)(c.q.tiles - c.t), c.left);
+    const int64_t all = (int64_t)c.q.e * p.heads, lo = (int64_t)s.set * rps + g * N, set_end = min((int64_t)(s.set + 1) * rps, all);
+    s.row_lo = (int32_t)lo;
+    s.nrows = (int32_t)max((int64_t)0, min((int64_t)N, all - lo));
+    s.q_row0 = c.q.q0 * p.heads + lo;
+    s.vis = max(0, c.q.len - c.q.e + (int32_t)((set_end - 1) / p.heads) + 1);
+    s.vis0 = c.q.len - c.q.e + 1;
+    s.t0 = c.t;
+    s.t1 = max(c.t, min(c.t + n, (s.vis + kLTile - 1) / kLTile));
+    s.first = c.t > 0;
+    s.ends = c.t + n == c.q.tiles;
+    s.whole = !s.first && s.ends;
+    c.left -= n;
+    c.t += n;
+    if (c.t == c.q.tiles) {
+        c.t = 0;
+        if (++c.j == c.q.sets) {
+            c.loaded = false;
+            ++c.r;
+        }
+    }
+    return true;
+}
+
+// The next piece with rows and tiles; the producer and the issuer see no others.
+template <int N>
+PKV_DEV bool next_work(const LatentParams &p, LCursor &c, LSeg &s, int g) {
+    while (next_seg<N>(p, c, s, g))
+        if (s.nrows > 0 && s.t1 > s.t0) return true;
+    return false;
+}
+
+// ------------------------------------------------------------------------------------------
+
+PKV_DEV bool lwait(uint64_t *bar, uint32_t parity, LMisc *m, const LatentParams &p, int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (it == 1 || (it & p.wait.check_mask) == 0) {
+            if (*reinterpret_cast<volatile int32_t *>(&m->abort_flag)) return false;
+            if (global_timer_ns() - t0 > p.wait.limit_ns) {
+                set_error(p.err, DERR_TIMEOUT | where);
+                *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// Lanes 0-15 of a warp's quarter: columns [col, col + n) to threads 0-15, [col + n, col + 2 n) to threads 16-31.
+template <int NC>
+PKV_DEV void tmem_ld_split(uint32_t taddr, uint32_t *r) {
+    if constexpr (NC == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+            "[%16], 16;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+    } else if constexpr (NC == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0, %1, %2, %3}, [%4], 4;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+    }
+}
+PKV_DEV void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+PKV_DEV void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
+}
+
+PKV_DEV bool finite(uint32_t bits) { return (bits & 0x7F800000u) != 0x7F800000u; }
+// whether one of eight bf16 values is an infinity or a NaN
+PKV_DEV bool nonfinite8(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+    return bad;
+}
+
+// Where the range begins: its first request, how many of that request's tiles come before it, and
+// its tiles.  Each thread takes a stretch of the batch; a scan over the threads' sums.
+template <int N>
+PKV_DEV void find_range(const LatentParams &p, LMisc *m, int range) {
+    const int rps = N * p.gs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.batch + kLThreads - 1) / kLThreads;
+    const int r0 = min(p.batch, (int)threadIdx.x * per), r1 = min(p.batch, r0 + per);
+    int64_t own = 0;
+    for (int r = r0; r < r1; ++r) {
+        const LReq q = load_req(p, r, rps, blockIdx.x == 0);
+        own += (int64_t)q.sets * q.tiles;
+    }
+    int64_t incl = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += x;
+    }
+    if (lane == 31) m->scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - own, total = 0;
+    for (int w = 0; w < kLThreads / 32; ++w) {
+        if (w < warp) before += m->scan[w];
+        total += m->scan[w];
+    }
+    const int64_t each = max((int64_t)kLMinTiles, (total + p.ranges - 1) / p.ranges), t0 = (int64_t)range * each;
+    if (threadIdx.x == 0) {
+        m->left = max((int64_t)0, min(each, total - t0));
+        m->start_r = p.batch;
+        m->start_off = 0;
+    }
+    __syncthreads();
+    if (t0 < total && t0 >= before && t0 < before + own) {
+        int64_t at = before;
+        for (int r = r0; r < r1; ++r) {
+            const LReq q = load_req(p, r, rps, false);
+            const int64_t cost = (int64_t)q.sets * q.tiles;
+            if (t0 < at + cost) {
+                m->start_r = r;
+                m->start_off = t0 - at;
+                break;
+            }
+            at += cost;
+        }
+    }
+    __syncthreads();
+}
+
+template <int R, int N>
+__global__ void __launch_bounds__(kLThreads, 1)
+    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap pmap) {
+    using C = LCfg<R, N>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    LMisc *m = reinterpret_cast<LMisc *>(smem + C::kMiscOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x % p.gs, range = blockIdx.x / p.gs;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&m->full[s], 1);
+            mbar_init(&m->empty[s], 1);
+        }
+        mbar_init(&m->qfull, 1);
+        mbar_init(&m->qempty, 1);
+        mbar_init(&m->sfull[0], 1);
+        mbar_init(&m->sfull[1], 1);
+        mbar_init(&m->pfull, kLSoftmax / 32);
+        mbar_init(&m->pvdone, 1);
+        mbar_init(&m->ofull, 1);
+        mbar_init(&m->drain, 1);
+        m->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&m->tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&qmap);
+        prefetch_tmap(&pmap);
+    }
+    tc_fence_before();
+    pdl_wait();
+    pdl_trigger();
+    find_range<N>(p, m, range);  // (its barriers cover the set-up above)
+    tc_fence_after();
+    const uint32_t tmem = m->tmem_base;
+    LCursor cur = cursor_at(p, m->start_r, m->start_off, m->left, N * p.gs);
+    LSeg s;
+
+    if (warp == 0) {
+        // ================= producer =================
+        const int kg = lane & 15;                        // this lane's four keys of a tile
+        constexpr int kHalf = (C::kBlocks + 1) / 2;      // and its blocks of their rows
+        const int b0 = lane < 16 ? 0 : kHalf, b1 = lane < 16 ? kHalf : C::kBlocks;
+        int tp = 0, nq = 0;
+        bool ok = true;
+        while (ok && next_work<N>(p, cur, s, g)) {
+            if (nq > 0) ok = __all_sync(0xffffffffu, lwait(&m->qempty, (nq - 1) & 1, m, p, 1));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&m->qfull, C::kBlocks * C::kQBlk);
+                for (int b = 0; b < C::kBlocks; ++b)
+                    tma_load_2d(sbase + C::kQOff + b * C::kQBlk, &qmap, b * 64, (int32_t)s.q_row0, &m->qfull);
+            }
+            ++nq;
+            const int32_t *row = p.table + (int64_t)s.row * p.stride;
+            // the four slots of a tile's keys; beyond the keys that are seen, and for a slot outside the pool, -1,
+            // whose row is zeros
+            auto slots_of = [&](int t, int32_t *slot) {
+                const int k0 = t * kLTile + kg * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) slot[i] = -1;
+                if (k0 >= s.vis) return;
+                if (p.shift >= 2) {
+                    const int32_t pg = ld(row + (k0 >> p.shift));
+                    const int64_t at = ((int64_t)pg << p.shift) + (k0 & ((1 << p.shift) - 1));
+                    const bool in = pg >= 0 && at + 3 < p.num_slots;
+                    if (in) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (k0 + i < s.vis) slot[i] = (int32_t)at + i;
+                        return;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (k0 + i >= s.vis) continue;
+                    const int32_t x = table_slot(row, k0 + i, p.shift, p.num_slots);
+                    const bool in = x >= 0 && x < p.num_slots;
+                    if (!in) set_error(p.err, DERR_SLOT_RANGE);
+                    slot[i] = in ? x : -1;
+                }
+            };
+            int32_t slot[4], next[4];
+            slots_of(s.t0, slot);
+            for (int t = s.t0; t < s.t1; ++t, ++tp) {
+                if (t + 1 < s.t1) slots_of(t + 1, next);
+                const int st = tp % C::kStages;
+                if (tp >= C::kStages) {
+                    ok = __all_sync(0xffffffffu, lwait(&m->empty[st], (tp / C::kStages - 1) & 1, m, p, 2));
+                    if (!ok) break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&m->full[st], C::kStage);
+                __syncwarp();
+                const uint32_t dst = sbase + st * C::kStage + kg * 512;
+                for (int b = b0; b < b1; ++b)
+                    tma_gather4(dst + b * C::kBlk, &pmap, b * 64, slot[0], slot[1], slot[2], slot[3], &m->full[st]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) slot[i] = next[i];
+            }
+        }
+        // every copy issued lands before the CTA leaves
+        if (nq > 0) mbar_wait(&m->qfull, (nq - 1) & 1);
+        for (int t = max(0, tp - C::kStages); t < tp; ++t) mbar_wait(&m->full[t % C::kStages], (t / C::kStages) & 1);
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ================= issuer =================
+            // Two cursors over the same tiles: the next S and, up to two behind it, the next P V.
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kLTile, N, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, 1, 1);
+            LCursor pcur = cur;
+            LSeg ps;
+            bool have_s = next_work<N>(p, cur, s, g), have_p = next_work<N>(p, pcur, ps, g);
+            int ts = have_s ? s.t0 : 0, tv = have_p ? ps.t0 : 0;
+            int ns = 0, np = 0, nqs = 0;  // S and P V issued; Q loads consumed
+            bool q_ready = false;
+            while (have_p) {
+                bool did = false;
+                uint64_t t0 = 0;
+                for (uint32_t it = 0; !did; ++it) {
+                    if (np < ns && mbar_test_wait(&m->pfull, np & 1)) {
+                        tc_fence_after();
+                        const int st = np % C::kStages;
+                        const uint32_t v_s = sbase + st * C::kStage, p_s = sbase + C::kPOff;
+#pragma unroll
+                        for (int mb = 0; mb < R / 128; ++mb)
+#pragma unroll
+                            for (int kk = 0; kk < kLTile / 16; ++kk)
+                                mma_ss(tmem + C::kColO + mb * N, sdesc_sw128(v_s + 2 * mb * C::kBlk + kk * 2048, C::kBlk, 1024),
+                                       sdesc_sw128(p_s + kk * 2048, C::kBlk, 1024), idesc_o, tv > ps.t0 || kk > 0 ? 1u : 0u);
+                        tc_commit(&m->empty[st]);
+                        tc_commit(&m->pvdone);
+                        ++np;
+                        if (++tv == ps.t1) {
+                            tc_commit(&m->ofull);
+                            have_p = next_work<N>(p, pcur, ps, g);
+                            tv = have_p ? ps.t0 : 0;
+                        }
+                        did = true;
+                    } else if (have_s && ns < np + 2) {
+                        if (!q_ready) q_ready = mbar_test_wait(&m->qfull, nqs & 1);
+                        const int st = ns % C::kStages;
+                        if (q_ready && mbar_test_wait(&m->full[st], (ns / C::kStages) & 1)) {
+                            tc_fence_after();
+                            const uint32_t k_s = sbase + st * C::kStage, q_s = sbase + C::kQOff;
+#pragma unroll
+                            for (int ks = 0; ks < (R + 64) / 16; ++ks)
+                                mma_ss(tmem + (ns & 1) * 64, sdesc_sw128(k_s + (ks >> 2) * C::kBlk + (ks & 3) * 32, 16, 1024),
+                                       sdesc_sw128(q_s + (ks >> 2) * C::kQBlk + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
+                            tc_commit(&m->sfull[ns & 1]);
+                            ++ns;
+                            if (++ts == s.t1) {
+                                tc_commit(&m->qempty);
+                                ++nqs;
+                                q_ready = false;
+                                have_s = next_work<N>(p, cur, s, g);
+                                ts = have_s ? s.t0 : 0;
+                            }
+                            did = true;
+                        }
+                    }
+                    if (!did && (it & p.wait.check_mask) == 0) {
+                        const uint64_t now = global_timer_ns();
+                        if (t0 == 0) t0 = now;
+                        if (*reinterpret_cast<volatile int32_t *>(&m->abort_flag)) break;
+                        if (now - t0 > p.wait.limit_ns) {
+                            set_error(p.err, DERR_TIMEOUT | 3);
+                            *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
+                            break;
+                        }
+                    }
+                }
+                if (!did) break;
+            }
+            tc_commit(&m->drain);  // every product issued completes before tensor memory is freed
+            mbar_wait(&m->drain, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================= softmax and output =================
+        constexpr int NC = C::kCols;
+        const int wq = warp & 3, hf = (warp - 4) >> 2;
+        const int k_in = wq * 16 + (lane & 15);                    // this thread's key in a tile
+        const int c0 = hf * (N / 2) + (lane >> 4) * NC;            // and its first column
+        const uint32_t quarter = (uint32_t)(wq * 32) << 16;
+        const int st_id = threadIdx.x - 128;
+        int n = 0, nseg = 0;                                       // tiles and pieces before this one
+        bool ok = true;
+        int32_t *units = p.units + range * 8;
+        if (g == 0 && st_id < 2) units[st_id * 4] = -1;
+        named_bar_sync(kLBarVote, kLSoftmax);
+        while (next_seg<N>(p, cur, s, g)) {
+            const int slot_rec = s.first ? 0 : 1;
+            if (g == 0 && st_id == 0 && !s.whole) {
+                units[slot_rec * 4 + 1] = s.set;
+                units[slot_rec * 4 + 2] = s.ends;
+                units[slot_rec * 4] = s.r;
+            }
+            if (s.nrows <= 0) continue;
+            // keys that each column sees; columns without a row see what the last row does
+            if (st_id < N) {
+                const int at = min(st_id, s.nrows - 1);
+                m->lim[st_id] = s.vis0 + (s.row_lo + at) / p.heads;
+            }
+            const int lim_min = s.vis0 + s.row_lo / p.heads;
+            float ref[NC], thr[NC], l[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                ref[c] = 0.f;
+                thr[c] = -INFINITY;  // no reference yet
+                l[c] = 0.f;
+            }
+            named_bar_sync(kLBarVote, kLSoftmax);
+            for (int t = s.t0; t < s.t1; ++t, ++n) {
+                ok = __all_sync(0xffffffffu, ok && lwait(&m->sfull[n & 1], (n >> 1) & 1, m, p, 4));
+                uint32_t sv[NC];
+                bool over = false;
+                const bool masked = (t + 1) * kLTile > lim_min;
+                uint32_t hidden = 0;
+                bool odd_row = false;
+                if (ok) {
+                    tc_fence_after();
+                    tmem_ld_split<NC>(tmem + quarter + (n & 1) * 64 + hf * (N / 2), sv);
+                    tmem_ld_wait();
+                    if (masked) {
+                        bool odd = false;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            if (t * kLTile + k_in >= m->lim[c0 + c]) hidden |= 1u << c;
+                            odd |= !finite(sv[c]);
+                        }
+                        odd_row = odd && hidden != 0;
+                    }
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const float x = __uint_as_float(sv[c]) * p.scale_log2;
+                        sv[c] = __float_as_uint(x);
+                        over |= x > thr[c] && !((hidden >> c) & 1u);
+                    }
+                }
+                if (!named_bar_and(kLBarVote, kLSoftmax, ok && !over)) {
+                    if (!named_bar_and(kLBarVote, kLSoftmax, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    // raise the references to the tile's maxima where those are higher
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        float x = (hidden >> c) & 1u ? -INFINITY : __uint_as_float(sv[c]);
+#pragma unroll
+                        for (int d = 8; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                        if ((lane & 15) == 0) m->colmax[wq][c0 + c] = x;
+                    }
+                    named_bar_sync(kLBarVote, kLSoftmax);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const float top = fmaxf(fmaxf(m->colmax[0][c0 + c], m->colmax[1][c0 + c]),
+                                                fmaxf(m->colmax[2][c0 + c], m->colmax[3][c0 + c]));
+                        float a = 1.f;
+                        if (thr[c] == -INFINITY) {
+                            if (top > -INFINITY) {
+                                ref[c] = top;
+                                thr[c] = top + kLagL;
+                            }
+                        } else if (top > ref[c]) {
+                            a = ex2(ref[c] - top);
+                            ref[c] = top;
+                            thr[c] = top + kLagL;
+                            l[c] *= a;
+                        }
+                        if (wq == 0 && (lane & 15) == 0) m->alpha[c0 + c] = a;
+                    }
+                    if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 5));
+                    named_bar_sync(kLBarVote, kLSoftmax);
+                    if (t > s.t0 && ok) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int mb = hf; mb < R / 128; mb += 2)
+#pragma unroll 1
+                            for (int cc = 0; cc < N; cc += 16) {
+                                uint32_t ov[16];
+                                const uint32_t at = tmem + quarter + C::kColO + mb * N + cc;
+                                tmem_ld16(at, ov);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
+                                tmem_st16(at, ov);
+                            }
+                        tmem_st_wait();
+                    }
+                }
+                // weights, rounded to bf16 for the product; what they are divided by sums the rounded ones
+                uint32_t pk[NC / 2];
+#pragma unroll
+                for (int c = 0; c < NC; c += 2) {
+                    float a = ex2(__uint_as_float(sv[c]) - ref[c]), b = ex2(__uint_as_float(sv[c + 1]) - ref[c + 1]);
+                    if (odd_row) {  // a key that is not finite has no weight to be 0
+                        if (__uint_as_float(sv[c]) == -INFINITY) a = NAN;
+                        if (__uint_as_float(sv[c + 1]) == -INFINITY) b = NAN;
+                    }
+                    if ((hidden >> c) & 1u) a = 0.f;
+                    if ((hidden >> (c + 1)) & 1u) b = 0.f;
+                    pk[c / 2] = pack_bf16x2(a, b);
+                    add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
+                }
+                if (n > 0) ok = __all_sync(0xffffffffu, ok && lwait(&m->pvdone, (n - 1) & 1, m, p, 5));
+                const int st = n % C::kStages;
+                if (odd_row && ok) {
+                    // A row with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
+                    // from them.  Its latent becomes zeros; the columns that see it have a weight of NaN.
+                    lwait(&m->full[st], (n / C::kStages) & 1, m, p, 7);  // (long complete: the copies, seen by this thread)
+                    uint8_t *at = smem + st * C::kStage + k_in * 128;
+                    bool bad = false;
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        for (int j = 0; j < 8; ++j) bad |= nonfinite8(*reinterpret_cast<const uint4 *>(at + b * C::kBlk + j * 16));
+                    if (bad)
+                        for (int b = 0; b < R / 64; ++b)
+                            for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(at + b * C::kBlk + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                {
+                    uint8_t *row = smem + C::kPOff + k_in * 128;
+                    if constexpr (NC == 16) {
+                        const int j = c0 / 8;
+                        *reinterpret_cast<uint4 *>(row + ((j ^ (k_in & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        *reinterpret_cast<uint4 *>(row + (((j + 1) ^ (k_in & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    } else if constexpr (NC == 8) {
+                        *reinterpret_cast<uint4 *>(row + (((c0 / 8) ^ (k_in & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    } else {
+                        *reinterpret_cast<uint2 *>(row + (((c0 / 8) ^ (k_in & 7)) << 4) + (c0 & 4) * 2) = make_uint2(pk[0], pk[1]);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m->pfull);
+            }
+            // the columns' sums, over a warp's keys and then the quarters (colmax and alpha may still be in use)
+            named_bar_sync(kLBarVote, kLSoftmax);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float x = l[c];
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                if ((lane & 15) == 0) {
+                    m->colmax[wq][c0 + c] = x;
+                    if (wq == 0) m->alpha[c0 + c] = thr[c] == -INFINITY ? -INFINITY : ref[c];
+                }
+            }
+            const bool any = s.t1 > s.t0;
+            if (any) ok = __all_sync(0xffffffffu, ok && lwait(&m->ofull, nseg & 1, m, p, 6));
+            if (!named_bar_and(kLBarVote, kLSoftmax, ok)) break;
+            if (any) ++nseg;
+            tc_fence_after();
+            const int64_t rec = ((int64_t)range * 2 + slot_rec) * p.gs + g;
+            if (!s.whole && st_id < s.nrows)
+                reinterpret_cast<float2 *>(p.rec_ml)[rec * N + st_id] =
+                    make_float2(m->alpha[st_id], m->colmax[0][st_id] + m->colmax[1][st_id] + m->colmax[2][st_id] + m->colmax[3][st_id]);
+            if (!s.whole && !any) continue;  // its (-inf, 0) says that there is nothing to add
+#pragma unroll 1
+            for (int mb = hf; mb < R / 128; mb += 2) {
+                const int col = mb * 128 + wq * 32 + lane;  // this thread's latent element
+#pragma unroll 1
+                for (int cc = 0; cc < N; cc += 16) {
+                    if (cc >= s.nrows) break;
+                    uint32_t ov[16];
+                    if (any) {
+                        tmem_ld16(tmem + quarter + C::kColO + mb * N + cc, ov);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) ov[c] = 0u;
+                    }
+                    if (!s.whole) {
+                        float *out = p.rec + (rec * N + cc) * R + col;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (cc + c < s.nrows) out[(int64_t)c * R] = __uint_as_float(ov[c]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        float x[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int k = cc + c + i;
+                            const float sum = m->colmax[0][k] + m->colmax[1][k] + m->colmax[2][k] + m->colmax[3][k];
+                            x[i] = sum == 0.f ? 0.f : __uint_as_float(ov[c + i]) / sum;
+                        }
+                        // neighbouring lanes trade a value: even lanes write column c, odd ones c + 1, two elements each
+                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[0] : x[1], 1);
+                        const uint32_t w = lane & 1 ? pack_bf16x2(other, x[1]) : pack_bf16x2(x[0], other);
+                        const int k = cc + c + (lane & 1);
+                        if (k < s.nrows) reinterpret_cast<uint32_t *>(p.o + (s.q_row0 + k) * R)[col >> 1] = w;
+                    }
+                }
+            }
+            tc_fence_before();
+            // colmax, alpha and lim are read before the next piece writes them
+            named_bar_sync(kLBarVote, kLSoftmax);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------------------
+// Joins the records of units that several ranges share.  A unit's pieces are range c's last record and the
+// first records of the ranges behind it, up to the one in which it ends.  A row of such a unit is a task: for a
+// warp where the units have few records, else for a CTA whose warps take every eighth one.
+
+struct LatentMerge {
+    const float *rec, *rec_ml;
+    const int32_t *units, *indptr;
+    int32_t ranges, gs, heads, N;
+    uint16_t *o;
+    const int32_t *err;
+};
+
+template <int R>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentMerge p) {
+    constexpr int V = R / 128;  // float4s a lane
+    __shared__ int32_t s_from[160], s_count[160];
+    __shared__ int32_t s_warp[8], s_most;
+    __shared__ float4 s_acc[8][R / 4];
+    __shared__ float2 s_ml[8];
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (*p.err & DERR_TIMEOUT) return;  // records may be missing
+    // the units to join, in the ranges' order: every CTA has the same list
+    int n = 0;
+    if ((int)threadIdx.x < p.ranges && ld(p.units + threadIdx.x * 8 + 4) >= 0) {
+        const int c = threadIdx.x;
+        n = 1;
+        while (c + n < p.ranges && ld(p.units + (c + n) * 8) >= 0) {
+            ++n;
+            if (ld(p.units + (c + n - 1) * 8 + 2)) break;
+        }
+    }
+    if (threadIdx.x == 0) s_most = 0;
+    const uint32_t here = __ballot_sync(0xffffffffu, n > 0);
+    if (lane == 0) s_warp[warp] = __popc(here);
+    __syncthreads();
+    int at_list = __popc(here & ((1u << lane) - 1)), s_n = 0;
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) at_list += s_warp[w];
+        s_n += s_warp[w];
+    }
+    if (n > 0) {
+        s_from[at_list] = threadIdx.x;
+        s_count[at_list] = n;
+        atomicMax(&s_most, n);
+    }
+    __syncthreads();
+    const int rows = p.N * p.gs, parts = s_most > 4 ? 8 : 1, tasks = s_n * rows;
+    const int per = 8 / parts, step = gridDim.x * per;
+    const int first = blockIdx.x * per + (parts == 1 ? warp : 0);
+    for (int i = first; (parts == 8 ? i : i - warp) < tasks; i += step) {
+        float acc[4 * V], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 * V; ++k) acc[k] = 0.f;
+        int64_t out_row = -1;
+        if (i < tasks) {
+            const int unit = i / rows, row = i - unit * rows, c = s_from[unit], n = s_count[unit];
+            const int gi = row / p.N, k = row - gi * p.N;
+            const int32_t r = ld(p.units + c * 8 + 4), set = ld(p.units + c * 8 + 5);
+            const int64_t q0 = p.indptr ? ld(p.indptr + r) : r, e = p.indptr ? ld(p.indptr + r + 1) - q0 : 1;
+            const int64_t at = (int64_t)set * rows + row;
+            if (at < e * p.heads) {
+                out_row = q0 * p.heads + at;
+                auto rec_of = [&](int j) { return ((((int64_t)c + j) * 2 + (j == 0)) * p.gs + gi) * p.N + k; };
+                for (int j = lane; j < n; j += 32) M = fmaxf(M, ld(p.rec_ml + 2 * rec_of(j)));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                const int j0 = parts == 8 ? warp : 0;
+#pragma unroll 2
+                for (int j = j0; j < n; j += parts) {
+                    const int64_t at_rec = rec_of(j);
+                    const float2 ml = ld(reinterpret_cast<const float2 *>(p.rec_ml) + at_rec);
+                    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there
+                    const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
+                    L = fmaf(w, ml.y, L);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float4 x = ld(reinterpret_cast<const float4 *>(p.rec + at_rec * R) + v * 32 + lane);
+                        acc[4 * v] = fmaf(w, x.x, acc[4 * v]);
+                        acc[4 * v + 1] = fmaf(w, x.y, acc[4 * v + 1]);
+                        acc[4 * v + 2] = fmaf(w, x.z, acc[4 * v + 2]);
+                        acc[4 * v + 3] = fmaf(w, x.w, acc[4 * v + 3]);
+                    }
+                }
+            }
+        }
+        if (parts == 8) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s_acc[warp][v * 32 + lane] = make_float4(acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3]);
+            if (lane == 0) s_ml[warp] = make_float2(L, 0.f);
+            __syncthreads();
+            if (out_row >= 0) {
+                float sum = 0.f;
+                for (int w = 0; w < 8; ++w) sum += s_ml[w].x;
+                for (int d = threadIdx.x; d < R / 2; d += blockDim.x) {
+                    float x = 0.f, y = 0.f;
+                    for (int w = 0; w < 8; ++w) {
+                        const float2 a = reinterpret_cast<const float2 *>(s_acc[w])[d];
+                        x += a.x;
+                        y += a.y;
+                    }
+                    reinterpret_cast<uint32_t *>(p.o + out_row * R)[d] = sum == 0.f ? 0u : pack_bf16x2(x / sum, y / sum);
+                }
+            }
+            __syncthreads();
+        } else if (out_row >= 0) {
+            uint2 *out = reinterpret_cast<uint2 *>(p.o + out_row * R);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                out[v * 32 + lane] = L == 0.f ? make_uint2(0u, 0u)
+                                              : make_uint2(pack_bf16x2(acc[4 * v] / L, acc[4 * v + 1] / L),
+                                                           pack_bf16x2(acc[4 * v + 2] / L, acc[4 * v + 3] / L));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+
+constexpr int kLMaxCtas = 160;  // the lists of latent_merge_kernel
+
+static int latent_ctas() { return std::min(num_sms(), kLMaxCtas) & ~1; }
+
+// The workspace: header | the ranges' units | (m, l) of the records | records, two a CTA of 64 rows.
+static size_t latent_bytes(int32_t r) {
+    const size_t ctas = (size_t)latent_ctas();
+    return kWorkspaceHeader + ctas * 32 + ctas * 2 * 64 * 8 + ctas * 2 * 64 * (size_t)r * 4;
+}
+
+template <int R, int N>
+static int launch_latent(LatentParams p, const CUtensorMap &qmap, const CUtensorMap &pmap, cudaStream_t s) {
+    using C = LCfg<R, N>;
+    static_assert(C::kSmem <= 232448, "shared memory");
+    static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_E_CUDA;
+    if (dev >= 64 || !((allowed.load(std::memory_order_relaxed) >> dev) & 1)) {
+        if (cudaFuncSetAttribute(latent_kernel<R, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+            return PKV_E_CUDA;
+        if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
+    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap, pmap) !=
+        cudaSuccess)
+        return PKV_E_CUDA;
+    LatentMerge mp{p.rec, p.rec_ml, p.units, p.indptr, p.ranges, p.gs, p.heads, N, p.o, p.err};
+    return launch_pdl(latent_merge_kernel<R>, dim3((unsigned)(2 * num_sms())), dim3(256), 0, s, true, mp) == cudaSuccess ? PKV_OK
+                                                                                                                        : PKV_E_CUDA;
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_latent_workspace(const pkv_latent_pool *pool, int32_t num_heads, size_t *bytes) {
+    using namespace pkv;
+    const int rc = validate_latent_pool(pool);
+    if (rc) return rc;
+    if (num_heads <= 0 || !bytes) return PKV_E_INVALID;
+    if (num_heads > 1024) return PKV_E_UNSUPPORTED;
+    *bytes = latent_bytes(pool->latent_dim);
+    return PKV_OK;
+}
+
+extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *batch, const void *q, void *o, int64_t total_q,
+                               const int32_t *qo_indptr, int32_t num_heads, float sm_scale, void *workspace, size_t ws_bytes,
+                               void *stream) {
+    using namespace pkv;
+    const int rc = validate_latent_pool(pool);
+    if (rc) return rc;
+    if (!batch || batch->batch < 0 || num_heads <= 0 || total_q < 0) return PKV_E_INVALID;
+    if (num_heads > 1024 || total_q * num_heads >= ((int64_t)1 << 31)) return PKV_E_UNSUPPORTED;
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return PKV_E_INVALID;
+    if (!qo_indptr && total_q != batch->batch) return PKV_E_INVALID;
+    if (batch->batch == 0 || total_q == 0) return PKV_OK;
+    if (!batch->req_to_token || !batch->req_pool_indices || !batch->seq_lens || !q || !o || !workspace) return PKV_E_INVALID;
+    const int shift = page_shift_of(batch);
+    if (shift < 0 || batch->stride < 0 || batch->stride >= ((int64_t)1 << 31) || batch->num_rows < 0) return PKV_E_INVALID;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o)) & 15) return PKV_E_INVALID;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return PKV_E_INVALID;
+    if (ws_bytes < latent_bytes(pool->latent_dim)) return PKV_E_WORKSPACE;
+
+    // Rows a CTA: the smallest N that holds an average request's, for a tile's products take the longer the wider
+    // they are; past 64 two CTAs share a range.  (Any N is right for any batch.)
+    const int64_t rows = (total_q + batch->batch - 1) / batch->batch * num_heads;
+    const int N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    LatentParams p{};
+    p.table = batch->req_to_token;
+    p.stride = batch->stride;
+    p.num_rows = batch->num_rows;
+    p.shift = shift;
+    p.rows = batch->req_pool_indices;
+    p.lens = batch->seq_lens;
+    p.indptr = qo_indptr;
+    p.batch = batch->batch;
+    p.heads = num_heads;
+    p.total_q = total_q;
+    p.num_slots = pool->num_slots;
+    p.o = static_cast<uint16_t *>(o);
+    p.scale_log2 = sm_scale * kLog2eL;
+    p.gs = rows > 64 ? 2 : 1;
+    p.ranges = latent_ctas() / p.gs;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.err = reinterpret_cast<int32_t *>(ws);
+    p.units = reinterpret_cast<int32_t *>(ws + kWorkspaceHeader);
+    p.rec_ml = reinterpret_cast<float *>(ws + kWorkspaceHeader + (size_t)latent_ctas() * 32);
+    p.rec = p.rec_ml + (size_t)latent_ctas() * 2 * 64 * 2;
+    p.wait = wait_policy(wait_limit_ns());
+
+    const int32_t R = pool->latent_dim, row = R + pool->rope_dim;
+    CUtensorMap qmap, pmap;
+    const cuuint64_t qdims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, qstride[1] = {(cuuint64_t)row * 2};
+    const cuuint64_t pdims[2] = {(cuuint64_t)row, (cuuint64_t)pool->num_slots}, pstride[1] = {(cuuint64_t)latent_stride(pool) * 2};
+    const cuuint32_t qbox[2] = {64, (cuuint32_t)N}, pbox[2] = {64, 1};
+    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), qdims, qstride, qbox,
+                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+        encode_tiled(&pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rows, pdims, pstride, pbox, CU_TENSOR_MAP_SWIZZLE_128B) !=
+            CUDA_SUCCESS)
+        return PKV_E_CUDA;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (R == 512)
+        return N == 16 ? launch_latent<512, 16>(p, qmap, pmap, s)
+                       : N == 32 ? launch_latent<512, 32>(p, qmap, pmap, s) : launch_latent<512, 64>(p, qmap, pmap, s);
+    return N == 16 ? launch_latent<256, 16>(p, qmap, pmap, s)
+                   : N == 32 ? launch_latent<256, 32>(p, qmap, pmap, s) : launch_latent<256, 64>(p, qmap, pmap, s);
+}

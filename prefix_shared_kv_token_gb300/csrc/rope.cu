@@ -1,0 +1,414 @@
+// Rotary positions: rope (any heads, in place or not), rope_store (q and k rotated, k and v stored
+// into pool slots in the same pass) and latent_store (a latent normalised, its rotary key rotated,
+// both written as one row of a latent pool).
+//
+// A pair (x1, x2) at frequency f and position p turns by the angle p f:
+//     y1 = m (x1 cos - x2 sin),  y2 = m (x2 cos + x1 sin).
+// f is held as the 64-bit fraction of a turn that one position adds, so the product with p wraps
+// modulo a whole turn by itself: the reduction of the angle is exact, and its error is that of f's
+// last bit, p * 2^-65 turns.  The top 32 bits go through sincospif.  (A float product p f is off by
+// 2^-24 of itself, 0.06 radians at position 10^6; a table of cosines would have to be read.)
+//
+// All three are bandwidth kernels: every element read once and written once, 16 bytes a load.  A
+// warp takes a token, or a part of its heads while there are too few tokens to fill the GPU; a lane
+// keeps one unit of 8 pairs (two 16-byte vectors) and walks the heads with it, so its 8 sines and
+// cosines are computed once for all of them.
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/pkv.h"
+#include "common.cuh"
+#include "latent.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+// A lane's 8 cosines and sines.
+struct Turn {
+    float c[8], s[8];
+};
+
+PKV_DEV Turn turn_of(const uint64_t *phases, int32_t pos, float magnitude) {
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t turns = (uint64_t)(int64_t)pos * ld(phases + i);  // modulo 2^64: modulo a turn
+        float s, c;
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);     // half turns in [-1, 1)
+        t.c[i] = c * magnitude;
+        t.s[i] = s * magnitude;
+    }
+    return t;
+}
+
+PKV_DEV void unpack8(const uint4 &v, float *x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+PKV_DEV uint4 pack8(const float *x) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// The 8 pairs of two vectors: (a[i], b[i]) in the half layout, (x[2i], x[2i + 1]) across a then b in the interleaved one.
+template <bool INTER>
+PKV_DEV void rotate16(float *a, float *b, const Turn &t) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float &x1 = INTER ? (i < 4 ? a[2 * i] : b[2 * i - 8]) : a[i];
+        float &x2 = INTER ? (i < 4 ? a[2 * i + 1] : b[2 * i - 7]) : b[i];
+        const float y1 = fmaf(x1, t.c[i], -x2 * t.s[i]), y2 = fmaf(x2, t.c[i], x1 * t.s[i]);
+        x1 = y1;
+        x2 = y2;
+    }
+}
+
+struct RopeParams {
+    const uint64_t *phases;
+    float magnitude;
+    int32_t rot_units, units;  // units of a head: rotated, in all
+    int32_t last_vecs;         // vectors of the last unit (1 where dim - rot is an odd number of vectors)
+    int32_t half;              // half layout: rot / 2, elements from a pair's first to its second
+    int32_t lane_shift;        // lanes a head: 1 << lane_shift >= units
+    int32_t rot;
+    const uint16_t *q;
+    uint16_t *q_out;
+    int64_t q_tok, q_head, o_tok, o_head;  // strides in elements
+    int32_t hq, hkv, d;
+    const uint16_t *k, *v;
+    int64_t k_tok, v_tok;
+    uint8_t *k_pool, *v_pool;
+    int64_t slot_bytes, num_slots;
+    float k_scale, v_scale;
+    const int32_t *positions, *loc;
+    int64_t n;
+    int32_t parts;             // warps a token
+    int32_t *err;
+};
+
+PKV_DEV void store8(uint16_t *dst, const float *x) { *reinterpret_cast<uint4 *>(dst) = pack8(x); }
+PKV_DEV void store8_e4m3(uint8_t *dst, const float *x, float scale) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
+               (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+}
+
+// STORE 0: rotate q only; 1, 2: k and v into a bf16 or an e4m3 pool too.
+template <bool INTER, int STORE>
+__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int per = 32 >> p.lane_shift;  // heads a warp takes at a time
+    const int u = lane & ((1 << p.lane_shift) - 1), h0 = lane >> p.lane_shift;
+    const bool on = u < p.units, turned = u < p.rot_units;
+    // offsets of the unit's two vectors in its head
+    const int off_a = !turned ? p.rot + 16 * (u - p.rot_units) : INTER ? 16 * u : 8 * u;
+    const int off_b = turned && !INTER ? off_a + p.half : off_a + 8;
+    const bool two = u != p.units - 1 || p.last_vecs == 2;
+    const int heads = p.hq + (STORE ? 2 * p.hkv : 0);
+    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < p.n * p.parts; w += warps) {
+        const int64_t tok = w / p.parts;
+        const int part = (int)(w - tok * p.parts);
+        int32_t slot = 0;
+        bool stored = true;
+        if constexpr (STORE != 0) {
+            slot = ld(p.loc + tok);
+            if (slot == -1) continue;  // a padded token
+            stored = slot >= 0 && slot < p.num_slots;
+            if (!stored && part == 0 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+        }
+        Turn t;
+        bool have = false;
+        constexpr int kInFlight = 4;
+        for (int h = part * per + h0; __any_sync(0xffffffffu, h < heads); h += kInFlight * per * p.parts) {
+            uint4 a[kInFlight], b[kInFlight];
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) {
+                const int hd = h + i * per * p.parts;
+                a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (!on || hd >= heads || (STORE && hd >= p.hq && !stored)) continue;
+                const uint16_t *src;
+                if (!STORE || hd < p.hq) src = p.q + tok * p.q_tok + hd * p.q_head;
+                else if (hd < p.hq + p.hkv) src = p.k + tok * p.k_tok + (hd - p.hq) * p.d;
+                else src = p.v + tok * p.v_tok + (hd - p.hq - p.hkv) * p.d;
+                a[i] = __ldcs(reinterpret_cast<const uint4 *>(src + off_a));
+                if (two) b[i] = __ldcs(reinterpret_cast<const uint4 *>(src + off_b));
+            }
+            if (!have) {  // behind the first loads
+                if (turned) t = turn_of(p.phases + 8 * u, ld(p.positions + tok), p.magnitude);
+                have = true;
+            }
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) {
+                const int hd = h + i * per * p.parts;
+                if (!on || hd >= heads) continue;
+                const bool is_q = !STORE || hd < p.hq, is_v = STORE && hd >= p.hq + p.hkv;
+                if (!is_q && !stored) continue;
+                float x[8], y[8];
+                unpack8(a[i], x);
+                unpack8(b[i], y);
+                if (turned && !is_v) rotate16<INTER>(x, y, t);
+                if (is_q) {
+                    uint16_t *dst = p.q_out + tok * p.o_tok + hd * p.o_head;
+                    store8(dst + off_a, x);
+                    if (two) store8(dst + off_b, y);
+                } else if constexpr (STORE != 0) {
+                    const int g = is_v ? hd - p.hq - p.hkv : hd - p.hq;
+                    uint8_t *dst = (is_v ? p.v_pool : p.k_pool) + (int64_t)slot * p.slot_bytes;
+                    if constexpr (STORE == 1) {
+                        uint16_t *row = reinterpret_cast<uint16_t *>(dst) + g * p.d;
+                        store8(row + off_a, x);
+                        if (two) store8(row + off_b, y);
+                    } else {
+                        const float scale = is_v ? p.v_scale : p.k_scale;
+                        store8_e4m3(dst + g * p.d + off_a, x, scale);
+                        if (two) store8_e4m3(dst + g * p.d + off_b, y, scale);
+                    }
+                }
+            }
+        }
+    }
+}
+
+static int check_spec(const pkv_rope_spec *r) {
+    if (!r || !r->phases || reinterpret_cast<uintptr_t>(r->phases) & 7) return PKV_E_INVALID;
+    if (r->rotary_dim <= 0 || r->rotary_dim % 16) return PKV_E_UNSUPPORTED;
+    if (r->interleaved != 0 && r->interleaved != 1) return PKV_E_INVALID;
+    if (!std::isfinite(r->magnitude)) return PKV_E_INVALID;
+    return PKV_OK;
+}
+
+// Rows of bf16 heads: 16-byte vectors, strides that keep them so.
+static bool rows_ok(const void *x, int64_t tok, int64_t head) {
+    return x && !(reinterpret_cast<uintptr_t>(x) & 15) && tok % 8 == 0 && head % 8 == 0;
+}
+// The same to write to: no two heads or tokens in one place.
+static bool out_ok(const void *x, int64_t tok, int64_t head, int64_t n, int32_t heads) {
+    return rows_ok(x, tok, head) && (tok != 0 || n == 1) && (head != 0 || heads == 1);
+}
+
+static int launch_rope(RopeParams p, const pkv_rope_spec *r, int store, cudaStream_t s) {
+    p.phases = r->phases;
+    p.magnitude = r->magnitude;
+    p.rot = r->rotary_dim;
+    p.half = r->rotary_dim / 2;
+    p.rot_units = r->rotary_dim / 16;
+    const int rest = (p.d - p.rot) / 8;  // vectors behind the rotated part
+    p.units = p.rot_units + (rest + 1) / 2;
+    p.last_vecs = rest & 1 ? 1 : 2;
+    p.lane_shift = 0;
+    while ((1 << p.lane_shift) < p.units) ++p.lane_shift;
+    const int heads = p.hq + (store ? 2 * p.hkv : 0), per = 32 >> p.lane_shift;
+    // Warps a token: all of a token's heads in one warp's steps of four once that fills the GPU
+    // (16 warps an SM), else as many as its heads give work, for then the time is a chain of loads.
+    // One token of 12 steps: 12 warps; 65,536 tokens: 1.
+    const int64_t steps = (heads + per - 1) / per, full = (int64_t)num_sms() * 16;
+    p.parts = (int32_t)std::min<int64_t>(steps, std::max<int64_t>(1, full / p.n));
+    const int64_t blocks = std::min<int64_t>((p.n * p.parts + 7) / 8, (int64_t)num_sms() * 64);
+    auto kern = r->interleaved ? (store == 0 ? rope_kernel<true, 0> : store == 1 ? rope_kernel<true, 1> : rope_kernel<true, 2>)
+                               : (store == 0 ? rope_kernel<false, 0> : store == 1 ? rope_kernel<false, 1> : rope_kernel<false, 2>);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, s, true, p) == cudaSuccess ? PKV_OK : PKV_E_CUDA;
+}
+
+// ------------------------------------------------------------------------------------------
+// latent_store
+
+struct LatentStoreParams {
+    const uint16_t *c, *pe, *w;
+    int64_t c_tok, pe_tok;
+    float eps;
+    const uint64_t *phases;
+    float magnitude;
+    uint16_t *rows;
+    int64_t stride, num_slots;
+    const int32_t *positions, *loc;
+    int64_t n;
+    int32_t *err;
+};
+
+// A warp a token: R / 256 vectors of the latent a lane, the sum of squares over the warp, and the
+// rotary key's four units in lanes 0 to 3, loaded with the rest.
+template <int R, bool INTER>
+__global__ void __launch_bounds__(256) latent_store_kernel(const LatentStoreParams p) {
+    constexpr int V = R / 256;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int off_a = INTER ? 16 * lane : 8 * lane, off_b = INTER ? off_a + 8 : off_a + kLatentRope / 2;
+    float w[8 * V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (p.w) unpack8(ld(reinterpret_cast<const uint4 *>(p.w) + 32 * i + lane), w + 8 * i);
+    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    for (int64_t tok = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; tok < p.n; tok += warps) {
+        const int32_t slot = ld(p.loc + tok);
+        if (slot < 0 || slot >= p.num_slots) {
+            if (slot != -1 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+            continue;  // -1: a padded token
+        }
+        uint4 x[V], a, b;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = __ldcs(reinterpret_cast<const uint4 *>(p.c + tok * p.c_tok) + 32 * i + lane);
+        if (lane < 4) {
+            a = __ldcs(reinterpret_cast<const uint4 *>(p.pe + tok * p.pe_tok + off_a));
+            b = __ldcs(reinterpret_cast<const uint4 *>(p.pe + tok * p.pe_tok + off_b));
+        }
+        uint16_t *row = p.rows + (int64_t)slot * p.stride;
+        if (p.w) {
+            float y[8 * V], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) unpack8(x[i], y + 8 * i);
+#pragma unroll
+            for (int i = 0; i < 8 * V; ++i) sum = fmaf(y[i], y[i], sum);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const float inv = rsqrtf(sum * (1.f / R) + p.eps);
+#pragma unroll
+            for (int i = 0; i < 8 * V; ++i) y[i] = y[i] * inv * w[i];
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = pack8(y + 8 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) reinterpret_cast<uint4 *>(row)[32 * i + lane] = x[i];
+        if (lane < 4) {
+            const Turn t = turn_of(p.phases + 8 * lane, ld(p.positions + tok), p.magnitude);
+            float ya[8], yb[8];
+            unpack8(a, ya);
+            unpack8(b, yb);
+            rotate16<INTER>(ya, yb, t);
+            store8(row + R + off_a, ya);
+            store8(row + R + off_b, yb);
+        }
+    }
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_rope_phases(const double *inv_freq, int32_t n, uint64_t *phases) {
+    if (!inv_freq || !phases || n < 0) return PKV_E_INVALID;
+    for (int32_t i = 0; i < n; ++i)
+        if (!std::isfinite(inv_freq[i])) return PKV_E_INVALID;
+    for (int32_t i = 0; i < n; ++i) {
+        double t = inv_freq[i] / 6.283185307179586476925;  // turns a position; whole ones do not show
+        t -= std::floor(t);
+        phases[i] = t < 1.0 ? (uint64_t)std::ldexp(t, 64) : 0u;
+    }
+    return PKV_OK;
+}
+
+extern "C" int pkv_rope(const pkv_rope_spec *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                        int64_t out_token_stride, int64_t out_head_stride, int32_t num_heads, int32_t dim,
+                        const int32_t *positions, int64_t n, void *stream) {
+    using namespace pkv;
+    const int rc = check_spec(rope);
+    if (rc) return rc;
+    if (n < 0 || num_heads < 0) return PKV_E_INVALID;
+    if (dim < rope->rotary_dim) return PKV_E_INVALID;
+    if (dim % 8 || dim > 512 || n >= ((int64_t)1 << 40) || num_heads > 65536) return PKV_E_UNSUPPORTED;
+    if (n == 0 || num_heads == 0) return PKV_OK;
+    if (!rows_ok(x, x_token_stride, x_head_stride) || !out_ok(out, out_token_stride, out_head_stride, n, num_heads) || !positions)
+        return PKV_E_INVALID;
+    RopeParams p{};
+    p.q = static_cast<const uint16_t *>(x);
+    p.q_tok = x_token_stride;
+    p.q_head = x_head_stride;
+    p.q_out = static_cast<uint16_t *>(out);
+    p.o_tok = out_token_stride;
+    p.o_head = out_head_stride;
+    p.hq = num_heads;
+    p.d = dim;
+    p.positions = positions;
+    p.n = n;
+    return launch_rope(p, rope, 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int pkv_rope_store(const pkv_pool *pool, const pkv_rope_spec *rope, const void *q, int64_t q_token_stride,
+                              int64_t q_head_stride, void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                              int32_t num_q_heads, const void *k_new, int64_t k_token_stride, const void *v_new,
+                              int64_t v_token_stride, const int32_t *positions, const int32_t *out_cache_loc, int64_t n,
+                              void *workspace, void *stream) {
+    using namespace pkv;
+    int rc = validate_pool(pool);
+    if (!rc) rc = check_spec(rope);
+    if (rc) return rc;
+    if (n < 0 || num_q_heads < 0) return PKV_E_INVALID;
+    if (pool->head_dim < rope->rotary_dim) return PKV_E_INVALID;
+    if (n >= ((int64_t)1 << 40) || num_q_heads > 65536 || pool->num_kv_heads > 65536) return PKV_E_UNSUPPORTED;
+    if (n == 0) return PKV_OK;
+    if (num_q_heads > 0 && (!rows_ok(q, q_token_stride, q_head_stride) || !out_ok(q_out, q_out_token_stride, q_out_head_stride, n, num_q_heads)))
+        return PKV_E_INVALID;
+    if (!rows_ok(k_new, k_token_stride, 0) || !rows_ok(v_new, v_token_stride, 0) || !positions || !out_cache_loc)
+        return PKV_E_INVALID;
+    RopeParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_tok = q_token_stride;
+    p.q_head = q_head_stride;
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.o_tok = q_out_token_stride;
+    p.o_head = q_out_head_stride;
+    p.hq = num_q_heads;
+    p.hkv = pool->num_kv_heads;
+    p.d = pool->head_dim;
+    p.k = static_cast<const uint16_t *>(k_new);
+    p.v = static_cast<const uint16_t *>(v_new);
+    p.k_tok = k_token_stride;
+    p.v_tok = v_token_stride;
+    p.k_pool = static_cast<uint8_t *>(pool->k);
+    p.v_pool = static_cast<uint8_t *>(pool->v);
+    p.slot_bytes = slot_bytes(pool);
+    p.num_slots = pool->num_slots;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.positions = positions;
+    p.loc = out_cache_loc;
+    p.n = n;
+    p.err = static_cast<int32_t *>(workspace);
+    return launch_rope(p, rope, pool->dtype == PKV_BF16 ? 1 : 2, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec *rope, const void *c_new, int64_t c_token_stride,
+                                const void *pe_new, int64_t pe_token_stride, const void *norm_weight, float eps,
+                                const int32_t *positions, const int32_t *out_cache_loc, int64_t n, void *workspace, void *stream) {
+    using namespace pkv;
+    int rc = validate_latent_pool(pool);
+    if (!rc) rc = check_spec(rope);
+    if (rc) return rc;
+    if (rope->rotary_dim != pool->rope_dim) return PKV_E_INVALID;
+    if (n < 0) return PKV_E_INVALID;
+    if (n >= ((int64_t)1 << 40)) return PKV_E_UNSUPPORTED;
+    if (n == 0) return PKV_OK;
+    if (!rows_ok(c_new, c_token_stride, 0) || !rows_ok(pe_new, pe_token_stride, 0) || !positions || !out_cache_loc)
+        return PKV_E_INVALID;
+    if (norm_weight && ((reinterpret_cast<uintptr_t>(norm_weight) & 15) || !(eps >= 0.f) || !std::isfinite(eps))) return PKV_E_INVALID;
+    LatentStoreParams p{};
+    p.c = static_cast<const uint16_t *>(c_new);
+    p.pe = static_cast<const uint16_t *>(pe_new);
+    p.w = static_cast<const uint16_t *>(norm_weight);
+    p.c_tok = c_token_stride;
+    p.pe_tok = pe_token_stride;
+    p.eps = eps;
+    p.phases = rope->phases;
+    p.magnitude = rope->magnitude;
+    p.rows = static_cast<uint16_t *>(pool->rows);
+    p.stride = latent_stride(pool);
+    p.num_slots = pool->num_slots;
+    p.positions = positions;
+    p.loc = out_cache_loc;
+    p.n = n;
+    p.err = static_cast<int32_t *>(workspace);
+    const int64_t blocks = std::min<int64_t>((n + 7) / 8, (int64_t)num_sms() * 64);
+    auto kern = pool->latent_dim == 512 ? (rope->interleaved ? latent_store_kernel<512, true> : latent_store_kernel<512, false>)
+                                        : (rope->interleaved ? latent_store_kernel<256, true> : latent_store_kernel<256, false>);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, p) == cudaSuccess
+               ? PKV_OK
+               : PKV_E_CUDA;
+}
