@@ -17,7 +17,8 @@
 // them, Q and P fill the 227 KB.
 //
 // A CTA of 12 warps:
-//   warp 0      gathers the tile's rows by TMA (tile::gather4, four slots a copy, a lane a few of them)
+//   warp 0      loads Q by TMA
+//   warps 2-3   copy the tile's rows, 16 bytes a cp.async, straight into the 128-byte swizzle
 //   warp 1      issues the products, whichever of the next S and the next P V has its operands first
 //   warps 4-11  softmax: S^T from tensor memory (16x32bx2: the 16 lanes that an M of 64 fills, columns split
 //               between the half-warps), a thread one key and N / 4 columns; P back through shared memory
@@ -58,6 +59,8 @@ struct LatentParams {
     const int32_t *rows, *lens, *indptr;  // indptr NULL: one token a request
     int32_t batch, heads;
     int64_t total_q, num_slots;
+    const uint16_t *pool;
+    int64_t pool_stride;                  // elements
     uint16_t *o;
     float scale_log2;
     int32_t gs, ranges;                   // CTAs that share a range; ranges
@@ -263,6 +266,11 @@ PKV_DEV void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32
         : "memory");
 }
 
+// Arrives on bar when this thread's copies so far have landed (the barrier counts on the arrival).
+PKV_DEV void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 PKV_DEV bool finite(uint32_t bits) { return (bits & 0x7F800000u) != 0x7F800000u; }
 // whether one of eight bf16 values is an infinity or a NaN
 PKV_DEV bool nonfinite8(const uint4 &v) {
@@ -323,7 +331,7 @@ PKV_DEV void find_range(const LatentParams &p, LMisc *m, int range) {
 
 template <int R, int N>
 __global__ void __launch_bounds__(kLThreads, 1)
-    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap pmap) {
+    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap) {
     using C = LCfg<R, N>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&m->full[s], 1);
+            mbar_init(&m->full[s], 64);
             mbar_init(&m->empty[s], 1);
         }
         mbar_init(&m->qfull, 1);
@@ -351,10 +359,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) {
-        prefetch_tmap(&qmap);
-        prefetch_tmap(&pmap);
-    }
+    if (warp == 0 && lane == 0) prefetch_tmap(&qmap);
     tc_fence_before();
     pdl_wait();
     pdl_trigger();
@@ -365,70 +370,60 @@ __global__ void __launch_bounds__(kLThreads, 1)
     LSeg s;
 
     if (warp == 0) {
-        // ================= producer =================
-        const int kg = lane & 15;                        // this lane's four keys of a tile
-        constexpr int kHalf = (C::kBlocks + 1) / 2;      // and its blocks of their rows
-        const int b0 = lane < 16 ? 0 : kHalf, b1 = lane < 16 ? kHalf : C::kBlocks;
-        int tp = 0, nq = 0;
-        bool ok = true;
-        while (ok && next_work<N>(p, cur, s, g)) {
-            if (nq > 0) ok = __all_sync(0xffffffffu, lwait(&m->qempty, (nq - 1) & 1, m, p, 1));
-            if (!ok) break;
-            if (lane == 0) {
+        // ================= Q =================
+        if (lane == 0) {
+            int nq = 0;
+            while (next_work<N>(p, cur, s, g)) {
+                if (nq > 0 && !lwait(&m->qempty, (nq - 1) & 1, m, p, 1)) break;
                 mbar_arrive_expect_tx(&m->qfull, C::kBlocks * C::kQBlk);
                 for (int b = 0; b < C::kBlocks; ++b)
                     tma_load_2d(sbase + C::kQOff + b * C::kQBlk, &qmap, b * 64, (int32_t)s.q_row0, &m->qfull);
+                ++nq;
             }
-            ++nq;
+            if (nq > 0) mbar_wait(&m->qfull, (nq - 1) & 1);  // the copies issued land before the CTA leaves
+        }
+    } else if (warp == 2 || warp == 3) {
+        // ================= rows =================
+        // Eight lanes a row's 128-byte block, eight rows a pass of both warps: a thread's rows are in_row + 8 i, so the
+        // swizzle (chunk ^ row mod 8) is the same for all of its copies.
+        const int chunk = threadIdx.x & 7, in_row = (threadIdx.x - 64) >> 3;
+        const uint32_t dst0 = sbase + in_row * 128 + ((chunk ^ in_row) << 4);
+        int tp = 0;
+        bool ok = true;
+        while (ok && next_work<N>(p, cur, s, g)) {
             const int32_t *row = p.table + (int64_t)s.row * p.stride;
-            // the four slots of a tile's keys; beyond the keys that are seen, and for a slot outside the pool, -1,
-            // whose row is zeros
-            auto slots_of = [&](int t, int32_t *slot) {
-                const int k0 = t * kLTile + kg * 4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) slot[i] = -1;
-                if (k0 >= s.vis) return;
-                if (p.shift >= 2) {
-                    const int32_t pg = ld(row + (k0 >> p.shift));
-                    const int64_t at = ((int64_t)pg << p.shift) + (k0 & ((1 << p.shift) - 1));
-                    const bool in = pg >= 0 && at + 3 < p.num_slots;
-                    if (in) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (k0 + i < s.vis) slot[i] = (int32_t)at + i;
-                        return;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (k0 + i >= s.vis) continue;
-                    const int32_t x = table_slot(row, k0 + i, p.shift, p.num_slots);
-                    const bool in = x >= 0 && x < p.num_slots;
-                    if (!in) set_error(p.err, DERR_SLOT_RANGE);
-                    slot[i] = in ? x : -1;
-                }
+            // the slot of this thread's one key of a tile; beyond the keys that are seen, and for a slot outside the pool,
+            // -1, whose row is zeros
+            auto slot_of = [&](int t) -> int32_t {
+                const int k = t * kLTile + in_row + 8 * chunk;
+                if (t >= s.t1 || k >= s.vis) return -1;
+                const int32_t x = table_slot(row, k, p.shift, p.num_slots);
+                if (x >= 0 && x < p.num_slots) return x;
+                set_error(p.err, DERR_SLOT_RANGE);
+                return -1;
             };
-            int32_t slot[4], next[4];
-            slots_of(s.t0, slot);
+            int32_t next = slot_of(s.t0);
             for (int t = s.t0; t < s.t1; ++t, ++tp) {
-                if (t + 1 < s.t1) slots_of(t + 1, next);
+                const int32_t mine = next;
+                next = slot_of(t + 1);
                 const int st = tp % C::kStages;
                 if (tp >= C::kStages) {
                     ok = __all_sync(0xffffffffu, lwait(&m->empty[st], (tp / C::kStages - 1) & 1, m, p, 2));
                     if (!ok) break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&m->full[st], C::kStage);
-                __syncwarp();
-                const uint32_t dst = sbase + st * C::kStage + kg * 512;
-                for (int b = b0; b < b1; ++b)
-                    tma_gather4(dst + b * C::kBlk, &pmap, b * 64, slot[0], slot[1], slot[2], slot[3], &m->full[st]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) slot[i] = next[i];
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t slot = __shfl_sync(0xffffffffu, mine, (lane & 24) | i);
+                    const uint16_t *src = p.pool + (int64_t)max(slot, 0) * p.pool_stride + chunk * 8;
+                    const uint32_t bytes = slot < 0 ? 0u : 16u, dst = dst0 + st * C::kStage + i * 1024;
+#pragma unroll
+                    for (int b = 0; b < C::kBlocks; ++b) cp_async_16(dst + b * C::kBlk, src + b * 64, bytes);
+                }
+                cp_async_arrive(&m->full[st]);
             }
         }
-        // every copy issued lands before the CTA leaves
-        if (nq > 0) mbar_wait(&m->qfull, (nq - 1) & 1);
-        for (int t = max(0, tp - C::kStages); t < tp; ++t) mbar_wait(&m->full[t % C::kStages], (t / C::kStages) & 1);
+        cp_async_commit();
+        cp_async_wait<0>();
     } else if (warp == 1) {
         if (lane == 0) {
             // ================= issuer =================
@@ -468,6 +463,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         if (!q_ready) q_ready = mbar_test_wait(&m->qfull, nqs & 1);
                         const int st = ns % C::kStages;
                         if (q_ready && mbar_test_wait(&m->full[st], (ns / C::kStages) & 1)) {
+                            fence_proxy_async_smem();  // the rows were written by ordinary copies
                             tc_fence_after();
                             const uint32_t k_s = sbase + st * C::kStage, q_s = sbase + C::kQOff;
 #pragma unroll
@@ -864,7 +860,7 @@ static size_t latent_bytes(int32_t r) {
 }
 
 template <int R, int N>
-static int launch_latent(LatentParams p, const CUtensorMap &qmap, const CUtensorMap &pmap, cudaStream_t s) {
+static int launch_latent(LatentParams p, const CUtensorMap &qmap, cudaStream_t s) {
     using C = LCfg<R, N>;
     static_assert(C::kSmem <= 232448, "shared memory");
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much
@@ -875,8 +871,7 @@ static int launch_latent(LatentParams p, const CUtensorMap &qmap, const CUtensor
             return PKV_E_CUDA;
         if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
     }
-    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap, pmap) !=
-        cudaSuccess)
+    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap) != cudaSuccess)
         return PKV_E_CUDA;
     LatentMerge mp{p.rec, p.rec_ml, p.units, p.indptr, p.ranges, p.gs, p.heads, N, p.o, p.err};
     return launch_pdl(latent_merge_kernel<R>, dim3((unsigned)(2 * num_sms())), dim3(256), 0, s, true, mp) == cudaSuccess ? PKV_OK
@@ -929,6 +924,8 @@ extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *bat
     p.heads = num_heads;
     p.total_q = total_q;
     p.num_slots = pool->num_slots;
+    p.pool = static_cast<const uint16_t *>(pool->rows);
+    p.pool_stride = latent_stride(pool);
     p.o = static_cast<uint16_t *>(o);
     p.scale_log2 = sm_scale * kLog2eL;
     p.gs = rows > 64 ? 2 : 1;
@@ -941,19 +938,16 @@ extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *bat
     p.wait = wait_policy(wait_limit_ns());
 
     const int32_t R = pool->latent_dim, row = R + pool->rope_dim;
-    CUtensorMap qmap, pmap;
-    const cuuint64_t qdims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, qstride[1] = {(cuuint64_t)row * 2};
-    const cuuint64_t pdims[2] = {(cuuint64_t)row, (cuuint64_t)pool->num_slots}, pstride[1] = {(cuuint64_t)latent_stride(pool) * 2};
-    const cuuint32_t qbox[2] = {64, (cuuint32_t)N}, pbox[2] = {64, 1};
-    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), qdims, qstride, qbox,
-                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-        encode_tiled(&pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rows, pdims, pstride, pbox, CU_TENSOR_MAP_SWIZZLE_128B) !=
-            CUDA_SUCCESS)
+    CUtensorMap qmap;
+    const cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, strides[1] = {(cuuint64_t)row * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)N};
+    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
         return PKV_E_CUDA;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (R == 512)
-        return N == 16 ? launch_latent<512, 16>(p, qmap, pmap, s)
-                       : N == 32 ? launch_latent<512, 32>(p, qmap, pmap, s) : launch_latent<512, 64>(p, qmap, pmap, s);
-    return N == 16 ? launch_latent<256, 16>(p, qmap, pmap, s)
-                   : N == 32 ? launch_latent<256, 32>(p, qmap, pmap, s) : launch_latent<256, 64>(p, qmap, pmap, s);
+        return N == 16 ? launch_latent<512, 16>(p, qmap, s)
+                       : N == 32 ? launch_latent<512, 32>(p, qmap, s) : launch_latent<512, 64>(p, qmap, s);
+    return N == 16 ? launch_latent<256, 16>(p, qmap, s)
+                   : N == 32 ? launch_latent<256, 32>(p, qmap, s) : launch_latent<256, 64>(p, qmap, s);
 }
