@@ -271,6 +271,14 @@ PKV_DEV void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One lane of a converged warp.  (A branch on this issues a product every 24 cycles, one on lane == 0 every 47 and
+// a predicate from it every 70, for the compiler knows only of this one that the lanes agree.)
+PKV_DEV bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 PKV_DEV bool finite(uint32_t bits) { return (bits & 0x7F800000u) != 0x7F800000u; }
 // whether one of eight bf16 values is an infinity or a NaN
 PKV_DEV bool nonfinite8(const uint4 &v) {
@@ -425,79 +433,91 @@ __global__ void __launch_bounds__(kLThreads, 1)
         cp_async_commit();
         cp_async_wait<0>();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ================= issuer =================
-            // Two cursors over the same tiles: the next S and, up to two behind it, the next P V.
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kLTile, N, 0, 0);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, 1, 1);
-            LCursor pcur = cur;
-            LSeg ps;
-            bool have_s = next_work<N>(p, cur, s, g), have_p = next_work<N>(p, pcur, ps, g);
-            int ts = have_s ? s.t0 : 0, tv = have_p ? ps.t0 : 0;
-            int ns = 0, np = 0, nqs = 0;  // S and P V issued; Q loads consumed
-            bool q_ready = false;
-            while (have_p) {
-                bool did = false;
-                uint64_t t0 = 0;
-                for (uint32_t it = 0; !did; ++it) {
-                    if (np < ns && mbar_test_wait(&m->pfull, np & 1)) {
-                        tc_fence_after();
-                        const int st = np % C::kStages;
-                        const uint32_t v_s = sbase + st * C::kStage, p_s = sbase + C::kPOff;
+        // ================= issuer =================
+        // Two cursors over the same tiles: the next S and, up to two behind it, the next P V.  The whole warp runs the
+        // loop, one lane issues.
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kLTile, N, 0, 0);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, 1, 1);
+        const bool leader = elect_one();
+        const uint64_t rows_k = sdesc_sw128(sbase, 16, 1024), rows_mn = sdesc_sw128(sbase, C::kBlk, 1024);
+        const uint64_t q_k = sdesc_sw128(sbase + C::kQOff, 16, 1024), p_mn = sdesc_sw128(sbase + C::kPOff, C::kBlk, 1024);
+        LCursor pcur = cur;
+        LSeg ps;
+        bool have_s = next_work<N>(p, cur, s, g), have_p = next_work<N>(p, pcur, ps, g);
+        int ts = have_s ? s.t0 : 0, tv = have_p ? ps.t0 : 0;
+        int ns = 0, np = 0, nqs = 0;  // S and P V issued; Q loads consumed
+        bool q_ready = false;
+        while (have_p) {
+            bool did = false;
+            uint64_t t0 = 0;
+            for (uint32_t it = 0; !did; ++it) {
+                if (np < ns && __all_sync(0xffffffffu, mbar_test_wait(&m->pfull, np & 1))) {
+                    tc_fence_after();
+                    const int st = __shfl_sync(0xffffffffu, np % C::kStages, 0);
+                    const uint64_t v = rows_mn + (uint32_t)(st * (C::kStage >> 4));
+                    const uint32_t more = __shfl_sync(0xffffffffu, tv > ps.t0, 0);
+                    const bool last = tv + 1 == ps.t1;
+                    if (leader) {
 #pragma unroll
-                        for (int mb = 0; mb < R / 128; ++mb)
+                        for (int kk = 0; kk < kLTile / 16; ++kk)
 #pragma unroll
-                            for (int kk = 0; kk < kLTile / 16; ++kk)
-                                mma_ss(tmem + C::kColO + mb * N, sdesc_sw128(v_s + 2 * mb * C::kBlk + kk * 2048, C::kBlk, 1024),
-                                       sdesc_sw128(p_s + kk * 2048, C::kBlk, 1024), idesc_o, tv > ps.t0 || kk > 0 ? 1u : 0u);
+                            for (int mb = 0; mb < R / 128; ++mb)
+                                mma_ss(tmem + C::kColO + mb * N, v + ((2 * mb * C::kBlk + kk * 2048) >> 4), p_mn + (kk * 2048 >> 4),
+                                       idesc_o, kk > 0 ? 1u : more);
                         tc_commit(&m->empty[st]);
                         tc_commit(&m->pvdone);
-                        ++np;
-                        if (++tv == ps.t1) {
-                            tc_commit(&m->ofull);
-                            have_p = next_work<N>(p, pcur, ps, g);
-                            tv = have_p ? ps.t0 : 0;
-                        }
-                        did = true;
-                    } else if (have_s && ns < np + 2) {
-                        if (!q_ready) q_ready = mbar_test_wait(&m->qfull, nqs & 1);
-                        const int st = ns % C::kStages;
-                        if (q_ready && mbar_test_wait(&m->full[st], (ns / C::kStages) & 1)) {
-                            fence_proxy_async_smem();  // the rows were written by ordinary copies
-                            tc_fence_after();
-                            const uint32_t k_s = sbase + st * C::kStage, q_s = sbase + C::kQOff;
+                        if (last) tc_commit(&m->ofull);
+                    }
+                    __syncwarp();
+                    ++np;
+                    if (++tv == ps.t1) {
+                        have_p = next_work<N>(p, pcur, ps, g);
+                        tv = have_p ? ps.t0 : 0;
+                    }
+                    did = true;
+                } else if (have_s && ns < np + 2) {
+                    if (!q_ready) q_ready = __all_sync(0xffffffffu, mbar_test_wait(&m->qfull, nqs & 1));
+                    const int st = __shfl_sync(0xffffffffu, ns % C::kStages, 0);
+                    if (q_ready && __all_sync(0xffffffffu, mbar_test_wait(&m->full[st], (ns / C::kStages) & 1))) {
+                        fence_proxy_async_smem();  // the rows were written by ordinary copies
+                        tc_fence_after();
+                        const uint64_t k = rows_k + (uint32_t)(st * (C::kStage >> 4));
+                        const uint32_t d = tmem + __shfl_sync(0xffffffffu, ns & 1, 0) * 64;
+                        const bool last = ts + 1 == s.t1;
+                        if (leader) {
 #pragma unroll
                             for (int ks = 0; ks < (R + 64) / 16; ++ks)
-                                mma_ss(tmem + (ns & 1) * 64, sdesc_sw128(k_s + (ks >> 2) * C::kBlk + (ks & 3) * 32, 16, 1024),
-                                       sdesc_sw128(q_s + (ks >> 2) * C::kQBlk + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
+                                mma_ss(d, k + (((ks >> 2) * C::kBlk + (ks & 3) * 32) >> 4),
+                                       q_k + (((ks >> 2) * C::kQBlk + (ks & 3) * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
                             tc_commit(&m->sfull[ns & 1]);
-                            ++ns;
-                            if (++ts == s.t1) {
-                                tc_commit(&m->qempty);
-                                ++nqs;
-                                q_ready = false;
-                                have_s = next_work<N>(p, cur, s, g);
-                                ts = have_s ? s.t0 : 0;
-                            }
-                            did = true;
+                            if (last) tc_commit(&m->qempty);
                         }
-                    }
-                    if (!did && (it & p.wait.check_mask) == 0) {
-                        const uint64_t now = global_timer_ns();
-                        if (t0 == 0) t0 = now;
-                        if (*reinterpret_cast<volatile int32_t *>(&m->abort_flag)) break;
-                        if (now - t0 > p.wait.limit_ns) {
-                            set_error(p.err, DERR_TIMEOUT | 3);
-                            *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
-                            break;
+                        __syncwarp();
+                        ++ns;
+                        if (++ts == s.t1) {
+                            ++nqs;
+                            q_ready = false;
+                            have_s = next_work<N>(p, cur, s, g);
+                            ts = have_s ? s.t0 : 0;
                         }
+                        did = true;
                     }
                 }
-                if (!did) break;
+                if (!did && (it & p.wait.check_mask) == 0) {
+                    const uint64_t now = global_timer_ns();
+                    if (t0 == 0) t0 = now;
+                    const bool late = now - t0 > p.wait.limit_ns;
+                    if (late) {
+                        set_error(p.err, DERR_TIMEOUT | 3);
+                        *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
+                    }
+                    if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int32_t *>(&m->abort_flag))) break;
+                }
             }
-            tc_commit(&m->drain);  // every product issued completes before tensor memory is freed
-            mbar_wait(&m->drain, 0);
+            if (!did) break;
         }
+        if (leader) tc_commit(&m->drain);  // every product issued completes before tensor memory is freed
+        mbar_wait(&m->drain, 0);
         __syncwarp();
     } else if (warp >= 4) {
         // ================= softmax and output =================
