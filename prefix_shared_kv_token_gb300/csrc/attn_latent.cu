@@ -47,7 +47,9 @@ namespace pkv {
 constexpr int kLTile = 64;              // keys a tile
 constexpr int kLThreads = 384;
 constexpr int kLSoftmax = 256;          // threads of the softmax warps
-constexpr int kLBarVote = 1;            // named barrier of the softmax warps
+constexpr int kLBarHalf = 1;            // named barriers of the softmax warps' halves: 1 and 2
+constexpr float kLUnset = -1e30f;       // a reference before any key was seen
+constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
 constexpr int kLMinTiles = 2;           // a range's tiles at least
 constexpr float kLog2eL = 1.4426950408889634f;
 constexpr float kLagL = 8.0f;           // log2 units by which a logit may pass its reference
@@ -59,8 +61,6 @@ struct LatentParams {
     const int32_t *rows, *lens, *indptr;  // indptr NULL: one token a request
     int32_t batch, heads;
     int64_t total_q, num_slots;
-    const uint16_t *pool;
-    int64_t pool_stride;                  // elements
     uint16_t *o;
     float scale_log2;
     int32_t gs, ranges;                   // CTAs that share a range; ranges
@@ -87,7 +87,7 @@ struct LCfg {
 };
 
 struct LMisc {
-    uint64_t full[4], empty[4];
+    uint64_t full[4], empty[16];  // [stage], [stage][16 keys]
     uint64_t qfull, qempty, sfull[2], pfull, pvdone, ofull, drain;
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -95,7 +95,7 @@ struct LMisc {
     int32_t pad;
     int64_t start_off, left;
     int64_t scan[12];
-    float colmax[4][64];  // a quarter's column maxima; sums at the end
+    float4 col[64];       // the quarters' column maxima; sums at the end
     float alpha[64];
     int32_t lim[64];      // keys that each row sees
 };
@@ -216,18 +216,19 @@ PKV_DEV bool next_work(const LatentParams &p, LCursor &c, LSeg &s, int g) {
 
 // ------------------------------------------------------------------------------------------
 
+// (The timer is read from the 256th retry on: a read takes as long as many a wait, some 700 cycles.)
 PKV_DEV bool lwait(uint64_t *bar, uint32_t parity, LMisc *m, const LatentParams &p, int where) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
         if (p.wait.quick ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if (it == 1 || (it & p.wait.check_mask) == 0) {
-            if (*reinterpret_cast<volatile int32_t *>(&m->abort_flag)) return false;
-            if (global_timer_ns() - t0 > p.wait.limit_ns) {
-                set_error(p.err, DERR_TIMEOUT | where);
-                *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
-                return false;
-            }
+        if ((it & p.wait.check_mask) != p.wait.check_mask) continue;
+        if (*reinterpret_cast<volatile int32_t *>(&m->abort_flag)) return false;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > p.wait.limit_ns) {
+            set_error(p.err, DERR_TIMEOUT | where);
+            *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
+            return false;
         }
     }
 }
@@ -252,23 +253,21 @@ PKV_DEV void tmem_ld_split(uint32_t taddr, uint32_t *r) {
                      : "r"(taddr));
     }
 }
-PKV_DEV void tmem_ld16(uint32_t taddr, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
+PKV_DEV void tmem_ld8(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+PKV_DEV void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 PKV_DEV void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
         : "memory");
-}
-
-// Arrives on bar when this thread's copies so far have landed (the barrier counts on the arrival).
-PKV_DEV void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // One lane of a converged warp.  (A branch on this issues a product every 24 cycles, one on lane == 0 every 47 and
@@ -339,7 +338,7 @@ PKV_DEV void find_range(const LatentParams &p, LMisc *m, int range) {
 
 template <int R, int N>
 __global__ void __launch_bounds__(kLThreads, 1)
-    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap) {
+    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap pmap) {
     using C = LCfg<R, N>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -348,10 +347,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const int g = blockIdx.x % p.gs, range = blockIdx.x / p.gs;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&m->full[s], 64);
-            mbar_init(&m->empty[s], 1);
-        }
+        for (int s = 0; s < C::kStages; ++s) mbar_init(&m->full[s], 2);
+        for (int s = 0; s < C::kStages * 4; ++s) mbar_init(&m->empty[s], 1);
         mbar_init(&m->qfull, 1);
         mbar_init(&m->qempty, 1);
         mbar_init(&m->sfull[0], 1);
@@ -367,7 +364,10 @@ __global__ void __launch_bounds__(kLThreads, 1)
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) prefetch_tmap(&qmap);
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&qmap);
+        prefetch_tmap(&pmap);
+    }
     tc_fence_before();
     pdl_wait();
     pdl_trigger();
@@ -392,50 +392,68 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
     } else if (warp == 2 || warp == 3) {
         // ================= rows =================
-        // Eight lanes a row's 128-byte block, eight rows a pass of both warps: a thread's rows are in_row + 8 i, so the
-        // swizzle (chunk ^ row mod 8) is the same for all of its copies.
-        const int chunk = threadIdx.x & 7, in_row = (threadIdx.x - 64) >> 3;
-        const uint32_t dst0 = sbase + in_row * 128 + ((chunk ^ in_row) << 4);
-        int tp = 0;
+        // Each of the two warps has 32 keys of a tile, 16 by 16 as the product gives them back: in pages of 16 tokens or
+        // more a box of 16 rows a 64-column block, else four gathers of four rows.  All blocks of a row are asked for
+        // together: by groups of columns, so that an S could start with the first, the rows were read from DRAM in
+        // pieces of 256 bytes and 64 ragged requests took 200 us instead of RAGGED_US.
+        const int half = warp - 2;
+        const bool leader = elect_one();
+        const bool box = p.shift >= 4;
+        int tp = 0, issued = 0;  // tiles; of them those with copies to wait for
         bool ok = true;
         while (ok && next_work<N>(p, cur, s, g)) {
             const int32_t *row = p.table + (int64_t)s.row * p.stride;
-            // the slot of this thread's one key of a tile; beyond the keys that are seen, and for a slot outside the pool,
-            // -1, whose row is zeros
+            // the slot of this lane's key (boxes: lanes 0 and 16, their first key's).  Beyond the keys that are seen, and for
+            // a slot outside the pool, a row that is not there, which the copy fills with zeros
             auto slot_of = [&](int t) -> int32_t {
-                const int k = t * kLTile + in_row + 8 * chunk;
-                if (t >= s.t1 || k >= s.vis) return -1;
+                const int k = t * kLTile + half * 32 + lane;
+                if (t >= s.t1 || k >= s.vis) return -16;
                 const int32_t x = table_slot(row, k, p.shift, p.num_slots);
                 if (x >= 0 && x < p.num_slots) return x;
                 set_error(p.err, DERR_SLOT_RANGE);
-                return -1;
+                return -16;
             };
             int32_t next = slot_of(s.t0);
-            for (int t = s.t0; t < s.t1; ++t, ++tp) {
-                const int32_t mine = next;
+            for (int t = s.t0; ok && t < s.t1; ++t, ++tp) {
+                int32_t slot[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) slot[i] = __shfl_sync(0xffffffffu, next, i);
                 next = slot_of(t + 1);
-                const int st = tp % C::kStages;
-                if (tp >= C::kStages) {
-                    ok = __all_sync(0xffffffffu, lwait(&m->empty[st], (tp / C::kStages - 1) & 1, m, p, 2));
+                const int st = __shfl_sync(0xffffffffu, tp % C::kStages, 0);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int quarter = half * 2 + i;
+                    if (tp >= C::kStages)
+                        ok = __all_sync(0xffffffffu, ok && lwait(&m->empty[st * 4 + quarter], (tp / C::kStages - 1) & 1, m, p, 2));
                     if (!ok) break;
-                }
+                    issued = tp + 1;
+                    if (leader) {
+                        const uint32_t dst = sbase + st * C::kStage + quarter * 2048;
+                        if (i == 0) mbar_arrive_expect_tx(&m->full[st], C::kStage / 2);
+                        if (box) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t slot = __shfl_sync(0xffffffffu, mine, (lane & 24) | i);
-                    const uint16_t *src = p.pool + (int64_t)max(slot, 0) * p.pool_stride + chunk * 8;
-                    const uint32_t bytes = slot < 0 ? 0u : 16u, dst = dst0 + st * C::kStage + i * 1024;
+                            for (int b = 0; b < C::kBlocks; ++b)
+                                tma_load_2d(dst + b * C::kBlk, &pmap, b * 64, slot[16 * i], &m->full[st]);
+                        } else {
 #pragma unroll
-                    for (int b = 0; b < C::kBlocks; ++b) cp_async_16(dst + b * C::kBlk, src + b * 64, bytes);
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int b = 0; b < C::kBlocks; ++b)
+                                    tma_gather4(dst + b * C::kBlk + q * 512, &pmap, b * 64, slot[16 * i + 4 * q], slot[16 * i + 4 * q + 1],
+                                                slot[16 * i + 4 * q + 2], slot[16 * i + 4 * q + 3], &m->full[st]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                cp_async_arrive(&m->full[st]);
             }
         }
-        cp_async_commit();
-        cp_async_wait<0>();
+        // every copy issued lands before the CTA leaves
+        for (int t = max(0, issued - C::kStages); t < issued; ++t) mbar_wait(&m->full[t % C::kStages], (t / C::kStages) & 1);
     } else if (warp == 1) {
         // ================= issuer =================
-        // Two cursors over the same tiles: the next S and, up to two behind it, the next P V.  The whole warp runs the
-        // loop, one lane issues.
+        // Two cursors over the same tiles: the next S and, up to two behind it, the next P V, whichever has its operands
+        // first.  A P V goes by 16 keys and gives their rows back as it is done with them.  The whole warp runs the loop,
+        // one lane issues.
         constexpr uint32_t idesc_s = idesc_bf16_f32(kLTile, N, 0, 0);
         constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, 1, 1);
         const bool leader = elect_one();
@@ -459,12 +477,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     const bool last = tv + 1 == ps.t1;
                     if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < kLTile / 16; ++kk)
+                        for (int kk = 0; kk < kLTile / 16; ++kk) {
 #pragma unroll
                             for (int mb = 0; mb < R / 128; ++mb)
                                 mma_ss(tmem + C::kColO + mb * N, v + ((2 * mb * C::kBlk + kk * 2048) >> 4), p_mn + (kk * 2048 >> 4),
                                        idesc_o, kk > 0 ? 1u : more);
-                        tc_commit(&m->empty[st]);
+                            tc_commit(&m->empty[st * 4 + kk]);
+                        }
                         tc_commit(&m->pvdone);
                         if (last) tc_commit(&m->ofull);
                     }
@@ -479,7 +498,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     if (!q_ready) q_ready = __all_sync(0xffffffffu, mbar_test_wait(&m->qfull, nqs & 1));
                     const int st = __shfl_sync(0xffffffffu, ns % C::kStages, 0);
                     if (q_ready && __all_sync(0xffffffffu, mbar_test_wait(&m->full[st], (ns / C::kStages) & 1))) {
-                        fence_proxy_async_smem();  // the rows were written by ordinary copies
                         tc_fence_after();
                         const uint64_t k = rows_k + (uint32_t)(st * (C::kStage >> 4));
                         const uint32_t d = tmem + __shfl_sync(0xffffffffu, ns & 1, 0) * 64;
@@ -503,7 +521,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         did = true;
                     }
                 }
-                if (!did && (it & p.wait.check_mask) == 0) {
+                if (!did && (it & p.wait.check_mask) == p.wait.check_mask) {
                     const uint64_t now = global_timer_ns();
                     if (t0 == 0) t0 = now;
                     const bool late = now - t0 > p.wait.limit_ns;
@@ -521,113 +539,109 @@ __global__ void __launch_bounds__(kLThreads, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ================= softmax and output =================
-        constexpr int NC = C::kCols;
+        // Four warps, a quarter of tensor memory each, have half of the columns from S to the output: the two halves share
+        // nothing but P's barrier.
+        constexpr int NC = C::kCols, NH = N / 2;                   // columns of a thread, of a half
         const int wq = warp & 3, hf = (warp - 4) >> 2;
         const int k_in = wq * 16 + (lane & 15);                    // this thread's key in a tile
-        const int c0 = hf * (N / 2) + (lane >> 4) * NC;            // and its first column
+        const int c0 = hf * NH + (lane >> 4) * NC;                 // and its first column
         const uint32_t quarter = (uint32_t)(wq * 32) << 16;
-        const int st_id = threadIdx.x - 128;
+        const int in_half = wq * 32 + lane, bar = kLBarHalf + hf;
+        const bool scribe = lane == 0 || lane == 16;               // writes what the 16 lanes of its columns have reduced
         int n = 0, nseg = 0;                                       // tiles and pieces before this one
         bool ok = true;
         int32_t *units = p.units + range * 8;
-        if (g == 0 && st_id < 2) units[st_id * 4] = -1;
-        named_bar_sync(kLBarVote, kLSoftmax);
+        if (g == 0 && warp == 4 && lane == 0) units[0] = units[4] = -1;
         while (next_seg<N>(p, cur, s, g)) {
             const int slot_rec = s.first ? 0 : 1;
-            if (g == 0 && st_id == 0 && !s.whole) {
+            if (g == 0 && warp == 4 && lane == 0 && !s.whole) {
                 units[slot_rec * 4 + 1] = s.set;
                 units[slot_rec * 4 + 2] = s.ends;
                 units[slot_rec * 4] = s.r;
             }
             if (s.nrows <= 0) continue;
             // keys that each column sees; columns without a row see what the last row does
-            if (st_id < N) {
-                const int at = min(st_id, s.nrows - 1);
-                m->lim[st_id] = s.vis0 + (s.row_lo + at) / p.heads;
-            }
+            if (in_half < NH) m->lim[hf * NH + in_half] = s.vis0 + (s.row_lo + min(hf * NH + in_half, s.nrows - 1)) / p.heads;
             const int lim_min = s.vis0 + s.row_lo / p.heads;
-            float ref[NC], thr[NC], l[NC];
+            float ref[NC], l[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                ref[c] = 0.f;
-                thr[c] = -INFINITY;  // no reference yet
+                ref[c] = kLUnset;
                 l[c] = 0.f;
             }
-            named_bar_sync(kLBarVote, kLSoftmax);
+            named_bar_sync(bar, kLSoftmax / 2);
             for (int t = s.t0; t < s.t1; ++t, ++n) {
                 ok = __all_sync(0xffffffffu, ok && lwait(&m->sfull[n & 1], (n >> 1) & 1, m, p, 4));
                 uint32_t sv[NC];
-                bool over = false;
-                const bool masked = (t + 1) * kLTile > lim_min;
                 uint32_t hidden = 0;
                 bool odd_row = false;
+                float most = -INFINITY;  // the largest logit above its reference
                 if (ok) {
                     tc_fence_after();
-                    tmem_ld_split<NC>(tmem + quarter + (n & 1) * 64 + hf * (N / 2), sv);
+                    tmem_ld_split<NC>(tmem + quarter + (n & 1) * 64 + hf * NH, sv);
                     tmem_ld_wait();
-                    if (masked) {
+                    if ((t + 1) * kLTile > lim_min) {
                         bool odd = false;
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
-                            if (t * kLTile + k_in >= m->lim[c0 + c]) hidden |= 1u << c;
                             odd |= !finite(sv[c]);
+                            if (t * kLTile + k_in >= m->lim[c0 + c]) {
+                                hidden |= 1u << c;
+                                sv[c] = __float_as_uint(-INFINITY);
+                            }
                         }
                         odd_row = odd && hidden != 0;
                     }
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const float x = __uint_as_float(sv[c]) * p.scale_log2;
-                        sv[c] = __float_as_uint(x);
-                        over |= x > thr[c] && !((hidden >> c) & 1u);
+                        const float x = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c]);
+                        most = fmaxf(most, x);
                     }
                 }
-                if (!named_bar_and(kLBarVote, kLSoftmax, ok && !over)) {
-                    if (!named_bar_and(kLBarVote, kLSoftmax, ok)) {
+                if (!named_bar_and(bar, kLSoftmax / 2, ok && !(most > kLagL))) {
+                    if (!named_bar_and(bar, kLSoftmax / 2, ok)) {
                         ok = false;
                         break;
                     }
                     // raise the references to the tile's maxima where those are higher
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        float x = (hidden >> c) & 1u ? -INFINITY : __uint_as_float(sv[c]);
+                        float x = __uint_as_float(sv[c]) * p.scale_log2;
 #pragma unroll
                         for (int d = 8; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if ((lane & 15) == 0) m->colmax[wq][c0 + c] = x;
+                        if (scribe) reinterpret_cast<float *>(&m->col[c0 + c])[wq] = x;
                     }
-                    named_bar_sync(kLBarVote, kLSoftmax);
+                    named_bar_sync(bar, kLSoftmax / 2);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const float top = fmaxf(fmaxf(m->colmax[0][c0 + c], m->colmax[1][c0 + c]),
-                                                fmaxf(m->colmax[2][c0 + c], m->colmax[3][c0 + c]));
+                        const float4 x = m->col[c0 + c];
+                        const float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
                         float a = 1.f;
-                        if (thr[c] == -INFINITY) {
-                            if (top > -INFINITY) {
-                                ref[c] = top;
-                                thr[c] = top + kLagL;
-                            }
-                        } else if (top > ref[c]) {
-                            a = ex2(ref[c] - top);
+                        if (top > ref[c]) {
+                            a = ex2(ref[c] - top);  // (0 where there was no reference, and l is)
                             ref[c] = top;
-                            thr[c] = top + kLagL;
                             l[c] *= a;
                         }
-                        if (wq == 0 && (lane & 15) == 0) m->alpha[c0 + c] = a;
+                        if (wq == 0 && scribe) m->alpha[c0 + c] = a;
                     }
                     if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 5));
-                    named_bar_sync(kLBarVote, kLSoftmax);
+                    named_bar_sync(bar, kLSoftmax / 2);
                     if (t > s.t0 && ok) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int mb = hf; mb < R / 128; mb += 2)
+                        for (int mb = 0; mb < R / 128; ++mb)
 #pragma unroll 1
-                            for (int cc = 0; cc < N; cc += 16) {
-                                uint32_t ov[16];
+                            for (int cc = hf * NH; cc < (hf + 1) * NH; cc += 8) {
+                                uint32_t ov[8];
                                 const uint32_t at = tmem + quarter + C::kColO + mb * N + cc;
-                                tmem_ld16(at, ov);
+                                tmem_ld8(at, ov);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
-                                tmem_st16(at, ov);
+                                for (int c = 0; c < 8; ++c) {
+                                    // what a column without a reference accumulated is 0, but for a NaN
+                                    ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
+                                }
+                                tmem_st8(at, ov);
                             }
                         tmem_st_wait();
                     }
@@ -635,22 +649,21 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 // weights, rounded to bf16 for the product; what they are divided by sums the rounded ones
                 uint32_t pk[NC / 2];
 #pragma unroll
-                for (int c = 0; c < NC; c += 2) {
-                    float a = ex2(__uint_as_float(sv[c]) - ref[c]), b = ex2(__uint_as_float(sv[c + 1]) - ref[c + 1]);
-                    if (odd_row) {  // a key that is not finite has no weight to be 0
-                        if (__uint_as_float(sv[c]) == -INFINITY) a = NAN;
-                        if (__uint_as_float(sv[c + 1]) == -INFINITY) b = NAN;
-                    }
-                    if ((hidden >> c) & 1u) a = 0.f;
-                    if ((hidden >> (c + 1)) & 1u) b = 0.f;
-                    pk[c / 2] = pack_bf16x2(a, b);
-                    add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
+                for (int c = 0; c < NC; c += 2)
+                    pk[c / 2] = pack_bf16x2(ex2(fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c])),
+                                            ex2(fmaf(__uint_as_float(sv[c + 1]), p.scale_log2, -ref[c + 1])));
+                if (odd_row) {  // a key that is not finite has no weight to be 0 in the columns that see it
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (!((hidden >> c) & 1u) && __uint_as_float(sv[c]) == -INFINITY) pk[c / 2] |= 0x7FFFu << (16 * (c & 1));
                 }
+#pragma unroll
+                for (int c = 0; c < NC; c += 2) add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
                 if (n > 0) ok = __all_sync(0xffffffffu, ok && lwait(&m->pvdone, (n - 1) & 1, m, p, 5));
-                const int st = n % C::kStages;
                 if (odd_row && ok) {
                     // A row with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
                     // from them.  Its latent becomes zeros; the columns that see it have a weight of NaN.
+                    const int st = n % C::kStages;
                     lwait(&m->full[st], (n / C::kStages) & 1, m, p, 7);  // (long complete: the copies, seen by this thread)
                     uint8_t *at = smem + st * C::kStage + k_in * 128;
                     bool bad = false;
@@ -677,69 +690,78 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m->pfull);
             }
-            // the columns' sums, over a warp's keys and then the quarters (colmax and alpha may still be in use)
-            named_bar_sync(kLBarVote, kLSoftmax);
+            // the columns' sums, over a warp's keys and then the quarters (col and alpha may still be in use)
+            named_bar_sync(bar, kLSoftmax / 2);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 float x = l[c];
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                if ((lane & 15) == 0) {
-                    m->colmax[wq][c0 + c] = x;
-                    if (wq == 0) m->alpha[c0 + c] = thr[c] == -INFINITY ? -INFINITY : ref[c];
+                if (scribe) {
+                    reinterpret_cast<float *>(&m->col[c0 + c])[wq] = x;
+                    if (wq == 0) m->alpha[c0 + c] = ref[c] == kLUnset ? -INFINITY : ref[c];
                 }
             }
             const bool any = s.t1 > s.t0;
             if (any) ok = __all_sync(0xffffffffu, ok && lwait(&m->ofull, nseg & 1, m, p, 6));
-            if (!named_bar_and(kLBarVote, kLSoftmax, ok)) break;
+            if (!named_bar_and(bar, kLSoftmax / 2, ok)) {
+                ok = false;
+                break;
+            }
             if (any) ++nseg;
             tc_fence_after();
+            auto sum_of = [&](int c) {
+                const float4 x = m->col[c];
+                return (x.x + x.y) + (x.z + x.w);
+            };
             const int64_t rec = ((int64_t)range * 2 + slot_rec) * p.gs + g;
-            if (!s.whole && st_id < s.nrows)
-                reinterpret_cast<float2 *>(p.rec_ml)[rec * N + st_id] =
-                    make_float2(m->alpha[st_id], m->colmax[0][st_id] + m->colmax[1][st_id] + m->colmax[2][st_id] + m->colmax[3][st_id]);
+            if (!s.whole && in_half < NH)
+                reinterpret_cast<float2 *>(p.rec_ml)[rec * N + hf * NH + in_half] =
+                    make_float2(m->alpha[hf * NH + in_half], sum_of(hf * NH + in_half));
             if (!s.whole && !any) continue;  // its (-inf, 0) says that there is nothing to add
 #pragma unroll 1
-            for (int mb = hf; mb < R / 128; mb += 2) {
-                const int col = mb * 128 + wq * 32 + lane;  // this thread's latent element
-#pragma unroll 1
-                for (int cc = 0; cc < N; cc += 16) {
-                    if (cc >= s.nrows) break;
-                    uint32_t ov[16];
+            for (int cc = hf * NH; cc < (hf + 1) * NH && cc < s.nrows; cc += 8) {
+                float inv[8];
+                if (s.whole) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float x = sum_of(cc + c);
+                        inv[c] = x == 0.f ? 0.f : 1.f / x;
+                    }
+                }
+#pragma unroll
+                for (int mb = 0; mb < R / 128; ++mb) {
+                    const int col = mb * 128 + wq * 32 + lane;  // this thread's latent element
+                    uint32_t ov[8];
                     if (any) {
-                        tmem_ld16(tmem + quarter + C::kColO + mb * N + cc, ov);
+                        tmem_ld8(tmem + quarter + C::kColO + mb * N + cc, ov);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) ov[c] = 0u;
+                        for (int c = 0; c < 8; ++c) ov[c] = 0u;
                     }
                     if (!s.whole) {
                         float *out = p.rec + (rec * N + cc) * R + col;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
+                        for (int c = 0; c < 8; ++c)
                             if (cc + c < s.nrows) out[(int64_t)c * R] = __uint_as_float(ov[c]);
                         continue;
                     }
 #pragma unroll
-                    for (int c = 0; c < 16; c += 2) {
-                        float x[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int k = cc + c + i;
-                            const float sum = m->colmax[0][k] + m->colmax[1][k] + m->colmax[2][k] + m->colmax[3][k];
-                            x[i] = sum == 0.f ? 0.f : __uint_as_float(ov[c + i]) / sum;
-                        }
+                    for (int c = 0; c < 8; c += 2) {
+                        const float x0 = inv[c] == 0.f ? 0.f : __uint_as_float(ov[c]) * inv[c];
+                        const float x1 = inv[c + 1] == 0.f ? 0.f : __uint_as_float(ov[c + 1]) * inv[c + 1];
                         // neighbouring lanes trade a value: even lanes write column c, odd ones c + 1, two elements each
-                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[0] : x[1], 1);
-                        const uint32_t w = lane & 1 ? pack_bf16x2(other, x[1]) : pack_bf16x2(x[0], other);
+                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
+                        const uint32_t w = lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
                         const int k = cc + c + (lane & 1);
                         if (k < s.nrows) reinterpret_cast<uint32_t *>(p.o + (s.q_row0 + k) * R)[col >> 1] = w;
                     }
                 }
             }
             tc_fence_before();
-            // colmax, alpha and lim are read before the next piece writes them
-            named_bar_sync(kLBarVote, kLSoftmax);
+            // col, alpha and lim are read before the next piece writes them
+            named_bar_sync(bar, kLSoftmax / 2);
         }
     }
     tc_fence_before();
@@ -750,8 +772,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
 
 // ------------------------------------------------------------------------------------------
 // Joins the records of units that several ranges share.  A unit's pieces are range c's last record and the
-// first records of the ranges behind it, up to the one in which it ends.  A row of such a unit is a task: for a
-// warp where the units have few records, else for a CTA whose warps take every eighth one.
+// first records of the ranges behind it, up to the one in which it ends.  A row of a unit with up to 8 records is a
+// warp's task; of one with more, 128 elements of a row are a CTA's, every eighth record a warp's.
 
 struct LatentMerge {
     const float *rec, *rec_ml;
@@ -761,115 +783,153 @@ struct LatentMerge {
     const int32_t *err;
 };
 
+// A record's factor under the common maximum; 0 where it saw nothing.  (A maximum of -inf beside a sum that is not 0
+// is a NaN's: no key had a logit to be a maximum.)
+PKV_DEV float weight_of(float2 ml, float M) {
+    if (ml.x == -INFINITY) return ml.y == 0.f ? 0.f : 1.f;
+    return ex2(ml.x - M);
+}
+
 template <int R>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentMerge p) {
+__global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge p) {
     constexpr int V = R / 128;  // float4s a lane
-    __shared__ int32_t s_from[160], s_count[160];
-    __shared__ int32_t s_warp[8], s_most;
-    __shared__ float4 s_acc[8][R / 4];
-    __shared__ float2 s_ml[8];
+    constexpr int kFew = 8;
+    __shared__ int4 s_first[kLMaxCtas], s_last[kLMaxCtas];    // the ranges' units, as they were written
+    __shared__ int32_t s_unit[2][kLMaxCtas];                  // units of few records from one end, of many: range | records << 16
+    __shared__ int32_t s_warp[2][8];
+    __shared__ float4 s_acc[8][32];
+    __shared__ float s_l[8];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (*p.err & DERR_TIMEOUT) return;  // records may be missing
-    // the units to join, in the ranges' order: every CTA has the same list
+    if ((int)threadIdx.x < p.ranges) {
+        s_first[threadIdx.x] = ld(reinterpret_cast<const int4 *>(p.units) + threadIdx.x * 2);
+        s_last[threadIdx.x] = ld(reinterpret_cast<const int4 *>(p.units) + threadIdx.x * 2 + 1);
+    }
+    __syncthreads();
+    // two lists in the ranges' order: every CTA has the same
     int n = 0;
-    if ((int)threadIdx.x < p.ranges && ld(p.units + threadIdx.x * 8 + 4) >= 0) {
+    if ((int)threadIdx.x < p.ranges && s_last[threadIdx.x].x >= 0) {
         const int c = threadIdx.x;
         n = 1;
-        while (c + n < p.ranges && ld(p.units + (c + n) * 8) >= 0) {
+        while (c + n < p.ranges && s_first[c + n].x >= 0) {
             ++n;
-            if (ld(p.units + (c + n - 1) * 8 + 2)) break;
+            if (s_first[c + n - 1].z) break;
         }
     }
-    if (threadIdx.x == 0) s_most = 0;
-    const uint32_t here = __ballot_sync(0xffffffffu, n > 0);
-    if (lane == 0) s_warp[warp] = __popc(here);
+    const uint32_t few = __ballot_sync(0xffffffffu, n > 0 && n <= kFew), many = __ballot_sync(0xffffffffu, n > kFew);
+    if (lane == 0) {
+        s_warp[0][warp] = __popc(few);
+        s_warp[1][warp] = __popc(many);
+    }
     __syncthreads();
-    int at_list = __popc(here & ((1u << lane) - 1)), s_n = 0;
+    int count[2] = {0, 0}, at_list = __popc((n > kFew ? many : few) & ((1u << lane) - 1));
     for (int w = 0; w < 8; ++w) {
-        if (w < warp) at_list += s_warp[w];
-        s_n += s_warp[w];
+        if (w < warp) at_list += s_warp[n > kFew][w];
+        count[0] += s_warp[0][w];
+        count[1] += s_warp[1][w];
     }
-    if (n > 0) {
-        s_from[at_list] = threadIdx.x;
-        s_count[at_list] = n;
-        atomicMax(&s_most, n);
-    }
+    if (n > 0) s_unit[n > kFew][at_list] = threadIdx.x | n << 16;
     __syncthreads();
-    const int rows = p.N * p.gs, parts = s_most > 4 ? 8 : 1, tasks = s_n * rows;
-    const int per = 8 / parts, step = gridDim.x * per;
-    const int first = blockIdx.x * per + (parts == 1 ? warp : 0);
-    for (int i = first; (parts == 8 ? i : i - warp) < tasks; i += step) {
-        float acc[4 * V], M = -INFINITY, L = 0.f;
+    const int rows = p.N * p.gs;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.rec_ml);
+    // where row `row` of a unit goes (-1: nowhere, the unit is shorter)
+    auto out_of = [&](int c, int row) -> int64_t {
+        const int32_t r = s_last[c].x, set = s_last[c].y;
+        const int64_t q0 = p.indptr ? ld(p.indptr + r) : r, e = p.indptr ? ld(p.indptr + r + 1) - q0 : 1;
+        const int64_t at = (int64_t)set * rows + row;
+        return at < e * p.heads ? q0 * p.heads + at : -1;
+    };
+
+    for (int i = blockIdx.x * 8 + warp; i < count[0] * rows; i += gridDim.x * 8) {
+        const int unit = i / rows, row = i - unit * rows, c = s_unit[0][unit] & 0xFFFF, cnt = s_unit[0][unit] >> 16;
+        const int64_t out_row = out_of(c, row);
+        if (out_row < 0) continue;
+        const int gi = row / p.N, k = row - gi * p.N;
+        auto rec_of = [&](int j) { return ((((int64_t)c + j) * 2 + (j == 0)) * p.gs + gi) * p.N + k; };
+        const float2 mine = lane < cnt ? ld(ml + rec_of(lane)) : make_float2(-INFINITY, 0.f);
+        float M = mine.x;
 #pragma unroll
-        for (int k = 0; k < 4 * V; ++k) acc[k] = 0.f;
-        int64_t out_row = -1;
-        if (i < tasks) {
-            const int unit = i / rows, row = i - unit * rows, c = s_from[unit], n = s_count[unit];
-            const int gi = row / p.N, k = row - gi * p.N;
-            const int32_t r = ld(p.units + c * 8 + 4), set = ld(p.units + c * 8 + 5);
-            const int64_t q0 = p.indptr ? ld(p.indptr + r) : r, e = p.indptr ? ld(p.indptr + r + 1) - q0 : 1;
-            const int64_t at = (int64_t)set * rows + row;
-            if (at < e * p.heads) {
-                out_row = q0 * p.heads + at;
-                auto rec_of = [&](int j) { return ((((int64_t)c + j) * 2 + (j == 0)) * p.gs + gi) * p.N + k; };
-                for (int j = lane; j < n; j += 32) M = fmaxf(M, ld(p.rec_ml + 2 * rec_of(j)));
+        for (int d = kFew / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        M = __shfl_sync(0xffffffffu, M, 0);
+        const float weight = weight_of(mine, M);
+        float4 acc[V];
+        float L = 0.f;
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                const int j0 = parts == 8 ? warp : 0;
+        for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-                for (int j = j0; j < n; j += parts) {
-                    const int64_t at_rec = rec_of(j);
-                    const float2 ml = ld(reinterpret_cast<const float2 *>(p.rec_ml) + at_rec);
-                    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there
-                    const float w = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);
-                    L = fmaf(w, ml.y, L);
+        for (int j = 0; j < cnt; ++j) {
+            const float w = __shfl_sync(0xffffffffu, weight, j);
+            L = fmaf(w, __shfl_sync(0xffffffffu, mine.y, j), L);
+            if (w == 0.f) continue;  // nothing was seen there (and nothing written), or nothing is left of it
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float4 x = ld(reinterpret_cast<const float4 *>(p.rec + at_rec * R) + v * 32 + lane);
-                        acc[4 * v] = fmaf(w, x.x, acc[4 * v]);
-                        acc[4 * v + 1] = fmaf(w, x.y, acc[4 * v + 1]);
-                        acc[4 * v + 2] = fmaf(w, x.z, acc[4 * v + 2]);
-                        acc[4 * v + 3] = fmaf(w, x.w, acc[4 * v + 3]);
-                    }
-                }
+            for (int v = 0; v < V; ++v) {
+                const float4 y = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + v * 32 + lane);
+                acc[v] = make_float4(fmaf(w, y.x, acc[v].x), fmaf(w, y.y, acc[v].y), fmaf(w, y.z, acc[v].z), fmaf(w, y.w, acc[v].w));
             }
         }
-        if (parts == 8) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint2 *out = reinterpret_cast<uint2 *>(p.o + out_row * R);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                s_acc[warp][v * 32 + lane] = make_float4(acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3]);
-            if (lane == 0) s_ml[warp] = make_float2(L, 0.f);
-            __syncthreads();
-            if (out_row >= 0) {
-                float sum = 0.f;
-                for (int w = 0; w < 8; ++w) sum += s_ml[w].x;
-                for (int d = threadIdx.x; d < R / 2; d += blockDim.x) {
-                    float x = 0.f, y = 0.f;
-                    for (int w = 0; w < 8; ++w) {
-                        const float2 a = reinterpret_cast<const float2 *>(s_acc[w])[d];
-                        x += a.x;
-                        y += a.y;
-                    }
-                    reinterpret_cast<uint32_t *>(p.o + out_row * R)[d] = sum == 0.f ? 0u : pack_bf16x2(x / sum, y / sum);
-                }
+        for (int v = 0; v < V; ++v)
+            out[v * 32 + lane] = make_uint2(pack_bf16x2(acc[v].x * inv, acc[v].y * inv), pack_bf16x2(acc[v].z * inv, acc[v].w * inv));
+    }
+
+    for (int i = blockIdx.x; i < count[1] * rows * V; i += gridDim.x) {
+        const int chunk = i % V, task = i / V, unit = task / rows, row = task - unit * rows;
+        const int c = s_unit[1][unit] & 0xFFFF, cnt = s_unit[1][unit] >> 16;
+        const int64_t out_row = out_of(c, row);
+        if (out_row < 0) continue;  // (the same for the CTA)
+        const int gi = row / p.N, k = row - gi * p.N;
+        auto rec_of = [&](int j) { return ((((int64_t)c + j) * 2 + (j == 0)) * p.gs + gi) * p.N + k; };
+        float M = -INFINITY, L = 0.f;
+        for (int j = lane; j < cnt; j += 32) M = fmaxf(M, ld(ml + rec_of(j)).x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kInFlight = 5;
+        for (int j0 = warp; j0 < cnt; j0 += 8 * kInFlight) {
+            float2 x[kInFlight];
+            float4 y[kInFlight];
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                const int j = j0 + 8 * u;
+                x[u] = make_float2(-INFINITY, 0.f);
+                y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j >= cnt) continue;
+                x[u] = ld(ml + rec_of(j));
+                y[u] = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + chunk * 32 + lane);
             }
-            __syncthreads();
-        } else if (out_row >= 0) {
-            uint2 *out = reinterpret_cast<uint2 *>(p.o + out_row * R);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                out[v * 32 + lane] = L == 0.f ? make_uint2(0u, 0u)
-                                              : make_uint2(pack_bf16x2(acc[4 * v] / L, acc[4 * v + 1] / L),
-                                                           pack_bf16x2(acc[4 * v + 2] / L, acc[4 * v + 3] / L));
+            for (int u = 0; u < kInFlight; ++u) {
+                const float w = weight_of(x[u], M);
+                L = fmaf(w, x[u].y, L);
+                if (w != 0.f)
+                    acc = make_float4(fmaf(w, y[u].x, acc.x), fmaf(w, y[u].y, acc.y), fmaf(w, y[u].z, acc.z), fmaf(w, y[u].w, acc.w));
+            }
         }
+        s_acc[warp][lane] = acc;
+        if (lane == 0) s_l[warp] = L;
+        __syncthreads();
+        if (warp == 0) {
+            float sum = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const float4 y = s_acc[w][lane];
+                acc = make_float4(acc.x + y.x, acc.y + y.y, acc.z + y.z, acc.w + y.w);
+                sum += s_l[w];
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            reinterpret_cast<uint2 *>(p.o + out_row * R)[chunk * 32 + lane] =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        }
+        __syncthreads();
     }
 }
 
 // ------------------------------------------------------------------------------------------
-
-constexpr int kLMaxCtas = 160;  // the lists of latent_merge_kernel
 
 static int latent_ctas() { return std::min(num_sms(), kLMaxCtas) & ~1; }
 
@@ -880,7 +940,7 @@ static size_t latent_bytes(int32_t r) {
 }
 
 template <int R, int N>
-static int launch_latent(LatentParams p, const CUtensorMap &qmap, cudaStream_t s) {
+static int launch_latent(LatentParams p, const CUtensorMap &qmap, const CUtensorMap &pmap, cudaStream_t s) {
     using C = LCfg<R, N>;
     static_assert(C::kSmem <= 232448, "shared memory");
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much
@@ -891,10 +951,11 @@ static int launch_latent(LatentParams p, const CUtensorMap &qmap, cudaStream_t s
             return PKV_E_CUDA;
         if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
     }
-    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap) != cudaSuccess)
+    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap, pmap) !=
+        cudaSuccess)
         return PKV_E_CUDA;
     LatentMerge mp{p.rec, p.rec_ml, p.units, p.indptr, p.ranges, p.gs, p.heads, N, p.o, p.err};
-    return launch_pdl(latent_merge_kernel<R>, dim3((unsigned)(2 * num_sms())), dim3(256), 0, s, true, mp) == cudaSuccess ? PKV_OK
+    return launch_pdl(latent_merge_kernel<R>, dim3((unsigned)(4 * num_sms())), dim3(256), 0, s, true, mp) == cudaSuccess ? PKV_OK
                                                                                                                         : PKV_E_CUDA;
 }
 
@@ -944,8 +1005,6 @@ extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *bat
     p.heads = num_heads;
     p.total_q = total_q;
     p.num_slots = pool->num_slots;
-    p.pool = static_cast<const uint16_t *>(pool->rows);
-    p.pool_stride = latent_stride(pool);
     p.o = static_cast<uint16_t *>(o);
     p.scale_log2 = sm_scale * kLog2eL;
     p.gs = rows > 64 ? 2 : 1;
@@ -958,16 +1017,20 @@ extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *bat
     p.wait = wait_policy(wait_limit_ns());
 
     const int32_t R = pool->latent_dim, row = R + pool->rope_dim;
-    CUtensorMap qmap;
-    const cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, strides[1] = {(cuuint64_t)row * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)N};
-    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    CUtensorMap qmap, pmap;
+    const cuuint64_t qdims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, qstride[1] = {(cuuint64_t)row * 2};
+    const cuuint64_t pdims[2] = {(cuuint64_t)row, (cuuint64_t)pool->num_slots}, pstride[1] = {(cuuint64_t)latent_stride(pool) * 2};
+    // the pool's rows: 16 neighbours of a page at once, or any four (a gather's box is one row high)
+    const cuuint32_t qbox[2] = {64, (cuuint32_t)N}, pbox[2] = {64, shift >= 4 ? 16u : 1u};
+    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), qdims, qstride, qbox,
+                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+        encode_tiled(&pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rows, pdims, pstride, pbox, CU_TENSOR_MAP_SWIZZLE_128B) !=
+            CUDA_SUCCESS)
         return PKV_E_CUDA;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (R == 512)
-        return N == 16 ? launch_latent<512, 16>(p, qmap, s)
-                       : N == 32 ? launch_latent<512, 32>(p, qmap, s) : launch_latent<512, 64>(p, qmap, s);
-    return N == 16 ? launch_latent<256, 16>(p, qmap, s)
-                   : N == 32 ? launch_latent<256, 32>(p, qmap, s) : launch_latent<256, 64>(p, qmap, s);
+        return N == 16 ? launch_latent<512, 16>(p, qmap, pmap, s)
+                       : N == 32 ? launch_latent<512, 32>(p, qmap, pmap, s) : launch_latent<512, 64>(p, qmap, pmap, s);
+    return N == 16 ? launch_latent<256, 16>(p, qmap, pmap, s)
+                   : N == 32 ? launch_latent<256, 32>(p, qmap, pmap, s) : launch_latent<256, 64>(p, qmap, pmap, s);
 }
