@@ -14,7 +14,7 @@
 // So one copy of a tile feeds both; the accumulator takes R / 128 * N columns of tensor memory,
 // where O itself would take all 512 for any M and leave no room for S; and N may be as small as the
 // rows there are (16, 32 or 64), with M still full.  A tile of 64 keys is 72 KB at R = 512: two of
-// them, Q and P fill the 227 KB.
+// them and Q fill the 227 KB; P takes the place of its tile's rotary keys, which are done with once S is.
 //
 // A CTA of 12 warps:
 //   warp 0      loads Q by TMA
@@ -61,6 +61,8 @@ struct LatentParams {
     const int32_t *rows, *lens, *indptr;  // indptr NULL: one token a request
     int32_t batch, heads;
     int64_t total_q, num_slots;
+    const uint16_t *pool;
+    int64_t pool_stride;                  // elements
     uint16_t *o;
     float scale_log2;
     int32_t gs, ranges;                   // CTAs that share a range; ranges
@@ -79,8 +81,7 @@ struct LCfg {
     static constexpr int kStages = R == 512 ? 2 : 4;
     static constexpr int kQBlk = N * 128;
     static constexpr int kQOff = kStages * kStage;
-    static constexpr int kPOff = kQOff + kBlocks * kQBlk;
-    static constexpr int kMiscOff = kPOff + kLTile * 128;
+    static constexpr int kMiscOff = kQOff + kBlocks * kQBlk;
     static constexpr int kSmem = kMiscOff + 2560;
     static constexpr int kCols = N / 4;                          // columns a softmax thread
     static constexpr uint32_t kColO = 128;                       // O^T block b at kColO + b * N
@@ -88,7 +89,7 @@ struct LCfg {
 
 struct LMisc {
     uint64_t full[4], empty[16];  // [stage], [stage][16 keys]
-    uint64_t qfull, qempty, sfull[2], pfull, pvdone, ofull, drain;
+    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone, ofull, drain;
     uint32_t tmem_base;
     int32_t abort_flag;
     int32_t start_r;      // the range's first request, and the tiles of it that earlier ranges have
@@ -270,6 +271,11 @@ PKV_DEV void tma_load_2d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32
         : "memory");
 }
 
+// Arrives on bar when this thread's copies so far have landed (the barrier counts on the arrival).
+PKV_DEV void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // One lane of a converged warp.  (A branch on this issues a product every 24 cycles, one on lane == 0 every 47 and
 // a predicate from it every 70, for the compiler knows only of this one that the lanes agree.)
 PKV_DEV bool elect_one() {
@@ -338,7 +344,7 @@ PKV_DEV void find_range(const LatentParams &p, LMisc *m, int range) {
 
 template <int R, int N>
 __global__ void __launch_bounds__(kLThreads, 1)
-    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap pmap) {
+    latent_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap) {
     using C = LCfg<R, N>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -347,13 +353,14 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const int g = blockIdx.x % p.gs, range = blockIdx.x / p.gs;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) mbar_init(&m->full[s], 2);
+        for (int s = 0; s < C::kStages; ++s) mbar_init(&m->full[s], 64);
         for (int s = 0; s < C::kStages * 4; ++s) mbar_init(&m->empty[s], 1);
         mbar_init(&m->qfull, 1);
         mbar_init(&m->qempty, 1);
         mbar_init(&m->sfull[0], 1);
         mbar_init(&m->sfull[1], 1);
-        mbar_init(&m->pfull, kLSoftmax / 32);
+        mbar_init(&m->pfull[0], kLSoftmax / 32);  // (two: a warp may be done with a tile before another is with the one before)
+        mbar_init(&m->pfull[1], kLSoftmax / 32);
         mbar_init(&m->pvdone, 1);
         mbar_init(&m->ofull, 1);
         mbar_init(&m->drain, 1);
@@ -364,10 +371,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) {
-        prefetch_tmap(&qmap);
-        prefetch_tmap(&pmap);
-    }
+    if (warp == 0 && lane == 0) prefetch_tmap(&qmap);
     tc_fence_before();
     pdl_wait();
     pdl_trigger();
@@ -392,32 +396,27 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
     } else if (warp == 2 || warp == 3) {
         // ================= rows =================
-        // Each of the two warps has 32 keys of a tile, 16 by 16 as the product gives them back: in pages of 16 tokens or
-        // more a box of 16 rows a 64-column block, else four gathers of four rows.  All blocks of a row are asked for
-        // together: by groups of columns, so that an S could start with the first, the rows were read from DRAM in
-        // pieces of 256 bytes and 64 ragged requests took 200 us instead of RAGGED_US.
-        const int half = warp - 2;
-        const bool leader = elect_one();
-        const bool box = p.shift >= 4;
-        int tp = 0, issued = 0;  // tiles; of them those with copies to wait for
+        // Each of the two warps has 32 keys of a tile, 16 by 16 as the product gives them back.  Four rows a copy, eight
+        // lanes a 128-byte block of each, all blocks of a row after one another: asked for by groups of columns, so that an
+        // S could start with the first, rows came out of DRAM in pieces of 256 bytes (64 ragged requests: 200 us instead of
+        // 128).  TMA is no better here: boxes of 16 rows of a page 138 us, gathers of four rows 180 us.
+        const int half = warp - 2, sub = lane >> 3;
+        int tp = 0;
         bool ok = true;
         while (ok && next_work<N>(p, cur, s, g)) {
             const int32_t *row = p.table + (int64_t)s.row * p.stride;
-            // the slot of this lane's key (boxes: lanes 0 and 16, their first key's).  Beyond the keys that are seen, and for
-            // a slot outside the pool, a row that is not there, which the copy fills with zeros
+            // the slot of this lane's key; beyond the keys that are seen, and for a slot outside the pool, -1: zeros
             auto slot_of = [&](int t) -> int32_t {
                 const int k = t * kLTile + half * 32 + lane;
-                if (t >= s.t1 || k >= s.vis) return -16;
+                if (t >= s.t1 || k >= s.vis) return -1;
                 const int32_t x = table_slot(row, k, p.shift, p.num_slots);
                 if (x >= 0 && x < p.num_slots) return x;
                 set_error(p.err, DERR_SLOT_RANGE);
-                return -16;
+                return -1;
             };
             int32_t next = slot_of(s.t0);
             for (int t = s.t0; ok && t < s.t1; ++t, ++tp) {
-                int32_t slot[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) slot[i] = __shfl_sync(0xffffffffu, next, i);
+                const int32_t mine = next;
                 next = slot_of(t + 1);
                 const int st = __shfl_sync(0xffffffffu, tp % C::kStages, 0);
 #pragma unroll
@@ -426,29 +425,22 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     if (tp >= C::kStages)
                         ok = __all_sync(0xffffffffu, ok && lwait(&m->empty[st * 4 + quarter], (tp / C::kStages - 1) & 1, m, p, 2));
                     if (!ok) break;
-                    issued = tp + 1;
-                    if (leader) {
-                        const uint32_t dst = sbase + st * C::kStage + quarter * 2048;
-                        if (i == 0) mbar_arrive_expect_tx(&m->full[st], C::kStage / 2);
-                        if (box) {
 #pragma unroll
-                            for (int b = 0; b < C::kBlocks; ++b)
-                                tma_load_2d(dst + b * C::kBlk, &pmap, b * 64, slot[16 * i], &m->full[st]);
-                        } else {
+                    for (int j = 0; j < 4; ++j) {
+                        const int32_t at = __shfl_sync(0xffffffffu, mine, 16 * i + 4 * j + sub);
+                        const int r = 4 * j + sub;  // of the quarter; its chunks lie at chunk ^ r mod 8
+                        const uint32_t dst = sbase + st * C::kStage + quarter * 2048 + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                        const uint16_t *src = p.pool + (int64_t)max(at, 0) * p.pool_stride + (lane & 7) * 8;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                                for (int b = 0; b < C::kBlocks; ++b)
-                                    tma_gather4(dst + b * C::kBlk + q * 512, &pmap, b * 64, slot[16 * i + 4 * q], slot[16 * i + 4 * q + 1],
-                                                slot[16 * i + 4 * q + 2], slot[16 * i + 4 * q + 3], &m->full[st]);
-                        }
+                        for (int b = 0; b < C::kBlocks; ++b) cp_async_16(dst + b * C::kBlk, src + b * 64, at < 0 ? 0u : 16u);
                     }
-                    __syncwarp();
                 }
+                if (!ok) break;
+                cp_async_arrive(&m->full[st]);
             }
         }
-        // every copy issued lands before the CTA leaves
-        for (int t = max(0, issued - C::kStages); t < issued; ++t) mbar_wait(&m->full[t % C::kStages], (t / C::kStages) & 1);
+        cp_async_commit();
+        cp_async_wait<0>();  // every copy issued lands before the CTA leaves
     } else if (warp == 1) {
         // ================= issuer =================
         // Two cursors over the same tiles: the next S and, up to two behind it, the next P V, whichever has its operands
@@ -458,7 +450,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, 1, 1);
         const bool leader = elect_one();
         const uint64_t rows_k = sdesc_sw128(sbase, 16, 1024), rows_mn = sdesc_sw128(sbase, C::kBlk, 1024);
-        const uint64_t q_k = sdesc_sw128(sbase + C::kQOff, 16, 1024), p_mn = sdesc_sw128(sbase + C::kPOff, C::kBlk, 1024);
+        const uint64_t q_k = sdesc_sw128(sbase + C::kQOff, 16, 1024);
         LCursor pcur = cur;
         LSeg ps;
         bool have_s = next_work<N>(p, cur, s, g), have_p = next_work<N>(p, pcur, ps, g);
@@ -469,7 +461,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             bool did = false;
             uint64_t t0 = 0;
             for (uint32_t it = 0; !did; ++it) {
-                if (np < ns && __all_sync(0xffffffffu, mbar_test_wait(&m->pfull, np & 1))) {
+                if (np < ns && __all_sync(0xffffffffu, mbar_test_wait(&m->pfull[np & 1], (np >> 1) & 1))) {
                     tc_fence_after();
                     const int st = __shfl_sync(0xffffffffu, np % C::kStages, 0);
                     const uint64_t v = rows_mn + (uint32_t)(st * (C::kStage >> 4));
@@ -480,8 +472,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         for (int kk = 0; kk < kLTile / 16; ++kk) {
 #pragma unroll
                             for (int mb = 0; mb < R / 128; ++mb)
-                                mma_ss(tmem + C::kColO + mb * N, v + ((2 * mb * C::kBlk + kk * 2048) >> 4), p_mn + (kk * 2048 >> 4),
-                                       idesc_o, kk > 0 ? 1u : more);
+                                mma_ss(tmem + C::kColO + mb * N, v + ((2 * mb * C::kBlk + kk * 2048) >> 4),
+                                       v + (((C::kBlocks - 1) * C::kBlk + kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : more);
                             tc_commit(&m->empty[st * 4 + kk]);
                         }
                         tc_commit(&m->pvdone);
@@ -498,6 +490,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     if (!q_ready) q_ready = __all_sync(0xffffffffu, mbar_test_wait(&m->qfull, nqs & 1));
                     const int st = __shfl_sync(0xffffffffu, ns % C::kStages, 0);
                     if (q_ready && __all_sync(0xffffffffu, mbar_test_wait(&m->full[st], (ns / C::kStages) & 1))) {
+                        fence_proxy_async_smem();  // rows that were written by ordinary copies
                         tc_fence_after();
                         const uint64_t k = rows_k + (uint32_t)(st * (C::kStage >> 4));
                         const uint32_t d = tmem + __shfl_sync(0xffffffffu, ns & 1, 0) * 64;
@@ -659,22 +652,21 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < NC; c += 2) add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
-                if (n > 0) ok = __all_sync(0xffffffffu, ok && lwait(&m->pvdone, (n - 1) & 1, m, p, 5));
-                if (odd_row && ok) {
-                    // A row with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
-                    // from them.  Its latent becomes zeros; the columns that see it have a weight of NaN.
-                    const int st = n % C::kStages;
+                const int st = n % C::kStages;
+                if (odd_row) {
+                    // A latent with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
+                    // from them.  It becomes zeros; the columns that see it have a weight of NaN.
                     lwait(&m->full[st], (n / C::kStages) & 1, m, p, 7);  // (long complete: the copies, seen by this thread)
                     uint8_t *at = smem + st * C::kStage + k_in * 128;
                     bool bad = false;
-                    for (int b = 0; b < C::kBlocks; ++b)
+                    for (int b = 0; b < R / 64; ++b)
                         for (int j = 0; j < 8; ++j) bad |= nonfinite8(*reinterpret_cast<const uint4 *>(at + b * C::kBlk + j * 16));
                     if (bad)
                         for (int b = 0; b < R / 64; ++b)
                             for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(at + b * C::kBlk + j * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 {
-                    uint8_t *row = smem + C::kPOff + k_in * 128;
+                    uint8_t *row = smem + st * C::kStage + (C::kBlocks - 1) * C::kBlk + k_in * 128;
                     if constexpr (NC == 16) {
                         const int j = c0 / 8;
                         *reinterpret_cast<uint4 *>(row + ((j ^ (k_in & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
@@ -688,7 +680,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&m->pfull);
+                if (lane == 0) mbar_arrive(&m->pfull[n & 1]);
             }
             // the columns' sums, over a warp's keys and then the quarters (col and alpha may still be in use)
             named_bar_sync(bar, kLSoftmax / 2);
@@ -940,7 +932,7 @@ static size_t latent_bytes(int32_t r) {
 }
 
 template <int R, int N>
-static int launch_latent(LatentParams p, const CUtensorMap &qmap, const CUtensorMap &pmap, cudaStream_t s) {
+static int launch_latent(LatentParams p, const CUtensorMap &qmap, cudaStream_t s) {
     using C = LCfg<R, N>;
     static_assert(C::kSmem <= 232448, "shared memory");
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may use that much
@@ -951,8 +943,7 @@ static int launch_latent(LatentParams p, const CUtensorMap &qmap, const CUtensor
             return PKV_E_CUDA;
         if (dev < 64) allowed.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
     }
-    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap, pmap) !=
-        cudaSuccess)
+    if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap) != cudaSuccess)
         return PKV_E_CUDA;
     LatentMerge mp{p.rec, p.rec_ml, p.units, p.indptr, p.ranges, p.gs, p.heads, N, p.o, p.err};
     return launch_pdl(latent_merge_kernel<R>, dim3((unsigned)(4 * num_sms())), dim3(256), 0, s, true, mp) == cudaSuccess ? PKV_OK
@@ -1005,6 +996,8 @@ extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *bat
     p.heads = num_heads;
     p.total_q = total_q;
     p.num_slots = pool->num_slots;
+    p.pool = static_cast<const uint16_t *>(pool->rows);
+    p.pool_stride = latent_stride(pool);
     p.o = static_cast<uint16_t *>(o);
     p.scale_log2 = sm_scale * kLog2eL;
     p.gs = rows > 64 ? 2 : 1;
@@ -1017,20 +1010,16 @@ extern "C" int pkv_attn_latent(const pkv_latent_pool *pool, const pkv_batch *bat
     p.wait = wait_policy(wait_limit_ns());
 
     const int32_t R = pool->latent_dim, row = R + pool->rope_dim;
-    CUtensorMap qmap, pmap;
-    const cuuint64_t qdims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, qstride[1] = {(cuuint64_t)row * 2};
-    const cuuint64_t pdims[2] = {(cuuint64_t)row, (cuuint64_t)pool->num_slots}, pstride[1] = {(cuuint64_t)latent_stride(pool) * 2};
-    // the pool's rows: 16 neighbours of a page at once, or any four (a gather's box is one row high)
-    const cuuint32_t qbox[2] = {64, (cuuint32_t)N}, pbox[2] = {64, shift >= 4 ? 16u : 1u};
-    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), qdims, qstride, qbox,
-                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-        encode_tiled(&pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->rows, pdims, pstride, pbox, CU_TENSOR_MAP_SWIZZLE_128B) !=
-            CUDA_SUCCESS)
+    CUtensorMap qmap;
+    const cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)(total_q * num_heads)}, strides[1] = {(cuuint64_t)row * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)N};
+    if (encode_tiled(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
         return PKV_E_CUDA;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (R == 512)
-        return N == 16 ? launch_latent<512, 16>(p, qmap, pmap, s)
-                       : N == 32 ? launch_latent<512, 32>(p, qmap, pmap, s) : launch_latent<512, 64>(p, qmap, pmap, s);
-    return N == 16 ? launch_latent<256, 16>(p, qmap, pmap, s)
-                   : N == 32 ? launch_latent<256, 32>(p, qmap, pmap, s) : launch_latent<256, 64>(p, qmap, pmap, s);
+        return N == 16 ? launch_latent<512, 16>(p, qmap, s)
+                       : N == 32 ? launch_latent<512, 32>(p, qmap, s) : launch_latent<512, 64>(p, qmap, s);
+    return N == 16 ? launch_latent<256, 16>(p, qmap, s)
+                   : N == 32 ? launch_latent<256, 32>(p, qmap, s) : launch_latent<256, 64>(p, qmap, s);
 }
