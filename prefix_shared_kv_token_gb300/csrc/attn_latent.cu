@@ -17,9 +17,8 @@
 // them and Q fill the 227 KB; P takes the place of its tile's rotary keys, which are done with once S is.
 //
 // A CTA of 12 warps:
-//   warp 0      loads Q by TMA
-//   warps 2-3   copy the tile's rows, 16 bytes a cp.async, straight into the 128-byte swizzle
-//   warp 1      issues the products, whichever of the next S and the next P V has its operands first
+//   warps 0, 1  issue the products, S and P V
+//   warps 2, 3  copy the tile's rows, 16 bytes a cp.async, straight into the 128-byte swizzle; Q by TMA
 //   warps 4-11  softmax: S^T from tensor memory (16x32bx2: the 16 lanes that an M of 64 fills, columns split
 //               between the half-warps), a thread one key and N / 4 columns; P back through shared memory
 // The softmax needs a column's maximum, which lies across lanes.  A running reference stands in for it: weights
@@ -89,7 +88,7 @@ struct LCfg {
 
 struct LMisc {
     uint64_t full[4], empty[16];  // [stage], [stage][16 keys]
-    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone, ofull, drain;
+    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone, ofull, drain[2];
     uint32_t tmem_base;
     int32_t abort_flag;
     int32_t start_r;      // the range's first request, and the tiles of it that earlier ranges have
@@ -363,7 +362,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
         mbar_init(&m->pfull[1], kLSoftmax / 32);
         mbar_init(&m->pvdone, 1);
         mbar_init(&m->ofull, 1);
-        mbar_init(&m->drain, 1);
+        mbar_init(&m->drain[0], 1);
+        mbar_init(&m->drain[1], 1);
         m->abort_flag = 0;
         fence_mbar_init();
     }
@@ -381,29 +381,91 @@ __global__ void __launch_bounds__(kLThreads, 1)
     LCursor cur = cursor_at(p, m->start_r, m->start_off, m->left, N * p.gs);
     LSeg s;
 
-    if (warp == 0) {
-        // ================= Q =================
-        if (lane == 0) {
-            int nq = 0;
-            while (next_work<N>(p, cur, s, g)) {
-                if (nq > 0 && !lwait(&m->qempty, (nq - 1) & 1, m, p, 1)) break;
-                mbar_arrive_expect_tx(&m->qfull, C::kBlocks * C::kQBlk);
-                for (int b = 0; b < C::kBlocks; ++b)
-                    tma_load_2d(sbase + C::kQOff + b * C::kQBlk, &qmap, b * 64, (int32_t)s.q_row0, &m->qfull);
+    if (warp < 2) {
+        // ================= issuers: warp 0 of S, warp 1 of P V =================
+        // A warp each, for neither's products may wait for the other's operands.  The whole warp runs the loop, one lane
+        // issues.
+        const bool leader = elect_one();
+        bool ok = true;
+        int n = 0, nq = 0;  // tiles; Q loads consumed
+        if (warp == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kLTile, N, 0, 0);
+            const uint64_t rows = sdesc_sw128(sbase, 16, 1024), q = sdesc_sw128(sbase + C::kQOff, 16, 1024);
+            while (ok && next_work<N>(p, cur, s, g)) {
+                ok = __all_sync(0xffffffffu, lwait(&m->qfull, nq & 1, m, p, 1));
+                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                    // the softmax has read what S's place held two tiles ago
+                    if (n >= 2) ok = __all_sync(0xffffffffu, lwait(&m->pfull[n & 1], ((n >> 1) - 1) & 1, m, p, 2));
+                    const int st = __shfl_sync(0xffffffffu, n % C::kStages, 0);
+                    ok = __all_sync(0xffffffffu, ok && lwait(&m->full[st], (n / C::kStages) & 1, m, p, 3));
+                    if (!ok) break;
+                    fence_proxy_async_smem();  // the rows were written by ordinary copies
+                    tc_fence_after();
+                    const uint64_t k = rows + (uint32_t)(st * (C::kStage >> 4));
+                    const uint32_t d = tmem + __shfl_sync(0xffffffffu, n & 1, 0) * 64;
+                    if (leader) {
+#pragma unroll
+                        for (int ks = 0; ks < (R + 64) / 16; ++ks)
+                            mma_ss(d, k + (((ks >> 2) * C::kBlk + (ks & 3) * 32) >> 4), q + (((ks >> 2) * C::kQBlk + (ks & 3) * 32) >> 4),
+                                   idesc, ks > 0 ? 1u : 0u);
+                        tc_commit(&m->sfull[n & 1]);
+                        if (t + 1 == s.t1) tc_commit(&m->qempty);
+                    }
+                    __syncwarp();
+                }
                 ++nq;
             }
-            if (nq > 0) mbar_wait(&m->qfull, (nq - 1) & 1);  // the copies issued land before the CTA leaves
+        } else {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, N, 1, 1);
+            const uint64_t rows = sdesc_sw128(sbase, C::kBlk, 1024);
+            while (ok && next_work<N>(p, cur, s, g)) {
+                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                    ok = __all_sync(0xffffffffu, lwait(&m->pfull[n & 1], (n >> 1) & 1, m, p, 4));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t v = rows + (uint32_t)(__shfl_sync(0xffffffffu, n % C::kStages, 0) * (C::kStage >> 4));
+                    const int st = __shfl_sync(0xffffffffu, n % C::kStages, 0);
+                    const uint32_t more = __shfl_sync(0xffffffffu, t > s.t0, 0);
+                    if (leader) {
+                        // by 16 keys, whose rows are given back as they are done with
+#pragma unroll
+                        for (int kk = 0; kk < kLTile / 16; ++kk) {
+#pragma unroll
+                            for (int mb = 0; mb < R / 128; ++mb)
+                                mma_ss(tmem + C::kColO + mb * N, v + ((2 * mb * C::kBlk + kk * 2048) >> 4),
+                                       v + (((C::kBlocks - 1) * C::kBlk + kk * 2048) >> 4), idesc, kk > 0 ? 1u : more);
+                            tc_commit(&m->empty[st * 4 + kk]);
+                        }
+                        tc_commit(&m->pvdone);
+                        if (t + 1 == s.t1) tc_commit(&m->ofull);
+                    }
+                    __syncwarp();
+                }
+            }
         }
-    } else if (warp == 2 || warp == 3) {
-        // ================= rows =================
+        if (leader) tc_commit(&m->drain[warp]);  // every product issued completes before tensor memory is freed
+        mbar_wait(&m->drain[warp], 0);
+        __syncwarp();
+    } else if (warp < 4) {
+        // ================= Q and rows =================
         // Each of the two warps has 32 keys of a tile, 16 by 16 as the product gives them back.  Four rows a copy, eight
         // lanes a 128-byte block of each, all blocks of a row after one another: asked for by groups of columns, so that an
         // S could start with the first, rows came out of DRAM in pieces of 256 bytes (64 ragged requests: 200 us instead of
         // 128).  TMA is no better here: boxes of 16 rows of a page 138 us, gathers of four rows 180 us.
         const int half = warp - 2, sub = lane >> 3;
-        int tp = 0;
+        int tp = 0, nq = 0;
         bool ok = true;
         while (ok && next_work<N>(p, cur, s, g)) {
+            if (half == 0) {
+                if (nq > 0) ok = __all_sync(0xffffffffu, lwait(&m->qempty, (nq - 1) & 1, m, p, 5));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&m->qfull, C::kBlocks * C::kQBlk);
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        tma_load_2d(sbase + C::kQOff + b * C::kQBlk, &qmap, b * 64, (int32_t)s.q_row0, &m->qfull);
+                }
+                ++nq;
+            }
             const int32_t *row = p.table + (int64_t)s.row * p.stride;
             // the slot of this lane's key; beyond the keys that are seen, and for a slot outside the pool, -1: zeros
             auto slot_of = [&](int t) -> int32_t {
@@ -423,7 +485,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 for (int i = 0; i < 2; ++i) {
                     const int quarter = half * 2 + i;
                     if (tp >= C::kStages)
-                        ok = __all_sync(0xffffffffu, ok && lwait(&m->empty[st * 4 + quarter], (tp / C::kStages - 1) & 1, m, p, 2));
+                        ok = __all_sync(0xffffffffu, ok && lwait(&m->empty[st * 4 + quarter], (tp / C::kStages - 1) & 1, m, p, 6));
                     if (!ok) break;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -441,95 +503,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
         cp_async_commit();
         cp_async_wait<0>();  // every copy issued lands before the CTA leaves
-    } else if (warp == 1) {
-        // ================= issuer =================
-        // Two cursors over the same tiles: the next S and, up to two behind it, the next P V, whichever has its operands
-        // first.  A P V goes by 16 keys and gives their rows back as it is done with them.  The whole warp runs the loop,
-        // one lane issues.
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kLTile, N, 0, 0);
-        constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, 1, 1);
-        const bool leader = elect_one();
-        const uint64_t rows_k = sdesc_sw128(sbase, 16, 1024), rows_mn = sdesc_sw128(sbase, C::kBlk, 1024);
-        const uint64_t q_k = sdesc_sw128(sbase + C::kQOff, 16, 1024);
-        LCursor pcur = cur;
-        LSeg ps;
-        bool have_s = next_work<N>(p, cur, s, g), have_p = next_work<N>(p, pcur, ps, g);
-        int ts = have_s ? s.t0 : 0, tv = have_p ? ps.t0 : 0;
-        int ns = 0, np = 0, nqs = 0;  // S and P V issued; Q loads consumed
-        bool q_ready = false;
-        while (have_p) {
-            bool did = false;
-            uint64_t t0 = 0;
-            for (uint32_t it = 0; !did; ++it) {
-                if (np < ns && __all_sync(0xffffffffu, mbar_test_wait(&m->pfull[np & 1], (np >> 1) & 1))) {
-                    tc_fence_after();
-                    const int st = __shfl_sync(0xffffffffu, np % C::kStages, 0);
-                    const uint64_t v = rows_mn + (uint32_t)(st * (C::kStage >> 4));
-                    const uint32_t more = __shfl_sync(0xffffffffu, tv > ps.t0, 0);
-                    const bool last = tv + 1 == ps.t1;
-                    if (leader) {
-#pragma unroll
-                        for (int kk = 0; kk < kLTile / 16; ++kk) {
-#pragma unroll
-                            for (int mb = 0; mb < R / 128; ++mb)
-                                mma_ss(tmem + C::kColO + mb * N, v + ((2 * mb * C::kBlk + kk * 2048) >> 4),
-                                       v + (((C::kBlocks - 1) * C::kBlk + kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : more);
-                            tc_commit(&m->empty[st * 4 + kk]);
-                        }
-                        tc_commit(&m->pvdone);
-                        if (last) tc_commit(&m->ofull);
-                    }
-                    __syncwarp();
-                    ++np;
-                    if (++tv == ps.t1) {
-                        have_p = next_work<N>(p, pcur, ps, g);
-                        tv = have_p ? ps.t0 : 0;
-                    }
-                    did = true;
-                } else if (have_s && ns < np + 2) {
-                    if (!q_ready) q_ready = __all_sync(0xffffffffu, mbar_test_wait(&m->qfull, nqs & 1));
-                    const int st = __shfl_sync(0xffffffffu, ns % C::kStages, 0);
-                    if (q_ready && __all_sync(0xffffffffu, mbar_test_wait(&m->full[st], (ns / C::kStages) & 1))) {
-                        fence_proxy_async_smem();  // rows that were written by ordinary copies
-                        tc_fence_after();
-                        const uint64_t k = rows_k + (uint32_t)(st * (C::kStage >> 4));
-                        const uint32_t d = tmem + __shfl_sync(0xffffffffu, ns & 1, 0) * 64;
-                        const bool last = ts + 1 == s.t1;
-                        if (leader) {
-#pragma unroll
-                            for (int ks = 0; ks < (R + 64) / 16; ++ks)
-                                mma_ss(d, k + (((ks >> 2) * C::kBlk + (ks & 3) * 32) >> 4),
-                                       q_k + (((ks >> 2) * C::kQBlk + (ks & 3) * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
-                            tc_commit(&m->sfull[ns & 1]);
-                            if (last) tc_commit(&m->qempty);
-                        }
-                        __syncwarp();
-                        ++ns;
-                        if (++ts == s.t1) {
-                            ++nqs;
-                            q_ready = false;
-                            have_s = next_work<N>(p, cur, s, g);
-                            ts = have_s ? s.t0 : 0;
-                        }
-                        did = true;
-                    }
-                }
-                if (!did && (it & p.wait.check_mask) == p.wait.check_mask) {
-                    const uint64_t now = global_timer_ns();
-                    if (t0 == 0) t0 = now;
-                    const bool late = now - t0 > p.wait.limit_ns;
-                    if (late) {
-                        set_error(p.err, DERR_TIMEOUT | 3);
-                        *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
-                    }
-                    if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int32_t *>(&m->abort_flag))) break;
-                }
-            }
-            if (!did) break;
-        }
-        if (leader) tc_commit(&m->drain);  // every product issued completes before tensor memory is freed
-        mbar_wait(&m->drain, 0);
-        __syncwarp();
+        if (nq > 0) mbar_wait(&m->qfull, (nq - 1) & 1);
     } else if (warp >= 4) {
         // ================= softmax and output =================
         // Four warps, a quarter of tensor memory each, have half of the columns from S to the output: the two halves share
@@ -564,7 +538,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             }
             named_bar_sync(bar, kLSoftmax / 2);
             for (int t = s.t0; t < s.t1; ++t, ++n) {
-                ok = __all_sync(0xffffffffu, ok && lwait(&m->sfull[n & 1], (n >> 1) & 1, m, p, 4));
+                ok = __all_sync(0xffffffffu, ok && lwait(&m->sfull[n & 1], (n >> 1) & 1, m, p, 7));
                 uint32_t sv[NC];
                 uint32_t hidden = 0;
                 bool odd_row = false;
@@ -617,7 +591,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         }
                         if (wq == 0 && scribe) m->alpha[c0 + c] = a;
                     }
-                    if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 5));
+                    if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 8));
                     named_bar_sync(bar, kLSoftmax / 2);
                     if (t > s.t0 && ok) {
                         tc_fence_after();
@@ -656,7 +630,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 if (odd_row) {
                     // A latent with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
                     // from them.  It becomes zeros; the columns that see it have a weight of NaN.
-                    lwait(&m->full[st], (n / C::kStages) & 1, m, p, 7);  // (long complete: the copies, seen by this thread)
+                    lwait(&m->full[st], (n / C::kStages) & 1, m, p, 9);  // (long complete: the copies, seen by this thread)
                     uint8_t *at = smem + st * C::kStage + k_in * 128;
                     bool bad = false;
                     for (int b = 0; b < R / 64; ++b)
@@ -695,7 +669,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 }
             }
             const bool any = s.t1 > s.t0;
-            if (any) ok = __all_sync(0xffffffffu, ok && lwait(&m->ofull, nseg & 1, m, p, 6));
+            if (any) ok = __all_sync(0xffffffffu, ok && lwait(&m->ofull, nseg & 1, m, p, 10));
             if (!named_bar_and(bar, kLSoftmax / 2, ok)) {
                 ok = false;
                 break;
