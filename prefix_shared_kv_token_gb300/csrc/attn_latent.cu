@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             for (int t = s.t0; t < s.t1; ++t, ++n) {
                 ok = __all_sync(0xffffffffu, ok && lwait(&m->sfull[n & 1], (n >> 1) & 1, m, p, 7));
                 uint32_t sv[NC];
+                float x[NC];  // logits above their references
                 uint32_t hidden = 0;
                 bool odd_row = false;
                 float most = -INFINITY;  // the largest logit above its reference
@@ -561,8 +562,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     }
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const float x = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c]);
-                        most = fmaxf(most, x);
+                        x[c] = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c]);
+                        most = fmaxf(most, x[c]);
                     }
                 }
                 if (!named_bar_and(bar, kLSoftmax / 2, ok && !(most > kLagL))) {
@@ -573,22 +574,23 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     // raise the references to the tile's maxima where those are higher
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        float x = __uint_as_float(sv[c]) * p.scale_log2;
+                        float y = __uint_as_float(sv[c]) * p.scale_log2;
 #pragma unroll
-                        for (int d = 8; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if (scribe) reinterpret_cast<float *>(&m->col[c0 + c])[wq] = x;
+                        for (int d = 8; d > 0; d >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                        if (scribe) reinterpret_cast<float *>(&m->col[c0 + c])[wq] = y;
                     }
                     named_bar_sync(bar, kLSoftmax / 2);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const float4 x = m->col[c0 + c];
-                        const float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+                        const float4 y = m->col[c0 + c];
+                        const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
                         float a = 1.f;
                         if (top > ref[c]) {
                             a = ex2(ref[c] - top);  // (0 where there was no reference, and l is)
                             ref[c] = top;
                             l[c] *= a;
                         }
+                        x[c] = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c]);
                         if (wq == 0 && scribe) m->alpha[c0 + c] = a;
                     }
                     if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 8));
@@ -617,15 +619,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 uint32_t pk[NC / 2];
 #pragma unroll
                 for (int c = 0; c < NC; c += 2)
-                    pk[c / 2] = pack_bf16x2(ex2(fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c])),
-                                            ex2(fmaf(__uint_as_float(sv[c + 1]), p.scale_log2, -ref[c + 1])));
+                    pk[c / 2] = pack_bf16x2(ex2(x[c]), ex2(x[c + 1]));
                 if (odd_row) {  // a key that is not finite has no weight to be 0 in the columns that see it
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
                         if (!((hidden >> c) & 1u) && __uint_as_float(sv[c]) == -INFINITY) pk[c / 2] |= 0x7FFFu << (16 * (c & 1));
                 }
-#pragma unroll
-                for (int c = 0; c < NC; c += 2) add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
                 const int st = n % C::kStages;
                 if (odd_row) {
                     // A latent with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
@@ -655,6 +654,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m->pfull[n & 1]);
+#pragma unroll
+                for (int c = 0; c < NC; c += 2) add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
             }
             // the columns' sums, over a warp's keys and then the quarters (col and alpha may still be in use)
             named_bar_sync(bar, kLSoftmax / 2);
