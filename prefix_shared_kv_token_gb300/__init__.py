@@ -560,26 +560,24 @@ class Rope:
 
 def _rows(name, t, device, shape) -> tuple:
     """(address, strides) of a bf16 tensor of this shape whose last dimension is dense."""
-    if _torch is not None and isinstance(t, _torch.Tensor) and t.get_device() == device and t.dtype is _torch.bfloat16 \
-            and t.dim() == len(shape) and t.shape == shape and (t.stride(-1) == 1 or shape[-1] == 1):
-        return t.data_ptr(), t.stride()
+    try:
+        if t.get_device() == device and t.dtype is _torch.bfloat16 and t.shape == shape:
+            strides = t.stride()
+            if strides[-1] == 1:
+                return t.data_ptr(), strides
+    except AttributeError:
+        pass
     if not isinstance(t, _torch.Tensor) or t.get_device() != device:
         raise ValueError(f"{name} must be a tensor on the current CUDA device")
-    if t.dtype is not _torch.bfloat16 or t.dim() != len(shape) or t.shape != shape:
+    if t.dtype is not _torch.bfloat16 or t.shape != shape:
         raise ValueError(f"{name} must be bfloat16 of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     raise ValueError(f"{name} must be dense in its last dimension")
 
 
-def _heads(name, t) -> tuple:
+def _heads(name, t):
     if not isinstance(t, _torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a [tokens, heads, dim] tensor")
-    return tuple(t.shape)
-
-
-def _apart(name, t) -> None:
-    """Refuses an output whose elements share memory (an expanded tensor)."""
-    if t.numel() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-        raise ValueError(f"{name} must have a place for each of its elements")
+    return t.shape
 
 
 def rope(x, positions, rope, out=None, stream=None):
@@ -593,7 +591,6 @@ def rope(x, positions, rope, out=None, stream=None):
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
     to, so = _rows("out", out, device, shape)
-    _apart("out", out)
     check("pkv_rope", lib.pkv_rope(spec, at, s[0], s[1], to, so[0], so[1], heads, dim,
                                    _fits("positions", positions, torch.int32, device, (n,)), n, stream))
     return out
@@ -618,7 +615,6 @@ def rope_store(pool: Pool, q, k_new, v_new, positions, out_cache_loc, rope, q_ou
     if q_out is None:
         q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     to, so = _rows("q_out", q_out, device, shape)
-    _apart("q_out", q_out)
     ws, size = (None, 4) if workspace is None else _space(workspace, device)
     if size < 4:
         raise ValueError("workspace must hold the error word (4 bytes)")

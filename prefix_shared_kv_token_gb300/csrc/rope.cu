@@ -29,11 +29,12 @@ struct Turn {
     float c[8], s[8];
 };
 
-PKV_DEV Turn turn_of(const uint64_t *phases, int32_t pos, float magnitude) {
+// Of pairs a .. a + 3 and b .. b + 3.
+PKV_DEV Turn turn_of(const uint64_t *phases, int a, int b, int32_t pos, float magnitude) {
     Turn t;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint64_t turns = (uint64_t)(int64_t)pos * ld(phases + i);  // modulo 2^64: modulo a turn
+        const uint64_t turns = (uint64_t)(int64_t)pos * ld(phases + (i < 4 ? a + i : b + i - 4));  // modulo 2^64: modulo a turn
         float s, c;
         sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);     // half turns in [-1, 1)
         t.c[i] = c * magnitude;
@@ -54,7 +55,7 @@ PKV_DEV uint4 pack8(const float *x) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
-// The 8 pairs of two vectors: (a[i], b[i]) in the half layout, (x[2i], x[2i + 1]) across a then b in the interleaved one.
+// The 8 pairs of two vectors: (a[i], b[i]) in the half layout; in the interleaved one four in a and four in b.
 template <bool INTER>
 PKV_DEV void rotate16(float *a, float *b, const Turn &t) {
 #pragma unroll
@@ -72,7 +73,7 @@ struct RopeParams {
     float magnitude;
     int32_t rot_units, units;  // units of a head: rotated, in all
     int32_t last_vecs;         // vectors of the last unit (1 where dim - rot is an odd number of vectors)
-    int32_t half;              // half layout: rot / 2, elements from a pair's first to its second
+    int32_t half;              // rot / 2
     int32_t lane_shift;        // lanes a head: 1 << lane_shift >= units
     int32_t rot;
     const uint16_t *q;
@@ -102,26 +103,37 @@ PKV_DEV void store8_e4m3(uint8_t *dst, const float *x, float scale) {
 
 // STORE 0: rotate q only; 1, 2: k and v into a bf16 or an e4m3 pool too.
 template <bool INTER, int STORE>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int per = 32 >> p.lane_shift;  // heads a warp takes at a time
     const int u = lane & ((1 << p.lane_shift) - 1), h0 = lane >> p.lane_shift;
     const bool on = u < p.units, turned = u < p.rot_units;
-    // offsets of the unit's two vectors in its head
-    const int off_a = !turned ? p.rot + 16 * (u - p.rot_units) : INTER ? 16 * u : 8 * u;
-    const int off_b = turned && !INTER ? off_a + p.half : off_a + 8;
+    // Offsets of the unit's two vectors in its head: neighbouring lanes have neighbouring vectors, the rotated part's
+    // first half and its second, then the rest's.  (Two neighbours a lane: 65,536 tokens into an e4m3 pool 288 us, not 256.)
+    const int off_a = turned ? 8 * u : p.rot + 8 * (u - p.rot_units);
+    const int off_b = off_a + (turned ? p.half : 8 * (p.units - p.rot_units));
+    const int pair_a = INTER ? 4 * u : 8 * u, pair_b = INTER ? 4 * (u + p.rot_units) : 8 * u + 4;
     const bool two = u != p.units - 1 || p.last_vecs == 2;
     const int heads = p.hq + (STORE ? 2 * p.hkv : 0);
-    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < p.n * p.parts; w += warps) {
+    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5, all = p.n * p.parts;
+    // a token's slot and position are loaded while the one before is worked on
+    int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    int32_t next_slot = 0, next_pos = 0;
+    auto look = [&](int64_t at) {
+        if (at >= all) return;
+        next_pos = ld(p.positions + at / p.parts);
+        if constexpr (STORE != 0) next_slot = ld(p.loc + at / p.parts);
+    };
+    look(w);
+    for (; w < all; w += warps) {
         const int64_t tok = w / p.parts;
         const int part = (int)(w - tok * p.parts);
-        int32_t slot = 0;
+        const int32_t slot = next_slot, pos = next_pos;
+        look(w + warps);
         bool stored = true;
         if constexpr (STORE != 0) {
-            slot = ld(p.loc + tok);
             if (slot == -1) continue;  // a padded token
             stored = slot >= 0 && slot < p.num_slots;
             if (!stored && part == 0 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
@@ -144,7 +156,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
                 if (two) b[i] = __ldcs(reinterpret_cast<const uint4 *>(src + off_b));
             }
             if (!have) {  // behind the first loads
-                if (turned) t = turn_of(p.phases + 8 * u, ld(p.positions + tok), p.magnitude);
+                if (turned) t = turn_of(p.phases, pair_a, pair_b, pos, p.magnitude);
                 have = true;
             }
 #pragma unroll
@@ -213,7 +225,7 @@ static int launch_rope(RopeParams p, const pkv_rope_spec *r, int store, cudaStre
     // One token of 12 steps: 12 warps; 65,536 tokens: 1.
     const int64_t steps = (heads + per - 1) / per, full = (int64_t)num_sms() * 16;
     p.parts = (int32_t)std::min<int64_t>(steps, std::max<int64_t>(1, full / p.n));
-    const int64_t blocks = std::min<int64_t>((p.n * p.parts + 7) / 8, (int64_t)num_sms() * 64);
+    const int64_t blocks = std::min<int64_t>((p.n * p.parts + 7) / 8, (int64_t)num_sms() * 32);
     auto kern = r->interleaved ? (store == 0 ? rope_kernel<true, 0> : store == 1 ? rope_kernel<true, 1> : rope_kernel<true, 2>)
                                : (store == 0 ? rope_kernel<false, 0> : store == 1 ? rope_kernel<false, 1> : rope_kernel<false, 2>);
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, s, true, p) == cudaSuccess ? PKV_OK : PKV_E_CUDA;
@@ -235,58 +247,77 @@ struct LatentStoreParams {
     int32_t *err;
 };
 
-// A warp a token: R / 256 vectors of the latent a lane, the sum of squares over the warp, and the
-// rotary key's four units in lanes 0 to 3, loaded with the rest.
+// A warp two tokens at a time: R / 256 vectors of a latent a lane, the sums of squares over the warp, and
+// the rotary key's four units in lanes 0 to 3 (the second token's in lanes 4 to 7), loaded with the rest.  A token's loads are
+// issued before its slot is known: what bounds the kernel is how many are in flight.  131,072 tokens 60 us, 5.1 TB/s (one at a time,
+// the slot first: 84 us).
 template <int R, bool INTER>
 __global__ void __launch_bounds__(256) latent_store_kernel(const LatentStoreParams p) {
     constexpr int V = R / 256;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int off_a = INTER ? 16 * lane : 8 * lane, off_b = INTER ? off_a + 8 : off_a + kLatentRope / 2;
-    float w[8 * V];
+    const int lane = threadIdx.x & 31, u = lane & 3, mine = lane >> 2;  // (lanes 8 and up have no unit)
+    const int off_a = 8 * u, off_b = off_a + kLatentRope / 2;
+    uint4 w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        if (p.w) unpack8(ld(reinterpret_cast<const uint4 *>(p.w) + 32 * i + lane), w + 8 * i);
+        if (p.w) w[i] = ld(reinterpret_cast<const uint4 *>(p.w) + 32 * i + lane);
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t tok = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; tok < p.n; tok += warps) {
-        const int32_t slot = ld(p.loc + tok);
-        if (slot < 0 || slot >= p.num_slots) {
-            if (slot != -1 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
-            continue;  // -1: a padded token
+    for (int64_t tok = (((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * 2; tok < p.n; tok += 2 * warps) {
+        const bool two = tok + 1 < p.n;
+        uint4 x[2][V], a, b;
+        int32_t slot[2], pos = 0;
+        const bool turns = mine == 0 || (mine == 1 && two);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            slot[k] = k == 0 || two ? ld(p.loc + tok + k) : -1;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (k == 0 || two) x[k][i] = __ldcs(reinterpret_cast<const uint4 *>(p.c + (tok + k) * p.c_tok) + 32 * i + lane);
         }
-        uint4 x[V], a, b;
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = __ldcs(reinterpret_cast<const uint4 *>(p.c + tok * p.c_tok) + 32 * i + lane);
-        if (lane < 4) {
-            a = __ldcs(reinterpret_cast<const uint4 *>(p.pe + tok * p.pe_tok + off_a));
-            b = __ldcs(reinterpret_cast<const uint4 *>(p.pe + tok * p.pe_tok + off_b));
-        }
-        uint16_t *row = p.rows + (int64_t)slot * p.stride;
-        if (p.w) {
-            float y[8 * V], sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) unpack8(x[i], y + 8 * i);
-#pragma unroll
-            for (int i = 0; i < 8 * V; ++i) sum = fmaf(y[i], y[i], sum);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float inv = rsqrtf(sum * (1.f / R) + p.eps);
-#pragma unroll
-            for (int i = 0; i < 8 * V; ++i) y[i] = y[i] * inv * w[i];
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = pack8(y + 8 * i);
+        if (turns) {
+            pos = ld(p.positions + tok + mine);
+            a = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (tok + mine) * p.pe_tok + off_a));
+            b = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (tok + mine) * p.pe_tok + off_b));
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) reinterpret_cast<uint4 *>(row)[32 * i + lane] = x[i];
-        if (lane < 4) {
-            const Turn t = turn_of(p.phases + 8 * lane, ld(p.positions + tok), p.magnitude);
+        for (int k = 0; k < 2; ++k) {
+            if (slot[k] < 0 || slot[k] >= p.num_slots) {
+                if (slot[k] != -1 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+                slot[k] = -1;  // padding, or not there
+                continue;
+            }
+            if (p.w) {
+                float y[8 * V], z[8], sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) unpack8(x[k][i], y + 8 * i);
+#pragma unroll
+                for (int i = 0; i < 8 * V; ++i) sum = fmaf(y[i], y[i], sum);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const float inv = rsqrtf(sum * (1.f / R) + p.eps);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    unpack8(w[i], z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[j] *= y[8 * i + j] * inv;
+                    x[k][i] = pack8(z);
+                }
+            }
+            uint4 *row = reinterpret_cast<uint4 *>(p.rows + (int64_t)slot[k] * p.stride);
+#pragma unroll
+            for (int i = 0; i < V; ++i) row[32 * i + lane] = x[k][i];
+        }
+        const int32_t to = mine == 0 ? slot[0] : slot[1];
+        if (turns && to >= 0) {
+            const Turn t = turn_of(p.phases, INTER ? 4 * u : 8 * u, INTER ? 4 * (u + 4) : 8 * u + 4, pos, p.magnitude);
             float ya[8], yb[8];
             unpack8(a, ya);
             unpack8(b, yb);
             rotate16<INTER>(ya, yb, t);
-            store8(row + R + off_a, ya);
-            store8(row + R + off_b, yb);
+            uint16_t *row = p.rows + (int64_t)to * p.stride + R;
+            store8(row + off_a, ya);
+            store8(row + off_b, yb);
         }
     }
 }
@@ -405,7 +436,7 @@ extern "C" int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec
     p.loc = out_cache_loc;
     p.n = n;
     p.err = static_cast<int32_t *>(workspace);
-    const int64_t blocks = std::min<int64_t>((n + 7) / 8, (int64_t)num_sms() * 64);
+    const int64_t blocks = std::min<int64_t>((n + 15) / 16, (int64_t)num_sms() * 4);
     auto kern = pool->latent_dim == 512 ? (rope->interleaved ? latent_store_kernel<512, true> : latent_store_kernel<512, false>)
                                         : (rope->interleaved ? latent_store_kernel<256, true> : latent_store_kernel<256, false>);
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, p) == cudaSuccess
