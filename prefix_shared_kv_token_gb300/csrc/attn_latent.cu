@@ -49,6 +49,7 @@ constexpr int kLSoftmax = 256;          // threads of the softmax warps
 constexpr int kLBarHalf = 1;            // named barriers of the softmax warps' halves: 1 and 2
 constexpr float kLUnset = -1e30f;       // a reference before any key was seen
 constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
+constexpr int32_t kLLongest = 0x7FFFFF00;  // keys of a request: tiles' ends stay within 32 bits
 constexpr int kLMinTiles = 2;           // a range's tiles at least
 constexpr float kLog2eL = 1.4426950408889634f;
 constexpr float kLagL = 8.0f;           // log2 units by which a logit may pass its reference
@@ -125,7 +126,8 @@ PKV_DEV LReq load_req(const LatentParams &p, int r, int rps, bool report) {
         bad = true;
         q.e = 0;
     }
-    if (q.row < 0 || q.row >= p.num_rows || q.len < 0 || (int64_t)q.len > (p.stride << p.shift)) {
+    if (q.row < 0 || q.row >= p.num_rows || q.len < 0 || q.len > kLLongest ||
+        (int64_t)q.len > (p.stride << p.shift)) {
         bad = true;
         q.len = 0;
     }
@@ -549,16 +551,14 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     tmem_ld_split<NC>(tmem + quarter + (n & 1) * 64 + hf * NH, sv);
                     tmem_ld_wait();
                     if ((t + 1) * kLTile > lim_min) {
-                        bool odd = false;
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
-                            odd |= !finite(sv[c]);
+                            odd_row |= !finite(sv[c]);
                             if (t * kLTile + k_in >= m->lim[c0 + c]) {
                                 hidden |= 1u << c;
                                 sv[c] = __float_as_uint(-INFINITY);
                             }
                         }
-                        odd_row = odd && hidden != 0;
                     }
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         ok = false;
                         break;
                     }
-                    // raise the references to the tile's maxima where those are higher
+                    // raise to the tile's maxima the references that those pass
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         float y = __uint_as_float(sv[c]) * p.scale_log2;
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         const float4 y = m->col[c0 + c];
                         const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
                         float a = 1.f;
-                        if (top > ref[c]) {
+                        if (top > ref[c] + kLagL) {  // (a column's references follow its own logits alone)
                             a = ex2(ref[c] - top);  // (0 where there was no reference, and l is)
                             ref[c] = top;
                             l[c] *= a;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 }
                 const int st = n % C::kStages;
                 if (odd_row) {
-                    // A latent with an infinity or a NaN that some columns do not see: a weight of 0 would not keep it
+                    // A latent with an infinity or a NaN that some columns may not see: a weight of 0 would not keep it
                     // from them.  It becomes zeros; the columns that see it have a weight of NaN.
                     lwait(&m->full[st], (n / C::kStages) & 1, m, p, 9);  // (long complete: the copies, seen by this thread)
                     uint8_t *at = smem + st * C::kStage + k_in * 128;

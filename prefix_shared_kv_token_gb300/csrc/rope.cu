@@ -331,7 +331,7 @@ extern "C" int pkv_rope_phases(const double *inv_freq, int32_t n, uint64_t *phas
     for (int32_t i = 0; i < n; ++i) {
         double t = inv_freq[i] / 6.283185307179586476925;  // turns a position; whole ones do not show
         t -= std::floor(t);
-        phases[i] = t < 1.0 ? (uint64_t)std::ldexp(t, 64) : 0u;
+        phases[i] = t < 1.0 ? (uint64_t)std::rint(std::ldexp(t, 64)) : 0u;
     }
     return PKV_OK;
 }
@@ -379,6 +379,7 @@ extern "C" int pkv_rope_store(const pkv_pool *pool, const pkv_rope_spec *rope, c
         return PKV_E_INVALID;
     if (!rows_ok(k_new, k_token_stride, 0) || !rows_ok(v_new, v_token_stride, 0) || !positions || !out_cache_loc)
         return PKV_E_INVALID;
+    if (reinterpret_cast<uintptr_t>(workspace) & 3) return PKV_E_INVALID;
     RopeParams p{};
     p.q = static_cast<const uint16_t *>(q);
     p.q_tok = q_token_stride;
@@ -419,6 +420,7 @@ extern "C" int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec
     if (n == 0) return PKV_OK;
     if (!rows_ok(c_new, c_token_stride, 0) || !rows_ok(pe_new, pe_token_stride, 0) || !positions || !out_cache_loc)
         return PKV_E_INVALID;
+    if (reinterpret_cast<uintptr_t>(workspace) & 3) return PKV_E_INVALID;
     if (norm_weight && ((reinterpret_cast<uintptr_t>(norm_weight) & 15) || !(eps >= 0.f) || !std::isfinite(eps))) return PKV_E_INVALID;
     LatentStoreParams p{};
     p.c = static_cast<const uint16_t *>(c_new);
