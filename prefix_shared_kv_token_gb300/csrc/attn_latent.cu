@@ -696,17 +696,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         inv[c] = x == 0.f ? 0.f : 1.f / x;
                     }
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int mb = 0; mb < R / 128; ++mb) {
                     const int col = mb * 128 + wq * 32 + lane;  // this thread's latent element
                     uint32_t ov[8];
-                    if (any) {
-                        tmem_ld8(tmem + quarter + C::kColO + mb * N + cc, ov);
-                        tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) ov[c] = 0u;
-                    }
+                    if (any) tmem_ld8(tmem + quarter + C::kColO + mb * N + cc, ov);
+                    tmem_ld_wait();
                     if (!s.whole) {
                         float *out = p.rec + (rec * N + cc) * R + col;
 #pragma unroll
@@ -740,7 +735,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
 // ------------------------------------------------------------------------------------------
 // Joins the records of units that several ranges share.  A unit's pieces are range c's last record and the
 // first records of the ranges behind it, up to the one in which it ends.  A row of a unit with up to 8 records is a
-// warp's task; of one with more, 128 elements of a row are a CTA's, every eighth record a warp's.
+// warp's task; of one with more, 64 elements of a row are a CTA's.
 
 struct LatentMerge {
     const float *rec, *rec_ml;
@@ -764,8 +759,8 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
     __shared__ int4 s_first[kLMaxCtas], s_last[kLMaxCtas];    // the ranges' units, as they were written
     __shared__ int32_t s_unit[2][kLMaxCtas];                  // units of few records from one end, of many: range | records << 16
     __shared__ int32_t s_warp[2][8];
-    __shared__ float4 s_acc[8][32];
-    __shared__ float s_l[8];
+    __shared__ float4 s_acc[16][16];
+    __shared__ float s_w[kLMaxCtas], s_m[8], s_l[8];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -843,53 +838,62 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
             out[v * 32 + lane] = make_uint2(pack_bf16x2(acc[v].x * inv, acc[v].y * inv), pack_bf16x2(acc[v].z * inv, acc[v].w * inv));
     }
 
-    for (int i = blockIdx.x; i < count[1] * rows * V; i += gridDim.x) {
-        const int chunk = i % V, task = i / V, unit = task / rows, row = task - unit * rows;
+    // 64 elements of a row: 16 threads a record, the CTA's 16 records at a time
+    constexpr int kChunks = R / 64;
+    for (int i = blockIdx.x; i < count[1] * rows * kChunks; i += gridDim.x) {
+        const int chunk = i % kChunks, task = i / kChunks, unit = task / rows, row = task - unit * rows;
         const int c = s_unit[1][unit] & 0xFFFF, cnt = s_unit[1][unit] >> 16;
         const int64_t out_row = out_of(c, row);
         if (out_row < 0) continue;  // (the same for the CTA)
         const int gi = row / p.N, k = row - gi * p.N;
         auto rec_of = [&](int j) { return ((((int64_t)c + j) * 2 + (j == 0)) * p.gs + gi) * p.N + k; };
-        float M = -INFINITY, L = 0.f;
-        for (int j = lane; j < cnt; j += 32) M = fmaxf(M, ld(ml + rec_of(j)).x);
+        const float2 mine = (int)threadIdx.x < cnt ? ld(ml + rec_of(threadIdx.x)) : make_float2(-INFINITY, 0.f);
+        float M = mine.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kInFlight = 5;
-        for (int j0 = warp; j0 < cnt; j0 += 8 * kInFlight) {
-            float2 x[kInFlight];
-            float4 y[kInFlight];
+        if (lane == 0) s_m[warp] = M;
+        __syncthreads();
 #pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const int j = j0 + 8 * u;
-                x[u] = make_float2(-INFINITY, 0.f);
-                y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j >= cnt) continue;
-                x[u] = ld(ml + rec_of(j));
-                y[u] = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + chunk * 32 + lane);
-            }
+        for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
+        const float w = weight_of(mine, M);
+        if ((int)threadIdx.x < cnt) s_w[threadIdx.x] = w;
+        float L = w * mine.y;
 #pragma unroll
-            for (int u = 0; u < kInFlight; ++u) {
-                const float w = weight_of(x[u], M);
-                L = fmaf(w, x[u].y, L);
-                if (w != 0.f)
-                    acc = make_float4(fmaf(w, y[u].x, acc.x), fmaf(w, y[u].y, acc.y), fmaf(w, y[u].z, acc.z), fmaf(w, y[u].w, acc.w));
-            }
-        }
-        s_acc[warp][lane] = acc;
+        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
         if (lane == 0) s_l[warp] = L;
         __syncthreads();
-        if (warp == 0) {
+        const int part = threadIdx.x >> 4, at = threadIdx.x & 15;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kInFlight = 5;
+        for (int j0 = part; j0 < cnt; j0 += 16 * kInFlight) {
+            float4 y[kInFlight];
+            float f[kInFlight];
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u) {
+                const int j = j0 + 16 * u;
+                f[u] = j < cnt ? s_w[j] : 0.f;
+                y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (f[u] != 0.f) y[u] = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + chunk * 16 + at);
+            }
+#pragma unroll
+            for (int u = 0; u < kInFlight; ++u)
+                acc = make_float4(fmaf(f[u], y[u].x, acc.x), fmaf(f[u], y[u].y, acc.y), fmaf(f[u], y[u].z, acc.z),
+                                  fmaf(f[u], y[u].w, acc.w));
+        }
+        s_acc[part][at] = acc;
+        __syncthreads();
+        if (threadIdx.x < 16) {
             float sum = 0.f;
             acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const float4 y = s_acc[w][lane];
+            for (int v = 0; v < 16; ++v) {
+                const float4 y = s_acc[v][threadIdx.x];
                 acc = make_float4(acc.x + y.x, acc.y + y.y, acc.z + y.z, acc.w + y.w);
-                sum += s_l[w];
             }
+#pragma unroll
+            for (int v = 0; v < 8; ++v) sum += s_l[v];
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            reinterpret_cast<uint2 *>(p.o + out_row * R)[chunk * 32 + lane] =
+            reinterpret_cast<uint2 *>(p.o + out_row * R)[chunk * 16 + threadIdx.x] =
                 make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         }
         __syncthreads();
