@@ -48,6 +48,7 @@ constexpr int kLThreads = 384;
 constexpr int kLSoftmax = 256;          // threads of the softmax warps
 constexpr int kLBarHalf = 1;            // named barriers of the softmax warps' halves: 1 and 2
 constexpr float kLUnset = -1e30f;       // a reference before any key was seen
+constexpr int kLCached = 64;            // requests of a range that are kept in shared memory
 constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
 constexpr int32_t kLLongest = 0x7FFFFF00;  // keys of a request: tiles' ends stay within 32 bits
 constexpr int kLMinTiles = 2;           // a range's tiles at least
@@ -82,7 +83,7 @@ struct LCfg {
     static constexpr int kQBlk = N * 128;
     static constexpr int kQOff = kStages * kStage;
     static constexpr int kMiscOff = kQOff + kBlocks * kQBlk;
-    static constexpr int kSmem = kMiscOff + 2560;
+    static constexpr int kSmem = kMiscOff + 4096;
     static constexpr int kCols = N / 4;                          // columns a softmax thread
     static constexpr uint32_t kColO = 128;                       // O^T block b at kColO + b * N
 };
@@ -96,112 +97,113 @@ struct LMisc {
     int32_t pad;
     int64_t start_off, left;
     int64_t scan[12];
+    int4 req[kLCached];   // the range's first requests
     float4 col[64];       // the quarters' column maxima; sums at the end
     float alpha[64];
     int32_t lim[64];      // keys that each row sees
 };
-static_assert(sizeof(LMisc) <= 2560, "LMisc");
+static_assert(sizeof(LMisc) <= 4096, "LMisc");
 
 // ------------------------------------------------------------------------------------------
 // the line of tiles
 
-struct LReq {
-    int32_t len, e, row, sets, tiles;  // tiles: what a unit of the request counts in the line
-    int64_t q0;
-};
-
-PKV_DEV LReq load_req(const LatentParams &p, int r, int rps, bool report) {
-    LReq q;
-    q.len = ld(p.lens + r);
-    q.row = ld(p.rows + r);
+// A request as it is read, (length, row, first query token, new tokens), with what is out of range set to 0.
+PKV_DEV int4 read_req(const LatentParams &p, int r, bool report) {
+    int4 q = make_int4(ld(p.lens + r), ld(p.rows + r), r, 1);
     if (p.indptr) {
-        q.q0 = ld(p.indptr + r);
-        q.e = ld(p.indptr + r + 1) - (int32_t)q.q0;
-    } else {
-        q.q0 = r;
-        q.e = 1;
+        q.z = ld(p.indptr + r);
+        q.w = ld(p.indptr + r + 1) - q.z;
     }
     bool bad = false;
-    if (q.q0 < 0 || q.e < 0 || q.q0 + q.e > p.total_q) {
+    if (q.z < 0 || q.w < 0 || (int64_t)q.z + q.w > p.total_q) {
         bad = true;
-        q.e = 0;
+        q.z = q.w = 0;
     }
-    if (q.row < 0 || q.row >= p.num_rows || q.len < 0 || q.len > kLLongest ||
-        (int64_t)q.len > (p.stride << p.shift)) {
+    if (q.y < 0 || q.y >= p.num_rows || q.x < 0 || q.x > kLLongest || (int64_t)q.x > (p.stride << p.shift)) {
         bad = true;
-        q.len = 0;
+        q.x = 0;
     }
     if (bad && report) set_error(p.err, DERR_POSITION);
-    q.sets = (int32_t)(((int64_t)q.e * p.heads + rps - 1) / rps);
-    q.tiles = max(1, (q.len + kLTile - 1) / kLTile);
     return q;
 }
+// Its units, and what each counts in the line.
+template <int N>
+PKV_DEV int32_t sets_of(const LatentParams &p, const int4 &q) {
+    const int rps = N * p.gs;
+    return (int32_t)(((uint32_t)q.w * (uint32_t)p.heads + rps - 1) / rps);
+}
+PKV_DEV int32_t tiles_of(const int4 &q) { return max(1, (q.x + kLTile - 1) / kLTile); }
 
 // A piece of one unit: this CTA's rows against tiles [t0, t1).
 struct LSeg {
     int32_t r, set, row, vis;     // vis: keys that the unit's last row sees
     int32_t t0, t1, nrows;        // nrows: this CTA's rows of the unit (0: none)
-    int64_t q_row0;               // first of them, in rows of q
-    int32_t vis0;                 // keys that their first token sees (0 or less: none), that is before its later tokens'
+    int32_t q_row0;               // first of them, in rows of q
+    int32_t vis0;                 // keys that the request's first new token sees (0 or less: none)
     int32_t row_lo;               // first of them, in rows of the request
     bool whole, first, ends;      // all of the unit is in this range; the range begins inside it; it ends in this range
 };
 
 struct LCursor {
-    int32_t r, j, t;
+    int32_t r, j, t;              // request; its unit and tile
     int64_t left;
-    bool loaded;
-    LReq q;
+    int4 q;                       // the request
+    int32_t sets, tiles;          // 0 sets: not read yet
 };
 
-PKV_DEV LCursor cursor_at(const LatentParams &p, int r, int64_t off, int64_t left, int rps) {
-    LCursor c{r, 0, 0, left, false, {}};
-    if (left > 0) {
-        c.q = load_req(p, r, rps, false);
-        c.loaded = true;
-        c.j = (int32_t)(off / c.q.tiles);
-        c.t = (int32_t)(off - (int64_t)c.j * c.q.tiles);
+template <int N>
+PKV_DEV void load_cursor(const LatentParams &p, const LMisc *m, LCursor &c) {
+    const int at = c.r - m->start_r;
+    c.q = at < kLCached ? m->req[at] : read_req(p, c.r, false);
+    c.sets = sets_of<N>(p, c.q);
+    c.tiles = tiles_of(c.q);
+}
+
+template <int N>
+PKV_DEV LCursor cursor_at(const LatentParams &p, const LMisc *m) {
+    LCursor c{m->start_r, 0, 0, m->left, make_int4(0, 0, 0, 0), 0, 0};
+    if (c.left > 0) {
+        load_cursor<N>(p, m, c);
+        c.j = (int32_t)(m->start_off / c.tiles);
+        c.t = (int32_t)(m->start_off - (int64_t)c.j * c.tiles);
     }
     return c;
 }
 
 template <int N>
-PKV_DEV bool next_seg(const LatentParams &p, LCursor &c, LSeg &s, int g) {
+PKV_DEV bool next_seg(const LatentParams &p, const LMisc *m, LCursor &c, LSeg &s, int g) {
     const int rps = N * p.gs;
     if (c.left <= 0) return false;
-    while (!c.loaded) {
+    while (c.sets == 0) {
         if (c.r >= p.batch) return false;
-        c.q = load_req(p, c.r, rps, false);
-        if (c.q.sets > 0) {
-            c.loaded = true;
-            c.j = c.t = 0;
-        } else {
-            ++c.r;
-        }
+        load_cursor<N>(p, m, c);
+        c.j = c.t = 0;
+        if (c.sets == 0) ++c.r;
     }
     // A request's units in the order first, last, second, last but one, ..: the earlier ones see fewer keys of the
     // new tokens than they count for, and so any stretch of the line has about its share of the work.
-    s.set = c.j & 1 ? c.q.sets - 1 - (c.j >> 1) : c.j >> 1;
+    s.set = c.j & 1 ? c.sets - 1 - (c.j >> 1) : c.j >> 1;
     s.r = c.r;
-    s.row = c.q.row;
-    const int32_t n = (int32_t)min((int64_t)(c.q.tiles - c.t), c.left);
-    const int64_t all = (int64_t)c.q.e * p.heads, lo = (int64_t)s.set * rps + g * N, set_end = min((int64_t)(s.set + 1) * rps, all);
+    s.row = c.q.y;
+    const int32_t n = (int32_t)min((int64_t)(c.tiles - c.t), c.left);
+    const uint32_t all = (uint32_t)c.q.w * (uint32_t)p.heads;  // (below 2^31, as all rows of q are)
+    const uint32_t lo = (uint32_t)s.set * rps + g * N, set_end = min((uint32_t)(s.set + 1) * rps, all);
     s.row_lo = (int32_t)lo;
-    s.nrows = (int32_t)max((int64_t)0, min((int64_t)N, all - lo));
-    s.q_row0 = c.q.q0 * p.heads + lo;
-    s.vis = max(0, c.q.len - c.q.e + (int32_t)((set_end - 1) / p.heads) + 1);
-    s.vis0 = c.q.len - c.q.e + 1;
+    s.nrows = lo < all ? (int32_t)min((uint32_t)N, all - lo) : 0;
+    s.q_row0 = (int32_t)((uint32_t)c.q.z * (uint32_t)p.heads + lo);
+    s.vis0 = c.q.x - c.q.w + 1;
+    s.vis = max(0, s.vis0 + (int32_t)((set_end - 1) / (uint32_t)p.heads));
     s.t0 = c.t;
     s.t1 = max(c.t, min(c.t + n, (s.vis + kLTile - 1) / kLTile));
     s.first = c.t > 0;
-    s.ends = c.t + n == c.q.tiles;
+    s.ends = c.t + n == c.tiles;
     s.whole = !s.first && s.ends;
     c.left -= n;
     c.t += n;
-    if (c.t == c.q.tiles) {
+    if (c.t == c.tiles) {
         c.t = 0;
-        if (++c.j == c.q.sets) {
-            c.loaded = false;
+        if (++c.j == c.sets) {
+            c.sets = 0;
             ++c.r;
         }
     }
@@ -210,8 +212,8 @@ PKV_DEV bool next_seg(const LatentParams &p, LCursor &c, LSeg &s, int g) {
 
 // The next piece with rows and tiles; the producer and the issuer see no others.
 template <int N>
-PKV_DEV bool next_work(const LatentParams &p, LCursor &c, LSeg &s, int g) {
-    while (next_seg<N>(p, c, s, g))
+PKV_DEV bool next_work(const LatentParams &p, const LMisc *m, LCursor &c, LSeg &s, int g) {
+    while (next_seg<N>(p, m, c, s, g))
         if (s.nrows > 0 && s.t1 > s.t0) return true;
     return false;
 }
@@ -296,16 +298,18 @@ PKV_DEV bool nonfinite8(const uint4 &v) {
 }
 
 // Where the range begins: its first request, how many of that request's tiles come before it, and
-// its tiles.  Each thread takes a stretch of the batch; a scan over the threads' sums.
+// its tiles.  Each thread takes a stretch of the batch (one request, up to 384); a scan over the threads' sums.
 template <int N>
 PKV_DEV void find_range(const LatentParams &p, LMisc *m, int range) {
-    const int rps = N * p.gs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.batch + kLThreads - 1) / kLThreads;
     const int r0 = min(p.batch, (int)threadIdx.x * per), r1 = min(p.batch, r0 + per);
+    auto cost = [&](const int4 &q) { return (int64_t)sets_of<N>(p, q) * tiles_of(q); };
+    int4 q = make_int4(0, 0, 0, 0);
     int64_t own = 0;
     for (int r = r0; r < r1; ++r) {
-        const LReq q = load_req(p, r, rps, blockIdx.x == 0);
-        own += (int64_t)q.sets * q.tiles;
+        q = read_req(p, r, blockIdx.x == 0);
+        own += cost(q);
     }
     int64_t incl = own;
 #pragma unroll
@@ -314,31 +318,34 @@ PKV_DEV void find_range(const LatentParams &p, LMisc *m, int range) {
         if (lane >= d) incl += x;
     }
     if (lane == 31) m->scan[warp] = incl;
+    if (threadIdx.x == 0) m->start_r = p.batch;
     __syncthreads();
     int64_t before = incl - own, total = 0;
+#pragma unroll
     for (int w = 0; w < kLThreads / 32; ++w) {
         if (w < warp) before += m->scan[w];
         total += m->scan[w];
     }
     const int64_t each = max((int64_t)kLMinTiles, (total + p.ranges - 1) / p.ranges), t0 = (int64_t)range * each;
-    if (threadIdx.x == 0) {
-        m->left = max((int64_t)0, min(each, total - t0));
-        m->start_r = p.batch;
-        m->start_off = 0;
+    if (threadIdx.x == 0) m->left = max((int64_t)0, min(each, total - t0));
+    if (t0 >= before && t0 < before + own) {  // one thread, where there is work
+        int64_t at = before;
+        int r = r0;
+        if (per > 1)
+            for (; r < r1 - 1; ++r) {
+                const int64_t c = cost(read_req(p, r, false));
+                if (t0 < at + c) break;
+                at += c;
+            }
+        m->start_r = r;
+        m->start_off = t0 - at;
     }
     __syncthreads();
-    if (t0 < total && t0 >= before && t0 < before + own) {
-        int64_t at = before;
-        for (int r = r0; r < r1; ++r) {
-            const LReq q = load_req(p, r, rps, false);
-            const int64_t cost = (int64_t)q.sets * q.tiles;
-            if (t0 < at + cost) {
-                m->start_r = r;
-                m->start_off = t0 - at;
-                break;
-            }
-            at += cost;
-        }
+    if (per == 1) {
+        const int at = (int)threadIdx.x - m->start_r;
+        if (r0 < r1 && at >= 0 && at < kLCached) m->req[at] = q;
+    } else if (threadIdx.x < kLCached && m->start_r + (int)threadIdx.x < p.batch) {
+        m->req[threadIdx.x] = read_req(p, m->start_r + threadIdx.x, false);
     }
     __syncthreads();
 }
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     find_range<N>(p, m, range);  // (its barriers cover the set-up above)
     tc_fence_after();
     const uint32_t tmem = m->tmem_base;
-    LCursor cur = cursor_at(p, m->start_r, m->start_off, m->left, N * p.gs);
+    LCursor cur = cursor_at<N>(p, m);
     LSeg s;
 
     if (warp < 2) {
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (warp == 0) {
             constexpr uint32_t idesc = idesc_bf16_f32(kLTile, N, 0, 0);
             const uint64_t rows = sdesc_sw128(sbase, 16, 1024), q = sdesc_sw128(sbase + C::kQOff, 16, 1024);
-            while (ok && next_work<N>(p, cur, s, g)) {
+            while (ok && next_work<N>(p, m, cur, s, g)) {
                 ok = __all_sync(0xffffffffu, lwait(&m->qfull, nq & 1, m, p, 1));
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                     // the softmax has read what S's place held two tiles ago
@@ -420,7 +427,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         } else {
             constexpr uint32_t idesc = idesc_bf16_f32(128, N, 1, 1);
             const uint64_t rows = sdesc_sw128(sbase, C::kBlk, 1024);
-            while (ok && next_work<N>(p, cur, s, g)) {
+            while (ok && next_work<N>(p, m, cur, s, g)) {
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
                     ok = __all_sync(0xffffffffu, lwait(&m->pfull[n & 1], (n >> 1) & 1, m, p, 4));
                     if (!ok) break;
@@ -457,14 +464,14 @@ __global__ void __launch_bounds__(kLThreads, 1)
         const int half = warp - 2, sub = lane >> 3;
         int tp = 0, nq = 0;
         bool ok = true;
-        while (ok && next_work<N>(p, cur, s, g)) {
+        while (ok && next_work<N>(p, m, cur, s, g)) {
             if (half == 0) {
                 if (nq > 0) ok = __all_sync(0xffffffffu, lwait(&m->qempty, (nq - 1) & 1, m, p, 5));
                 if (!ok) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&m->qfull, C::kBlocks * C::kQBlk);
                     for (int b = 0; b < C::kBlocks; ++b)
-                        tma_load_2d(sbase + C::kQOff + b * C::kQBlk, &qmap, b * 64, (int32_t)s.q_row0, &m->qfull);
+                        tma_load_2d(sbase + C::kQOff + b * C::kQBlk, &qmap, b * 64, s.q_row0, &m->qfull);
                 }
                 ++nq;
             }
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         bool ok = true;
         int32_t *units = p.units + range * 8;
         if (g == 0 && warp == 4 && lane == 0) units[0] = units[4] = -1;
-        while (next_seg<N>(p, cur, s, g)) {
+        while (next_seg<N>(p, m, cur, s, g)) {
             const int slot_rec = s.first ? 0 : 1;
             if (g == 0 && warp == 4 && lane == 0 && !s.whole) {
                 units[slot_rec * 4 + 1] = s.set;
@@ -530,8 +537,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
             }
             if (s.nrows <= 0) continue;
             // keys that each column sees; columns without a row see what the last row does
-            if (in_half < NH) m->lim[hf * NH + in_half] = s.vis0 + (s.row_lo + min(hf * NH + in_half, s.nrows - 1)) / p.heads;
-            const int lim_min = s.vis0 + s.row_lo / p.heads;
+            if (in_half < NH) m->lim[hf * NH + in_half] = s.vis0 + (int32_t)((uint32_t)(s.row_lo + min(hf * NH + in_half, s.nrows - 1)) / (uint32_t)p.heads);
+            const int lim_min = s.vis0 + (int32_t)((uint32_t)s.row_lo / (uint32_t)p.heads);
             float ref[NC], l[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
                         const uint32_t w = lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
                         const int k = cc + c + (lane & 1);
-                        if (k < s.nrows) reinterpret_cast<uint32_t *>(p.o + (s.q_row0 + k) * R)[col >> 1] = w;
+                        if (k < s.nrows) reinterpret_cast<uint32_t *>(p.o + (int64_t)(s.q_row0 + k) * R)[col >> 1] = w;
                     }
                 }
             }
@@ -759,6 +766,7 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
     __shared__ int4 s_first[kLMaxCtas], s_last[kLMaxCtas];    // the ranges' units, as they were written
     __shared__ int32_t s_unit[2][kLMaxCtas];                  // units of few records from one end, of many: range | records << 16
     __shared__ int32_t s_warp[2][8];
+    __shared__ uint32_t s_ends[8];
     __shared__ float4 s_acc[16][16];
     __shared__ float s_w[kLMaxCtas], s_m[8], s_l[8];
     pdl_wait();
@@ -770,14 +778,18 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
         s_last[threadIdx.x] = ld(reinterpret_cast<const int4 *>(p.units) + threadIdx.x * 2 + 1);
     }
     __syncthreads();
-    // two lists in the ranges' order: every CTA has the same
+    // Two lists in the ranges' order: every CTA has the same.  A unit ends with the first range behind its own whose first
+    // piece ends there.
+    const uint32_t ends = __ballot_sync(0xffffffffu, (int)threadIdx.x < p.ranges && s_first[threadIdx.x].x >= 0 && s_first[threadIdx.x].z);
+    if (lane == 0) s_ends[warp] = ends;
+    __syncthreads();
     int n = 0;
     if ((int)threadIdx.x < p.ranges && s_last[threadIdx.x].x >= 0) {
-        const int c = threadIdx.x;
         n = 1;
-        while (c + n < p.ranges && s_first[c + n].x >= 0) {
-            ++n;
-            if (s_first[c + n - 1].z) break;
+        const int from = threadIdx.x + 1;
+        for (int w = from >> 5; w < 8 && n == 1; ++w) {
+            const uint32_t bits = s_ends[w] & (w == from >> 5 ? 0xffffffffu << (from & 31) : 0xffffffffu);
+            if (bits) n = w * 32 + __ffs(bits) - (int)threadIdx.x;
         }
     }
     const uint32_t few = __ballot_sync(0xffffffffu, n > 0 && n <= kFew), many = __ballot_sync(0xffffffffu, n > kFew);
