@@ -490,6 +490,14 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 const int32_t mine = next;
                 next = slot_of(t + 1);
                 const int st = __shfl_sync(0xffffffffu, tp % C::kStages, 0);
+                const uint16_t *src[8];
+                uint32_t there = 0;  // bit j: row 4 j + sub has a slot
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int32_t at = __shfl_sync(0xffffffffu, mine, 4 * j + sub);
+                    src[j] = p.pool + (int64_t)max(at, 0) * p.pool_stride + (lane & 7) * 8;
+                    there |= at < 0 ? 0u : 1u << j;
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int quarter = half * 2 + i;
@@ -497,13 +505,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         ok = __all_sync(0xffffffffu, ok && lwait(&m->empty[st * 4 + quarter], (tp / C::kStages - 1) & 1, m, p, 6));
                     if (!ok) break;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int32_t at = __shfl_sync(0xffffffffu, mine, 16 * i + 4 * j + sub);
-                        const int r = 4 * j + sub;  // of the quarter; its chunks lie at chunk ^ r mod 8
-                        const uint32_t dst = sbase + st * C::kStage + quarter * 2048 + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-                        const uint16_t *src = p.pool + (int64_t)max(at, 0) * p.pool_stride + (lane & 7) * 8;
+                    for (int j = 4 * i; j < 4 * i + 4; ++j) {
+                        const int r = 4 * j + sub;  // of the warp's 32; its chunks lie at chunk ^ r mod 8
+                        const uint32_t dst = sbase + st * C::kStage + (half * 32 + r) * 128 + (((lane & 7) ^ (r & 7)) << 4);
 #pragma unroll
-                        for (int b = 0; b < C::kBlocks; ++b) cp_async_16(dst + b * C::kBlk, src + b * 64, at < 0 ? 0u : 16u);
+                        for (int b = 0; b < C::kBlocks; ++b) cp_async_16(dst + b * C::kBlk, src[j] + b * 64, there >> j & 1u ? 16u : 0u);
                     }
                 }
                 if (!ok) break;
