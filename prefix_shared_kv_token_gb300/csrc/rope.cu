@@ -222,7 +222,7 @@ static int launch_rope(RopeParams p, const pkv_rope_spec *r, int store, cudaStre
     const int heads = p.hq + (store ? 2 * p.hkv : 0), per = 32 >> p.lane_shift;
     // Warps a token: all of a token's heads in one warp's steps of four once that fills the GPU
     // (16 warps an SM), else as many as its heads give work, for then the time is a chain of loads.
-    // One token of 12 steps: 12 warps; 65,536 tokens: 1.
+    // 256 tokens of 128 heads: 5.3 us by 9 warps a token, 8.9 by one.
     const int64_t steps = (heads + per - 1) / per, full = (int64_t)num_sms() * 16;
     p.parts = (int32_t)std::min<int64_t>(steps, std::max<int64_t>(1, full / p.n));
     const int64_t blocks = std::min<int64_t>((p.n * p.parts + 7) / 8, (int64_t)num_sms() * 32);
@@ -247,75 +247,78 @@ struct LatentStoreParams {
     int32_t *err;
 };
 
-// A warp two tokens at a time: R / 256 vectors of a latent a lane, the sums of squares over the warp, and
-// the rotary key's four units in lanes 0 to 3 (the second token's in lanes 4 to 7), loaded with the rest.  A token's loads are
-// issued before its slot is known: what bounds the kernel is how many are in flight.  131,072 tokens 60 us, 5.1 TB/s (one at a time,
-// the slot first: 84 us).
-template <int R, bool INTER>
+// A warp T tokens at a time, two by two: R / 256 vectors of a latent a lane, the sums of squares over the warp.  The
+// T tokens' rotary keys, four units each, go to four lanes a token: with T = 8 to all lanes at once, where with two the sines
+// and cosines of 8 lanes took half of the kernel's instructions (131,072 tokens 60 us, with 8 56).  A
+// token's loads are issued before its slot is known.
+template <int R, bool INTER, int T>
 __global__ void __launch_bounds__(256) latent_store_kernel(const LatentStoreParams p) {
     constexpr int V = R / 256;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, u = lane & 3, mine = lane >> 2;  // (lanes 8 and up have no unit)
+    const int lane = threadIdx.x & 31, u = lane & 3, mine = lane >> 2;  // (with T = 2, lanes 8 and up have no unit)
     const int off_a = 8 * u, off_b = off_a + kLatentRope / 2;
     uint4 w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         if (p.w) w[i] = ld(reinterpret_cast<const uint4 *>(p.w) + 32 * i + lane);
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t tok = (((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * 2; tok < p.n; tok += 2 * warps) {
-        const bool two = tok + 1 < p.n;
-        uint4 x[2][V], a, b;
-        int32_t slot[2], pos = 0;
-        const bool turns = mine == 0 || (mine == 1 && two);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            slot[k] = k == 0 || two ? ld(p.loc + tok + k) : -1;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (k == 0 || two) x[k][i] = __ldcs(reinterpret_cast<const uint4 *>(p.c + (tok + k) * p.c_tok) + 32 * i + lane);
-        }
+    for (int64_t first = (((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * T; first < p.n; first += T * warps) {
+        const bool turns = mine < T && first + mine < p.n;
+        uint4 a, b;
+        int32_t own_slot = -1, pos = 0;
         if (turns) {
-            pos = ld(p.positions + tok + mine);
-            a = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (tok + mine) * p.pe_tok + off_a));
-            b = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (tok + mine) * p.pe_tok + off_b));
+            own_slot = ld(p.loc + first + mine);
+            pos = ld(p.positions + first + mine);
+            a = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (first + mine) * p.pe_tok + off_a));
+            b = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (first + mine) * p.pe_tok + off_b));
         }
+#pragma unroll 1
+        for (int pair = 0; pair < T; pair += 2) {
+            const int64_t tok = first + pair;
+            if (tok >= p.n) break;
+            uint4 x[2][V];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (slot[k] < 0 || slot[k] >= p.num_slots) {
-                if (slot[k] != -1 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
-                slot[k] = -1;  // padding, or not there
-                continue;
-            }
-            if (p.w) {
-                float y[8 * V], z[8], sum = 0.f;
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < V; ++i) unpack8(x[k][i], y + 8 * i);
+                for (int i = 0; i < V; ++i)
+                    if (tok + k < p.n) x[k][i] = __ldcs(reinterpret_cast<const uint4 *>(p.c + (tok + k) * p.c_tok) + 32 * i + lane);
 #pragma unroll
-                for (int i = 0; i < 8 * V; ++i) sum = fmaf(y[i], y[i], sum);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float inv = rsqrtf(sum * (1.f / R) + p.eps);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    unpack8(w[i], z);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) z[j] *= y[8 * i + j] * inv;
-                    x[k][i] = pack8(z);
+            for (int k = 0; k < 2; ++k) {
+                const int32_t slot = __shfl_sync(0xffffffffu, own_slot, 4 * (pair + k));
+                if (slot < 0 || slot >= p.num_slots) {
+                    if (slot != -1 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+                    continue;  // padding (or past the end), or not there
                 }
-            }
-            uint4 *row = reinterpret_cast<uint4 *>(p.rows + (int64_t)slot[k] * p.stride);
+                if (p.w) {
+                    float y[8 * V], z[8], sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) row[32 * i + lane] = x[k][i];
+                    for (int i = 0; i < V; ++i) unpack8(x[k][i], y + 8 * i);
+#pragma unroll
+                    for (int i = 0; i < 8 * V; ++i) sum = fmaf(y[i], y[i], sum);
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    const float inv = rsqrtf(sum * (1.f / R) + p.eps);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        unpack8(w[i], z);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) z[j] *= y[8 * i + j] * inv;
+                        x[k][i] = pack8(z);
+                    }
+                }
+                uint4 *row = reinterpret_cast<uint4 *>(p.rows + (int64_t)slot * p.stride);
+#pragma unroll
+                for (int i = 0; i < V; ++i) row[32 * i + lane] = x[k][i];
+            }
         }
-        const int32_t to = mine == 0 ? slot[0] : slot[1];
-        if (turns && to >= 0) {
+        if (own_slot >= 0 && own_slot < p.num_slots) {
             const Turn t = turn_of(p.phases, INTER ? 4 * u : 8 * u, INTER ? 4 * (u + 4) : 8 * u + 4, pos, p.magnitude);
             float ya[8], yb[8];
             unpack8(a, ya);
             unpack8(b, yb);
             rotate16<INTER>(ya, yb, t);
-            uint16_t *row = p.rows + (int64_t)to * p.stride + R;
+            uint16_t *row = p.rows + (int64_t)own_slot * p.stride + R;
             store8(row + off_a, ya);
             store8(row + off_b, yb);
         }
@@ -438,9 +441,16 @@ extern "C" int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec
     p.loc = out_cache_loc;
     p.n = n;
     p.err = static_cast<int32_t *>(workspace);
-    const int64_t blocks = std::min<int64_t>((n + 15) / 16, (int64_t)num_sms() * 4);
-    auto kern = pool->latent_dim == 512 ? (rope->interleaved ? latent_store_kernel<512, true> : latent_store_kernel<512, false>)
-                                        : (rope->interleaved ? latent_store_kernel<256, true> : latent_store_kernel<256, false>);
+    // Eight tokens a warp once that leaves every SM 16 warps (256 tokens: 5.1 us with two, 8.4 with eight).
+    const bool many = n >= (int64_t)num_sms() * 16 * 8;
+    const int64_t per_block = 8 * (many ? 8 : 2), blocks = std::min<int64_t>((n + per_block - 1) / per_block, (int64_t)num_sms() * 12);
+    void (*kern)(const LatentStoreParams);
+    if (pool->latent_dim == 512)
+        kern = rope->interleaved ? (many ? latent_store_kernel<512, true, 8> : latent_store_kernel<512, true, 2>)
+                                 : (many ? latent_store_kernel<512, false, 8> : latent_store_kernel<512, false, 2>);
+    else
+        kern = rope->interleaved ? (many ? latent_store_kernel<256, true, 8> : latent_store_kernel<256, true, 2>)
+                                 : (many ? latent_store_kernel<256, false, 8> : latent_store_kernel<256, false, 2>);
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, p) == cudaSuccess
                ? PKV_OK
                : PKV_E_CUDA;
