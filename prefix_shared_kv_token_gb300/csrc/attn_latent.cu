@@ -51,6 +51,9 @@ constexpr float kLUnset = -1e30f;       // a reference before any key was seen
 constexpr int kLCached = 64;            // requests of a range that are kept in shared memory
 constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
 constexpr int32_t kLLongest = 0x7FFFFF00;  // keys of a request: tiles' ends stay within 32 bits
+// What a unit counts in the line beside its tiles, for its start and its output: 256 requests of 33 tiles take 235 us with
+// 0, 229 with 2, 225 with 3 or 4; 64 requests of 1 to 200 keys 21, 15, 16 and 16.
+constexpr int kLUnitTiles = 3;
 constexpr int kLMinTiles = 2;           // a range's tiles at least
 constexpr float kLog2eL = 1.4426950408889634f;
 constexpr float kLagL = 8.0f;           // log2 units by which a logit may pass its reference
@@ -132,7 +135,7 @@ PKV_DEV int32_t sets_of(const LatentParams &p, const int4 &q) {
     const int rps = N * p.gs;
     return (int32_t)(((uint32_t)q.w * (uint32_t)p.heads + rps - 1) / rps);
 }
-PKV_DEV int32_t tiles_of(const int4 &q) { return max(1, (q.x + kLTile - 1) / kLTile); }
+PKV_DEV int32_t tiles_of(const int4 &q) { return max(1, (q.x + kLTile - 1) / kLTile) + kLUnitTiles; }
 
 // A piece of one unit: this CTA's rows against tiles [t0, t1).
 struct LSeg {
