@@ -102,7 +102,8 @@ struct LMisc {
     int64_t scan[12];
     int4 req[kLCached];   // the range's first requests
     float4 col[64];       // the quarters' column maxima; sums at the end
-    float alpha[64];
+    float ref[64];        // columns' references
+    float alpha[64];      // factors of a rescaling; 1 / sum at the end
     int32_t lim[64];      // keys that each row sees
 };
 static_assert(sizeof(LMisc) <= 4096, "LMisc");
@@ -265,6 +266,18 @@ PKV_DEV void tmem_ld8(uint32_t taddr, uint32_t *r) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
+PKV_DEV void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+template <int n>
+PKV_DEV void tmem_ldn(uint32_t taddr, uint32_t *r) {
+    if constexpr (n == 16) tmem_ld16(taddr, r);
+    else tmem_ld8(taddr, r);
+}
 PKV_DEV void tmem_st8(uint32_t taddr, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -298,6 +311,33 @@ PKV_DEV bool nonfinite8(const uint4 &v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
     return bad;
+}
+
+// The sum, or the maximum, of each of a thread's NC values over its half-warp's 16 lanes: lane i of them gets that of
+// column i mod NC.  Lanes halve what they hold at each step (15 shuffles for 16 values; 64 with every sum in every lane).
+template <int NC, bool MAX>
+PKV_DEV float reduce_keys(float (&v)[NC], int lane) {
+    auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    int w = NC;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) {
+        if (w == 2 * d) {
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i) {
+                if (i >= d) break;
+                const float mine = lane & d ? v[i + d] : v[i], other = lane & d ? v[i] : v[i + d];
+                v[i] = join(mine, __shfl_xor_sync(0xffffffffu, other, d));
+            }
+            w = d;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                if (i >= w) break;
+                v[i] = join(v[i], __shfl_xor_sync(0xffffffffu, v[i], d));
+            }
+        }
+    }
+    return v[0];
 }
 
 // Where the range begins: its first request, how many of that request's tiles come before it, and
@@ -532,7 +572,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
         const int c0 = hf * NH + (lane >> 4) * NC;                 // and its first column
         const uint32_t quarter = (uint32_t)(wq * 32) << 16;
         const int in_half = wq * 32 + lane, bar = kLBarHalf + hf;
-        const bool scribe = lane == 0 || lane == 16;               // writes what the 16 lanes of its columns have reduced
         int n = 0, nseg = 0;                                       // tiles and pieces before this one
         bool ok = true;
         int32_t *units = p.units + range * 8;
@@ -548,6 +587,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             // keys that each column sees; columns without a row see what the last row does
             if (in_half < NH) m->lim[hf * NH + in_half] = s.vis0 + (int32_t)((uint32_t)(s.row_lo + min(hf * NH + in_half, s.nrows - 1)) / (uint32_t)p.heads);
             const int lim_min = s.vis0 + (int32_t)((uint32_t)s.row_lo / (uint32_t)p.heads);
+            if (in_half < NH) m->ref[hf * NH + in_half] = kLUnset;
             float ref[NC], l[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -587,47 +627,47 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         ok = false;
                         break;
                     }
-                    // raise to the tile's maxima the references that those pass
+                    // Raise to the tile's maxima the references that those pass.  Maxima over a warp's keys, a column
+                    // a lane at the end; a thread a column joins the quarters; all read what concerns them.
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        float y = __uint_as_float(sv[c]) * p.scale_log2;
-#pragma unroll
-                        for (int d = 8; d > 0; d >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                        if (scribe) reinterpret_cast<float *>(&m->col[c0 + c])[wq] = y;
-                    }
+                    for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(sv[c]) * p.scale_log2;
+                    const float most_of = reduce_keys<NC, true>(x, lane);
+                    if ((lane & 15) < NC) reinterpret_cast<float *>(&m->col[c0 + (lane & (NC - 1))])[wq] = most_of;
                     named_bar_sync(bar, kLSoftmax / 2);
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float4 y = m->col[c0 + c];
-                        const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-                        float a = 1.f;
-                        if (top > ref[c] + kLagL) {  // (a column's references follow its own logits alone)
-                            a = ex2(ref[c] - top);  // (0 where there was no reference, and l is)
-                            ref[c] = top;
-                            l[c] *= a;
-                        }
-                        x[c] = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c]);
-                        if (wq == 0 && scribe) m->alpha[c0 + c] = a;
+                    if (in_half < NH) {
+                        const int c = hf * NH + in_half;
+                        const float4 y = m->col[c];
+                        const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)), had = m->ref[c];
+                        const bool up = top > had + kLagL;  // (a column's references follow its own logits alone)
+                        m->alpha[c] = up ? ex2(had - top) : 1.f;  // (0 where there was no reference, and l is)
+                        if (up) m->ref[c] = top;
                     }
                     if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 8));
                     named_bar_sync(bar, kLSoftmax / 2);
+#pragma unroll
+                    for (int c = 0; c < NC; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&m->alpha[c0 + c]), y = *reinterpret_cast<const float4 *>(&m->ref[c0 + c]);
+                        const float fs[4] = {f.x, f.y, f.z, f.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            l[c + i] *= fs[i];
+                            ref[c + i] = ys[i];
+                            x[c + i] = fmaf(__uint_as_float(sv[c + i]), p.scale_log2, -ys[i]);
+                        }
+                    }
                     if (t > s.t0 && ok) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int mb = 0; mb < R / 128; ++mb)
-#pragma unroll 1
-                            for (int cc = hf * NH; cc < (hf + 1) * NH; cc += 8) {
-                                uint32_t ov[8];
-                                const uint32_t at = tmem + quarter + C::kColO + mb * N + cc;
-                                tmem_ld8(at, ov);
-                                tmem_ld_wait();
+                        for (int i = 0; i < R / 128 * (NH / 8); ++i) {
+                            const int cc = hf * NH + i % (NH / 8) * 8;
+                            const uint32_t at = tmem + quarter + C::kColO + i / (NH / 8) * N + cc;
+                            uint32_t ov[8];
+                            tmem_ld8(at, ov);
+                            tmem_ld_wait();
 #pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    // what a column without a reference accumulated is 0, but for a NaN
-                                    ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
-                                }
-                                tmem_st8(at, ov);
-                            }
+                            for (int c = 0; c < 8; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
+                            tmem_st8(at, ov);
+                        }
                         tmem_st_wait();
                     }
                 }
@@ -674,17 +714,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 for (int c = 0; c < NC; c += 2) add_bf16x2_f32(pk[c / 2], l[c], l[c + 1]);
             }
             // the columns' sums, over a warp's keys and then the quarters (col and alpha may still be in use)
+            const float part = reduce_keys<NC, false>(l, lane);
             named_bar_sync(bar, kLSoftmax / 2);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                float x = l[c];
-#pragma unroll
-                for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                if (scribe) {
-                    reinterpret_cast<float *>(&m->col[c0 + c])[wq] = x;
-                    if (wq == 0) m->alpha[c0 + c] = ref[c] == kLUnset ? -INFINITY : ref[c];
-                }
-            }
+            if ((lane & 15) < NC) reinterpret_cast<float *>(&m->col[c0 + (lane & (NC - 1))])[wq] = part;
             const bool any = s.t1 > s.t0;
             if (any) ok = __all_sync(0xffffffffu, ok && lwait(&m->ofull, nseg & 1, m, p, 10));
             if (!named_bar_and(bar, kLSoftmax / 2, ok)) {
@@ -693,52 +725,51 @@ __global__ void __launch_bounds__(kLThreads, 1)
             }
             if (any) ++nseg;
             tc_fence_after();
-            auto sum_of = [&](int c) {
-                const float4 x = m->col[c];
-                return (x.x + x.y) + (x.z + x.w);
-            };
             const int64_t rec = ((int64_t)range * 2 + slot_rec) * p.gs + g;
-            if (!s.whole && in_half < NH)
-                reinterpret_cast<float2 *>(p.rec_ml)[rec * N + hf * NH + in_half] =
-                    make_float2(m->alpha[hf * NH + in_half], sum_of(hf * NH + in_half));
+            if (in_half < NH) {
+                const int c = hf * NH + in_half;
+                const float4 y = m->col[c];
+                const float sum = (y.x + y.y) + (y.z + y.w);
+                m->alpha[c] = !s.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                if (!s.whole)
+                    reinterpret_cast<float2 *>(p.rec_ml)[rec * N + c] = make_float2(m->ref[c] == kLUnset ? -INFINITY : m->ref[c], sum);
+            }
+            named_bar_sync(bar, kLSoftmax / 2);
             if (!s.whole && !any) continue;  // its (-inf, 0) says that there is nothing to add
+            constexpr int CH = NH < 16 ? NH : 16;  // columns at a time
+            const int chunks = (min(s.nrows - hf * NH, NH) + CH - 1) / CH;
 #pragma unroll 1
-            for (int cc = hf * NH; cc < (hf + 1) * NH && cc < s.nrows; cc += 8) {
-                float inv[8];
-                if (s.whole) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float x = sum_of(cc + c);
-                        inv[c] = x == 0.f ? 0.f : 1.f / x;
-                    }
-                }
-#pragma unroll 1
-                for (int mb = 0; mb < R / 128; ++mb) {
-                    const int col = mb * 128 + wq * 32 + lane;  // this thread's latent element
-                    uint32_t ov[8];
-                    if (any) tmem_ld8(tmem + quarter + C::kColO + mb * N + cc, ov);
+            for (int i = 0; i < chunks * (R / 128); ++i) {
+                const int cc = hf * NH + i / (R / 128) * CH, mb = i % (R / 128);
+                const int col = mb * 128 + wq * 32 + lane;  // this thread's latent element
+                uint32_t ov[CH];
+                if (any) {
+                    tmem_ldn<CH>(tmem + quarter + C::kColO + mb * N + cc, ov);
                     tmem_ld_wait();
-                    if (!s.whole) {
-                        float *out = p.rec + (rec * N + cc) * R + col;
+                } else {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            if (cc + c < s.nrows) out[(int64_t)c * R] = __uint_as_float(ov[c]);
-                        continue;
-                    }
+                    for (int c = 0; c < CH; ++c) ov[c] = 0u;
+                }
+                if (!s.whole) {
+                    float *out = p.rec + (rec * N + cc) * R + col;
 #pragma unroll
-                    for (int c = 0; c < 8; c += 2) {
-                        const float x0 = inv[c] == 0.f ? 0.f : __uint_as_float(ov[c]) * inv[c];
-                        const float x1 = inv[c + 1] == 0.f ? 0.f : __uint_as_float(ov[c + 1]) * inv[c + 1];
-                        // neighbouring lanes trade a value: even lanes write column c, odd ones c + 1, two elements each
-                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
-                        const uint32_t w = lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
-                        const int k = cc + c + (lane & 1);
-                        if (k < s.nrows) reinterpret_cast<uint32_t *>(p.o + (int64_t)(s.q_row0 + k) * R)[col >> 1] = w;
-                    }
+                    for (int c = 0; c < CH; ++c)
+                        if (cc + c < s.nrows) out[c * R] = __uint_as_float(ov[c]);
+                    continue;
+                }
+                uint32_t *out = reinterpret_cast<uint32_t *>(p.o + (int64_t)(s.q_row0 + cc + (lane & 1)) * R) + (col >> 1);
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                    const float2 inv = *reinterpret_cast<const float2 *>(&m->alpha[cc + c]);
+                    const float x0 = __uint_as_float(ov[c]) * inv.x, x1 = __uint_as_float(ov[c + 1]) * inv.y;
+                    // neighbouring lanes trade a value: even lanes write column c, odd ones c + 1, two elements each
+                    const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
+                    const uint32_t w = lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
+                    if (cc + c + (lane & 1) < s.nrows) out[c * (R / 2)] = w;
                 }
             }
             tc_fence_before();
-            // col, alpha and lim are read before the next piece writes them
+            // col, ref, alpha and lim are read before the next piece writes them
             named_bar_sync(bar, kLSoftmax / 2);
         }
     }
