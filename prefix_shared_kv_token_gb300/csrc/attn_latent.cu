@@ -738,6 +738,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
             if (!s.whole && !any) continue;  // its (-inf, 0) says that there is nothing to add
             constexpr int CH = NH < 16 ? NH : 16;  // columns at a time
             const int chunks = (min(s.nrows - hf * NH, NH) + CH - 1) / CH;
+            const uint32_t trade = lane & 1 ? 0x3276u : 0x5410u;
+            // (Few instructions: this code is run once a piece, and their fetch is what it costs.)
 #pragma unroll 1
             for (int i = 0; i < chunks * (R / 128); ++i) {
                 const int cc = hf * NH + i / (R / 128) * CH, mb = i % (R / 128);
@@ -750,22 +752,26 @@ __global__ void __launch_bounds__(kLThreads, 1)
 #pragma unroll
                     for (int c = 0; c < CH; ++c) ov[c] = 0u;
                 }
-                if (!s.whole) {
+                const bool all = cc + CH <= s.nrows;
+                if (!s.whole) {  // (the workspace has room for rows that are not there)
                     float *out = p.rec + (rec * N + cc) * R + col;
 #pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        if (cc + c < s.nrows) out[c * R] = __uint_as_float(ov[c]);
+                    for (int c = 0; c < CH; ++c) out[c * R] = __uint_as_float(ov[c]);
                     continue;
                 }
                 uint32_t *out = reinterpret_cast<uint32_t *>(p.o + (int64_t)(s.q_row0 + cc + (lane & 1)) * R) + (col >> 1);
+                const int rows = s.nrows - cc - (lane & 1);
 #pragma unroll
-                for (int c = 0; c < CH; c += 2) {
-                    const float2 inv = *reinterpret_cast<const float2 *>(&m->alpha[cc + c]);
-                    const float x0 = __uint_as_float(ov[c]) * inv.x, x1 = __uint_as_float(ov[c + 1]) * inv.y;
-                    // neighbouring lanes trade a value: even lanes write column c, odd ones c + 1, two elements each
-                    const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x0 : x1, 1);
-                    const uint32_t w = lane & 1 ? pack_bf16x2(other, x1) : pack_bf16x2(x0, other);
-                    if (cc + c + (lane & 1) < s.nrows) out[c * (R / 2)] = w;
+                for (int c = 0; c < CH; c += 4) {
+                    const float4 inv = *reinterpret_cast<const float4 *>(&m->alpha[cc + c]);
+                    const uint32_t w[2] = {pack_bf16x2(__uint_as_float(ov[c]) * inv.x, __uint_as_float(ov[c + 1]) * inv.y),
+                                           pack_bf16x2(__uint_as_float(ov[c + 2]) * inv.z, __uint_as_float(ov[c + 3]) * inv.w)};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // neighbouring lanes trade a value: even lanes write column c, odd ones c + 1, two elements each
+                        const uint32_t y = __byte_perm(w[k], __shfl_xor_sync(0xffffffffu, w[k], 1), trade);
+                        if (all || c + 2 * k < rows) out[(c + 2 * k) * (R / 2)] = y;
+                    }
                 }
             }
             tc_fence_before();
