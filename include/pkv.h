@@ -524,8 +524,8 @@ int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec *rope, con
  * Logits and sums are fp32, weights bf16 (their sum, which divides, is of the rounded ones).  A NaN or an
  * infinity in a row reaches the tokens that see it and no others.  Latents times 2^8 times the context's
  * length have to stay in fp32's range.
- * Past some 170 new tokens a request, multiplying the latents out into per-head keys and values costs
- * fewer operations than this form; pkv_attn_extend serves those.
+ * Every new token costs num_heads * (2 latent_dim + rope_dim) products a position: for whole prompts,
+ * multiplying the latents out into keys and values a head costs fewer (from some 170 new tokens on).
  *   num_heads  1 to 1024; total_q * num_heads < 2^31
  *   workspace  device, 256-byte aligned, >= pkv_latent_workspace bytes (whatever the batch), first word
  *              zeroed once.  Calls that may overlap on the GPU need one each. */

@@ -26,6 +26,12 @@
 // reduced, ref raised and O^T rescaled: once at a range's start, seldom after.  Weights stay below 2^8, in
 // bf16 (their own sum is what they are divided by).  Sums are fp32.
 //
+// What bounds it (R = 512).  64 ragged requests of 32 heads, 648 MB: 115 us, 5.6 TB/s, 83 % of a copy's rate: DRAM.
+// With 128 heads the products, 1,920 cycles a tile and 64 rows (S 36 of 32 cycles, half of a full M's rate; P V 16 of 48, for a
+// product of N 64 is bound by reading A), are busy half of the time: 256 requests 205 us, 740 TFLOP/s, 39 % of cuBLAS's
+// rate.  A tile lives for some 6,000 cycles in its stage (2,700 to be copied, 1,900 in S beside the other tile's P V, 1,200 in
+// the softmax, 200 in its own P V's first 16 keys), there is room for two, and so one is done every 3,000.
+//
 // Work is divided on the device, from seq_lens: tiles of all requests in a line, an equal range of them a
 // CTA (or pair, below), so a captured graph follows the lengths.  A request's rows beyond N are further units of the
 // line; with more than 64 rows two CTAs take the same range, 64 rows each, so that the second one's tiles
@@ -51,9 +57,9 @@ constexpr float kLUnset = -1e30f;       // a reference before any key was seen
 constexpr int kLCached = 64;            // requests of a range that are kept in shared memory
 constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
 constexpr int32_t kLLongest = 0x7FFFFF00;  // keys of a request: tiles' ends stay within 32 bits
-// What a unit counts in the line beside its tiles, for its start and its output: 256 requests of 33 tiles take 235 us with
-// 0, 229 with 2, 225 with 3 or 4; 64 requests of 1 to 200 keys 21, 15, 16 and 16.
-constexpr int kLUnitTiles = 3;
+// What a unit counts in the line beside its tiles, for its start and its output: 32 requests of 500 to 1,500 keys take 25.7 us
+// with 0, 22.6 with 2; 64 of 1 to 200 keys 16.9 and 14.5.
+constexpr int kLUnitTiles = 2;
 constexpr int kLMinTiles = 2;           // a range's tiles at least
 constexpr float kLog2eL = 1.4426950408889634f;
 constexpr float kLagL = 8.0f;           // log2 units by which a logit may pass its reference
@@ -224,7 +230,7 @@ PKV_DEV bool next_work(const LatentParams &p, const LMisc *m, LCursor &c, LSeg &
 
 // ------------------------------------------------------------------------------------------
 
-// (The timer is read from the 256th retry on: a read takes as long as many a wait, some 700 cycles.)
+// (The timer is read from the 256th retry on.)
 PKV_DEV bool lwait(uint64_t *bar, uint32_t parity, LMisc *m, const LatentParams &p, int where) {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
