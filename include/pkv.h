@@ -499,7 +499,7 @@ typedef struct pkv_latent_pool {
 } pkv_latent_pool;
 
 /* Writes new tokens' rows into their slots: the latent, normalised, and the rotated rotary key.
- *     row = [ c * norm_weight / sqrt(mean(c^2) + eps), rope(pe) ]      fp32, rounded once
+ *     row = [ c * norm_weight / sqrt(mean(c^2) + eps), rope(pe) ]      fp32 (the squares' sum too), rounded once
  *   c_new, pe_new  bf16 [n][latent_dim] and [n][rope_dim], rows token_stride elements apart (a multiple of
  *                  8; slices of one projection's rows); 16-byte aligned
  *   norm_weight    bf16 [latent_dim], 16-byte aligned, or NULL: the latent is copied as it is

@@ -53,7 +53,7 @@ constexpr int kLTile = 64;              // keys a tile
 constexpr int kLThreads = 384;
 constexpr int kLSoftmax = 256;          // threads of the softmax warps
 constexpr int kLBarHalf = 1;            // named barriers of the softmax warps' halves: 1 and 2
-constexpr float kLUnset = -1e30f;       // a reference before any key was seen
+constexpr float kLUnset = -3.4028234e38f;  // a reference before any key was seen: below every finite logit
 constexpr int kLCached = 64;            // requests of a range that are kept in shared memory
 constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
 constexpr int32_t kLLongest = 0x7FFFFF00;  // keys of a request: tiles' ends stay within 32 bits
@@ -622,9 +622,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
                             }
                         }
                     }
+                    // (not one fma: a reference is a rounded product, and among logits past 2^31 the difference from an
+                    // unrounded one is more than a weight has room for)
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        x[c] = fmaf(__uint_as_float(sv[c]), p.scale_log2, -ref[c]);
+                        sv[c] = __float_as_uint(__fmul_rn(__uint_as_float(sv[c]), p.scale_log2));
+                        x[c] = __uint_as_float(sv[c]) - ref[c];
                         most = fmaxf(most, x[c]);
                     }
                 }
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                     // Raise to the tile's maxima the references that those pass.  Maxima over a warp's keys, a column
                     // a lane at the end; a thread a column joins the quarters; all read what concerns them.
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(sv[c]) * p.scale_log2;
+                    for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(sv[c]);
                     const float most_of = reduce_keys<NC, true>(x, lane);
                     if ((lane & 15) < NC) reinterpret_cast<float *>(&m->col[c0 + (lane & (NC - 1))])[wq] = most_of;
                     named_bar_sync(bar, kLSoftmax / 2);
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         for (int i = 0; i < 4; ++i) {
                             l[c + i] *= fs[i];
                             ref[c + i] = ys[i];
-                            x[c + i] = fmaf(__uint_as_float(sv[c + i]), p.scale_log2, -ys[i]);
+                            x[c + i] = __uint_as_float(sv[c + i]) - ys[i];
                         }
                     }
                     if (t > s.t0 && ok) {

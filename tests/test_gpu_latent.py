@@ -392,6 +392,17 @@ def test_one_key_gives_its_latent(pkv):
         assert np.array_equal(o[i], np.broadcast_to(c.data[c.slots(i)][:, :512], (16, 512)))
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_far_out(pkv, sign):
+    """Equal keys under logits of some 10^31 in size, above or below 0: the weights are equal, and the output is their latent."""
+    c = Case(pkv, 16, 512, 1, [100, 70], [4, 1], seed=2)
+    row = ref.bf16(np.random.default_rng(1).choice([-1.0, 1.0], 576) * 1e15)
+    c.pool.rows.copy_(torch.from_numpy(np.broadcast_to(row, c.data.shape).astype(np.float32)))
+    c.q.copy_(torch.from_numpy(np.broadcast_to(sign * row, c.q.shape).astype(np.float32)))
+    o = values(c.run())
+    assert np.array_equal(o, np.broadcast_to(row[:512], o.shape))
+
+
 def test_shared_prefixes(pkv):
     c = Case(pkv, 16, 512, 16, [300, 260, 400, 257], [1, 3, 2, 1], seed=6, shared=256)
     c.check(c.run())
