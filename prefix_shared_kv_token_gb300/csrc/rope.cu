@@ -87,6 +87,7 @@ struct RopeParams {
     float k_scale, v_scale;
     const int32_t *positions, *loc;
     int64_t n;
+    int32_t head_shift;        // heads a warp takes at a time: 1 << head_shift; tokens: what lanes are left
     int32_t parts;             // warps a token
     int32_t *err;
 };
@@ -106,9 +107,8 @@ template <bool INTER, int STORE>
 __global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int per = 32 >> p.lane_shift;  // heads a warp takes at a time
-    const int u = lane & ((1 << p.lane_shift) - 1), h0 = lane >> p.lane_shift;
+    const int lane = threadIdx.x & 31, per = 1 << p.head_shift, tokens = 32 >> (p.lane_shift + p.head_shift);
+    const int u = lane & ((1 << p.lane_shift) - 1), h0 = (lane >> p.lane_shift) & (per - 1), sub = lane >> (p.lane_shift + p.head_shift);
     const bool on = u < p.units, turned = u < p.rot_units;
     // Offsets of the unit's two vectors in its head: neighbouring lanes have neighbouring vectors, the rotated part's
     // first half and its second, then the rest's.  (Two neighbours a lane: 65,536 tokens into an e4m3 pool 288 us, not 256.)
@@ -117,37 +117,39 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
     const int pair_a = INTER ? 4 * u : 8 * u, pair_b = INTER ? 4 * (u + p.rot_units) : 8 * u + 4;
     const bool two = u != p.units - 1 || p.last_vecs == 2;
     const int heads = p.hq + (STORE ? 2 * p.hkv : 0);
-    const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5, all = p.n * p.parts;
-    // a token's slot and position are loaded while the one before is worked on
-    int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    // The warps go through the tokens once; where a token has several, each has only its part of that one.  A
+    // token's slot and position are loaded while the one before is worked on.
+    const uint32_t w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int part = (int)(w % p.parts);
+    const int64_t step = (int64_t)((gridDim.x * blockDim.x) >> 5) * tokens;
     int32_t next_slot = 0, next_pos = 0;
-    auto look = [&](int64_t at) {
-        if (at >= all) return;
-        next_pos = ld(p.positions + at / p.parts);
-        if constexpr (STORE != 0) next_slot = ld(p.loc + at / p.parts);
+    auto look = [&](int64_t tok) {
+        if (tok >= p.n) return;
+        next_pos = ld(p.positions + tok);
+        if constexpr (STORE != 0) next_slot = ld(p.loc + tok);
     };
-    look(w);
-    for (; w < all; w += warps) {
-        const int64_t tok = w / p.parts;
-        const int part = (int)(w - tok * p.parts);
+    int64_t tok = (int64_t)(w / p.parts) * tokens + sub;
+    look(tok);
+    for (; tok < p.n; tok += step) {
         const int32_t slot = next_slot, pos = next_pos;
-        look(w + warps);
+        look(tok + step);
+        if (!on) continue;
         bool stored = true;
         if constexpr (STORE != 0) {
             if (slot == -1) continue;  // a padded token
             stored = slot >= 0 && slot < p.num_slots;
-            if (!stored && part == 0 && lane == 0) set_error(p.err, DERR_SLOT_RANGE);
+            if (!stored && part == 0 && u == 0 && h0 == 0) set_error(p.err, DERR_SLOT_RANGE);
         }
         Turn t;
         bool have = false;
         constexpr int kInFlight = 4;
-        for (int h = part * per + h0; __any_sync(0xffffffffu, h < heads); h += kInFlight * per * p.parts) {
+        for (int h = part * per + h0; h < heads; h += kInFlight * per * p.parts) {
             uint4 a[kInFlight], b[kInFlight];
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) {
                 const int hd = h + i * per * p.parts;
                 a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (!on || hd >= heads || (STORE && hd >= p.hq && !stored)) continue;
+                if (hd >= heads || (STORE && hd >= p.hq && !stored)) continue;
                 const uint16_t *src;
                 if (!STORE || hd < p.hq) src = p.q + tok * p.q_tok + hd * p.q_head;
                 else if (hd < p.hq + p.hkv) src = p.k + tok * p.k_tok + (hd - p.hq) * p.d;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) {
                 const int hd = h + i * per * p.parts;
-                if (!on || hd >= heads) continue;
+                if (hd >= heads) continue;
                 const bool is_q = !STORE || hd < p.hq, is_v = STORE && hd >= p.hq + p.hkv;
                 if (!is_q && !stored) continue;
                 float x[8], y[8];
@@ -219,13 +221,19 @@ static int launch_rope(RopeParams p, const pkv_rope_spec *r, int store, cudaStre
     p.last_vecs = rest & 1 ? 1 : 2;
     p.lane_shift = 0;
     while ((1 << p.lane_shift) < p.units) ++p.lane_shift;
-    const int heads = p.hq + (store ? 2 * p.hkv : 0), per = 32 >> p.lane_shift;
+    // Heads side by side in a warp, as many as there are; where that leaves lanes, several tokens (262,144 tokens of one
+    // head of 64: 152 us by a token a warp, 22 by eight).
+    const int heads = p.hq + (store ? 2 * p.hkv : 0);
+    p.head_shift = 0;
+    while ((1 << p.head_shift) < heads && p.head_shift < 5 - p.lane_shift) ++p.head_shift;
+    const int per = 1 << p.head_shift, tokens = 32 >> (p.lane_shift + p.head_shift);
     // Warps a token: all of a token's heads in one warp's steps of four once that fills the GPU
     // (16 warps an SM), else as many as its heads give work, for then the time is a chain of loads.
     // 256 tokens of 128 heads: 5.3 us by 9 warps a token, 8.9 by one.
     const int64_t steps = (heads + per - 1) / per, full = (int64_t)num_sms() * 16;
     p.parts = (int32_t)std::min<int64_t>(steps, std::max<int64_t>(1, full / p.n));
-    const int64_t blocks = std::min<int64_t>((p.n * p.parts + 7) / 8, (int64_t)num_sms() * 32);
+    const int64_t warps = (p.n + tokens - 1) / tokens * p.parts;
+    const int64_t blocks = std::min<int64_t>((warps + 7) / 8, (int64_t)num_sms() * 32);
     auto kern = r->interleaved ? (store == 0 ? rope_kernel<true, 0> : store == 1 ? rope_kernel<true, 1> : rope_kernel<true, 2>)
                                : (store == 0 ? rope_kernel<false, 0> : store == 1 ? rope_kernel<false, 1> : rope_kernel<false, 2>);
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, s, true, p) == cudaSuccess ? PKV_OK : PKV_E_CUDA;
