@@ -6,7 +6,7 @@
 //     y1 = m (x1 cos - x2 sin),  y2 = m (x2 cos + x1 sin).
 // f is held as the 64-bit fraction of a turn that one position adds, so the product with p wraps
 // modulo a whole turn by itself: the reduction of the angle is exact, and its error is that of f's
-// last bit, p * 2^-65 turns.  The top 32 bits go through sincospif.  (A float product p f is off by
+// last bit, p * 2^-65 turns.  The top 32 bits are the angle.  (A float product p f is off by
 // 2^-24 of itself, 0.06 radians at position 10^6; a table of cosines would have to be read.)
 //
 // All three are bandwidth kernels: every element read once and written once, 16 bytes a load.  A
@@ -29,6 +29,20 @@ struct Turn {
     float c[8], s[8];
 };
 
+// Sine and cosine of h * 2^-32 turns.  To the nearest quarter turn in integers; what remains, an angle of at most
+// pi / 4, by the Taylor series up to the 9th and 8th power (the next terms are below 2e-9 and 3e-8).
+PKV_DEV void sincos_of(int32_t h, float &sine, float &cosine) {
+    const int32_t quarter = (int32_t)(((uint32_t)h + 0x20000000u) >> 30);
+    const float x = (float)(int32_t)((uint32_t)h - ((uint32_t)quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float z = x * x;
+    const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+    sine = quarter & 1 ? c : s;
+    cosine = quarter & 1 ? s : c;
+    if (quarter & 2) sine = -sine;
+    if ((quarter + 1) & 2) cosine = -cosine;
+}
+
 // Of pairs a .. a + 3 and b .. b + 3.
 PKV_DEV Turn turn_of(const uint64_t *phases, int a, int b, int32_t pos, float magnitude) {
     Turn t;
@@ -36,7 +50,7 @@ PKV_DEV Turn turn_of(const uint64_t *phases, int a, int b, int32_t pos, float ma
     for (int i = 0; i < 8; ++i) {
         const uint64_t turns = (uint64_t)(int64_t)pos * ld(phases + (i < 4 ? a + i : b + i - 4));  // modulo 2^64: modulo a turn
         float s, c;
-        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);     // half turns in [-1, 1)
+        sincos_of((int32_t)(turns >> 32), s, c);
         t.c[i] = c * magnitude;
         t.s[i] = s * magnitude;
     }

@@ -68,6 +68,17 @@ def test_rope(pkv, layout, n, heads, dim, rot):
     near(values(x), want, slack)
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("n,heads,dim,rot", [(1001, 1, 64, 64), (30001, 1, 16, 16), (777, 2, 64, 32), (95, 3, 32, 16), (5, 1, 128, 128), (7, 1, 24, 16)])
+def test_rope_of_few_heads(pkv, layout, n, heads, dim, rot):
+    """Several tokens to a warp, the last warp with fewer."""
+    rope = pkv.Rope(rot, layout=layout)
+    x, xv = draws((n, heads, dim), n)
+    pos = np.random.default_rng(n).integers(0, 2 ** 18, n)
+    want, slack = ref.rotate(xv, pos, rope.inv_freq, layout == "interleaved")
+    near(values(pkv.rope(x, dev(pos), rope)), want, slack)
+
+
 def test_rope_negative_positions_turn_back(pkv):
     rope = pkv.Rope(64)
     x, xv = draws((50, 4, 64), 1)
@@ -124,7 +135,8 @@ def e4m3_near(codes, want, slack):
 @pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
 @pytest.mark.parametrize("n,hq,hkv,d,rot,layout,pools", [
     (1, 8, 2, 64, 64, "half", "separate"), (4, 32, 8, 128, 128, "half", "interleaved"), (300, 5, 5, 64, 32, "interleaved", "separate"),
-    (2001, 16, 1, 128, 64, "interleaved", "interleaved"), (700, 64, 8, 128, 96, "half", "separate"), (33, 0, 3, 64, 16, "half", "separate")])
+    (2001, 16, 1, 128, 64, "interleaved", "interleaved"), (700, 64, 8, 128, 96, "half", "separate"), (33, 0, 3, 64, 16, "half", "separate"),
+    (4003, 0, 1, 64, 64, "half", "interleaved"), (901, 1, 1, 64, 48, "interleaved", "separate")])
 def test_rope_store(pkv, dtype, n, hq, hkv, d, rot, layout, pools):
     rope = pkv.Rope(rot, layout=layout, scaling=YARN if rot == 64 else None)
     rng = np.random.default_rng(n)
