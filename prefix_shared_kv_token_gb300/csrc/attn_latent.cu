@@ -23,7 +23,7 @@
 //               between the half-warps), a thread one key and N / 4 columns; P back through shared memory
 // The softmax needs a column's maximum, which lies across lanes.  A running reference stands in for it: weights
 // are 2^(s - ref), and only where a logit passes ref by more than 8 (a vote a tile) is the tile's maximum
-// reduced, ref raised and O^T rescaled: once at a range's start, seldom after.  Weights stay below 2^8, in
+// reduced, ref raised and O^T rescaled: once at a unit's start, seldom after.  Weights stay below 2^8, in
 // bf16 (their own sum is what they are divided by).  Sums are fp32.
 //
 // What bounds it (R = 512).  64 ragged requests of 32 heads, 648 MB: 115 us, 5.6 TB/s, 83 % of a copy's rate: DRAM.
@@ -36,7 +36,7 @@
 // CTA (or pair, below), so a captured graph follows the lengths.  A request's rows beyond N are further units of the
 // line; with more than 64 rows two CTAs take the same range, 64 rows each, so that the second one's tiles
 // come from L2.  A range's first and last unit may be shared with its neighbours: their partial sums go to records
-// in the workspace, which merge_kernel joins.
+// in the workspace, which latent_merge_kernel joins.
 
 #include <algorithm>
 #include <atomic>
@@ -99,7 +99,7 @@ struct LCfg {
 
 struct LMisc {
     uint64_t full[4], empty[16];  // [stage], [stage][16 keys]
-    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone, ofull, drain[2];
+    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone[2], ofull, drain[2];
     uint32_t tmem_base;
     int32_t abort_flag;
     int32_t start_r;      // the range's first request, and the tiles of it that earlier ranges have
@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
         mbar_init(&m->sfull[1], 1);
         mbar_init(&m->pfull[0], kLSoftmax / 32);  // (two: a warp may be done with a tile before another is with the one before)
         mbar_init(&m->pfull[1], kLSoftmax / 32);
-        mbar_init(&m->pvdone, 1);
+        mbar_init(&m->pvdone[0], 1);
+        mbar_init(&m->pvdone[1], 1);
         mbar_init(&m->ofull, 1);
         mbar_init(&m->drain[0], 1);
         mbar_init(&m->drain[1], 1);
@@ -452,8 +453,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
             while (ok && next_work<N>(p, m, cur, s, g)) {
                 ok = __all_sync(0xffffffffu, lwait(&m->qfull, nq & 1, m, p, 1));
                 for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
-                    // the softmax has read what S's place held two tiles ago
-                    if (n >= 2) ok = __all_sync(0xffffffffu, lwait(&m->pfull[n & 1], ((n >> 1) - 1) & 1, m, p, 2));
+                    // S's place is free: the P V of two tiles ago is done.  (Not merely its P written: the issuer of P V
+                    // has then seen that, before the same barrier can pass its next phase.)
+                    if (n >= 2) ok = __all_sync(0xffffffffu, lwait(&m->pvdone[n & 1], ((n >> 1) - 1) & 1, m, p, 2));
                     const int st = __shfl_sync(0xffffffffu, n % C::kStages, 0);
                     ok = __all_sync(0xffffffffu, ok && lwait(&m->full[st], (n / C::kStages) & 1, m, p, 3));
                     if (!ok) break;
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                                        v + (((C::kBlocks - 1) * C::kBlk + kk * 2048) >> 4), idesc, kk > 0 ? 1u : more);
                             tc_commit(&m->empty[st * 4 + kk]);
                         }
-                        tc_commit(&m->pvdone);
+                        tc_commit(&m->pvdone[n & 1]);
                         if (t + 1 == s.t1) tc_commit(&m->ofull);
                     }
                     __syncwarp();
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         m->alpha[c] = up ? ex2(had - top) : 1.f;  // (0 where there was no reference, and l is)
                         if (up) m->ref[c] = top;
                     }
-                    if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone, (n - 1) & 1, m, p, 8));
+                    if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, m, p, 8));
                     named_bar_sync(bar, kLSoftmax / 2);
 #pragma unroll
                     for (int c = 0; c < NC; c += 4) {
