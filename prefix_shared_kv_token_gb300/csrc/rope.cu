@@ -106,14 +106,15 @@ struct RopeParams {
     int32_t *err;
 };
 
-PKV_DEV void store8(uint16_t *dst, const float *x) { *reinterpret_cast<uint4 *>(dst) = pack8(x); }
+// (Written to be the first to leave L2, as they are read once: 65,536 tokens into an e4m3 pool 234 us, else 244.)
+PKV_DEV void store8(uint16_t *dst, const float *x) { __stcs(reinterpret_cast<uint4 *>(dst), pack8(x)); }
 PKV_DEV void store8_e4m3(uint8_t *dst, const float *x, float scale) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         w[i] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
                (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w[0], w[1]));
 }
 
 // STORE 0: rotate q only; 1, 2: k and v into a bf16 or an e4m3 pool too.
@@ -271,7 +272,7 @@ struct LatentStoreParams {
 
 // A warp T tokens at a time, two by two: R / 256 vectors of a latent a lane, the sums of squares over the warp.  The
 // T tokens' rotary keys, four units each, go to four lanes a token: with T = 8 to all lanes at once, where with two the sines
-// and cosines of 8 lanes took half of the kernel's instructions (131,072 tokens 60 us, with 8 56).  A
+// and cosines of 8 lanes took half of the kernel's instructions (131,072 tokens 60 us, with 8 56, and 53 with loads past L1).  A
 // token's loads are issued before its slot is known.
 template <int R, bool INTER, int T>
 __global__ void __launch_bounds__(256) latent_store_kernel(const LatentStoreParams p) {
@@ -292,8 +293,8 @@ __global__ void __launch_bounds__(256) latent_store_kernel(const LatentStorePara
         if (turns) {
             own_slot = ld(p.loc + first + mine);
             pos = ld(p.positions + first + mine);
-            a = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (first + mine) * p.pe_tok + off_a));
-            b = __ldcs(reinterpret_cast<const uint4 *>(p.pe + (first + mine) * p.pe_tok + off_b));
+            a = __ldcg(reinterpret_cast<const uint4 *>(p.pe + (first + mine) * p.pe_tok + off_a));
+            b = __ldcg(reinterpret_cast<const uint4 *>(p.pe + (first + mine) * p.pe_tok + off_b));
         }
 #pragma unroll 1
         for (int pair = 0; pair < T; pair += 2) {
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(256) latent_store_kernel(const LatentStorePara
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (tok + k < p.n) x[k][i] = __ldcs(reinterpret_cast<const uint4 *>(p.c + (tok + k) * p.c_tok) + 32 * i + lane);
+                    if (tok + k < p.n) x[k][i] = __ldcg(reinterpret_cast<const uint4 *>(p.c + (tok + k) * p.c_tok) + 32 * i + lane);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int32_t slot = __shfl_sync(0xffffffffu, own_slot, 4 * (pair + k));
