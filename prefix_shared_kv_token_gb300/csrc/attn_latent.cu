@@ -28,7 +28,7 @@
 //
 // What bounds it (R = 512).  64 ragged requests of 32 heads, 648 MB: 115 us, 5.6 TB/s, 83 % of a copy's rate: DRAM.
 // With 128 heads the products, 1,920 cycles a tile and 64 rows (S 36 of 32 cycles, half of a full M's rate; P V 16 of 48, for a
-// product of N 64 is bound by reading A), are busy half of the time: 256 requests 205 us, 740 TFLOP/s, 39 % of cuBLAS's
+// product of N 64 is bound by reading A), are busy half of the time: 256 requests 207 us, 733 TFLOP/s, 38 % of cuBLAS's
 // rate.  A tile lives for some 6,000 cycles in its stage (2,700 to be copied, 1,900 in S beside the other tile's P V, 1,200 in
 // the softmax, 200 in its own P V's first 16 keys), there is room for two, and so one is done every 3,000.
 //
