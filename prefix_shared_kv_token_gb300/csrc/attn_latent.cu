@@ -111,6 +111,7 @@ struct LMisc {
     float ref[64];        // columns' references
     float alpha[64];      // factors of a rescaling; 1 / sum at the end
     int32_t lim[64];      // keys that each row sees
+    int32_t zeroed[2][kLTile];  // [tile mod 2]: the last tile, from 1, in which a key's latent was not finite
 };
 static_assert(sizeof(LMisc) <= 4096, "LMisc");
 
@@ -426,6 +427,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         m->abort_flag = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x < 2 * kLTile) m->zeroed[threadIdx.x / kLTile][threadIdx.x % kLTile] = 0;
     if (warp == 1) {
         tmem_alloc(&m->tmem_base, 512);
         tmem_relinquish();
@@ -687,23 +689,30 @@ __global__ void __launch_bounds__(kLThreads, 1)
 #pragma unroll
                 for (int c = 0; c < NC; c += 2)
                     pk[c / 2] = pack_bf16x2(ex2(x[c]), ex2(x[c + 1]));
-                if (odd_row) {  // a key that is not finite has no weight to be 0 in the columns that see it
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if (!((hidden >> c) & 1u) && __uint_as_float(sv[c]) == -INFINITY) pk[c / 2] |= 0x7FFFu << (16 * (c & 1));
-                }
                 const int st = n % C::kStages;
                 if (odd_row) {
                     // A latent with an infinity or a NaN that some columns may not see: a weight of 0 would not keep it
-                    // from them.  It becomes zeros; the columns that see it have a weight of NaN.
+                    // from them.  It becomes zeros; the columns that see it get a weight of NaN.  (One under a logit of -inf and
+                    // a finite latent, by an infinity in the rotary key, keeps its 0, as in a tile without hidden keys.)
                     lwait(&m->full[st], (n / C::kStages) & 1, m, p, 9);  // (long complete: the copies, seen by this thread)
                     uint8_t *at = smem + st * C::kStage + k_in * 128;
                     bool bad = false;
                     for (int b = 0; b < R / 64; ++b)
                         for (int j = 0; j < 8; ++j) bad |= nonfinite8(*reinterpret_cast<const uint4 *>(at + b * C::kBlk + j * 16));
-                    if (bad)
+                    // Four threads have a key.  One that finds zeros where another was first finds that one's mark behind them.
+                    // (The halves are a tile apart at most: S of n + 2 waits for P V of n, and that for both.)
+                    volatile int32_t *mark = &m->zeroed[n & 1][k_in];
+                    __threadfence_block();
+                    bad |= *mark == n + 1;
+                    if (bad) {
+                        *mark = n + 1;
+                        __threadfence_block();
                         for (int b = 0; b < R / 64; ++b)
                             for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(at + b * C::kBlk + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            if (!((hidden >> c) & 1u)) pk[c / 2] |= 0x7FFFu << (16 * (c & 1));
+                    }
                 }
                 {
                     uint8_t *row = smem + st * C::kStage + (C::kBlocks - 1) * C::kBlk + k_in * 128;

@@ -1,0 +1,50 @@
+"""Rotary positions and the latent pool where they can go wrong: logits and rows that are not finite, sizes past one pass
+of a grid, ranges of many requests, joins of many records, waits that run out, rows of few keys, other streams."""
+
+import numpy as np
+import pytest
+import torch
+
+import latent_reference as ref
+from test_gpu_latent import SLOT_RANGE, POSITION, TIMEOUT, YARN, Case, dev, draws, e4m3_near, near, values, words
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    import prefix_shared_kv_token_gb300 as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# ----------------------------------------------------------------------------------------
+# logits that are not finite
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("length,new,at", [(128, 1, 70), (128, 1, 3), (100, 1, 99), (100, 1, 3), (65, 1, 64), (64, 1, 5), (63, 1, 62),
+                                           (200, 10, 195), (200, 10, 20), (700, 1, 690), (9000, 1, 8999), (9000, 1, 4444)])
+def test_an_infinite_rotary_key_weighs_the_same_anywhere(pkv, heads, length, new, at):
+    """Odd heads see it with a logit of -inf, and so as if it were not there; even ones with +inf, and get NaN."""
+    c = Case(pkv, heads, 512, 1, [length], [new], seed=at)
+    c.pool.rows[int(c.slots(0)[at]), 520] = float("inf")
+    sign = np.where(np.arange(heads) % 2, -1.0, 1.0)
+    c.q[:, :, 520] = torch.from_numpy(sign).cuda().to(torch.bfloat16)
+    c.qv[:, :, 520] = sign
+    o = values(c.run())
+    rows, seen = c.data[c.slots(0)], length - new + np.arange(new) + 1
+    blind = seen <= at
+    want, bound = ref.attend(c.qv, np.delete(rows, at, 0), 512, float(np.float32(c.scale)), seen - ~blind)
+    assert np.all(np.abs(o[:, 1::2] - want[:, 1::2]) <= bound[:, 1::2])
+    assert np.isnan(o[~blind, ::2]).all() and np.all(np.abs(o[blind, ::2] - want[blind, ::2]) <= bound[blind, ::2])
