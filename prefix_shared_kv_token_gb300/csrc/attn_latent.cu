@@ -750,9 +750,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 const int c = hf * NH + in_half;
                 const float4 y = m->col[c];
                 const float sum = (y.x + y.y) + (y.z + y.w);
-                m->alpha[c] = !s.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                // (A sum of 0 over keys that were seen, all logits -inf, divides to NaN.)
+                m->alpha[c] = !s.whole ? 1.f : m->lim[c] <= 0 ? 0.f : 1.f / sum;
+                // a reference of -inf: no key of this piece was seen
                 if (!s.whole)
-                    reinterpret_cast<float2 *>(p.rec_ml)[rec * N + c] = make_float2(m->ref[c] == kLUnset ? -INFINITY : m->ref[c], sum);
+                    reinterpret_cast<float2 *>(p.rec_ml)[rec * N + c] = make_float2(m->lim[c] <= s.t0 * kLTile ? -INFINITY : m->ref[c], sum);
             }
             named_bar_sync(bar, kLSoftmax / 2);
             if (!s.whole && !any) continue;  // its (-inf, 0) says that there is nothing to add
@@ -818,12 +820,9 @@ struct LatentMerge {
     const int32_t *err;
 };
 
-// A record's factor under the common maximum; 0 where it saw nothing.  (A maximum of -inf beside a sum that is not 0
-// is a NaN's: no key had a logit to be a maximum.)
-PKV_DEV float weight_of(float2 ml, float M) {
-    if (ml.x == -INFINITY) return ml.y == 0.f ? 0.f : 1.f;
-    return ex2(ml.x - M);
-}
+// A record's factor under the common maximum; 0 where it saw nothing.  (Where it saw keys and none had a logit to raise the
+// reference, only NaN and -inf, that is kLUnset still, below all others.)
+PKV_DEV float weight_of(float2 ml, float M) { return ml.x == -INFINITY ? 0.f : ex2(ml.x - M); }
 
 template <int R>
 __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge p) {
@@ -909,7 +908,7 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
                 acc[v] = make_float4(fmaf(w, y.x, acc[v].x), fmaf(w, y.y, acc[v].y), fmaf(w, y.z, acc[v].z), fmaf(w, y.w, acc[v].w));
             }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = M == -INFINITY ? 0.f : 1.f / L;  // zeros where no record saw a key
         uint2 *out = reinterpret_cast<uint2 *>(p.o + out_row * R);
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -970,7 +969,7 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
             }
 #pragma unroll
             for (int v = 0; v < 8; ++v) sum += s_l[v];
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = M == -INFINITY ? 0.f : 1.f / sum;
             reinterpret_cast<uint2 *>(p.o + out_row * R)[chunk * 16 + threadIdx.x] =
                 make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         }

@@ -48,3 +48,16 @@ def test_an_infinite_rotary_key_weighs_the_same_anywhere(pkv, heads, length, new
     want, bound = ref.attend(c.qv, np.delete(rows, at, 0), 512, float(np.float32(c.scale)), seen - ~blind)
     assert np.all(np.abs(o[:, 1::2] - want[:, 1::2]) <= bound[:, 1::2])
     assert np.isnan(o[~blind, ::2]).all() and np.all(np.abs(o[blind, ::2] - want[blind, ::2]) <= bound[blind, ::2])
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("length", [1, 63, 64, 65, 700, 9000])
+def test_logits_that_are_all_minus_infinity_give_nan(pkv, heads, length):
+    """The largest of them is -inf too, and their differences NaN.  Zeros are for tokens that see nothing."""
+    c = Case(pkv, heads, 512, 1, [length, 2, 0], [1, 4, 1], seed=length)
+    c.pool.rows[torch.from_numpy(c.slots(0)).cuda(), 530] = float("inf")
+    c.pool.rows[torch.from_numpy(c.slots(1)).cuda(), 530] = float("inf")
+    c.q[:, :, 530] = -1.0
+    o = values(c.run())
+    assert np.isnan(o[0]).all() and np.isnan(o[3:5]).all()
+    assert np.all(o[1:3] == 0) and np.all(o[5] == 0)
