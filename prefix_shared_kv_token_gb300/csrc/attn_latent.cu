@@ -901,7 +901,8 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
         for (int j = 0; j < cnt; ++j) {
             const float w = __shfl_sync(0xffffffffu, weight, j);
             L = fmaf(w, __shfl_sync(0xffffffffu, mine.y, j), L);
-            if (w == 0.f) continue;  // nothing was seen there (and nothing written), or nothing is left of it
+            // Nothing was seen there, and nothing written.  (Not by a weight of 0: a NaN stays one.)
+            if (__shfl_sync(0xffffffffu, mine.x, j) == -INFINITY) continue;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float4 y = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + v * 32 + lane);
@@ -933,7 +934,7 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
 #pragma unroll
         for (int w = 0; w < 8; ++w) M = fmaxf(M, s_m[w]);
         const float w = weight_of(mine, M);
-        if ((int)threadIdx.x < cnt) s_w[threadIdx.x] = w;
+        if ((int)threadIdx.x < cnt) s_w[threadIdx.x] = mine.x == -INFINITY ? -1.f : w;  // -1: nothing seen, nothing written
         float L = w * mine.y;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
@@ -948,9 +949,9 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
                 const int j = j0 + 16 * u;
-                f[u] = j < cnt ? s_w[j] : 0.f;
+                f[u] = j < cnt ? s_w[j] : -1.f;
                 y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (f[u] != 0.f) y[u] = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + chunk * 16 + at);
+                if (!(f[u] < 0.f)) y[u] = ld(reinterpret_cast<const float4 *>(p.rec + rec_of(j) * R) + chunk * 16 + at);
             }
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u)

@@ -61,3 +61,21 @@ def test_logits_that_are_all_minus_infinity_give_nan(pkv, heads, length):
     o = values(c.run())
     assert np.isnan(o[0]).all() and np.isnan(o[3:5]).all()
     assert np.all(o[1:3] == 0) and np.all(o[5] == 0)
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("length,loud", [(150, 70), (700, 600), (9000, 6000)])
+def test_a_nan_survives_the_join(pkv, heads, length, loud):
+    """A latent with an infinity under a logit of -inf: 0 times it is NaN, in that element alone, and stays so beside a key of
+    another range whose logit leaves all others without weight."""
+    c = Case(pkv, heads, 512, 1, [length], seed=length)
+    rows = c.slots(0)
+    c.pool.rows[int(rows[10]), 7] = float("inf")
+    c.q[:, :, 7] = -1.0
+    c.pool.rows[int(rows[loud]), 530] = 1024.0
+    c.q[:, :, 530] = 128.0
+    o = values(c.run())
+    rest = np.arange(512) != 7
+    assert np.isnan(o[:, :, 7]).all()
+    # the others' weights are below e^-5000: the output is the loud key's latent
+    assert np.array_equal(o[..., rest], np.broadcast_to(c.data[rows[loud], :512][rest], o[..., rest].shape))
