@@ -389,6 +389,21 @@ def _where(stream):
     return torch, device, _raw_stream(device) if stream is None else _stream(stream)
 
 
+def _made(shape, device, stream):
+    """A bf16 tensor for the output of a call on this stream.  On another stream than the current one it comes from that
+    stream's memory: the current one's may still be read by what is queued there.  The current stream's use of it
+    is recorded, as its reader is likely there."""
+    torch = _torch
+    if stream == _raw_stream(device):
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    # (an ExternalStream of handle 0 would be a stream of the pool)
+    at = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(at):
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def _space(workspace, device):
     """(address, bytes) of a workspace."""
     at = _fits("workspace", workspace, getattr(workspace, "dtype", None), device, getattr(workspace, "shape", None))
@@ -589,7 +604,7 @@ def rope(x, positions, rope, out=None, stream=None):
     spec = rope.c(device)
     at, s = _rows("x", x, device, shape)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        out = _made(shape, device, stream)
     to, so = _rows("out", out, device, shape)
     check("pkv_rope", lib.pkv_rope(spec, at, s[0], s[1], to, so[0], so[1], heads, dim,
                                    _fits("positions", positions, torch.int32, device, (n,)), n, stream))
@@ -613,7 +628,7 @@ def rope_store(pool: Pool, q, k_new, v_new, positions, out_cache_loc, rope, q_ou
         if p.num_kv_heads > 1 and st[1] != p.head_dim:
             raise ValueError(f"{name} must have its heads side by side")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        q_out = _made(shape, device, stream)
     to, so = _rows("q_out", q_out, device, shape)
     ws, size = (None, 4) if workspace is None else _space(workspace, device)
     if size < 4:

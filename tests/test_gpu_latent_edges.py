@@ -79,3 +79,81 @@ def test_a_nan_survives_the_join(pkv, heads, length, loud):
     assert np.isnan(o[:, :, 7]).all()
     # the others' weights are below e^-5000: the output is the loud key's latent
     assert np.array_equal(o[..., rest], np.broadcast_to(c.data[rows[loud], :512][rest], o[..., rest].shape))
+
+
+# ----------------------------------------------------------------------------------------
+# other streams
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("call", ["rope", "rope_store"])
+def test_an_output_made_for_another_stream_is_that_streams(pkv, call, raw):
+    """The current stream still reads memory that it has given back: the call on the other stream takes none of it."""
+    n, heads, dim = 3000, 16, 64
+    rope, side = pkv.Rope(dim), torch.cuda.Stream()
+    x, xv = draws((n, heads, dim), 1)
+    k, _ = draws((n, 1, dim), 2)
+    pool, pos, loc = pkv.Pool.allocate(n, 1, dim), dev(np.arange(n)), dev(np.arange(n))
+    want, slack = ref.rotate(xv, np.arange(n), rope.inv_freq, False)
+    handle = side.cuda_stream if raw else side
+    side.wait_stream(torch.cuda.current_stream())
+    for turn in range(4):
+        old = torch.full((n, heads, dim), 5.0, dtype=torch.bfloat16, device="cuda")
+        kept = torch.empty_like(old)
+        torch.cuda._sleep(100_000_000)     # some 50 ms
+        kept.copy_(old)
+        del old
+        if call == "rope":
+            got = pkv.rope(x, pos, rope, stream=handle)
+        else:
+            got = pkv.rope_store(pool, x, k, k, pos, loc, rope, stream=handle)
+        side.synchronize()
+        # the read has not been made yet (but for the first time, when memory and kernels were new, which waits for it)
+        assert turn == 0 or not torch.cuda.current_stream().query()
+        near(values_on(got, side), want, slack)
+        assert bool((kept == 5.0).all())
+        del got
+
+
+def values_on(t, stream):
+    with torch.cuda.stream(stream):
+        return values(t)
+
+
+def test_the_default_stream_by_its_handle(pkv):
+    """Handle 0, from a stream of one's own."""
+    rope = pkv.Rope(64)
+    x, xv = draws((50, 4, 64), 1)
+    pos = dev(np.arange(50))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        out = pkv.rope(x, pos, rope, stream=0)
+    torch.cuda.synchronize()
+    want, slack = ref.rotate(xv, np.arange(50), rope.inv_freq, False)
+    near(values(out), want, slack)
+
+
+def test_every_call_runs_on_the_stream_it_is_given(pkv):
+    """Behind work of that stream, which makes its inputs."""
+    side = torch.cuda.Stream()
+    rope = pkv.Rope(64)
+    c = Case(pkv, 16, 512, 1, [100, 80], seed=8)
+    clean = c.run()
+    q, qv = draws((90, 16, 64), 3)
+    rows, rv = draws((90, 576), 4)
+    pool, pos, loc = pkv.LatentPool.allocate(90), dev(np.arange(90)), dev(np.arange(90)[::-1].copy())
+    batch, o = c.batch(), torch.zeros_like(clean)
+    late = [torch.full_like(t, float("nan")) for t in (q, rows, c.q)]
+    turned = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        for t, x in zip(late, (q, rows, c.q)):
+            t.copy_(x)
+    pkv.rope(late[0], pos, rope, out=turned, stream=side)
+    pkv.latent_store(pool, late[1][:, :512], late[1][:, 512:], pos, loc, rope, stream=side)
+    pkv.attn_latent(c.pool, batch, late[2], o, c.scale, c.ws, stream=side.cuda_stream)
+    side.synchronize()
+    want, slack = ref.rotate(qv, np.arange(90), rope.inv_freq, False)
+    near(values(turned), want, slack)
+    assert torch.equal(pool.rows.flip(0)[:, :512], rows[:, :512]) and torch.equal(o, clean)
