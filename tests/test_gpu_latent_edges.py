@@ -157,3 +157,27 @@ def test_every_call_runs_on_the_stream_it_is_given(pkv):
     want, slack = ref.rotate(qv, np.arange(90), rope.inv_freq, False)
     near(values(turned), want, slack)
     assert torch.equal(pool.rows.flip(0)[:, :512], rows[:, :512]) and torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("aside", [False, True])
+def test_rows_of_padded_tokens_are_zeros_in_a_new_output(pkv, aside):
+    rope = pkv.Rope(64)
+    q, qv = draws((300, 4, 64), 3)
+    k, _ = draws((300, 1, 64), 4)
+    loc = np.arange(300)
+    loc[::3] = -1
+    pool, side = pkv.Pool.allocate(300, 1, 64), torch.cuda.Stream()
+    pos, at = dev(np.arange(300)), dev(loc)
+    torch.cuda.synchronize()
+    for _ in range(3):                     # memory that held something else
+        for s in (side, torch.cuda.current_stream()):
+            with torch.cuda.stream(s):
+                torch.full((300, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        out = pkv.rope_store(pool, q, k, k, pos, at, rope, stream=side if aside else None)
+        torch.cuda.synchronize()
+        want, slack = ref.rotate(qv, np.arange(300), rope.inv_freq, False)
+        got = values(out)
+        assert np.all(got[loc < 0] == 0)
+        near(got[loc >= 0], want[loc >= 0], slack[loc >= 0])
+        del out
