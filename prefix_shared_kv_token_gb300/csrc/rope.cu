@@ -107,7 +107,14 @@ struct RopeParams {
 };
 
 // (Written to be the first to leave L2, as they are read once: 65,536 tokens into an e4m3 pool 234 us, else 244.)
-PKV_DEV void store8(uint16_t *dst, const float *x) { __stcs(reinterpret_cast<uint4 *>(dst), pack8(x)); }
+// What did not turn keeps its bits, a NaN's payload too: its upper halves are what was read.
+PKV_DEV void store8(uint16_t *dst, const float *x, bool turned) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = turned ? pack_bf16x2(x[2 * i], x[2 * i + 1]) : __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
+    __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+}
 PKV_DEV void store8_e4m3(uint8_t *dst, const float *x, float scale) {
     uint32_t w[2];
 #pragma unroll
@@ -188,15 +195,15 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
                 if (turned && !is_v) rotate16<INTER>(x, y, t);
                 if (is_q) {
                     uint16_t *dst = p.q_out + tok * p.o_tok + hd * p.o_head;
-                    store8(dst + off_a, x);
-                    if (two) store8(dst + off_b, y);
+                    store8(dst + off_a, x, turned);
+                    if (two) store8(dst + off_b, y, turned);
                 } else if constexpr (STORE != 0) {
                     const int g = is_v ? hd - p.hq - p.hkv : hd - p.hq;
                     uint8_t *dst = (is_v ? p.v_pool : p.k_pool) + (int64_t)slot * p.slot_bytes;
                     if constexpr (STORE == 1) {
                         uint16_t *row = reinterpret_cast<uint16_t *>(dst) + g * p.d;
-                        store8(row + off_a, x);
-                        if (two) store8(row + off_b, y);
+                        store8(row + off_a, x, turned && !is_v);
+                        if (two) store8(row + off_b, y, turned && !is_v);
                     } else {
                         const float scale = is_v ? p.v_scale : p.k_scale;
                         store8_e4m3(dst + g * p.d + off_a, x, scale);
@@ -342,8 +349,8 @@ __global__ void __launch_bounds__(256) latent_store_kernel(const LatentStorePara
             unpack8(b, yb);
             rotate16<INTER>(ya, yb, t);
             uint16_t *row = p.rows + (int64_t)own_slot * p.stride + R;
-            store8(row + off_a, ya);
-            store8(row + off_b, yb);
+            store8(row + off_a, ya, true);
+            store8(row + off_b, yb, true);
         }
     }
 }

@@ -181,3 +181,28 @@ def test_rows_of_padded_tokens_are_zeros_in_a_new_output(pkv, aside):
         assert np.all(got[loc < 0] == 0)
         near(got[loc >= 0], want[loc >= 0], slack[loc >= 0])
         del out
+
+
+# ----------------------------------------------------------------------------------------
+# what is copied
+
+
+def test_what_is_not_rotated_keeps_its_bits(pkv):
+    """NaNs with their payloads among them, in the rest of a head and in v, as kv_store keeps them."""
+    rope = pkv.Rope(16)
+    odd = torch.tensor([0x7FA1, -0x3D, 0x7FFF, 0x7F81, 0x0001, -0x8000, 0x7F80, 0x1234], dtype=torch.int16, device="cuda")
+    for n, heads, dim in ((3, 5, 64), (200, 2, 72), (1, 1, 24)):
+        x = torch.zeros((n, heads, dim), dtype=torch.bfloat16, device="cuda")
+        x.view(torch.int16)[..., 16:] = odd.repeat(dim // 8 - 2)
+        out = pkv.rope(x, words(n), rope)
+        assert torch.equal(out.view(torch.int16)[..., 16:], x.view(torch.int16)[..., 16:])
+    pool, plain = pkv.Pool.allocate(12, 3, 64), pkv.Pool.allocate(12, 3, 64)
+    q, _ = draws((9, 4, 64), 1)
+    k, _ = draws((9, 3, 64), 2)
+    v = odd.repeat(9 * 3 * 8).view(9, 3, 64).view(torch.bfloat16)
+    k.view(torch.int16)[..., 16:] = odd.repeat(6)
+    pos, loc = dev(np.arange(9)), dev(np.arange(9) + 1)
+    pkv.rope_store(pool, q, k, v, pos, loc, rope)
+    pkv.kv_store(plain, pkv.rope(k, pos, rope), v, loc)
+    assert torch.equal(pool.v.view(torch.int16), plain.v.view(torch.int16)) and torch.equal(pool.k.view(torch.int16), plain.k.view(torch.int16))
+    assert torch.equal(pool.v[1:10].view(torch.int16), v.view(torch.int16))
