@@ -52,7 +52,8 @@ extern "C" {
 #define PKV_E_DEVICE      -7  /* a kernel recorded an error in the workspace error word    */
 #define PKV_E_PLAN        -8  /* plan blob does not match the call                         */
 
-/* values a kernel may leave in the workspace error word (first error wins) */
+/* values a kernel may leave in the workspace error word (first error wins; pkv_attn_latent's timeout
+ * takes the place of a lesser one) */
 #define PKV_DERR_SLOT_RANGE 0x100  /* a slot read from a table was outside [0, num_slots)     */
 #define PKV_DERR_TIMEOUT    0x200  /* a bounded wait inside a kernel gave up (low byte: which) */
 #define PKV_DERR_POSITION   0x400  /* a work item addressed positions outside its row         */
@@ -527,6 +528,7 @@ int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec *rope, con
  * Every new token costs num_heads * (2 latent_dim + rope_dim) products a position: for whole prompts,
  * multiplying the latents out into keys and values a head costs fewer (from some 170 new tokens on).
  *   num_heads  1 to 1024; total_q * num_heads < 2^31
+ * A call that gives up on a wait (PKV_DERR_TIMEOUT) leaves rows of o as they are, and writes no wrong ones.
  *   workspace  device, 256-byte aligned, >= pkv_latent_workspace bytes (whatever the batch), first word
  *              zeroed once.  Calls that may overlap on the GPU need one each. */
 int pkv_latent_workspace(const pkv_latent_pool *pool, int32_t num_heads, size_t *bytes);

@@ -78,7 +78,8 @@ struct LatentParams {
     int32_t gs, ranges;                   // CTAs that share a range; ranges
     float *rec;                           // [range][2][gs][N][R]
     float *rec_ml;                        // [range][2][gs][N][2]
-    int32_t *units;                       // [range][8]: first unit (request, set, ends there), last unit (request, set)
+    int32_t *units;                       // [range][8]: first unit (request, set, ends there), last unit (request, set);
+                                          // words 3 and 7: whether the range's first CTA gave up, and its second
     int32_t *err;
     WaitPolicy wait;
 };
@@ -231,6 +232,12 @@ PKV_DEV bool next_work(const LatentParams &p, const LMisc *m, LCursor &c, LSeg &
 
 // ------------------------------------------------------------------------------------------
 
+// A wait that gave up: unlike what else may stand in the word, it leaves outputs unwritten, and so takes that one's place.
+PKV_DEV void set_timeout(int32_t *err, int32_t code) {
+    const int32_t had = atomicCAS(err, 0, code);
+    if (had != 0 && !(had & DERR_TIMEOUT)) atomicCAS(err, had, code);
+}
+
 // (The timer is read from the 256th retry on.)
 PKV_DEV bool lwait(uint64_t *bar, uint32_t parity, LMisc *m, const LatentParams &p, int where) {
     uint64_t t0 = 0;
@@ -241,7 +248,7 @@ PKV_DEV bool lwait(uint64_t *bar, uint32_t parity, LMisc *m, const LatentParams 
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
         if (now - t0 > p.wait.limit_ns) {
-            set_error(p.err, DERR_TIMEOUT | where);
+            set_timeout(p.err, DERR_TIMEOUT | where);
             *reinterpret_cast<volatile int32_t *>(&m->abort_flag) = 1;
             return false;
         }
@@ -805,19 +812,20 @@ __global__ void __launch_bounds__(kLThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0) p.units[range * 8 + 3 + 4 * g] = m->abort_flag;
 }
 
 // ------------------------------------------------------------------------------------------
 // Joins the records of units that several ranges share.  A unit's pieces are range c's last record and the
 // first records of the ranges behind it, up to the one in which it ends.  A row of a unit with up to 8 records is a
-// warp's task; of one with more, 64 elements of a row are a CTA's.
+// warp's task; of one with more, 64 elements of a row are a CTA's.  A unit that reaches into a range that gave up is left
+// out: records of it may be missing, or another call's.
 
 struct LatentMerge {
     const float *rec, *rec_ml;
     const int32_t *units, *indptr;
     int32_t ranges, gs, heads, N;
     uint16_t *o;
-    const int32_t *err;
 };
 
 // A record's factor under the common maximum; 0 where it saw nothing.  (Where it saw keys and none had a logit to raise the
@@ -837,12 +845,12 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (*p.err & DERR_TIMEOUT) return;  // records may be missing
+    auto gave_up = [&](int c) { return s_first[c].w != 0 || (p.gs == 2 && s_last[c].w != 0); };
     if ((int)threadIdx.x < p.ranges) {
         s_first[threadIdx.x] = ld(reinterpret_cast<const int4 *>(p.units) + threadIdx.x * 2);
         s_last[threadIdx.x] = ld(reinterpret_cast<const int4 *>(p.units) + threadIdx.x * 2 + 1);
     }
-    __syncthreads();
+    const bool any_gave_up = __syncthreads_or((int)threadIdx.x < p.ranges && gave_up(threadIdx.x));
     // Two lists in the ranges' order: every CTA has the same.  A unit ends with the first range behind its own whose first
     // piece ends there.
     const uint32_t ends = __ballot_sync(0xffffffffu, (int)threadIdx.x < p.ranges && s_first[threadIdx.x].x >= 0 && s_first[threadIdx.x].z);
@@ -856,6 +864,9 @@ __global__ void __launch_bounds__(256, 4) latent_merge_kernel(const LatentMerge 
             const uint32_t bits = s_ends[w] & (w == from >> 5 ? 0xffffffffu << (from & 31) : 0xffffffffu);
             if (bits) n = w * 32 + __ffs(bits) - (int)threadIdx.x;
         }
+        if (any_gave_up)
+            for (int c = threadIdx.x, to = n == 1 ? p.ranges : c + n; c < to; ++c)
+                if (gave_up(c)) n = 0;
     }
     const uint32_t few = __ballot_sync(0xffffffffu, n > 0 && n <= kFew), many = __ballot_sync(0xffffffffu, n > kFew);
     if (lane == 0) {
@@ -1002,7 +1013,7 @@ static int launch_latent(LatentParams p, const CUtensorMap &qmap, cudaStream_t s
     }
     if (launch_pdl(latent_kernel<R, N>, dim3((unsigned)(p.ranges * p.gs)), dim3(kLThreads), C::kSmem, s, true, p, qmap) != cudaSuccess)
         return PKV_E_CUDA;
-    LatentMerge mp{p.rec, p.rec_ml, p.units, p.indptr, p.ranges, p.gs, p.heads, N, p.o, p.err};
+    LatentMerge mp{p.rec, p.rec_ml, p.units, p.indptr, p.ranges, p.gs, p.heads, N, p.o};
     return launch_pdl(latent_merge_kernel<R>, dim3((unsigned)(4 * num_sms())), dim3(256), 0, s, true, mp) == cudaSuccess ? PKV_OK
                                                                                                                         : PKV_E_CUDA;
 }

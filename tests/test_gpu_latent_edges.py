@@ -206,3 +206,32 @@ def test_what_is_not_rotated_keeps_its_bits(pkv):
     pkv.kv_store(plain, pkv.rope(k, pos, rope), v, loc)
     assert torch.equal(pool.v.view(torch.int16), plain.v.view(torch.int16)) and torch.equal(pool.k.view(torch.int16), plain.k.view(torch.int16))
     assert torch.equal(pool.v[1:10].view(torch.int16), v.view(torch.int16))
+
+
+# ----------------------------------------------------------------------------------------
+# waits that run out
+
+
+@pytest.mark.parametrize("heads,seq", [(16, [20000]), (128, [3000, 100, 900]), (32, [500] * 300)])
+def test_a_timeout_shows_behind_an_earlier_error(pkv, heads, seq):
+    """It takes the place of the lesser error in the word, and what it kept from being computed is left as it was: no records of
+    an earlier call are joined."""
+    c = Case(pkv, heads, 512, 1, seq, seed=3)
+    other = Case(pkv, heads, 512, 1, seq, seed=4)
+    other.run(ws=c.ws)                     # records of other rows
+    torch.cuda.synchronize()
+    c.ws[0] = SLOT_RANGE
+    pkv.set_wait_limit_ns(1)
+    try:
+        o = values(c.run())
+    finally:
+        pkv.set_wait_limit_ns(0)
+    assert pkv.get_device_error(c.ws) & TIMEOUT
+    for i in range(len(seq)):
+        w, bound = c.want(i)
+        left = (o[i] == 11.0).all(-1)
+        assert np.all(left | (np.abs(o[i] - w[0]) <= bound[0]).all(-1)), i
+    again = c.run()                        # the word still holds the error: it is the caller's to clear
+    assert pkv.get_device_error(c.ws) & TIMEOUT
+    c.ws[0] = 0
+    c.check(again)
