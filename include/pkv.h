@@ -444,8 +444,8 @@ int pkv_attn_extend_block(const pkv_block_pool *pool, const pkv_batch *batch, co
 /* (x1, x2), at frequency f_i by the angle p f_i,                                           */
 /*     y1 = magnitude (x1 cos - x2 sin),  y2 = magnitude (x2 cos + x1 sin).                 */
 /* Pair i is elements (i, i + rotary_dim / 2), or interleaved (2i, 2i + 1).  The elements     */
-/* behind rotary_dim are copied.  Arithmetic is fp32, rounded once; the angle's error is       */
-/* below 2^-22 of a radian at any int32 position (also a negative one).                      */
+/* behind rotary_dim are copied.  Arithmetic is fp32, rounded once; the angle's error is below    */
+/* 2^-23 + |p f_i| 2^-52 radians (of a frequency of 1 at the farthest int32 position 2^-20.7).        */
 
 typedef struct pkv_rope_spec {
     const uint64_t *phases;  /* device, [rotary_dim / 2]: 2^64ths of a turn a position         */

@@ -5,8 +5,9 @@
 // A pair (x1, x2) at frequency f and position p turns by the angle p f:
 //     y1 = m (x1 cos - x2 sin),  y2 = m (x2 cos + x1 sin).
 // f is held as the 64-bit fraction of a turn that one position adds, so the product with p wraps
-// modulo a whole turn by itself: the reduction of the angle is exact, and its error is that of f's
-// last bit, p * 2^-65 turns.  The top 32 bits are the angle.  (A float product p f is off by
+// modulo a whole turn by itself: the reduction of the angle is exact, and its error is that of the
+// fraction: p * 2^-65 turns for its last bit, and |p f| 2^-52 radians at most for f and its division by
+// 2 pi in 64-bit floats.  The top 32 bits are the angle.  (A float product p f is off by
 // 2^-24 of itself, 0.06 radians at position 10^6; a table of cosines would have to be read.)
 //
 // All three are bandwidth kernels: every element read once and written once, 16 bytes a load.  A
@@ -362,9 +363,10 @@ extern "C" int pkv_rope_phases(const double *inv_freq, int32_t n, uint64_t *phas
     for (int32_t i = 0; i < n; ++i)
         if (!std::isfinite(inv_freq[i])) return PKV_E_INVALID;
     for (int32_t i = 0; i < n; ++i) {
-        double t = inv_freq[i] / 6.283185307179586476925;  // turns a position; whole ones do not show
-        t -= std::floor(t);
-        phases[i] = t < 1.0 ? (uint64_t)std::rint(std::ldexp(t, 64)) : 0u;
+        double t = std::fabs(inv_freq[i]) / 6.283185307179586476925;  // turns a position
+        t -= std::floor(t);  // whole ones do not show (exact; of a negative t it would round to the bits of 1 - |t|)
+        const uint64_t turns = (uint64_t)std::rint(std::ldexp(t, 64));
+        phases[i] = inv_freq[i] < 0 ? 0 - turns : turns;
     }
     return PKV_OK;
 }
