@@ -26,6 +26,13 @@
 // reduced, ref raised and O^T rescaled: once at a unit's start, seldom after.  Weights stay below 2^8, in
 // bf16 (their own sum is what they are divided by).  Sums are fp32.
 //
+// Where a row sees fewer than kPreciseKeys keys, each with a large share of the output, a rounded weight would cost as much as
+// the output's own rounding leaves: such a unit's first tile is gone through a second time, with what the first time's
+// rounding left of those rows' weights.  (There is no room for both parts of P at once.)  At 2, 8 and 31 keys the relative
+// error is then that of the output's rounding, 0.00166; with one part it is 0.00175, 0.00190 and 0.00202, and stays near
+// that (0.0020 to 0.0022 from 32 keys on).  64 requests of 1 to 31 keys and 16 heads take 12.8 us, 11.7 with one part; 8
+// prompts of 128 tokens and 128 heads 106 and 85.
+//
 // What bounds it (R = 512).  64 ragged requests of 32 heads, 648 MB: 115 us, 5.6 TB/s, 83 % of a copy's rate: DRAM.
 // With 128 heads the products, 1,920 cycles a tile and 64 rows (S 36 of 32 cycles, half of a full M's rate; P V 16 of 48, for a
 // product of N 64 is bound by reading A), are busy half of the time: 256 requests 207 us, 733 TFLOP/s, 38 % of cuBLAS's
@@ -154,6 +161,9 @@ struct LSeg {
     int32_t vis0;                 // keys that the request's first new token sees (0 or less: none)
     int32_t row_lo;               // first of them, in rows of the request
     bool whole, first, ends;      // all of the unit is in this range; the range begins inside it; it ends in this range
+    int32_t twice;                // 1: tile 0 is gone through twice (see kPreciseKeys).  Steps i are start() .. t1 - 1, their
+                                  // tiles max(i, 0)
+    PKV_DEV int32_t start() const { return t0 - twice; }
 };
 
 struct LCursor {
@@ -210,6 +220,9 @@ PKV_DEV bool next_seg(const LatentParams &p, const LMisc *m, LCursor &c, LSeg &s
     s.first = c.t > 0;
     s.ends = c.t + n == c.tiles;
     s.whole = !s.first && s.ends;
+    // keys that this CTA's first row sees, and its last one: some row from 2 to kPreciseKeys - 1?
+    const int32_t fewest = s.vis0 + (int32_t)(lo / (uint32_t)p.heads), most = s.vis0 + (int32_t)((lo + s.nrows - 1) / (uint32_t)p.heads);
+    s.twice = s.t0 == 0 && s.t1 > 0 && s.nrows > 0 && fewest < kPreciseKeys && most > 1;
     c.left -= n;
     c.t += n;
     if (c.t == c.tiles) {
@@ -461,7 +474,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             const uint64_t rows = sdesc_sw128(sbase, 16, 1024), q = sdesc_sw128(sbase + C::kQOff, 16, 1024);
             while (ok && next_work<N>(p, m, cur, s, g)) {
                 ok = __all_sync(0xffffffffu, lwait(&m->qfull, nq & 1, m, p, 1));
-                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                for (int i = s.start(); ok && i < s.t1; ++i, ++n) {
                     // S's place is free: the P V of two tiles ago is done.  (Not merely its P written: the issuer of P V
                     // has then seen that, before the same barrier can pass its next phase.)
                     if (n >= 2) ok = __all_sync(0xffffffffu, lwait(&m->pvdone[n & 1], ((n >> 1) - 1) & 1, m, p, 2));
@@ -478,7 +491,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                             mma_ss(d, k + (((ks >> 2) * C::kBlk + (ks & 3) * 32) >> 4), q + (((ks >> 2) * C::kQBlk + (ks & 3) * 32) >> 4),
                                    idesc, ks > 0 ? 1u : 0u);
                         tc_commit(&m->sfull[n & 1]);
-                        if (t + 1 == s.t1) tc_commit(&m->qempty);
+                        if (i + 1 == s.t1) tc_commit(&m->qempty);
                     }
                     __syncwarp();
                 }
@@ -488,13 +501,13 @@ __global__ void __launch_bounds__(kLThreads, 1)
             constexpr uint32_t idesc = idesc_bf16_f32(128, N, 1, 1);
             const uint64_t rows = sdesc_sw128(sbase, C::kBlk, 1024);
             while (ok && next_work<N>(p, m, cur, s, g)) {
-                for (int t = s.t0; ok && t < s.t1; ++t, ++n) {
+                for (int i = s.start(); ok && i < s.t1; ++i, ++n) {
                     ok = __all_sync(0xffffffffu, lwait(&m->pfull[n & 1], (n >> 1) & 1, m, p, 4));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v = rows + (uint32_t)(__shfl_sync(0xffffffffu, n % C::kStages, 0) * (C::kStage >> 4));
                     const int st = __shfl_sync(0xffffffffu, n % C::kStages, 0);
-                    const uint32_t more = __shfl_sync(0xffffffffu, t > s.t0, 0);
+                    const uint32_t more = __shfl_sync(0xffffffffu, i > s.start(), 0);
                     if (leader) {
                         // by 16 keys, whose rows are given back as they are done with
 #pragma unroll
@@ -506,7 +519,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                             tc_commit(&m->empty[st * 4 + kk]);
                         }
                         tc_commit(&m->pvdone[n & 1]);
-                        if (t + 1 == s.t1) tc_commit(&m->ofull);
+                        if (i + 1 == s.t1) tc_commit(&m->ofull);
                     }
                     __syncwarp();
                 }
@@ -546,9 +559,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 return -1;
             };
             int32_t next = slot_of(s.t0);
-            for (int t = s.t0; ok && t < s.t1; ++t, ++tp) {
+            for (int i = s.start(); ok && i < s.t1; ++i, ++tp) {
                 const int32_t mine = next;
-                next = slot_of(t + 1);
+                next = slot_of(i + 1);
                 const int st = __shfl_sync(0xffffffffu, tp % C::kStages, 0);
                 const uint16_t *src[8];
                 uint32_t there = 0;  // bit j: row 4 j + sub has a slot
@@ -612,7 +625,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 l[c] = 0.f;
             }
             named_bar_sync(bar, kLSoftmax / 2);
-            for (int t = s.t0; t < s.t1; ++t, ++n) {
+            for (int i = s.start(); i < s.t1; ++i, ++n) {
+                const int t = max(i, 0);
+                const bool split = i < s.twice;  // weights in two parts: the first at i = -1, the second at 0
                 ok = __all_sync(0xffffffffu, ok && lwait(&m->sfull[n & 1], (n >> 1) & 1, m, p, 7));
                 uint32_t sv[NC];
                 float x[NC];  // logits above their references
@@ -642,53 +657,67 @@ __global__ void __launch_bounds__(kLThreads, 1)
                         most = fmaxf(most, x[c]);
                     }
                 }
-                if (!named_bar_and(bar, kLSoftmax / 2, ok && !(most > kLagL))) {
+                if (!named_bar_and(bar, kLSoftmax / 2, ok && !split && !(most > kLagL))) {
                     if (!named_bar_and(bar, kLSoftmax / 2, ok)) {
                         ok = false;
                         break;
                     }
-                    // Raise to the tile's maxima the references that those pass.  Maxima over a warp's keys, a column
-                    // a lane at the end; a thread a column joins the quarters; all read what concerns them.
+                    if (!split || i < 0) {
+                        // Raise to the tile's maxima the references that those pass.  Maxima over a warp's keys, a column
+                        // a lane at the end; a thread a column joins the quarters; all read what concerns them.
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(sv[c]);
-                    const float most_of = reduce_keys<NC, true>(x, lane);
-                    if ((lane & 15) < NC) reinterpret_cast<float *>(&m->col[c0 + (lane & (NC - 1))])[wq] = most_of;
-                    named_bar_sync(bar, kLSoftmax / 2);
-                    if (in_half < NH) {
-                        const int c = hf * NH + in_half;
-                        const float4 y = m->col[c];
-                        const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)), had = m->ref[c];
-                        const bool up = top > had + kLagL;  // (a column's references follow its own logits alone)
-                        m->alpha[c] = up ? ex2(had - top) : 1.f;  // (0 where there was no reference, and l is)
-                        if (up) m->ref[c] = top;
-                    }
-                    if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, m, p, 8));
-                    named_bar_sync(bar, kLSoftmax / 2);
-#pragma unroll
-                    for (int c = 0; c < NC; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&m->alpha[c0 + c]), y = *reinterpret_cast<const float4 *>(&m->ref[c0 + c]);
-                        const float fs[4] = {f.x, f.y, f.z, f.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            l[c + i] *= fs[i];
-                            ref[c + i] = ys[i];
-                            x[c + i] = __uint_as_float(sv[c + i]) - ys[i];
+                        for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(sv[c]);
+                        const float most_of = reduce_keys<NC, true>(x, lane);
+                        if ((lane & 15) < NC) reinterpret_cast<float *>(&m->col[c0 + (lane & (NC - 1))])[wq] = most_of;
+                        named_bar_sync(bar, kLSoftmax / 2);
+                        if (in_half < NH) {
+                            const int c = hf * NH + in_half;
+                            const float4 y = m->col[c];
+                            const float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)), had = m->ref[c];
+                            const bool up = top > had + kLagL;  // (a column's references follow its own logits alone)
+                            m->alpha[c] = up ? ex2(had - top) : 1.f;  // (0 where there was no reference, and l is)
+                            if (up) m->ref[c] = top;
                         }
-                    }
-                    if (t > s.t0 && ok) {
-                        tc_fence_after();
+                        if (n > 0) ok = __all_sync(0xffffffffu, lwait(&m->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, m, p, 8));
+                        named_bar_sync(bar, kLSoftmax / 2);
+#pragma unroll
+                        for (int c = 0; c < NC; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&m->alpha[c0 + c]), y = *reinterpret_cast<const float4 *>(&m->ref[c0 + c]);
+                            const float fs[4] = {f.x, f.y, f.z, f.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                l[c + i] *= fs[i];
+                                ref[c + i] = ys[i];
+                                x[c + i] = __uint_as_float(sv[c + i]) - ys[i];
+                            }
+                        }
+                        if (i > s.start() && ok) {
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int i = 0; i < R / 128 * (NH / 8); ++i) {
-                            const int cc = hf * NH + i % (NH / 8) * 8;
-                            const uint32_t at = tmem + quarter + C::kColO + i / (NH / 8) * N + cc;
-                            uint32_t ov[8];
-                            tmem_ld8(at, ov);
-                            tmem_ld_wait();
+                            for (int i = 0; i < R / 128 * (NH / 8); ++i) {
+                                const int cc = hf * NH + i % (NH / 8) * 8;
+                                const uint32_t at = tmem + quarter + C::kColO + i / (NH / 8) * N + cc;
+                                uint32_t ov[8];
+                                tmem_ld8(at, ov);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
-                            tmem_st8(at, ov);
+                                for (int c = 0; c < 8; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * m->alpha[cc + c]);
+                                tmem_st8(at, ov);
+                            }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
+                    }
+                    if (split) {
+                        // The part of a weight that its first 8 bits hold, or what is left (no less than 0): their logarithms,
+                        // as exponents of what follows, which rounds the first back to itself.  (In this branch, so that the
+                        // usual tile pays one predicate: 256 requests 207 us, 211 with a choice behind the exponential.)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            const float w = ex2(x[c]), first = __uint_as_float(__float_as_uint(w) & 0xFFFF0000u);
+                            const bool few = m->lim[c0 + c] < kPreciseKeys;
+                            if (few) x[c] = __log2f(i < 0 ? first : w - first);
+                            else if (i == 0) x[c] = -INFINITY;
+                        }
                     }
                 }
                 // weights, rounded to bf16 for the product; what they are divided by sums the rounded ones

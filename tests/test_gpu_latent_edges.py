@@ -235,3 +235,41 @@ def test_a_timeout_shows_behind_an_earlier_error(pkv, heads, seq):
     assert pkv.get_device_error(c.ws) & TIMEOUT
     c.ws[0] = 0
     c.check(again)
+
+
+# ----------------------------------------------------------------------------------------
+# rows of few keys
+
+
+def few_keys(q, rows, latent, scale, seen):
+    """(o, bound) as latent_reference.attend, for rows of fewer than 32 keys: their weights are two bf16 numbers, the second
+    the rounding of what the first leaves, and so within 2^-16 of themselves (2^-8 of the 2^-8 that is left)."""
+    n, heads, width = q.shape
+    o, bound = np.zeros((n, heads, latent)), np.zeros((n, heads, latent))
+    for i in range(n):
+        k = rows[:int(seen[i])]
+        v = k[:, :latent]
+        s = q[i] @ k.T * scale
+        w = np.exp(s - s.max(-1, keepdims=True))
+        p = w / w.sum(-1, keepdims=True)
+        o[i] = p @ v
+        logit = (width + 4) * 2.0 ** -24 * scale * (np.abs(q[i]) @ np.abs(k).T).max(-1)
+        err = 2.0 ** -16 + 2 * logit + 2.0 ** -21
+        spread = np.stack([p[h] @ np.abs(v - o[i, h]) for h in range(heads)])
+        bound[i] = 2.0 ** -8 * np.abs(o[i]) + err[:, None] * spread + (len(k) + 8) * 2.0 ** -24 * (p @ np.abs(v)) + 1e-37
+    return o, bound
+
+
+@pytest.mark.parametrize("heads,latent", [(16, 512), (20, 256), (128, 512), (1, 512)])
+def test_weights_of_rows_of_few_keys(pkv, heads, latent):
+    """Decode over short contexts, and the first tokens of prompts."""
+    lengths = np.arange(1, 34)
+    for c in (Case(pkv, heads, latent, 16, lengths, seed=heads), Case(pkv, heads, latent, 1, [40, 3, 100], [40, 3, 90], seed=heads)):
+        o = values(c.run())
+        assert pkv.get_device_error(c.ws) == 0
+        for i in range(len(c.seq)):
+            seen = c.seq[i] - c.new[i] + np.arange(c.new[i]) + 1
+            few = np.flatnonzero(seen < 32)
+            want, bound = few_keys(c.qv[c.qo[i] + few], c.data[c.slots(i)], latent, float(np.float32(c.scale)), seen[few])
+            assert np.all(np.abs(o[c.qo[i] + few] - want) <= bound), i
+        c.check(torch.from_numpy(o).cuda())
