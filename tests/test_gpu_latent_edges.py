@@ -273,3 +273,145 @@ def test_weights_of_rows_of_few_keys(pkv, heads, latent):
             want, bound = few_keys(c.qv[c.qo[i] + few], c.data[c.slots(i)], latent, float(np.float32(c.scale)), seen[few])
             assert np.all(np.abs(o[c.qo[i] + few] - want) <= bound), i
         c.check(torch.from_numpy(o).cuda())
+
+
+# ----------------------------------------------------------------------------------------
+# sizes that take other code
+
+
+@pytest.mark.parametrize("heads,dim,rot,layout", [(32, 64, 64, "half"), (3, 72, 16, "interleaved"), (1, 64, 64, "interleaved"), (2, 16, 16, "half")])
+@pytest.mark.parametrize("times", [1, 2])
+def test_rope_past_one_pass_of_the_grid(pkv, sms, heads, dim, rot, layout, times):
+    """32 blocks an SM of 8 warps, a token or several each: the next ones after them."""
+    units = rot // 16 + ((dim - rot) // 8 + 1) // 2
+    lanes = 1 << (units - 1).bit_length()
+    per = min(32 // lanes, 1 << (heads - 1).bit_length())
+    n = sms * 256 * (32 // (lanes * per)) * times + 5
+    rope = pkv.Rope(rot, layout=layout)
+    x, xv = draws((n, heads, dim), n)
+    pos = np.random.default_rng(n).integers(0, 2 ** 18, n)
+    got = values(pkv.rope(x, dev(pos), rope))
+    for at in range(0, n, 65536):
+        part = slice(at, at + 65536)
+        want, slack = ref.rotate(xv[part], pos[part], rope.inv_freq, layout == "interleaved")
+        near(got[part], want, slack)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("hq,hkv,d,layout", [(4, 2, 64, "half"), (0, 1, 64, "interleaved")])
+def test_rope_store_past_one_pass_of_the_grid(pkv, sms, dtype, hq, hkv, d, layout):
+    rope = pkv.Rope(d, layout=layout)
+    n = sms * 256 * (1 if hq else 4) + 77
+    rng = np.random.default_rng(n)
+    pool = pkv.Pool.allocate(n + 40, hkv, d, dtype, *((0.013, 0.5) if dtype != "bf16" else (1.0, 1.0)))
+    qkv, xv = draws((n, hq + 2 * hkv, d), n, 4.0)
+    loc = rng.permutation(n + 40)[:n]
+    padded = rng.random(n) < 0.1
+    loc[padded] = -1
+    loc[n - 3] = n + 40                    # one out of range, in the last step
+    live = ~padded
+    live[n - 3] = False
+    pos, ws = rng.integers(0, 2 ** 18, n), words()
+    q_out = torch.full((n, hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    pkv.rope_store(pool, qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], dev(pos), dev(loc), rope, q_out=q_out, workspace=ws)
+    assert pkv.get_device_error(ws) == SLOT_RANGE
+    want, slack = ref.rotate(xv, pos, rope.inv_freq, layout == "interleaved")
+    turned = live.copy()
+    turned[n - 3] = True
+    if hq:
+        near(values(q_out)[turned], want[turned, :hq], slack[turned, :hq])
+        assert np.all(values(q_out)[~turned] == 9.0)
+    at = torch.from_numpy(loc[live]).cuda()
+    for t, w, sl, scale in ((pool.k, want[:, hq:hq + hkv], slack[:, hq:hq + hkv], pool.k_scale), (pool.v, xv[:, hq + hkv:], 0 * xv[:, :hkv], pool.v_scale)):
+        if dtype == "bf16":
+            near(values(t[at]), w[live], sl[live])
+        else:
+            s32 = float(np.float32(scale))
+            e4m3_near(t[at].contiguous(), w[live] / s32, sl[live] / s32 + 2.0 ** -23 * np.abs(w[live] / s32))
+        rest = torch.ones(n + 40, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert bool((t[rest] == 0).all())
+
+
+@pytest.mark.parametrize("latent,layout,normed,extra", [(512, "half", True, 5), (512, "interleaved", True, 20547), (256, "half", False, 0),
+                                                        (256, "interleaved", True, 1), (512, "half", True, -1)])
+def test_latent_store_of_many_tokens(pkv, sms, latent, layout, normed, extra):
+    """Eight tokens a warp from 128 an SM on, the last warp's fewer; and one less."""
+    n = sms * 128 + extra
+    rope = pkv.Rope(64, layout=layout, scaling=YARN)
+    rng = np.random.default_rng(n)
+    pool, ws = pkv.LatentPool.allocate(n + 30, latent), words()
+    pool.rows.fill_(5.0)
+    rows, rv = draws((n, latent + 64), n, 3.0)
+    w, wv = draws((latent,), 3)
+    loc = rng.permutation(n + 30)[:n]
+    padded = rng.random(n) < 0.1
+    loc[padded] = -1
+    loc[n - 2] = n + 30
+    live = ~padded
+    live[n - 2] = False
+    pos = rng.integers(0, 10 ** 6, n)
+    pkv.latent_store(pool, rows[:, :latent], rows[:, latent:], dev(pos), dev(loc), rope, norm_weight=w if normed else None, workspace=ws)
+    assert pkv.get_device_error(ws) == SLOT_RANGE
+    at = torch.from_numpy(loc[live]).cuda()
+    got = values(pool.rows[at])
+    want, slack = ref.normalise(rv[:, :latent], wv, 1e-6) if normed else (rv[:, :latent], 0 * rv[:, :latent])
+    near(got[:, :latent], want[live], slack[live])
+    turned, slack = ref.rotate(rv[:, None, latent:], pos, rope.inv_freq, layout == "interleaved", rope.magnitude)
+    near(got[:, latent:], turned[live, 0], slack[live, 0])
+    rest = torch.ones(n + 30, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert bool((pool.rows[rest] == 5.0).all())
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_more_requests_than_a_range_keeps(pkv, heads):
+    """Over a hundred requests a range, empty ones and short ones, and runs of requests without new tokens."""
+    rng = np.random.default_rng(heads)
+    seq = rng.integers(0, 4, 16000)
+    seq[5000] = 300
+    c = Case(pkv, heads, 256, 1, seq, seed=heads)
+    c.check(c.run(), list(range(0, 16000, 41)) + [4999, 5000, 5001, 15999])
+    new = np.minimum(rng.integers(0, 3, 16000), seq)
+    new[2000:2300] = new[9000:12000] = new[-500:] = 0
+    c = Case(pkv, heads, 256, 1, seq, new, seed=heads)
+    c.check(c.run(), [i for i in range(0, 16000, 7) if new[i]] + [5000])
+
+
+@pytest.mark.parametrize("heads,length", [(32, 60000), (16, 100001), (128, 9000), (200, 30000), (1, 700)])
+def test_every_tile_of_a_long_request_counts(pkv, heads, length):
+    """One key of each 64 outweighs the rest, all of them alike, and has a 1 in its own element of the latent: an element is the
+    share of the tiles that have it, and a tile lost or counted twice changes its element by half of it or more."""
+    c = Case(pkv, heads, 512, 64, [length, 10, 4000, 128], seed=9)
+    tiles = -(-length // 64)
+    rng = np.random.default_rng(1)
+    rows = np.zeros((length, 576))
+    own = [t * 64 + int(rng.integers(0, min(64, length - t * 64))) for t in range(tiles)]
+    rows[own, np.arange(tiles) % 512] = 1.0
+    rows[own, 512] = 100.0                 # a logit of 100 beside 0: e^-100 of the others' weights is left
+    c.pool.rows[torch.from_numpy(c.slots(0)).cuda()] = torch.from_numpy(rows.astype(np.float32)).cuda().to(torch.bfloat16)
+    q = np.zeros(576)
+    q[512] = 1.0 / c.scale                 # 24: exact
+    c.q[0] = torch.from_numpy(q.astype(np.float32)).cuda().to(torch.bfloat16)
+    o = c.run()
+    want = np.bincount(np.arange(tiles) % 512, minlength=512) / tiles
+    got = values(o)[0]
+    # equal weights of 1 and their sums are exact; what is left is the output's rounding, and the division's
+    assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -20) * want + 1e-30)
+    c.check(o, [1, 2, 3])
+
+
+def test_a_request_left_out_leaves_the_others(pkv):
+    """Offsets out of range: that request's rows stay as they were, the others are right."""
+    c = Case(pkv, 16, 512, 16, [100, 80, 60], [2, 3, 4], seed=5)
+    for qo, good in (([0, 2, 5, 40], [0, 1]), ([-4, 2, 5, 9], [1, 2]), ([0, 2, 1, 1], [0]), ([5, 2, 5, 9], [1, 2])):
+        o = torch.full((9, 16, 512), 11.0, dtype=torch.bfloat16, device="cuda")
+        ws = c.workspace()
+        pkv.attn_latent(c.pool, c.batch(), c.q, o, c.scale, ws, qo_indptr=dev(qo))
+        assert pkv.get_device_error(ws) == POSITION
+        got, rest = values(o), np.ones(9, bool)
+        for i in good:
+            w, bound = c.want(i)
+            assert np.all(np.abs(got[qo[i]:qo[i + 1]] - w) <= bound), (qo, i)
+            rest[qo[i]:qo[i + 1]] = False
+        assert np.all(got[rest] == 11.0), qo
