@@ -481,6 +481,11 @@ int pkv_rope_store(const pkv_pool *pool, const pkv_rope_spec *rope, const void *
                    int64_t v_token_stride, const int32_t *positions, const int32_t *out_cache_loc, int64_t n,
                    void *workspace, void *stream);
 
+/* Zeros in the rows of padded tokens (out_cache_loc -1), which pkv_rope_store leaves as they are: num_heads heads of
+ * dim elements, bf16, laid out as pkv_rope's out.  Nothing else is written. */
+int pkv_zero_padded(void *out, int64_t token_stride, int64_t head_stride, int32_t num_heads, int32_t dim,
+                    const int32_t *out_cache_loc, int64_t n, void *stream);
+
 /* ------------------------------------------------------------------------------------ */
 /* the latent pool: keys and values of all heads from one vector a token                  */
 /*                                                                                      */

@@ -389,18 +389,17 @@ def _where(stream):
     return torch, device, _raw_stream(device) if stream is None else _stream(stream)
 
 
-def _made(shape, device, stream, zeroed=False):
+def _made(shape, device, stream):
     """A bf16 tensor for the output of a call on this stream.  On another stream than the current one it comes from that
     stream's memory: the current one's may still be read by what is queued there.  The current stream's use of it
     is recorded, as its reader is likely there."""
     torch = _torch
-    make = torch.zeros if zeroed else torch.empty
     if stream == _raw_stream(device):
-        return make(shape, dtype=torch.bfloat16, device=device)
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
     # (an ExternalStream of handle 0 would be a stream of the pool)
     at = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
     with torch.cuda.stream(at):
-        out = make(shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
     out.record_stream(torch.cuda.current_stream(device))
     return out
 
@@ -614,9 +613,9 @@ def rope(x, positions, rope, out=None, stream=None):
 
 def rope_store(pool: Pool, q, k_new, v_new, positions, out_cache_loc, rope, q_out=None, workspace=None, stream=None):
     """Rotates q [n, num_q_heads, head_dim] and k_new [n, heads, head_dim] and stores the rotated k and v_new into
-    the slots out_cache_loc, in one pass; the tensors may be slices of one projection's rows.  Returns q_out; it may be
-    q, and is a new tensor of zeros by default (a pass over it that a q_out of one's own saves).  A token whose slot is -1
-    is padding: nothing of it is touched (see pkv_rope_store)."""
+    the slots out_cache_loc, in one pass; the tensors may be slices of one projection's rows.  Returns q_out, a new
+    tensor by default; it may be q.  A token whose slot is -1 is padding: nothing of it is touched (see pkv_rope_store);
+    its row of a new q_out is zeros."""
     torch, device, stream = _where(stream)
     if not isinstance(pool.k, torch.Tensor) or pool.k.get_device() != device or pool.v.get_device() != device:
         raise ValueError("Pool is not on the current CUDA device")
@@ -629,16 +628,19 @@ def rope_store(pool: Pool, q, k_new, v_new, positions, out_cache_loc, rope, q_ou
     for name, st in (("k_new", sk), ("v_new", sv)):
         if p.num_kv_heads > 1 and st[1] != p.head_dim:
             raise ValueError(f"{name} must have its heads side by side")
-    if q_out is None:
-        q_out = _made(shape, device, stream, zeroed=True)  # padded tokens' rows are not written
+    made = q_out is None
+    if made:
+        q_out = _made(shape, device, stream)
     to, so = _rows("q_out", q_out, device, shape)
     ws, size = (None, 4) if workspace is None else _space(workspace, device)
     if size < 4:
         raise ValueError("workspace must hold the error word (4 bytes)")
+    loc = _fits("out_cache_loc", out_cache_loc, torch.int32, device, (n,))
     check("pkv_rope_store", lib.pkv_rope_store(
-        p, spec, at, s[0], s[1], to, so[0], so[1], hq, k, sk[0], v, sv[0],
-        _fits("positions", positions, torch.int32, device, (n,)), _fits("out_cache_loc", out_cache_loc, torch.int32, device, (n,)),
+        p, spec, at, s[0], s[1], to, so[0], so[1], hq, k, sk[0], v, sv[0], _fits("positions", positions, torch.int32, device, (n,)), loc,
         n, ws, stream))
+    if made:  # padded tokens' rows hold what the memory held
+        check("pkv_zero_padded", lib.pkv_zero_padded(to, so[0], so[1], hq, p.head_dim, loc, n, stream))
     return q_out
 
 

@@ -104,6 +104,7 @@ SIGNATURES = {
     "pkv_rope": (C.c_int, [C.POINTER(PkvRopeSpec), _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _P]),
     "pkv_rope_store": (C.c_int, [C.POINTER(PkvPool), C.POINTER(PkvRopeSpec), _P, _I64, _I64, _P, _I64, _I64, _I32, _P,
                                  _I64, _P, _I64, _P, _P, _I64, _P, _P]),
+    "pkv_zero_padded": (C.c_int, [_P, _I64, _I64, _I32, _I32, _P, _I64, _P]),
     "pkv_latent_store": (C.c_int, [C.POINTER(PkvLatentPool), C.POINTER(PkvRopeSpec), _P, _I64, _P, _I64, _P, _F, _P, _P,
                                    _I64, _P, _P]),
     "pkv_latent_workspace": (C.c_int, [C.POINTER(PkvLatentPool), _I32, C.POINTER(_SZ)]),

@@ -216,6 +216,23 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
     }
 }
 
+// Rows of padded tokens, heads of d elements, to zeros: a lane looks at a token's slot, a warp writes a row.
+__global__ void __launch_bounds__(256) zero_padded_kernel(uint16_t *out, int64_t tok_stride, int64_t head_stride, int32_t heads,
+                                                          int32_t vecs, const int32_t *loc, int64_t n) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) & ~(int64_t)31; first < n; first += step) {
+        uint32_t padded = __ballot_sync(0xffffffffu, first + lane < n && ld(loc + first + lane) == -1);
+        for (; padded; padded &= padded - 1) {
+            uint16_t *row = out + (first + __ffs(padded) - 1) * tok_stride;
+            for (int v = lane; v < heads * vecs; v += 32)
+                *reinterpret_cast<uint4 *>(row + v / vecs * head_stride + v % vecs * 8) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
 static int check_spec(const pkv_rope_spec *r) {
     if (!r || !r->phases || reinterpret_cast<uintptr_t>(r->phases) & 7) return PKV_E_INVALID;
     if (r->rotary_dim <= 0 || r->rotary_dim % 16) return PKV_E_UNSUPPORTED;
@@ -440,6 +457,20 @@ extern "C" int pkv_rope_store(const pkv_pool *pool, const pkv_rope_spec *rope, c
     p.n = n;
     p.err = static_cast<int32_t *>(workspace);
     return launch_rope(p, rope, pool->dtype == PKV_BF16 ? 1 : 2, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int pkv_zero_padded(void *out, int64_t token_stride, int64_t head_stride, int32_t num_heads, int32_t dim,
+                               const int32_t *out_cache_loc, int64_t n, void *stream) {
+    using namespace pkv;
+    if (n < 0 || num_heads < 0 || dim <= 0) return PKV_E_INVALID;
+    if (dim % 8 || dim > 512 || n >= ((int64_t)1 << 40) || num_heads > 65536) return PKV_E_UNSUPPORTED;
+    if (n == 0 || num_heads == 0) return PKV_OK;
+    if (!out_ok(out, token_stride, head_stride, n, num_heads) || !out_cache_loc) return PKV_E_INVALID;
+    const int64_t blocks = std::min<int64_t>((n + 255) / 256, (int64_t)num_sms() * 8);
+    return launch_pdl(zero_padded_kernel, dim3((unsigned)blocks), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true,
+                      static_cast<uint16_t *>(out), token_stride, head_stride, num_heads, dim / 8, out_cache_loc, n) == cudaSuccess
+               ? PKV_OK
+               : PKV_E_CUDA;
 }
 
 extern "C" int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec *rope, const void *c_new, int64_t c_token_stride,

@@ -159,6 +159,21 @@ def test_every_call_runs_on_the_stream_it_is_given(pkv):
     assert torch.equal(pool.rows.flip(0)[:, :512], rows[:, :512]) and torch.equal(o, clean)
 
 
+@pytest.mark.parametrize("n", [1, 31, 33, 5000, 400000])
+def test_padded_rows_alone_are_zeroed(pkv, n):
+    from prefix_shared_kv_token_gb300 import _lib
+    rng = np.random.default_rng(n)
+    loc = rng.integers(-2, 3, n)
+    for heads, dim, wide in ((3, 64, 72), (1, 24, 24)):
+        held = torch.full((n, heads + 1, wide), 7.0, dtype=torch.bfloat16, device="cuda")
+        at, st = dev(loc), held.stride()
+        rc = _lib.lib.pkv_zero_padded(held.data_ptr(), st[0], st[1], heads, dim, at.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        want = torch.full_like(held, 7.0)
+        want[at == -1, :heads, :dim] = 0
+        assert torch.equal(held, want)
+
+
 @pytest.mark.parametrize("aside", [False, True])
 def test_rows_of_padded_tokens_are_zeros_in_a_new_output(pkv, aside):
     rope = pkv.Rope(64)

@@ -42,3 +42,17 @@ def test_phases_of_any_sign_are_a_doubles():
         off = (Fraction(a, 1 << 64) - turns + Fraction(1, 2)) % 1 - Fraction(1, 2)
         assert abs(off) <= turns / (1 << 52) + Fraction(1, 1 << 65), f
         assert (a + b) % (1 << 64) == 0, f         # turns back by as much
+
+
+def test_zero_padded_refusals():
+    P = 0x10000                                    # stands for a device address (never read)
+
+    def call(out=P, tok=1024, head=128, heads=8, dim=128, loc=P, n=4):
+        return lib.pkv_zero_padded(out, tok, head, heads, dim, loc, n, None)
+
+    for kw in (dict(out=None), dict(out=P + 8), dict(tok=0), dict(tok=1020), dict(head=0), dict(head=4), dict(heads=-1), dict(dim=0),
+               dict(loc=None), dict(n=-1)):
+        assert call(**kw) == -1, kw
+    for kw in (dict(dim=132), dict(dim=520), dict(heads=65537), dict(n=1 << 40)):
+        assert call(**kw) == -2, kw
+    assert call(n=0, out=None) == 0 and call(heads=0, out=None) == 0
