@@ -527,9 +527,10 @@ int pkv_latent_store(const pkv_latent_pool *pool, const pkv_rope_spec *rope, con
  * are.  A token that sees no position (length 0, or more new tokens than positions) gets zeros, and so do the
  * tokens of a request whose row or length is out of range, which also sets PKV_DERR_POSITION; a request whose offsets are
  * out of range is left out and sets it too.  A slot outside the pool reads as a zero row and sets PKV_DERR_SLOT_RANGE.
- * Logits and sums are fp32, weights bf16 (their sum, which divides, is of the rounded ones), and two bf16 parts
- * for tokens that see fewer than 32 positions.  A NaN or an
- * infinity in a row reaches the tokens that see it and no others.  Latents times 2^8 times the context's
+ * Logits and sums are fp32, weights bf16 (their sum, which divides, is of the rounded ones), in two bf16 parts for
+ * tokens that see fewer than 32 positions.  A NaN or an infinity in a row reaches the tokens that see it and no
+ * others; under a logit of -inf (an infinity in the rotary key) a row has no weight, and a token all of whose
+ * logits are -inf gets NaN.  Latents times 2^8 times the context's
  * length have to stay in fp32's range.
  * Every new token costs num_heads * (2 latent_dim + rope_dim) products a position: for whole prompts,
  * multiplying the latents out into keys and values a head costs fewer (from some 170 new tokens on).

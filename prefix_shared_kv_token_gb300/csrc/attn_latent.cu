@@ -60,12 +60,13 @@ constexpr int kLTile = 64;              // keys a tile
 constexpr int kLThreads = 384;
 constexpr int kLSoftmax = 256;          // threads of the softmax warps
 constexpr int kLBarHalf = 1;            // named barriers of the softmax warps' halves: 1 and 2
-constexpr float kLUnset = -3.4028234e38f;  // a reference before any key was seen: below every finite logit
+constexpr float kLUnset = -3.4028234e38f;  // a reference before any key was seen: no finite logit is below it
 constexpr int kLCached = 64;            // requests of a range that are kept in shared memory
 constexpr int kLMaxCtas = 160;          // the lists of latent_merge_kernel
 constexpr int32_t kLLongest = 0x7FFFFF00;  // keys of a request: tiles' ends stay within 32 bits
-// What a unit counts in the line beside its tiles, for its start and its output: 32 requests of 500 to 1,500 keys take 25.7 us
-// with 0, 22.6 with 2; 64 of 1 to 200 keys 16.9 and 14.5.
+// What a unit counts in the line beside its tiles, for its start and its output: 32 requests of 500 to 1,500 keys and 32 heads
+// take 21.2 us with 0, 18.8 with 2 and 19.6 with 3; 64 of 1 to 200 keys 19.0, 15.0 and 15.4; 256 of 1,200 to 3,000 keys and 128
+// heads 214, 211 and 213.
 constexpr int kLUnitTiles = 2;
 constexpr int kLMinTiles = 2;           // a range's tiles at least
 constexpr float kLog2eL = 1.4426950408889634f;

@@ -126,6 +126,8 @@ PKV_DEV void store8_e4m3(uint8_t *dst, const float *x, float scale) {
 }
 
 // STORE 0: rotate q only; 1, 2: k and v into a bf16 or an e4m3 pool too.
+// Three CTAs an SM leave 80 registers, of which each form spills 20 to 120 bytes; with two and no spills 65,536 tokens take
+// 257 us into an e4m3 pool, not 234, 236 into a bf16 one, not 240, and rope of 262,144 tokens of one head 24, not 21.
 template <bool INTER, int STORE>
 __global__ void __launch_bounds__(256, 3) rope_kernel(const RopeParams p) {
     pdl_wait();
