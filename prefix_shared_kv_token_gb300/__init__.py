@@ -561,6 +561,8 @@ class Rope:
             pair = lambda turns: dim * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
             lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), dim - 1)
             ramp = np.clip((np.arange(dim // 2) - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+            if pair(slow) < 0:
+                ramp[:] = 1.0      # the first pair, too, turns fewer times
             freq = freq * (1 - ramp) + freq / factor * ramp
             magnitude = float(opts.pop("magnitude", 0.1 * math.log(factor) + 1.0))
         if opts:

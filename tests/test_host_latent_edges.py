@@ -4,7 +4,9 @@ import ctypes as C
 from fractions import Fraction
 
 import numpy as np
+import pytest
 
+import prefix_shared_kv_token_gb300 as pkv
 from prefix_shared_kv_token_gb300 import _lib
 
 lib = _lib.lib
@@ -56,3 +58,17 @@ def test_zero_padded_refusals():
     for kw in (dict(dim=132), dict(dim=520), dict(heads=65537), dict(n=1 << 40)):
         assert call(**kw) == -2, kw
     assert call(n=0, out=None) == 0 and call(heads=0, out=None) == 0
+
+
+@pytest.mark.parametrize("original,fast,slow", [(4096, 32, 1), (6, 32, 1), (3, 32, 1), (100, 64, 32), (100, 20, 15), (10 ** 9, 32, 1)])
+def test_yarn_keeps_fast_pairs_and_divides_slow_ones(original, fast, slow):
+    """Also where no pair is fast, or all are, within the original context."""
+    plain = pkv.Rope(64, device="cpu").inv_freq
+    ratio = pkv.Rope(64, scaling=dict(kind="yarn", factor=8, original=original, beta_fast=fast, beta_slow=slow), device="cpu").inv_freq / plain
+    turns = original * plain / (2 * np.pi)
+    # the ramp's ends are whole pairs, one further out at most
+    step = 10000.0 ** (1 / 32)
+    assert np.allclose(ratio[turns > fast * step], 1.0, rtol=1e-15) and np.allclose(ratio[turns < slow / step], 1 / 8, rtol=1e-15)
+    assert np.all((ratio <= 1 + 1e-15) & (ratio >= 1 / 8 - 1e-15) & (np.diff(ratio, prepend=1.0) <= 1e-15))
+    if turns.max() < slow:
+        assert np.allclose(ratio, 1 / 8, rtol=1e-15)
